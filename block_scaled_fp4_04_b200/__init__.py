@@ -27,7 +27,7 @@ F32, BF16 = 0, 1
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_CUDA, ERR_TIMEOUT, ERR_NONFINITE = range(6)
 GEMM_WEIGHTS_READY = 1
 QUANT_E8M0_FLOOR = 1
-ACT_NONE, ACT_RELU = 0, 1
+ACT_NONE, ACT_RELU, ACT_SILU, ACT_GELU, ACT_GELU_TANH = range(5)
 _STATUS_NAMES = {0: "FP4_OK", 1: "FP4_ERR_INVALID_ARG", 2: "FP4_ERR_UNSUPPORTED", 3: "FP4_ERR_CUDA",
                  4: "FP4_ERR_TIMEOUT", 5: "FP4_ERR_NONFINITE"}
 
@@ -76,6 +76,21 @@ def lib() -> ctypes.CDLL:
                 "fp4_gemm_bf16a_workspace_size": (SZ, [I64, I64, I64]),
                 "fp4_gemm_bf16a": (I32, [P, P, P, P, I64, I64, I64, P, I32, P, P, P, P, SZ, ctypes.c_uint, P]),
                 "fp4_gemm_grouped": (I32, [I32, I32, P, P, P, P, P, P, P, I64, I64, I64, P, I32, P, SZ, P]),
+                "fp4_gemm_epilogue_ex": (I32, [I32, P, P, P, P, P, P, I64, I64, I64, P, I32, P, I32, P, I32, P, P, P, P,
+                                               P, P, SZ, ctypes.c_uint, P]),
+                "fp4_gemm_gated_workspace_size": (SZ, [I64, I64, I64, I32, I32]),
+                "fp4_gemm_gated": (I32, [I32, P, P, P, P, P, P, P, P, P, I64, I64, I64, P, P, I32, P, I32, P, P, P, P, P,
+                                         P, P, SZ, ctypes.c_uint, P]),
+                "fp4_gemm_gated_bf16a_workspace_size": (SZ, [I64, I64, I64]),
+                "fp4_gemm_gated_bf16a": (I32, [P, P, P, P, P, P, P, I64, I64, I64, P, P, I32, P, I32, P, P, P, P, P, P,
+                                               SZ, ctypes.c_uint, P]),
+                "fp4_gemm_gated_grouped": (I32, [I32, I32, P, P, P, P, P, P, P, P, P, P, I64, I64, I64, P, P, I32, P,
+                                                 I32, P, P, P]),
+                "fp4_act_backward_workspace_size": (SZ, [I64, I64, I32]),
+                "fp4_act_backward": (I32, [P, P, P, I64, I64, I32, I32, P, I32, P, I32, P, P, P, P, P, SZ, P]),
+                "fp4_layernorm": (I32, [P, I64, I64, I32, P, P, ctypes.c_float, P, I32, P, P, I32, P, P, P, P, P]),
+                "fp4_layernorm_backward_workspace_size": (SZ, [I64, I64]),
+                "fp4_layernorm_backward": (I32, [P, P, I64, I64, I32, P, P, P, P, P, I32, P, P, P, SZ, P]),
                 "fp4_get_status": (I32, [P]),
                 "fp4_debug_encode": (I32, [P, I64, I32, P, P]),
                 "fp4_debug_stall_next_decode": (I32, [I32]),
@@ -220,6 +235,72 @@ def fp4_gemm_bf16a(X, B, sB, gB, M, N, K, D, out_dtype, Xcodes, Xscales, gX, wor
                    stream=None):
     _check(lib().fp4_gemm_bf16a(_p(X), _p(B), _p(sB), _p(gB), M, N, K, _p(D), out_dtype, _p(Xcodes), _p(Xscales),
                                 _p(gX), _p(workspace), workspace_bytes, flags, _s(stream)))
+
+
+def fp4_gemm_epilogue_ex(fmt, A, sA, gA, B, sB, gB, M, N, K, bias, act, residual, residual_dtype, D, out_dtype,
+                         pre=None, Dcodes=None, Dscales=None, gD=None, amax_out=None, workspace=None,
+                         workspace_bytes=0, flags=0, stream=None):
+    _check(lib().fp4_gemm_epilogue_ex(fmt, _p(A), _p(sA), _p(gA), _p(B), _p(sB), _p(gB), M, N, K, _p(bias), act,
+                                      _p(residual), residual_dtype, _p(D), out_dtype, _p(pre), _p(Dcodes), _p(Dscales),
+                                      _p(gD), _p(amax_out), _p(workspace), workspace_bytes, flags, _s(stream)))
+
+
+def fp4_gemm_gated_workspace_size(M: int, F: int, K: int, fmt: int, rows_in_place: bool) -> int:
+    return int(lib().fp4_gemm_gated_workspace_size(M, F, K, fmt, 1 if rows_in_place else 0))
+
+
+def fp4_gemm_gated(fmt, A, sA, gA, Wg, sWg, gWg, Wu, sWu, gWu, M, F, K, bias_g, bias_u, act, H, out_dtype, G=None,
+                   U=None, Hcodes=None, Hscales=None, gH=None, amax_out=None, workspace=None, workspace_bytes=0,
+                   flags=0, stream=None):
+    _check(lib().fp4_gemm_gated(fmt, _p(A), _p(sA), _p(gA), _p(Wg), _p(sWg), _p(gWg), _p(Wu), _p(sWu), _p(gWu), M, F,
+                                K, _p(bias_g), _p(bias_u), act, _p(H), out_dtype, _p(G), _p(U), _p(Hcodes),
+                                _p(Hscales), _p(gH), _p(amax_out), _p(workspace), workspace_bytes, flags, _s(stream)))
+
+
+def fp4_gemm_gated_bf16a_workspace_size(M: int, F: int, K: int) -> int:
+    return int(lib().fp4_gemm_gated_bf16a_workspace_size(M, F, K))
+
+
+def fp4_gemm_gated_bf16a(X, Wg, sWg, gWg, Wu, sWu, gWu, M, F, K, bias_g, bias_u, act, H, out_dtype, G, U, Xcodes,
+                         Xscales, gX, workspace, workspace_bytes, flags=0, stream=None):
+    _check(lib().fp4_gemm_gated_bf16a(_p(X), _p(Wg), _p(sWg), _p(gWg), _p(Wu), _p(sWu), _p(gWu), M, F, K, _p(bias_g),
+                                      _p(bias_u), act, _p(H), out_dtype, _p(G), _p(U), _p(Xcodes), _p(Xscales),
+                                      _p(gX), _p(workspace), workspace_bytes, flags, _s(stream)))
+
+
+def fp4_gemm_gated_grouped(fmt, num_groups, offsets, A, sA, gA, Wg, sWg, gWg, Wu, sWu, gWu, total_rows, F, K, bias_g,
+                           bias_u, act, H, out_dtype, G=None, U=None, stream=None):
+    _check(lib().fp4_gemm_gated_grouped(fmt, num_groups, _p(offsets), _p(A), _p(sA), _p(gA), _p(Wg), _p(sWg), _p(gWg),
+                                        _p(Wu), _p(sWu), _p(gWu), total_rows, F, K, _p(bias_g), _p(bias_u), act, _p(H),
+                                        out_dtype, _p(G), _p(U), _s(stream)))
+
+
+def fp4_act_backward_workspace_size(rows: int, cols: int, gated: bool) -> int:
+    return int(lib().fp4_act_backward_workspace_size(rows, cols, 1 if gated else 0))
+
+
+def fp4_act_backward(dH, G, U, rows, cols, in_dtype, act, dZ, out_dtype, dbias=None, fmt=NVFP4, codes=None,
+                     scales=None, global_in=None, amax_out=None, workspace=None, workspace_bytes=0, stream=None):
+    _check(lib().fp4_act_backward(_p(dH), _p(G), _p(U), rows, cols, in_dtype, act, _p(dZ), out_dtype, _p(dbias), fmt,
+                                  _p(codes), _p(scales), _p(global_in), _p(amax_out), _p(workspace), workspace_bytes,
+                                  _s(stream)))
+
+
+def fp4_layernorm(x, rows, cols, in_dtype, weight, bias, eps, y, out_dtype, mean=None, rstd=None, fmt=NVFP4,
+                  codes=None, scales=None, global_in=None, amax_out=None, stream=None):
+    _check(lib().fp4_layernorm(_p(x), rows, cols, in_dtype, _p(weight), _p(bias), eps, _p(y), out_dtype, _p(mean),
+                               _p(rstd), fmt, _p(codes), _p(scales), _p(global_in), _p(amax_out), _s(stream)))
+
+
+def fp4_layernorm_backward_workspace_size(rows: int, cols: int) -> int:
+    return int(lib().fp4_layernorm_backward_workspace_size(rows, cols))
+
+
+def fp4_layernorm_backward(dy, x, rows, cols, in_dtype, weight, mean, rstd, dres, dx, out_dtype, dweight=None,
+                           dbias=None, workspace=None, workspace_bytes=0, stream=None):
+    _check(lib().fp4_layernorm_backward(_p(dy), _p(x), rows, cols, in_dtype, _p(weight), _p(mean), _p(rstd), _p(dres),
+                                        _p(dx), out_dtype, _p(dweight), _p(dbias), _p(workspace), workspace_bytes,
+                                        _s(stream)))
 
 
 def fp4_gemm_noalloc(fmt, A, sA, gA, B, sB, gB, M, N, K, D, out_dtype, stream=None):

@@ -7,6 +7,7 @@
 
 #include "fp4.h"
 #include "fp4_internal.h"
+#include "fp4_ops.h"
 #include "fp4_ptx.cuh"
 
 namespace fp4 {
@@ -258,7 +259,8 @@ size_t fp4_gemm_workspace_size(int64_t M, int64_t N, int64_t K, fp4_fmt fmt) {
   return gemm_workspace_bytes(M, N, K, fmt == FP4_MXFP4);
 }
 
-static fp4_status gemm_common(const GemmProblem& g, fp4_fmt fmt, fp4_dtype out_dtype, void* stream) {
+static fp4_status gemm_common(const GemmProblem& g, fp4_fmt fmt, fp4_dtype out_dtype, void* stream,
+                              const GemmFull* full = nullptr) {
   if (fmt != FP4_NVFP4 && fmt != FP4_MXFP4) return fail(FP4_ERR_INVALID_ARG, "fmt");
   if (out_dtype != FP4_F32 && out_dtype != FP4_BF16) return fail(FP4_ERR_INVALID_ARG, "out_dtype");
   if (!g.A || !g.B || !g.sA || !g.sB || (!g.D && !g.q_codes)) return fail(FP4_ERR_INVALID_ARG, "null pointer");
@@ -272,7 +274,7 @@ static fp4_status gemm_common(const GemmProblem& g, fp4_fmt fmt, fp4_dtype out_d
   if (s != FP4_OK) return s;
   const char* why = nullptr;
   cudaError_t err = cudaSuccess;
-  const int rc = launch_gemm(g, status, static_cast<cudaStream_t>(stream), &why, &err);
+  const int rc = launch_gemm_full(GemmProblemFull{g, full}, status, static_cast<cudaStream_t>(stream), &why, &err);
   if (rc == 1) return fail(FP4_ERR_INVALID_ARG, why);
   if (rc == 2) return cuda_fail(err, "gemm launch");
   return FP4_OK;
@@ -345,17 +347,20 @@ fp4_status fp4_gemm(fp4_fmt fmt, const uint8_t* A, const uint8_t* sA, const floa
   return fp4_gemm_ex(fmt, A, sA, gA, B, sB, gB, M, N, K, D, out_dtype, workspace, workspace_bytes, 0u, stream);
 }
 
-fp4_status fp4_gemm_epilogue(fp4_fmt fmt, const uint8_t* A, const uint8_t* sA, const float* gA, const uint8_t* B,
-                             const uint8_t* sB, const float* gB, int64_t M, int64_t N, int64_t K, const float* bias,
-                             fp4_act act, void* D, fp4_dtype out_dtype, uint8_t* Dcodes, uint8_t* Dscales,
-                             const float* gD, float* amax_out, void* workspace, size_t workspace_bytes,
-                             void* stream) {
-  if (act != FP4_ACT_NONE && act != FP4_ACT_RELU) return fail(FP4_ERR_INVALID_ARG, "act");
+static bool act_ok(fp4_act act) { return act >= FP4_ACT_NONE && act <= FP4_ACT_GELU_TANH; }
+static bool dtype_ok(fp4_dtype t) { return t == FP4_F32 || t == FP4_BF16; }
+static bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+static fp4_status epilogue_common(fp4_fmt fmt, const uint8_t* A, const uint8_t* sA, const float* gA, const uint8_t* B,
+                                  const uint8_t* sB, const float* gB, int64_t M, int64_t N, int64_t K,
+                                  const float* bias, fp4_act act, void* D, fp4_dtype out_dtype, uint8_t* Dcodes,
+                                  uint8_t* Dscales, const float* gD, float* amax_out, void* workspace,
+                                  size_t workspace_bytes, unsigned flags, void* stream, const GemmFull* full) {
   if (!D && !Dcodes) return fail(FP4_ERR_INVALID_ARG, "no output: D and Dcodes are both NULL");
   if (Dcodes && (!Dscales || !gD)) return fail(FP4_ERR_INVALID_ARG, "FP4 output needs Dscales and gD");
   if (Dcodes && N % 32 != 0) return fail(FP4_ERR_INVALID_ARG, "FP4 output needs N % 32 == 0");
   if (Dcodes && (!aligned16(Dcodes) || !aligned16(Dscales))) return fail(FP4_ERR_INVALID_ARG, "Dcodes / Dscales alignment");
-  if (bias && (reinterpret_cast<uintptr_t>(bias) & 3u)) return fail(FP4_ERR_INVALID_ARG, "bias alignment");
+  if (bias && !aligned4(bias)) return fail(FP4_ERR_INVALID_ARG, "bias alignment");
   GemmProblem g{};
   g.mx = fmt == FP4_MXFP4;
   g.A = A;
@@ -371,14 +376,15 @@ fp4_status fp4_gemm_epilogue(fp4_fmt fmt, const uint8_t* A, const uint8_t* sA, c
   g.out_bf16 = out_dtype == FP4_BF16;
   g.ws = workspace;
   g.ws_bytes = workspace_bytes;
+  g.weights_ready = (flags & FP4_GEMM_WEIGHTS_READY) ? 1 : 0;
   g.bias = bias;
-  g.act = act == FP4_ACT_RELU ? 1 : 0;
+  g.act = act;
   g.q_codes = Dcodes;
   g.q_scales = Dscales;
   g.q_g = gD;
   g.amax_out = amax_out;
   if (amax_out) {
-    if (reinterpret_cast<uintptr_t>(amax_out) & 3u) return fail(FP4_ERR_INVALID_ARG, "amax_out alignment");
+    if (!aligned4(amax_out)) return fail(FP4_ERR_INVALID_ARG, "amax_out alignment");
     const cudaError_t e = cudaMemsetAsync(amax_out, 0, sizeof(float), static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "zeroing amax_out");
   }
@@ -389,7 +395,389 @@ fp4_status fp4_gemm_epilogue(fp4_fmt fmt, const uint8_t* A, const uint8_t* sA, c
         cudaMemsetAsync(Dscales, 0, fp4_scales_bytes(M, N, FP4_NVFP4), static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "zero-filling the scale pads");
   }
-  return gemm_common(g, fmt, out_dtype, stream);
+  return gemm_common(g, fmt, out_dtype, stream, full);
+}
+
+fp4_status fp4_gemm_epilogue(fp4_fmt fmt, const uint8_t* A, const uint8_t* sA, const float* gA, const uint8_t* B,
+                             const uint8_t* sB, const float* gB, int64_t M, int64_t N, int64_t K, const float* bias,
+                             fp4_act act, void* D, fp4_dtype out_dtype, uint8_t* Dcodes, uint8_t* Dscales,
+                             const float* gD, float* amax_out, void* workspace, size_t workspace_bytes,
+                             void* stream) {
+  if (act != FP4_ACT_NONE && act != FP4_ACT_RELU) return fail(FP4_ERR_INVALID_ARG, "act");
+  return epilogue_common(fmt, A, sA, gA, B, sB, gB, M, N, K, bias, act, D, out_dtype, Dcodes, Dscales, gD, amax_out,
+                         workspace, workspace_bytes, 0u, stream, nullptr);
+}
+
+fp4_status fp4_gemm_epilogue_ex(fp4_fmt fmt, const uint8_t* A, const uint8_t* sA, const float* gA, const uint8_t* B,
+                                const uint8_t* sB, const float* gB, int64_t M, int64_t N, int64_t K, const float* bias,
+                                fp4_act act, const void* residual, fp4_dtype residual_dtype, void* D,
+                                fp4_dtype out_dtype, void* pre, uint8_t* Dcodes, uint8_t* Dscales, const float* gD,
+                                float* amax_out, void* workspace, size_t workspace_bytes, unsigned flags,
+                                void* stream) {
+  if (!act_ok(act)) return fail(FP4_ERR_INVALID_ARG, "act");
+  if (flags & ~static_cast<unsigned>(FP4_GEMM_WEIGHTS_READY)) return fail(FP4_ERR_INVALID_ARG, "unknown flag");
+  if (residual && !dtype_ok(residual_dtype)) return fail(FP4_ERR_INVALID_ARG, "residual_dtype");
+  if (!aligned16(residual) || !aligned16(pre)) return fail(FP4_ERR_INVALID_ARG, "residual and pre must be 16-byte aligned");
+  if (residual && residual == D && residual_dtype != out_dtype)
+    return fail(FP4_ERR_INVALID_ARG, "a residual in D's place needs D's type");
+  if (pre && (pre == D || pre == residual)) return fail(FP4_ERR_INVALID_ARG, "pre must be a buffer of its own");
+  const GemmFull full{residual, residual_dtype == FP4_BF16, pre};
+  // scale, bias and ReLU alone are the plain epilogue
+  const bool plain = !residual && !pre && (act == FP4_ACT_NONE || act == FP4_ACT_RELU);
+  return epilogue_common(fmt, A, sA, gA, B, sB, gB, M, N, K, bias, act, D, out_dtype, Dcodes, Dscales, gD, amax_out,
+                         workspace, workspace_bytes, flags, stream, plain ? nullptr : &full);
+}
+
+size_t fp4_gemm_gated_workspace_size(int64_t M, int64_t F, int64_t K, fp4_fmt fmt, int rows_in_place) {
+  if (M <= 0 || F <= 0 || K <= 0) return 0;
+  return gated_workspace_bytes(M, F, K, fmt == FP4_MXFP4, rows_in_place != 0);
+}
+
+// Checks what every gated product needs; launches it.
+static fp4_status gated_common(GatedProblem& g, fp4_fmt fmt, fp4_act act, fp4_dtype out_dtype, void* stream) {
+  if (fmt != FP4_NVFP4 && fmt != FP4_MXFP4) return fail(FP4_ERR_INVALID_ARG, "fmt");
+  if (!dtype_ok(out_dtype)) return fail(FP4_ERR_INVALID_ARG, "out_dtype");
+  if (!act_ok(act)) return fail(FP4_ERR_INVALID_ARG, "act");
+  if (!g.A || !g.sA || !g.Wg || !g.sWg || !g.Wu || !g.sWu) return fail(FP4_ERR_INVALID_ARG, "null pointer");
+  if (!g.H && !g.q_codes) return fail(FP4_ERR_INVALID_ARG, "no output: H and Hcodes are both NULL");
+  if (!g.G != !g.U) return fail(FP4_ERR_INVALID_ARG, "G and U: both or neither");
+  if (g.G && (g.G == g.U || g.G == g.H || g.U == g.H)) return fail(FP4_ERR_INVALID_ARG, "H, G and U must be different buffers");
+  if (g.M <= 0 || g.F <= 0 || g.K <= 0) return fail(FP4_ERR_INVALID_ARG, "M, F, K must be positive");
+  if (g.K % 32 != 0) return fail(FP4_ERR_INVALID_ARG, "K must be a multiple of 32");
+  const int64_t most = (1ll << 31) - 256;
+  if (g.M > most || g.F > most || g.K > most) return fail(FP4_ERR_UNSUPPORTED, "dimension too large");
+  if (g.num_groups > 0 && g.F > most / g.num_groups) return fail(FP4_ERR_UNSUPPORTED, "too many weight rows");
+  if (!aligned16(g.A) || !aligned16(g.sA) || !aligned16(g.Wg) || !aligned16(g.sWg) || !aligned16(g.Wu) ||
+      !aligned16(g.sWu) || !aligned16(g.H) || !aligned16(g.G) || !aligned16(g.U))
+    return fail(FP4_ERR_INVALID_ARG, "A, weights, scales, H, G and U must be 16-byte aligned");
+  if (!aligned4(g.bias_g) || !aligned4(g.bias_u)) return fail(FP4_ERR_INVALID_ARG, "bias alignment");
+  if (g.q_codes && (!g.q_scales || !g.q_g)) return fail(FP4_ERR_INVALID_ARG, "FP4 output needs Hscales and gH");
+  if (g.q_codes && g.F % 32 != 0) return fail(FP4_ERR_INVALID_ARG, "FP4 output needs F % 32 == 0");
+  if (g.q_codes && (!aligned16(g.q_codes) || !aligned16(g.q_scales))) return fail(FP4_ERR_INVALID_ARG, "Hcodes / Hscales alignment");
+  if (!aligned4(g.amax_out)) return fail(FP4_ERR_INVALID_ARG, "amax_out alignment");
+  g.mx = fmt == FP4_MXFP4;
+  g.act = act;
+  g.out_bf16 = out_dtype == FP4_BF16;
+  if (g.num_groups == 0) {
+    const size_t need = gated_workspace_bytes(g.M, g.F, g.K, g.mx, g.q_codes || g.amax_out);
+    if (need && (!g.ws || g.ws_bytes < need || !aligned16(g.ws)))
+      return fail(FP4_ERR_INVALID_ARG, "workspace too small or misaligned (see fp4_gemm_gated_workspace_size)");
+  }
+  unsigned* status;
+  const fp4_status s = device_state(&status);
+  if (s != FP4_OK) return s;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (g.amax_out) {
+    const cudaError_t e = cudaMemsetAsync(g.amax_out, 0, sizeof(float), st);
+    if (e != cudaSuccess) return cuda_fail(e, "zeroing amax_out");
+  }
+  if (g.q_codes && (g.M % 128 != 0 || (g.F / 16) % 4 != 0)) {  // the scale layout's pads read as 0
+    const cudaError_t e = cudaMemsetAsync(g.q_scales, 0, fp4_scales_bytes(g.M, g.F, FP4_NVFP4), st);
+    if (e != cudaSuccess) return cuda_fail(e, "zero-filling the scale pads");
+  }
+  const char* why = nullptr;
+  cudaError_t err = cudaSuccess;
+  const int rc = launch_gated(g, status, st, &why, &err);
+  if (rc == 1) return fail(FP4_ERR_INVALID_ARG, why);
+  if (rc == 2) return cuda_fail(err, "gated GEMM launch");
+  return FP4_OK;
+}
+
+fp4_status fp4_gemm_gated(fp4_fmt fmt, const uint8_t* A, const uint8_t* sA, const float* gA, const uint8_t* Wg,
+                          const uint8_t* sWg, const float* gWg, const uint8_t* Wu, const uint8_t* sWu, const float* gWu,
+                          int64_t M, int64_t F, int64_t K, const float* bias_g, const float* bias_u, fp4_act act,
+                          void* H, fp4_dtype out_dtype, void* G, void* U, uint8_t* Hcodes, uint8_t* Hscales,
+                          const float* gH, float* amax_out, void* workspace, size_t workspace_bytes, unsigned flags,
+                          void* stream) {
+  if (flags & ~static_cast<unsigned>(FP4_GEMM_WEIGHTS_READY)) return fail(FP4_ERR_INVALID_ARG, "unknown flag");
+  GatedProblem g{};
+  g.A = A;
+  g.sA = sA;
+  g.gA = gA;
+  g.Wg = Wg;
+  g.sWg = sWg;
+  g.gWg = gWg;
+  g.Wu = Wu;
+  g.sWu = sWu;
+  g.gWu = gWu;
+  g.M = M;
+  g.F = F;
+  g.K = K;
+  g.bias_g = bias_g;
+  g.bias_u = bias_u;
+  g.H = H;
+  g.G = G;
+  g.U = U;
+  g.q_codes = Hcodes;
+  g.q_scales = Hscales;
+  g.q_g = gH;
+  g.amax_out = amax_out;
+  g.ws = workspace;
+  g.ws_bytes = workspace_bytes;
+  g.weights_ready = (flags & FP4_GEMM_WEIGHTS_READY) ? 1 : 0;
+  return gated_common(g, fmt, act, out_dtype, stream);
+}
+
+static size_t quant_ws_aligned() { return (kQuantWorkspaceBytes + 255) / 256 * 256; }
+
+size_t fp4_gemm_gated_bf16a_workspace_size(int64_t M, int64_t F, int64_t K) {
+  if (M <= 0 || F <= 0 || K <= 0) return 0;
+  return quant_ws_aligned() + gated_workspace_bytes(M, F, K, 0, false);
+}
+
+fp4_status fp4_gemm_gated_bf16a(const void* X, const uint8_t* Wg, const uint8_t* sWg, const float* gWg,
+                                const uint8_t* Wu, const uint8_t* sWu, const float* gWu, int64_t M, int64_t F,
+                                int64_t K, const float* bias_g, const float* bias_u, fp4_act act, void* H,
+                                fp4_dtype out_dtype, void* G, void* U, uint8_t* Xcodes, uint8_t* Xscales, float* gX,
+                                void* workspace, size_t workspace_bytes, unsigned flags, void* stream) {
+  if (!X || !Wg || !sWg || !Wu || !sWu || !H || !Xcodes || !Xscales || !gX || !workspace)
+    return fail(FP4_ERR_INVALID_ARG, "null pointer");
+  if (M <= 0 || F <= 0 || K <= 0 || K % 32 != 0) return fail(FP4_ERR_INVALID_ARG, "shape (K % 32 == 0)");
+  const int64_t most = (1ll << 31) - 256;
+  if (M > most || F > most || K > most) return fail(FP4_ERR_UNSUPPORTED, "dimension too large");
+  if (!dtype_ok(out_dtype)) return fail(FP4_ERR_INVALID_ARG, "out_dtype");
+  if (!act_ok(act)) return fail(FP4_ERR_INVALID_ARG, "act");
+  if (flags & ~static_cast<unsigned>(FP4_GEMM_WEIGHTS_READY)) return fail(FP4_ERR_INVALID_ARG, "unknown flag");
+  if (!G != !U) return fail(FP4_ERR_INVALID_ARG, "G and U: both or neither");
+  if (G && (G == U || G == H || U == H)) return fail(FP4_ERR_INVALID_ARG, "H, G and U must be different buffers");
+  if (!aligned16(X) || !aligned16(Wg) || !aligned16(sWg) || !aligned16(Wu) || !aligned16(sWu) || !aligned16(H) ||
+      !aligned16(G) || !aligned16(U) || !aligned16(Xcodes) || !aligned16(Xscales) || !aligned16(workspace))
+    return fail(FP4_ERR_INVALID_ARG, "buffers must be 16-byte aligned");
+  if (!aligned4(bias_g) || !aligned4(bias_u)) return fail(FP4_ERR_INVALID_ARG, "bias alignment");
+  if (workspace_bytes < fp4_gemm_gated_bf16a_workspace_size(M, F, K))
+    return fail(FP4_ERR_INVALID_ARG, "workspace too small (see fp4_gemm_gated_bf16a_workspace_size)");
+  uint8_t* const ws = static_cast<uint8_t*>(workspace) + quant_ws_aligned();
+  const size_t ws_bytes = workspace_bytes - quant_ws_aligned();
+  if (!decode_eligible(M, F, K)) {
+    const fp4_status s = fp4_quantize(X, M, K, FP4_BF16, FP4_NVFP4, 16, Xcodes, Xscales, gX, nullptr, nullptr, nullptr,
+                                      workspace, kQuantWorkspaceBytes, stream);
+    if (s != FP4_OK) return s;
+    return fp4_gemm_gated(FP4_NVFP4, Xcodes, Xscales, gX, Wg, sWg, gWg, Wu, sWu, gWu, M, F, K, bias_g, bias_u, act, H,
+                          out_dtype, G, U, nullptr, nullptr, nullptr, nullptr, ws, ws_bytes, flags, stream);
+  }
+  unsigned* status;
+  const fp4_status ds = device_state(&status);
+  if (ds != FP4_OK) return ds;
+  DecodeProblem q{};
+  q.W = Wg;
+  q.sW = sWg;
+  q.gW = gWg;
+  q.X = X;
+  q.Xq_out = Xcodes;
+  q.Xs_out = Xscales;
+  q.gX_out = gX;
+  q.M = M;
+  q.N = F;
+  q.K = K;
+  q.D = H;
+  q.out_bf16 = out_dtype == FP4_BF16;
+  q.ws = ws;
+  q.ws_bytes = ws_bytes;
+  q.weights_ready = (flags & FP4_GEMM_WEIGHTS_READY) ? 1 : 0;
+  q.bias = bias_g;
+  q.act = act;
+  DecodeExtra x{};
+  x.W2 = Wu;
+  x.sW2 = sWu;
+  x.gW2 = gWu;
+  x.bias2 = bias_u;
+  x.pre = G;
+  x.pre2 = U;
+  const char* why = nullptr;
+  cudaError_t err = cudaSuccess;
+  const int rc = launch_decode_extra(q, x, status, static_cast<cudaStream_t>(stream), &why, &err);
+  if (rc == 1) return fail(FP4_ERR_INVALID_ARG, why);
+  if (rc == 2) return cuda_fail(err, "gated decode GEMM launch");
+  return FP4_OK;
+}
+
+fp4_status fp4_gemm_gated_grouped(fp4_fmt fmt, int num_groups, const int32_t* offsets, const uint8_t* A,
+                                  const uint8_t* sA, const float* gA, const uint8_t* Wg, const uint8_t* sWg,
+                                  const float* gWg, const uint8_t* Wu, const uint8_t* sWu, const float* gWu,
+                                  int64_t total_rows, int64_t F, int64_t K, const float* bias_g, const float* bias_u,
+                                  fp4_act act, void* H, fp4_dtype out_dtype, void* G, void* U, void* stream) {
+  if (num_groups <= 0 || num_groups > kMaxGroups || !offsets) return fail(FP4_ERR_INVALID_ARG, "groups / offsets");
+  if (!aligned4(gWg) || !aligned4(gWu)) return fail(FP4_ERR_INVALID_ARG, "global scale alignment");
+  GatedProblem g{};
+  g.A = A;
+  g.sA = sA;
+  g.gA = gA;
+  g.Wg = Wg;
+  g.sWg = sWg;
+  g.gWg = gWg;
+  g.Wu = Wu;
+  g.sWu = sWu;
+  g.gWu = gWu;
+  g.M = total_rows;
+  g.F = F;
+  g.K = K;
+  g.bias_g = bias_g;
+  g.bias_u = bias_u;
+  g.H = H;
+  g.G = G;
+  g.U = U;
+  g.num_groups = num_groups;
+  g.offsets = offsets;
+  return gated_common(g, fmt, act, out_dtype, stream);
+}
+
+// Checks of a block-scaled copy that a row kernel writes, and its scale pads' zero-fill.
+static fp4_status check_codes(fp4_fmt fmt, const uint8_t* codes, const uint8_t* scales, const float* global, int64_t cols,
+                              CodesOut* q) {
+  *q = CodesOut{0, nullptr, nullptr, nullptr};
+  if (!codes) return FP4_OK;
+  if (fmt != FP4_NVFP4 && fmt != FP4_MXFP4) return fail(FP4_ERR_INVALID_ARG, "fmt");
+  if (!scales) return fail(FP4_ERR_INVALID_ARG, "FP4 output needs scales");
+  if (fmt == FP4_NVFP4 && !global) return fail(FP4_ERR_INVALID_ARG, "NVFP4 output needs the caller's global scale");
+  if (cols % 32 != 0) return fail(FP4_ERR_INVALID_ARG, "FP4 output needs cols % 32 == 0");
+  if (!aligned16(codes) || !aligned16(scales)) return fail(FP4_ERR_INVALID_ARG, "codes and scales must be 16-byte aligned");
+  q->fmt = fmt == FP4_MXFP4 ? 2 : 1;
+  q->codes = const_cast<uint8_t*>(codes);
+  q->scales = const_cast<uint8_t*>(scales);
+  q->g = global;
+  return FP4_OK;
+}
+
+static cudaError_t clear_row_outputs(const CodesOut& q, fp4_fmt fmt, int64_t rows, int64_t cols, float* amax_out,
+                                     cudaStream_t st) {
+  cudaError_t e = cudaSuccess;
+  if (amax_out) e = cudaMemsetAsync(amax_out, 0, sizeof(float), st);
+  if (e == cudaSuccess && q.codes && (rows % 128 != 0 || (cols / (fmt == FP4_MXFP4 ? 32 : 16)) % 4 != 0))
+    e = cudaMemsetAsync(q.scales, 0, fp4_scales_bytes(rows, cols, fmt), st);  // the layout's pads read as 0
+  return e;
+}
+
+size_t fp4_act_backward_workspace_size(int64_t rows, int64_t cols, int gated) {
+  if (rows <= 0 || cols <= 0) return 0;
+  return act_grad_workspace_bytes(rows, cols, gated != 0);
+}
+
+fp4_status fp4_act_backward(const void* dH, const void* G, const void* U, int64_t rows, int64_t cols, fp4_dtype in_dtype,
+                            fp4_act act, void* dZ, fp4_dtype out_dtype, float* dbias, fp4_fmt fmt, uint8_t* codes,
+                            uint8_t* scales, const float* global, float* amax_out, void* workspace,
+                            size_t workspace_bytes, void* stream) {
+  if (!dH || !G) return fail(FP4_ERR_INVALID_ARG, "null pointer");
+  if (!dZ && !codes) return fail(FP4_ERR_INVALID_ARG, "no output: dZ and codes are both NULL");
+  if (rows <= 0 || cols <= 0) return fail(FP4_ERR_INVALID_ARG, "rows and cols must be positive");
+  if (rows > (1ll << 31) - 256 || cols > (1ll << 30) - 256) return fail(FP4_ERR_UNSUPPORTED, "dimension too large");
+  if (!dtype_ok(in_dtype) || !dtype_ok(out_dtype)) return fail(FP4_ERR_INVALID_ARG, "in_dtype / out_dtype");
+  if (!act_ok(act)) return fail(FP4_ERR_INVALID_ARG, "act");
+  if (!aligned16(dH) || !aligned16(G) || !aligned16(U) || !aligned16(dZ))
+    return fail(FP4_ERR_INVALID_ARG, "dH, G, U and dZ must be 16-byte aligned");
+  if (dZ && (dZ == dH || dZ == G || dZ == U)) return fail(FP4_ERR_INVALID_ARG, "dZ must be a buffer of its own");
+  if (!aligned4(dbias) || !aligned4(amax_out)) return fail(FP4_ERR_INVALID_ARG, "dbias / amax_out alignment");
+  CodesOut q;
+  const fp4_status cs = check_codes(fmt, codes, scales, global, cols, &q);
+  if (cs != FP4_OK) return cs;
+  if (dbias && (!workspace || !aligned16(workspace) || workspace_bytes < act_grad_workspace_bytes(rows, cols, U != nullptr)))
+    return fail(FP4_ERR_INVALID_ARG, "workspace too small or misaligned (see fp4_act_backward_workspace_size)");
+  unsigned* status;
+  const fp4_status s = device_state(&status);
+  if (s != FP4_OK) return s;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  cudaError_t e = clear_row_outputs(q, fmt, rows, U ? 2 * cols : cols, amax_out, st);
+  if (e != cudaSuccess) return cuda_fail(e, "clearing outputs");
+  ActGradProblem p{};
+  p.dh = dH;
+  p.g = G;
+  p.u = U;
+  p.bf16 = in_dtype == FP4_BF16;
+  p.rows = rows;
+  p.cols = cols;
+  p.act = act;
+  p.dz = dZ;
+  p.dz_bf16 = out_dtype == FP4_BF16;
+  p.dbias = dbias;
+  p.q = q;
+  p.amax_out = amax_out;
+  p.ws = static_cast<float*>(workspace);
+  e = launch_act_grad(p, status, st);
+  return e == cudaSuccess ? FP4_OK : cuda_fail(e, "activation backward launch");
+}
+
+fp4_status fp4_layernorm(const void* x, int64_t rows, int64_t cols, fp4_dtype in_dtype, const float* weight,
+                         const float* bias, float eps, void* y, fp4_dtype out_dtype, float* mean, float* rstd,
+                         fp4_fmt fmt, uint8_t* codes, uint8_t* scales, const float* global, float* amax_out,
+                         void* stream) {
+  if (!x) return fail(FP4_ERR_INVALID_ARG, "null pointer");
+  if (!y && !codes) return fail(FP4_ERR_INVALID_ARG, "no output: y and codes are both NULL");
+  if (rows <= 0 || cols <= 0) return fail(FP4_ERR_INVALID_ARG, "rows and cols must be positive");
+  if (rows > (1ll << 31) - 256 || cols > (1ll << 30)) return fail(FP4_ERR_UNSUPPORTED, "dimension too large");
+  if (!dtype_ok(in_dtype) || !dtype_ok(out_dtype)) return fail(FP4_ERR_INVALID_ARG, "in_dtype / out_dtype");
+  if (!(eps >= 0.0f) || eps > 3.4e38f) return fail(FP4_ERR_INVALID_ARG, "eps must be finite and not negative");
+  if (!aligned16(x) || !aligned16(y)) return fail(FP4_ERR_INVALID_ARG, "x and y must be 16-byte aligned");
+  if (!aligned4(weight) || !aligned4(bias) || !aligned4(mean) || !aligned4(rstd) || !aligned4(amax_out))
+    return fail(FP4_ERR_INVALID_ARG, "weight / bias / mean / rstd / amax_out alignment");
+  CodesOut q;
+  const fp4_status cs = check_codes(fmt, codes, scales, global, cols, &q);
+  if (cs != FP4_OK) return cs;
+  if (q.codes && (!aligned16(weight) || !aligned16(bias)))
+    return fail(FP4_ERR_INVALID_ARG, "FP4 output needs 16-byte aligned weight and bias");
+  unsigned* status;
+  const fp4_status s = device_state(&status);
+  if (s != FP4_OK) return s;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  cudaError_t e = clear_row_outputs(q, fmt, rows, cols, amax_out, st);
+  if (e != cudaSuccess) return cuda_fail(e, "clearing outputs");
+  LayerNormProblem p{};
+  p.x = x;
+  p.bf16 = in_dtype == FP4_BF16;
+  p.rows = rows;
+  p.cols = cols;
+  p.weight = weight;
+  p.bias = bias;
+  p.eps = eps;
+  p.y = y;
+  p.y_bf16 = out_dtype == FP4_BF16;
+  p.mean = mean;
+  p.rstd = rstd;
+  p.q = q;
+  p.amax_out = amax_out;
+  e = launch_layernorm(p, status, st);
+  return e == cudaSuccess ? FP4_OK : cuda_fail(e, "layer norm launch");
+}
+
+size_t fp4_layernorm_backward_workspace_size(int64_t rows, int64_t cols) {
+  if (rows <= 0 || cols <= 0) return 0;
+  return layernorm_grad_workspace_bytes(rows, cols);
+}
+
+fp4_status fp4_layernorm_backward(const void* dy, const void* x, int64_t rows, int64_t cols, fp4_dtype in_dtype,
+                                  const float* weight, const float* mean, const float* rstd, const void* dres, void* dx,
+                                  fp4_dtype out_dtype, float* dweight, float* dbias, void* workspace,
+                                  size_t workspace_bytes, void* stream) {
+  if (!dy || !x || !mean || !rstd || !dx) return fail(FP4_ERR_INVALID_ARG, "null pointer");
+  if (rows <= 0 || cols <= 0) return fail(FP4_ERR_INVALID_ARG, "rows and cols must be positive");
+  if (rows > (1ll << 31) - 256 || cols > (1ll << 30)) return fail(FP4_ERR_UNSUPPORTED, "dimension too large");
+  if (!dtype_ok(in_dtype) || !dtype_ok(out_dtype)) return fail(FP4_ERR_INVALID_ARG, "in_dtype / out_dtype");
+  if (!aligned16(dy) || !aligned16(x) || !aligned16(dres) || !aligned16(dx))
+    return fail(FP4_ERR_INVALID_ARG, "dy, x, dres and dx must be 16-byte aligned");
+  if (!aligned4(weight) || !aligned4(mean) || !aligned4(rstd) || !aligned4(dweight) || !aligned4(dbias))
+    return fail(FP4_ERR_INVALID_ARG, "weight / mean / rstd / dweight / dbias alignment");
+  if (dx == x || ((dx == dy || dx == dres) && in_dtype != out_dtype))
+    return fail(FP4_ERR_INVALID_ARG, "dx may be dy or dres of the same type, not x");
+  if ((dweight || dbias) && (!workspace || !aligned16(workspace) || workspace_bytes < layernorm_grad_workspace_bytes(rows, cols)))
+    return fail(FP4_ERR_INVALID_ARG, "workspace too small or misaligned (see fp4_layernorm_backward_workspace_size)");
+  unsigned* status;
+  const fp4_status s = device_state(&status);
+  if (s != FP4_OK) return s;
+  LayerNormGradProblem p{};
+  p.dy = dy;
+  p.x = x;
+  p.bf16 = in_dtype == FP4_BF16;
+  p.rows = rows;
+  p.cols = cols;
+  p.weight = weight;
+  p.mean = mean;
+  p.rstd = rstd;
+  p.dres = dres;
+  p.dx = dx;
+  p.dx_bf16 = out_dtype == FP4_BF16;
+  p.dweight = dweight;
+  p.dbias = dbias;
+  p.ws = static_cast<float*>(workspace);
+  const cudaError_t e = launch_layernorm_grad(p, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? FP4_OK : cuda_fail(e, "layer norm backward launch");
 }
 
 size_t fp4_gemm_epilogue_workspace_size(int64_t M, int64_t N, int64_t K, fp4_fmt fmt, int rows_in_place) {

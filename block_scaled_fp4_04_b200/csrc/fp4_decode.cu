@@ -23,14 +23,19 @@
 //   TMA would have written it) and scale atoms; the first CTA of each segment also
 //   writes those codes and scales to the caller's buffers.  Meanwhile the producers are
 //   already streaming weight stages into their rings.
+//   A gated product (two weights of the same shape, H = act(G) U) runs as twice the weight
+//   tiles, gate and up tiles in turn: both stream through the same rings, and the owner of an
+//   output tile waits for the counters of both its halves before it writes H.
 // Every wait is bounded; a timeout latches the status word and unwinds.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <cuda_bf16.h>
 #include <cstdint>
 
+#include "fp4_act.cuh"
 #include "fp4_codes.cuh"
 #include "fp4_internal.h"
+#include "fp4_ops.h"
 #include "fp4_ptx.cuh"
 
 namespace fp4 {
@@ -58,6 +63,13 @@ struct DecodeArgs {
   int act;                // 0: none, 1: ReLU
   int stall_plus1;        // test hook for the bounded waits: CTA stall_plus1 - 1 does not
                           // publish its share of the amax (0: every CTA publishes)
+  int out_tiles;          // 128-column tiles of the output: tiles, or half of them (gated)
+  // kEpiFull, kEpiGated (see DecodeExtra)
+  const uint8_t* sfw2;
+  const float *gw2, *bias2;
+  const void* res;
+  int res_bf16;
+  void *pre, *pre2;
 };
 
 // K steps of one segment at most (the activations' scale factors for a segment take 16
@@ -121,6 +133,78 @@ __device__ __forceinline__ void d_store(const DecodeArgs& p, int row, int col, f
   else reinterpret_cast<float*>(p.out)[o] = v;
 }
 
+// The same for another matrix of the output's shape and type.
+__device__ __forceinline__ void d_store_to(const DecodeArgs& p, void* out, int row, int col, float v) {
+  const int64_t o = static_cast<int64_t>(col) * p.N + row;
+  if (p.out_bf16) static_cast<__nv_bfloat16*>(out)[o] = __float2bfloat16_rn(v);
+  else static_cast<float*>(out)[o] = v;
+}
+
+// Reads the BN summed partials of one weight row (p.M of them exist) and clears them.
+template <int BN>
+__device__ __forceinline__ void d_take_sums(const DecodeArgs& p, float* wsrow, float (&v)[BN]) {
+#pragma unroll
+  for (int j = 0; j < BN; ++j) v[j] = 0.0f;
+  if ((p.M & 3) == 0) {
+#pragma unroll
+    for (int j = 0; j < BN; j += 4)
+      if (j < p.M) {
+        const float4 f = __ldcg(reinterpret_cast<const float4*>(wsrow + j));
+        v[j] = f.x;
+        v[j + 1] = f.y;
+        v[j + 2] = f.z;
+        v[j + 3] = f.w;
+      }
+#pragma unroll
+    for (int j = 0; j < BN; j += 4)
+      if (j < p.M) __stcg(reinterpret_cast<float4*>(wsrow + j), make_float4(0.f, 0.f, 0.f, 0.f));
+  } else {
+#pragma unroll
+    for (int j = 0; j < BN; ++j)
+      if (j < p.M) v[j] = __ldcg(wsrow + j);
+#pragma unroll
+    for (int j = 0; j < BN; ++j)
+      if (j < p.M) __stcg(wsrow + j, 0.0f);
+  }
+}
+
+// Finishes one output column (weight row `row`) of every activation row in the long epilogues.
+template <int BN, bool GATED>
+__device__ __forceinline__ void d_finish(const DecodeArgs& p, int row, float scale, float scale2, float (&v)[BN],
+                                         float (&u)[BN]) {
+  const float b = p.bias ? __ldg(p.bias + row) : 0.0f;
+  const float b2 = GATED && p.bias2 ? __ldg(p.bias2 + row) : 0.0f;
+#pragma unroll
+  for (int j = 0; j < BN; ++j) {
+    v[j] *= scale;
+    if (p.bias) v[j] = __fadd_rn(v[j], b);
+    if (GATED) {
+      u[j] *= scale2;
+      if (p.bias2) u[j] = __fadd_rn(u[j], b2);
+    }
+    if (j < p.M) {
+      if (p.pre) d_store_to(p, p.pre, row, j, v[j]);
+      if (GATED && p.pre2) d_store_to(p, p.pre2, row, j, u[j]);
+    }
+  }
+  with_act(p.act, [&](auto tag) {
+    constexpr int A = decltype(tag)::value;
+#pragma unroll
+    for (int j = 0; j < BN; ++j) v[j] = GATED ? act_value<A>(v[j]) * u[j] : act_value<A>(v[j]);
+  });
+  if (!GATED && p.res) {
+#pragma unroll
+    for (int j = 0; j < BN; ++j)
+      if (j < p.M) {
+        const int64_t o = static_cast<int64_t>(j) * p.N + row;
+        v[j] += p.res_bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(p.res)[o]) : static_cast<const float*>(p.res)[o];
+      }
+  }
+#pragma unroll
+  for (int j = 0; j < BN; ++j)
+    if (j < p.M) d_store(p, row, j, v[j]);
+}
+
 // The (weight tile, K step) units of one pipeline: units u in [u0, u1) of its segment,
 // u -> tile u / seg_len, K step kb0 + u % seg_len; consecutive units of one tile form
 // one accumulation.  In the fused kernel a range that starts inside a tile (and goes on
@@ -171,11 +255,12 @@ constexpr int kMaxBatch = 8;
 #endif
 constexpr int kFusedPrefill = FP4_FUSED_PREFILL;
 
-template <int BN, bool FUSED>
+template <int BN, bool FUSED, int EPI = kEpiPlain>
 __global__ void __launch_bounds__(DecodeCfg<BN>::kThreads, 1)
     fp4_decode_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
-                      const DecodeArgs p) {
+                      const __grid_constant__ CUtensorMap tmW2, const DecodeArgs p) {
   using C = DecodeCfg<BN>;
+  constexpr bool kGated = EPI == kEpiGated;  // tile t: 128-row block t / 2 of the gate (even t) or up weight
   constexpr int S = C::kStages;
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint32_t s_tmem_base;
@@ -237,6 +322,7 @@ __global__ void __launch_bounds__(DecodeCfg<BN>::kThreads, 1)
   }
   if (warp == 0 && lane == 0) {
     tma_prefetch_desc(&tmW);
+    if (kGated) tma_prefetch_desc(&tmW2);
     if (!FUSED) tma_prefetch_desc(&tmX);
   }
   if (sub == 0 && warp == 1) {
@@ -288,9 +374,16 @@ __global__ void __launch_bounds__(DecodeCfg<BN>::kThreads, 1)
           const int atoms = min(4, p.atoms_k - kb * 4);
           mbar_arrive_expect_tx(&full[stage], static_cast<uint32_t>(C::kABytes + atoms * 512));
           uint8_t* st = ring + stage * C::kStageBytes;
+          if constexpr (kGated) {
+            const int rb = tile >> 1;
+            tma_load_2d(st, tile & 1 ? &tmW2 : &tmW, &full[stage], kb * 128, rb * 128, pol_w);
+            bulk_load(st + C::kABytes, (tile & 1 ? p.sfw2 : p.sfw) + rb * p.sfw_rb_bytes + static_cast<int64_t>(kb) * 4 * 512,
+                      static_cast<uint32_t>(atoms) * 512u, &full[stage], pol_w);
+          } else {
           tma_load_2d(st, &tmW, &full[stage], kb * 128, tile * 128, pol_w);
           bulk_load(st + C::kABytes, p.sfw + tile * p.sfw_rb_bytes + static_cast<int64_t>(kb) * 4 * 512,
                     static_cast<uint32_t>(atoms) * 512u, &full[stage], pol_w);
+          }
           issued |= 1u << stage;
           issued_par = (issued_par & ~(1u << stage)) | (phase << stage);
           if (++stage == S) {
@@ -634,6 +727,12 @@ __global__ void __launch_bounds__(DecodeCfg<BN>::kThreads, 1)
     } else {
       scale = (p.gx ? *p.gx : 1.0f) * gw;
     }
+    float scale2 = 0.0f;  // the up weight's scale
+    if constexpr (kGated) {
+      const float gx = FUSED ? (__uint_as_float(s_red[0]) > 0.0f ? __fdiv_rn(__uint_as_float(s_red[0]), 2688.0f) : 1.0f)
+                             : (p.gx ? *p.gx : 1.0f);
+      scale2 = gx * (p.gw2 ? *p.gw2 : 1.0f);
+    }
     const int q4 = (threadIdx.x >> 5) & 3;  // the TMEM lane quarter this warp may read
     const int rl = q4 * 32 + lane;
     // Tiles whose partial sums this pipeline added but has not yet counted.  Counting
@@ -662,14 +761,21 @@ __global__ void __launch_bounds__(DecodeCfg<BN>::kThreads, 1)
     const int gp = blockIdx.x * C::kP + sub, np = gridDim.x * C::kP;
     int next_owned = gp;
     auto write_owned = [&]() {
-      while (next_owned < p.tiles && !*s_epi_fail && !*s_xfail) {
+      while (next_owned < p.out_tiles && !*s_epi_fail && !*s_xfail) {
         const int t = next_owned;
         if (et == 0) {
           const uint64_t t0 = globaltimer_ns();
           int ready = 0;
           for (uint32_t it = 1; it < kWaitMaxIters; ++it) {
             int c;
+            if constexpr (kGated) {
+              int c2;
+              asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(c) : "l"(p.tile_cnt + 2 * t) : "memory");
+              asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(c2) : "l"(p.tile_cnt + 2 * t + 1) : "memory");
+              c = min(c, c2);
+            } else {
             asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(c) : "l"(p.tile_cnt + t) : "memory");
+            }
             if (c >= p.num_kb) {
               ready = 1;
               break;
@@ -689,6 +795,15 @@ __global__ void __launch_bounds__(DecodeCfg<BN>::kThreads, 1)
         named_sync(1 + sub, 128);  // s_last is rewritten on the next turn
         if (*s_epi_fail || !ready) return;
         const int row = t * 128 + rl;
+        if constexpr (EPI != kEpiPlain) {
+          if (row < p.N) {
+            float v[BN], u[BN];
+            float* wsrow = p.ws + static_cast<int64_t>(row) * p.M;
+            d_take_sums<BN>(p, wsrow, v);
+            if constexpr (kGated) d_take_sums<BN>(p, wsrow + static_cast<int64_t>(p.N) * p.M, u);
+            d_finish<BN, kGated>(p, row, scale, scale2, v, u);
+          }
+        } else
         if (row < p.N) {
           float* wsrow = p.ws + static_cast<int64_t>(row) * p.M;
           float v[BN];
@@ -724,7 +839,14 @@ __global__ void __launch_bounds__(DecodeCfg<BN>::kThreads, 1)
               d_store(p, row, j, o);
             }
         }
-        if (et == 0) p.tile_cnt[t] = 0;
+        if (et == 0) {
+          if constexpr (kGated) {
+            p.tile_cnt[2 * t] = 0;
+            p.tile_cnt[2 * t + 1] = 0;
+          } else {
+            p.tile_cnt[t] = 0;
+          }
+        }
         next_owned += np;
       }
     };
@@ -740,9 +862,9 @@ __global__ void __launch_bounds__(DecodeCfg<BN>::kThreads, 1)
       named_sync(1 + sub, 128);
       if (*s_epi_fail) break;
       tc_fence_after();
-      const int row = tile * 128 + rl;  // weight row = output column
+      const int row = (kGated ? tile >> 1 : tile) * 128 + rl;  // weight row = output column
       const bool row_ok = row < p.N;
-      float* wsrow = p.ws + static_cast<int64_t>(row) * p.M;
+      float* wsrow = p.ws + (static_cast<int64_t>(row) + (kGated && (tile & 1) ? p.N : 0)) * p.M;
 #pragma unroll
       for (int c = 0; c < BN; c += 16) {
         uint32_t r[16];
@@ -791,10 +913,11 @@ struct DecodePlan {
   int nseg, seg_len, ctas_per_seg, tiles, num_kb;
 };
 
-static DecodePlan decode_plan(int64_t N, int64_t K, int bn) {
+// `weights`: matrices of [N, K] (2: a gated product).
+static DecodePlan decode_plan(int64_t N, int64_t K, int bn, int weights) {
   DecodePlan d{};
   d.num_kb = static_cast<int>((K + 255) / 256);
-  d.tiles = static_cast<int>((N + 127) / 128);
+  d.tiles = static_cast<int>((N + 127) / 128) * weights;
   const int sms = num_sms();
   // segments of at most decode_max_seg(bn) K steps
   const int max_seg = decode_max_seg(bn);
@@ -818,15 +941,20 @@ static DecodePlan decode_plan(int64_t N, int64_t K, int bn) {
 static size_t ws_partials(int64_t M, int64_t N) { return (static_cast<size_t>(M * N) * 4 + 255) / 256 * 256; }
 static size_t ws_counters(int64_t N) { return (static_cast<size_t>((N + 127) / 128) * 4 + 255) / 256 * 256; }
 
+// A gated product has two [F, M] sums and two counters per output tile.
+size_t decode_gated_workspace_bytes(int64_t M, int64_t F) {
+  return 2 * ws_partials(M, F) + 2 * ws_counters(F) + 128 + static_cast<size_t>(kDecodeMaxCtas) * 128;
+}
+
 size_t decode_workspace_bytes(int64_t M, int64_t N) {
   return ws_partials(M, N) + ws_counters(N) + 128 + static_cast<size_t>(kDecodeMaxCtas) * 128;
 }
 
-template <int BN, bool FUSED>
-static cudaError_t run_decode(const CUtensorMap& tw, const CUtensorMap& tx, const DecodeArgs& a, int grid,
-                              cudaStream_t st) {
+template <int BN, bool FUSED, int EPI = kEpiPlain>
+static cudaError_t run_decode(const CUtensorMap& tw, const CUtensorMap& tx, const CUtensorMap& tw2, const DecodeArgs& a,
+                              int grid, cudaStream_t st) {
   using C = DecodeCfg<BN>;
-  auto kern = fp4_decode_kernel<BN, FUSED>;
+  auto kern = fp4_decode_kernel<BN, FUSED, EPI>;
   static bool attr_done[64] = {false};
   int dev = 0;
   cudaGetDevice(&dev);
@@ -849,21 +977,24 @@ static cudaError_t run_decode(const CUtensorMap& tw, const CUtensorMap& tx, cons
   attr[1].val.cooperative = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, kern, tw, tx, a);
+  return cudaLaunchKernelEx(&cfg, kern, tw, tx, tw2, a);
 }
 
-int launch_decode(const DecodeProblem& q, unsigned* status, cudaStream_t st, const char** why, cudaError_t* err) {
+static int launch_decode_any(const DecodeProblem& q, const DecodeExtra* x, unsigned* status, cudaStream_t st,
+                             const char** why, cudaError_t* err) {
+  const bool gated = x && x->W2;
+  const size_t need = gated ? decode_gated_workspace_bytes(q.M, q.N) : decode_workspace_bytes(q.M, q.N);
   if (!decode_eligible(q.M, q.N, q.K)) {
     *why = "decode kernel: 1 <= M <= 32";
     return 1;
   }
-  if (q.ws_bytes < decode_workspace_bytes(q.M, q.N) || !q.ws) {
+  if (q.ws_bytes < need || !q.ws) {
     *why = "workspace too small (see fp4_gemm_workspace_size)";
     return 1;
   }
   const int BN = q.M <= 16 ? 16 : 32;
-  const DecodePlan pl = decode_plan(q.N, q.K, BN);
-  CUtensorMap tw, tx;
+  const DecodePlan pl = decode_plan(q.N, q.K, BN, gated ? 2 : 1);
+  CUtensorMap tw, tx, tw2;
   if (!make_tensor_map_u8(&tw, q.W, static_cast<uint64_t>(q.K / 2), static_cast<uint64_t>(q.N), 128)) {
     *why = "cuTensorMapEncodeTiled failed (alignment or driver)";
     return 1;
@@ -872,6 +1003,11 @@ int launch_decode(const DecodeProblem& q, unsigned* status, cudaStream_t st, con
     tx = tw;  // unused by the fused kernel
   } else if (!make_tensor_map_u8(&tx, q.Xq, static_cast<uint64_t>(q.K / 2), static_cast<uint64_t>(q.M),
                                  static_cast<uint32_t>(BN))) {
+    *why = "cuTensorMapEncodeTiled failed (alignment or driver)";
+    return 1;
+  }
+  tw2 = tw;
+  if (gated && !make_tensor_map_u8(&tw2, x->W2, static_cast<uint64_t>(q.K / 2), static_cast<uint64_t>(q.N), 128)) {
     *why = "cuTensorMapEncodeTiled failed (alignment or driver)";
     return 1;
   }
@@ -898,8 +1034,11 @@ int launch_decode(const DecodeProblem& q, unsigned* status, cudaStream_t st, con
   a.out = q.D;
   a.out_bf16 = q.out_bf16;
   a.ws = static_cast<float*>(q.ws);
-  a.tile_cnt = reinterpret_cast<int*>(static_cast<uint8_t*>(q.ws) + ws_partials(q.M, q.N));
-  a.gbar = reinterpret_cast<unsigned*>(static_cast<uint8_t*>(q.ws) + ws_partials(q.M, q.N) + ws_counters(q.N));
+  const int halves = gated ? 2 : 1;
+  uint8_t* const counters = static_cast<uint8_t*>(q.ws) + halves * ws_partials(q.M, q.N);
+  a.tile_cnt = reinterpret_cast<int*>(counters);
+  a.gbar = reinterpret_cast<unsigned*>(counters + halves * ws_counters(q.N));
+  a.out_tiles = pl.tiles / halves;
   a.weights_ready = q.weights_ready;
   a.status = status;
   a.bias = q.bias;
@@ -907,13 +1046,46 @@ int launch_decode(const DecodeProblem& q, unsigned* status, cudaStream_t st, con
   a.stall_plus1 = q.stall_plus1;
   const int grid = pl.nseg * pl.ctas_per_seg;
   cudaError_t e;
-  if (q.X) e = BN == 16 ? run_decode<16, true>(tw, tx, a, grid, st) : run_decode<32, true>(tw, tx, a, grid, st);
-  else e = BN == 16 ? run_decode<16, false>(tw, tx, a, grid, st) : run_decode<32, false>(tw, tx, a, grid, st);
+  if (x) {
+    a.sfw2 = x->sW2;
+    a.gw2 = x->gW2;
+    a.bias2 = x->bias2;
+    a.res = x->res;
+    a.res_bf16 = x->res_bf16;
+    a.pre = x->pre;
+    a.pre2 = x->pre2;
+  }
+  if (gated && q.X)
+    e = BN == 16 ? run_decode<16, true, kEpiGated>(tw, tx, tw2, a, grid, st)
+                 : run_decode<32, true, kEpiGated>(tw, tx, tw2, a, grid, st);
+  else if (gated)
+    e = BN == 16 ? run_decode<16, false, kEpiGated>(tw, tx, tw2, a, grid, st)
+                 : run_decode<32, false, kEpiGated>(tw, tx, tw2, a, grid, st);
+  else if (x)
+    e = BN == 16 ? run_decode<16, false, kEpiFull>(tw, tx, tw2, a, grid, st)
+                 : run_decode<32, false, kEpiFull>(tw, tx, tw2, a, grid, st);
+  else if (q.X)
+    e = BN == 16 ? run_decode<16, true>(tw, tx, tw2, a, grid, st) : run_decode<32, true>(tw, tx, tw2, a, grid, st);
+  else
+    e = BN == 16 ? run_decode<16, false>(tw, tx, tw2, a, grid, st) : run_decode<32, false>(tw, tx, tw2, a, grid, st);
   if (e != cudaSuccess) {
     *err = e;
     return 2;
   }
   return 0;
+}
+
+int launch_decode(const DecodeProblem& q, unsigned* status, cudaStream_t st, const char** why, cudaError_t* err) {
+  return launch_decode_any(q, nullptr, status, st, why, err);
+}
+
+int launch_decode_extra(const DecodeProblem& q, const DecodeExtra& x, unsigned* status, cudaStream_t st,
+                        const char** why, cudaError_t* err) {
+  if (!x.W2 && q.X) {  // the long epilogue takes quantized activations only
+    *why = "BF16 activations with a residual or a pre-activation";
+    return 1;
+  }
+  return launch_decode_any(q, &x, status, st, why, err);
 }
 
 }  // namespace fp4

@@ -1,0 +1,1389 @@
+// fp4_gemm_kernel.cuh -- the block-scaled GEMM kernel and its launch, shared by the plain,
+// the extended-epilogue and the gated translation units (fp4_gemm.cu describes its structure).
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <cuda_bf16.h>
+#include <cstdint>
+#include <cstring>
+#include <mutex>
+
+#include "fp4_act.cuh"
+#include "fp4_codes.cuh"
+#include "fp4_internal.h"
+#include "fp4_ptx.cuh"
+
+namespace fp4 {
+
+enum { kModeTile = 0, kModeStreamK = 1, kModeGrouped = 2 };
+
+struct GemmArgs {
+  const uint8_t* sfa;
+  const uint8_t* sfb;
+  int64_t sfa_rb_bytes;     // bytes per 128-row block of A's scales
+  int64_t sfb_rb_bytes;
+  int64_t sfb_group_bytes;  // grouped: bytes of one expert's B scales
+  int sf_atoms_k;           // scale atoms along K per row-block
+  int sfb_rbs;              // row-blocks of B (per expert)
+  const float* ga;
+  const float* gb;
+  int Mk, Nk, K, num_kb;    // kernel orientation
+  void* out;
+  int64_t ldo;
+  int out_bf16, transposed, vec_store;
+  int indep;  // 1: kernel A, 2: kernel B may be read before the preceding kernel finishes
+  float* ws;        // stream-K: FP32 partial sums [Mk, Nk], zero between calls
+  int* tile_cnt;    // stream-K: K steps summed so far per tile, zero between calls
+  int mode;
+  int tiles_m, tiles_n, group_m;
+  int64_t total_units;
+  int num_groups;
+  const int32_t* offsets;
+  int b_rows_per_group;
+  unsigned* status;
+  // epilogue after the scale ("Rubin FP4 GEMM overview" 3.2 / 4.2): + bias[n], activation,
+  // and optionally an NVFP4 copy of the result (16-blocks along n, caller's global scale)
+  const float* bias;   // [N] (output columns), or null
+  int act;             // 0: none, 1: ReLU
+  uint8_t* q_codes;    // [M, N/2] NVFP4 codes of the result, or null
+  uint8_t* q_scales;   // swizzled scale atoms of the [M, N/16] block scales
+  const float* q_g;    // global scale of the NVFP4 result (device)
+  int64_t q_atoms;     // scale atoms per 128-row block of the result: ceil(N/16, 4) / 4
+  unsigned* amax_out;  // max |result| as float bits (zeroed before the launch), or null
+  uint32_t f8_fmt;     // kind::mxf8f6f4: A's format | B's format << 3 (E4M3 0, E2M1 5)
+  // kEpiFull, kEpiGated
+  const void* res;       // [M, N] added after the activation, or null
+  int res_bf16, vec_res;
+  void* pre;             // kEpiFull: the pre-activation; kEpiGated: G; [M, N] in the output type, or null
+  void* pre2;            // kEpiGated: U
+  const uint8_t* sfb2;   // kEpiGated: the up operand's scales, global scale, bias
+  const float* gb2;
+  const float* bias2;
+  int64_t bias_group;    // grouped: floats between two experts' biases
+};
+
+struct Work {
+  int a_row, b_row;    // TMA row coordinates of the A and B boxes
+  int out_row0;        // first output row (kernel orientation)
+  int rows_valid;      // rows of the tile that exist
+  int n0;              // first column (kernel orientation)
+  int sfa_rb;          // A scale row-block
+  int64_t sfb_off;     // byte offset of B's first scale row-block
+  int group;
+  int kb0, kb1;
+  int tile;
+};
+
+// TN: output columns per tile (BN, or half of it where a tile holds gate and up columns).
+template <int BN, int TN = BN>
+struct Sched {
+  const GemmArgs& p;
+  const int* s_mt;   // grouped: 128-row block prefix per group (= A scale row-blocks)
+  const int* s_off;  // grouped: row offsets
+  const int* s_pt;   // grouped CTA pairs: 256-row tile prefix per group
+  int64_t u, u_end;  // stream-K: current / end unit; tile modes: current unit
+  int64_t total;
+
+  int vgrid;         // pipelines in the grid; this one is number vb
+  int mtile;         // output rows per M tile: 128, or 256 for a CTA pair
+  int sub_row;       // CTA pair: this CTA's first row (and first B row) within the tile
+  // vb / vg: this pipeline's index among all pipelines of the grid, and their count
+  __device__ Sched(const GemmArgs& args, const int* mt, const int* off, int vb, int vg, int mtile_ = 128,
+                   int sub_row_ = 0, const int* pt = nullptr)
+      : p(args), s_mt(mt), s_off(off), s_pt(pt), vgrid(vg), mtile(mtile_), sub_row(sub_row_) {
+    if (p.mode == kModeStreamK) {
+      const int64_t T = p.total_units;
+      u = T * vb / vg;
+      u_end = T * (vb + 1) / vg;
+      total = T;
+    } else if (p.mode == kModeGrouped) {
+      total = static_cast<int64_t>(tiles_prefix()[p.num_groups]) * p.tiles_n;
+      u = vb;
+    } else {
+      total = p.total_units;
+      u = vb;
+    }
+  }
+
+  __device__ bool next(Work& w) {
+    if (p.mode == kModeStreamK) {
+      if (u >= u_end) return false;
+      const int tile = static_cast<int>(u / p.num_kb);
+      const int kb0 = static_cast<int>(u % p.num_kb);
+      const int64_t kb1_ = static_cast<int64_t>(kb0) + (u_end - u);
+      const int kb1 = static_cast<int>(kb1_ < p.num_kb ? kb1_ : p.num_kb);
+      u += kb1 - kb0;
+      const int mt = tile / p.tiles_n, nt = tile % p.tiles_n;
+      plain(w, mt, nt);
+      w.kb0 = kb0;
+      w.kb1 = kb1;
+      w.tile = tile;
+      return true;
+    }
+    if (u >= total) return false;
+    const int64_t cur = u;
+    u += vgrid;
+    if (p.mode == kModeGrouped) {
+      const int E = p.num_groups;
+      const int* tp = tiles_prefix();
+      int lo = 0, hi = E - 1;  // last group e with tp[e] * tiles_n <= cur
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (static_cast<int64_t>(tp[mid]) * p.tiles_n <= cur) lo = mid;
+        else hi = mid - 1;
+      }
+      const int e = lo;
+      const int mte = tp[e + 1] - tp[e];
+      const int64_t local = cur - static_cast<int64_t>(tp[e]) * p.tiles_n;
+      const int nt = static_cast<int>(local / mte), mt = static_cast<int>(local % mte);
+      // a pair's second CTA may get rows of the next group (or none): they are loaded
+      // and multiplied but never stored
+      w.a_row = s_off[e] + mt * mtile + sub_row;
+      w.out_row0 = w.a_row;
+      w.rows_valid = max(0, min(128, s_off[e + 1] - w.a_row));
+      w.n0 = nt * TN;
+      w.b_row = e * p.b_rows_per_group + w.n0 + (TN == BN ? sub_row : 0);
+      w.sfa_rb = s_mt[e] + mt * (mtile / 128) + sub_row / 128;
+      w.sfb_off = e * p.sfb_group_bytes + static_cast<int64_t>(w.n0 / 128) * p.sfb_rb_bytes;
+      w.group = e;
+      w.kb0 = 0;
+      w.kb1 = p.num_kb;
+      w.tile = static_cast<int>(cur);
+      return true;
+    }
+    // tile mode: rasterize in groups of group_m m-tiles so concurrently running CTAs
+    // share A and B tiles in L2
+    const int per_group = p.group_m * p.tiles_n;
+    const int gi = static_cast<int>(cur / per_group);
+    const int first_m = gi * p.group_m;
+    const int gsize = min(p.tiles_m - first_m, p.group_m);
+    const int r = static_cast<int>(cur % per_group);
+    plain(w, first_m + r % gsize, r / gsize);
+    w.kb0 = 0;
+    w.kb1 = p.num_kb;
+    w.tile = static_cast<int>(cur);
+    return true;
+  }
+
+  // grouped: M-tile prefix per group in this schedule's tile height
+  __device__ const int* tiles_prefix() const { return mtile == 256 ? s_pt : s_mt; }
+
+  __device__ void plain(Work& w, int mt, int nt) {
+    w.a_row = mt * mtile + sub_row;
+    w.out_row0 = w.a_row;
+    w.rows_valid = max(0, min(128, p.Mk - w.a_row));
+    w.n0 = nt * TN;
+    // a pair's CTAs each load half of the tile's B rows (gated: the gate's, the up's)
+    w.b_row = w.n0 + (TN == BN ? sub_row : 0);
+    w.sfa_rb = w.a_row / 128;
+    w.sfb_off = static_cast<int64_t>(w.n0 / 128) * p.sfb_rb_bytes;
+    w.group = 0;
+  }
+};
+
+// Small-N tiles (decode) run two independent pipelines per CTA ("sub-CTAs" of 192
+// threads, each with its own producer, MMA issuer, epilogue warps, shared-memory ring
+// and TMEM columns).  One thread issues all tcgen05 operations of a pipeline, and at
+// N = 16..64 the issue latency of that thread -- not the tensor pipe -- bounds how fast
+// weight stages are consumed, so two issuers per SM double the rate.  (Two CTAs per SM
+// would do the same, but a kernel that allocates TMEM is scheduled one CTA per SM.)
+#ifndef FP4_SMALL_N_PIPES
+#define FP4_SMALL_N_PIPES 2
+#endif
+template <int BN>
+constexpr int pipes_per_cta() { return BN <= 32 ? FP4_SMALL_N_PIPES : BN <= 64 ? 2 : 1; }
+
+// F8: the kind::mxf8f6f4 MMA (E2M1 or E4M3 operands, one byte per element in shared
+// memory, an E8M0 scale per 32): a stage holds 128 K elements, one scale atom per row-block.
+template <int BN, bool MX, int ACC, bool PAIR = false, bool F8 = false, int EPI = kEpiPlain>
+struct Cfg {
+  static_assert(EPI != kEpiGated || BN == 256, "gated tiles: 128 gate and 128 up columns");
+  static_assert(EPI == kEpiPlain || !F8, "mixed-format products have the plain epilogue");
+  static_assert(!F8 || MX, "mixed-format MMAs: E8M0 scales");
+  static_assert(!PAIR || (BN == 256 && ACC == 1), "CTA pairs run 256 x 256 tiles");
+  static constexpr int kP = pipes_per_cta<BN>();
+  // Single-pipeline kernels (128/256-wide tiles) add copier warps that move each stage's
+  // scale factors into TMEM, so that these copies are not serialised behind the MMA
+  // thread's own MMAs: one for A's atoms and one per 128-row block of B's.
+  static constexpr bool kSepCp = kP == 1;
+  // The longer epilogues hold a whole accumulator half (128 FP32 values per thread) in
+  // registers: two copiers instead of three leave 12 warps, and 168 registers per thread.
+  static constexpr bool kLong = kSepCp && EPI != kEpiPlain;
+  static constexpr int kCopiers = !kSepCp ? 0 : kLong ? 2 : 1 + (BN >= 128 ? BN / 128 : 1);
+  // One-pipeline kernels run two epilogue warps per TMEM lane quarter, one per column
+  // half: twice the TMEM read and store rate, and half a row of packed BF16 per thread
+  // is few enough registers to hold the tile while TMEM is already handed back.
+  static constexpr int kEpiWarps = kSepCp ? 8 : 4;
+  static constexpr int kEpiCols = BN * 4 / kEpiWarps;  // accumulator columns per epilogue thread
+  static constexpr int kTileCols = EPI == kEpiGated ? BN / 2 : BN;  // output columns of a tile
+  // Registers per thread of a long epilogue's launch (384 threads), and what its warpgroups
+  // take: 128 threads of loads, MMAs and copies, 256 of epilogue.
+  static constexpr int kLaunchRegs = 168, kIssueRegs = 64, kEpiRegs = 216;
+  static_assert(128 * kIssueRegs + 256 * kEpiRegs <= 384 * kLaunchRegs, "register split");
+  static constexpr int kThreads = kSepCp ? 64 + 32 * kEpiWarps + 32 * kCopiers : 192 * kP;
+  // first epilogue / copier warp: the long epilogues' warps are two whole warpgroups
+  static constexpr int kEpiWarp0 = kLong ? 4 : 2;
+  static constexpr int kCopyWarp0 = kLong ? 2 : 2 + kEpiWarps;
+  static constexpr int kAtomsKT = F8 ? 1 : MX ? 2 : 4;  // scale atoms per stage (256 K; 128 K for F8)
+  static constexpr int kNRB = BN >= 128 ? BN / 128 : 1;  // B scale row-blocks per tile
+  static constexpr int kABytes = 128 * 128;
+  static constexpr int kBBytes = (PAIR ? BN / 2 : BN) * 128;  // a pair's CTA holds half of B's rows
+  static constexpr int kSFABytes = kAtomsKT * 512;
+  static constexpr int kSFBBytes = kNRB * kAtomsKT * 512;
+  // rounded up to 1024 bytes (the 128-byte swizzle's alignment): only the mixed-format
+  // stages (one scale atom per row-block) need the padding
+  static constexpr int kStageBytes = (kABytes + kBBytes + kSFABytes + kSFBBytes + 1023) / 1024 * 1024;
+  // grouped schedules use 128-wide tiles only, so multi-pipeline kernels skip the group tables
+  static constexpr int kGroupBytes = kP == 1 ? (PAIR ? 3 : 2) * (kMaxGroups + 1) * 4 : 0;
+  static constexpr int kMiscBytes = 1024 /*barriers, flags*/ + kGroupBytes;
+  // the opt-in limit per block, less the alignment slack and the static shared memory
+  static constexpr int kSmemLimit = 227 * 1024 - 1024 - 256;
+  static constexpr int kStagesFit = (kSmemLimit / kP - kMiscBytes) / kStageBytes;
+  static constexpr int kStages = kStagesFit > 12 ? 12 : kStagesFit;
+  // one pipeline's share; the next pipeline's stages start 1024-byte aligned
+  static constexpr int kSubBytes = (kStages * kStageBytes + kMiscBytes + 1023) / 1024 * 1024;
+  static constexpr int kSmemBytes = kP == 1 ? kStages * kStageBytes + kMiscBytes + 1024 : kP * kSubBytes + 1024;
+  static_assert(kSmemBytes + 256 <= 227 * 1024, "shared memory opt-in limit");
+  static constexpr int kSFACols = kAtomsKT * 4;
+  static constexpr int kSFBCols = kNRB * kAtomsKT * 4;
+  static constexpr int kSFSlot = kSFACols + kSFBCols;
+  // TMEM slots for the stages' scale factors: with a separate copier, as many as fit
+  // (up to 4, and fewer than the ring's stages) so that it can run ahead of the MMAs
+  static constexpr int kSlotsFit = (512 - ACC * BN) / kSFSlot;
+  static constexpr int kSFSlots = !kSepCp ? 2 : (kSlotsFit < 4 ? kSlotsFit : 4) < kStages ? (kSlotsFit < 4 ? kSlotsFit : 4)
+                                                                                           : kStages - 1;
+  static constexpr int kColsUsed = ACC * BN + kSFSlots * kSFSlot;
+  static constexpr int kTmemCols = kColsUsed <= 32 ? 32 : kColsUsed <= 64 ? 64 : kColsUsed <= 128 ? 128
+                                   : kColsUsed <= 256 ? 256 : 512;  // per pipeline
+  // one allocation for all pipelines: a power of two of at least 32 columns
+  static constexpr int kTmemAlloc = kP * kTmemCols <= 32 ? 32 : kP * kTmemCols <= 64 ? 64
+                                    : kP * kTmemCols <= 128 ? 128 : kP * kTmemCols <= 256 ? 256 : 512;
+  static_assert(kP * kTmemCols <= 512, "TMEM budget");
+  static_assert(kSFSlots >= 2 && kSFSlots < kStages, "scale-factor slots");
+  static_assert(kStageBytes % 1024 == 0 && kSubBytes % 1024 == 0, "128-byte swizzled stages need 1024-byte alignment");
+  static_assert(kStages >= 2, "shared memory budget");
+  static_assert(BN % 16 == 0 && BN >= 16 && BN <= 256, "MMA N");
+};
+
+__device__ __forceinline__ void latch_timeout(volatile int* abort, unsigned* status) {
+  *abort = 1;
+  atomicOr(status, kStatusTimeout);
+}
+
+__device__ __forceinline__ uint32_t pack_bf16x2(float a, float b) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+__device__ __forceinline__ void red_add_v4(float* addr, float a, float b, float c, float d) {
+  asm volatile("red.relaxed.gpu.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(addr), "f"(a), "f"(b), "f"(c),
+               "f"(d)
+               : "memory");
+}
+
+// Waits until the grids this one depends on (programmatic dependent launch) have
+// finished and their writes are visible; a no-op when launched without the attribute.
+__device__ __forceinline__ void wait_prior_grids() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// Lets the kernel launched after this one on the stream start its prologue now (it still
+// waits for this grid's completion before it reads what this grid writes).
+__device__ __forceinline__ void allow_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+__device__ __forceinline__ void store_out(const GemmArgs& p, int64_t off, float v) {
+  if (p.out_bf16) reinterpret_cast<__nv_bfloat16*>(p.out)[off] = __float2bfloat16_rn(v);
+  else reinterpret_cast<float*>(p.out)[off] = v;
+}
+
+// Stores 16 consecutive kernel columns [col, col+16) of one kernel row.  With swapped
+// operands (transposed) kernel row = output column and kernel column = output row.
+__device__ __forceinline__ void store_row16(const GemmArgs& p, int row, int col, const float (&v)[16]) {
+  if (p.transposed) {
+#pragma unroll
+    for (int j = 0; j < 16; ++j)
+      if (col + j < p.Nk) store_out(p, static_cast<int64_t>(col + j) * p.ldo + row, v[j]);
+    return;
+  }
+  const int64_t base = static_cast<int64_t>(row) * p.ldo + col;
+  if (p.vec_store && col + 16 <= p.Nk) {
+    if (p.out_bf16) {
+      uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(p.out) + base);
+      dst[0] = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                          pack_bf16x2(v[6], v[7]));
+      dst[1] = make_uint4(pack_bf16x2(v[8], v[9]), pack_bf16x2(v[10], v[11]), pack_bf16x2(v[12], v[13]),
+                          pack_bf16x2(v[14], v[15]));
+    } else {
+      float4* dst = reinterpret_cast<float4*>(reinterpret_cast<float*>(p.out) + base);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) dst[j] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+    }
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < 16; ++j)
+    if (col + j < p.Nk) store_out(p, base + j, v[j]);
+}
+
+// Bias and activation of 16 consecutive kernel columns [col, col+16) of kernel row `row`
+// (values already multiplied by gA * gB).  With swapped operands the kernel row is the
+// output column, which indexes the bias.
+__device__ __forceinline__ void epi_bias_act(const GemmArgs& p, int row, int col, float (&v)[16]) {
+  if (p.bias) {
+    if (p.transposed) {
+      const float b = p.bias[row];
+#pragma unroll
+      for (int j = 0; j < 16; ++j) v[j] = __fadd_rn(v[j], b);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 16; ++j)
+        if (col + j < p.Nk) v[j] = __fadd_rn(v[j], __ldg(p.bias + col + j));
+    }
+  }
+  if (p.act == 1) {
+#pragma unroll
+    for (int j = 0; j < 16; ++j) v[j] = fmaxf(v[j], 0.0f);
+  }
+}
+
+// NVFP4 copy of 16 output columns [col, col+16) of output row `row` (one block; the
+// caller guarantees N % 32 == 0 and a row-major kernel orientation): block scale and
+// codes exactly as the quantize kernels compute them, with the caller's global scale.
+__device__ __forceinline__ void epi_quantize16(const GemmArgs& p, int row, int col, const float (&v)[16]) {
+  const float g = *p.q_g;
+  uint32_t m = 0;
+#pragma unroll
+  for (int j = 0; j < 16; ++j) m = max(m, __float_as_uint(v[j]) & 0x7FFFFFFFu);
+  uint32_t sb;
+  const float mul = nvfp4_block_scale(__uint_as_float(m), g, sb);
+  float a[8], b[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    a[j] = v[j] == 0.0f ? v[j] : __fmul_rn(v[j], mul);  // a zero stays zero if 1/denom overflowed
+    b[j] = v[8 + j] == 0.0f ? v[8 + j] : __fmul_rn(v[8 + j], mul);
+  }
+  *reinterpret_cast<uint2*>(p.q_codes + static_cast<int64_t>(row) * (p.Nk / 2) + col / 2) =
+      make_uint2(pack8<kE2M1Hardware>(a), pack8<kE2M1Hardware>(b));
+  const int c = col / 16;
+  p.q_scales[((row / 128) * p.q_atoms + c / 4) * 512 + (row % 32) * 16 + ((row % 128) / 32) * 4 + c % 4] =
+      static_cast<uint8_t>(sb);
+}
+
+// Finishes 16 consecutive kernel columns of one kernel row: bias, activation, the
+// BF16 / FP32 store and the NVFP4 copy.
+__device__ __forceinline__ void epi_row16(const GemmArgs& p, int row, int col, float (&v)[16], uint32_t& tmax) {
+  epi_bias_act(p, row, col, v);
+  if (p.out) store_row16(p, row, col, v);
+  if (p.q_codes && col < p.Nk) epi_quantize16(p, row, col, v);
+  if (p.amax_out) {  // the result's amax, for the global scale of its next quantization
+#pragma unroll
+    for (int j = 0; j < 16; ++j)
+      if (p.transposed || col + j < p.Nk) tmax = max(tmax, __float_as_uint(v[j]) & 0x7FFFFFFFu);
+  }
+}
+
+// Reads 16 summed partials of one row (columns [col, col + 16) of n), clears them, scales.
+__device__ __forceinline__ void take_sums16(float* row, int col, int n, float scale, float (&v)[16]) {
+  if ((n & 3) == 0 && col + 16 <= n) {
+#pragma unroll
+    for (int j = 0; j < 16; j += 4) {
+      float4* at = reinterpret_cast<float4*>(row + col + j);
+      const float4 t = __ldcg(at);
+      __stcg(at, make_float4(0.f, 0.f, 0.f, 0.f));
+      v[j] = t.x * scale;
+      v[j + 1] = t.y * scale;
+      v[j + 2] = t.z * scale;
+      v[j + 3] = t.w * scale;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      v[j] = 0.0f;
+      if (col + j < n) {
+        v[j] = __ldcg(row + col + j) * scale;
+        __stcg(row + col + j, 0.0f);
+      }
+    }
+  }
+}
+
+// 16 consecutive elements at offset `at` of a BF16 or FP32 matrix, 16-byte aligned.
+__device__ __forceinline__ void store_vec16(void* out, int bf16, int64_t at, const float (&v)[16]) {
+  if (bf16) {
+    uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(out) + at);
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      __stcs(dst + j, make_uint4(pack_bf16x2(v[8 * j], v[8 * j + 1]), pack_bf16x2(v[8 * j + 2], v[8 * j + 3]),
+                                 pack_bf16x2(v[8 * j + 4], v[8 * j + 5]), pack_bf16x2(v[8 * j + 6], v[8 * j + 7])));
+  } else {
+    float4* dst = reinterpret_cast<float4*>(static_cast<float*>(out) + at);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) __stcs(dst + j, make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]));
+  }
+}
+
+__device__ __forceinline__ void load_vec16(const void* in, int bf16, int64_t at, float (&v)[16]) {
+  if (bf16) {
+    const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(in) + at);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const uint4 t = src[h];
+      const uint32_t w4[4] = {t.x, t.y, t.z, t.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        v[8 * h + 2 * j] = __uint_as_float(w4[j] << 16);
+        v[8 * h + 2 * j + 1] = __uint_as_float(w4[j] & 0xFFFF0000u);
+      }
+    }
+  } else {
+    const float4* src = reinterpret_cast<const float4*>(static_cast<const float*>(in) + at);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float4 t = src[j];
+      v[4 * j] = t.x;
+      v[4 * j + 1] = t.y;
+      v[4 * j + 2] = t.z;
+      v[4 * j + 3] = t.w;
+    }
+  }
+}
+
+// The same at any alignment.
+__device__ __forceinline__ void load_vec16_any(const void* in, int bf16, int64_t at, float (&v)[16]) {
+#pragma unroll
+  for (int j = 0; j < 16; ++j)
+    v[j] = bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(in)[at + j]) : static_cast<const float*>(in)[at + j];
+}
+
+// v += 16 FP32 parameters (every row of the tile reads the same ones).
+__device__ __forceinline__ void add_vec16(const float* b, float (&v)[16]) {
+#pragma unroll
+  for (int j = 0; j < 16; ++j) v[j] = __fadd_rn(v[j], __ldg(b + j));
+}
+
+// Offset in the output of kernel row `row`, column `col`.
+__device__ __forceinline__ int64_t out_offset(const GemmArgs& p, int row, int col) {
+  return p.transposed ? static_cast<int64_t>(col) * p.ldo + row : static_cast<int64_t>(row) * p.ldo + col;
+}
+
+// Stores 16 values of kernel row `row`, columns [col, col + 16), to a matrix laid out as the
+// output is (`out` in the output's type); columns past the matrix are left out.
+__device__ __forceinline__ void store_like_out(const GemmArgs& p, void* out, int row, int col, const float (&v)[16]) {
+  if (!p.transposed && p.vec_store && col + 16 <= p.Nk) {
+    store_vec16(out, p.out_bf16, out_offset(p, row, col), v);
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < 16; ++j)
+    if (col + j < p.Nk) {
+      const int64_t off = out_offset(p, row, col + j);
+      if (p.out_bf16) static_cast<__nv_bfloat16*>(out)[off] = __float2bfloat16_rn(v[j]);
+      else static_cast<float*>(out)[off] = v[j];
+    }
+}
+
+// Adds 16 elements of the residual (same rows and columns as the output, its own type).
+__device__ __forceinline__ void add_residual16(const GemmArgs& p, int row, int col, float (&v)[16]) {
+#pragma unroll
+  for (int j = 0; j < 16; ++j)
+    if (col + j < p.Nk) {
+      const int64_t off = out_offset(p, row, col + j);
+      v[j] += p.res_bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(p.res)[off]) : static_cast<const float*>(p.res)[off];
+    }
+}
+
+// Bias of 16 kernel columns (swapped operands: of the kernel row, which is the output column).
+__device__ __forceinline__ void add_bias16(const GemmArgs& p, const float* bias, int row, int col, float (&v)[16]) {
+  if (p.transposed) {
+    const float b = __ldg(bias + row);
+#pragma unroll
+    for (int j = 0; j < 16; ++j) v[j] = __fadd_rn(v[j], b);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 16; ++j)
+      if (col + j < p.Nk) v[j] = __fadd_rn(v[j], __ldg(bias + col + j));
+  }
+}
+
+// Finishes 16 consecutive kernel columns of one kernel row in the long epilogues (values
+// already multiplied by their global scales): biases, copies of the pre-activations,
+// activation, product with u (gated) or residual, output, NVFP4 copy, maximum.
+template <bool GATED>
+__device__ __forceinline__ void epi_finish16(const GemmArgs& p, int row, int col, int group, float (&v)[16],
+                                             float (&u)[16], uint32_t& tmax) {
+  if (p.bias) add_bias16(p, p.bias + group * p.bias_group, row, col, v);
+  if (GATED && p.bias2) add_bias16(p, p.bias2 + group * p.bias_group, row, col, u);
+  if (p.pre) store_like_out(p, p.pre, row, col, v);
+  if (GATED && p.pre2) store_like_out(p, p.pre2, row, col, u);
+  with_act(p.act, [&](auto tag) {
+    constexpr int A = decltype(tag)::value;
+#pragma unroll
+    for (int j = 0; j < 16; ++j) v[j] = GATED ? act_value<A>(v[j]) * u[j] : act_value<A>(v[j]);
+  });
+  if (!GATED && p.res) add_residual16(p, row, col, v);
+  if (p.out) store_like_out(p, p.out, row, col, v);
+  if (p.q_codes) epi_quantize16(p, row, col, v);
+  if (p.amax_out) {
+#pragma unroll
+    for (int j = 0; j < 16; ++j)
+      if (col + j < p.Nk) tmax = max(tmax, __float_as_uint(v[j]) & 0x7FFFFFFFu);
+  }
+}
+
+// Named barrier among the epilogue threads of one pipeline.
+__device__ __forceinline__ void epi_sync(int sub, int nthreads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(1 + sub), "r"(nthreads) : "memory");
+}
+
+// Operands as tensor maps (b2, sfb2: the up operand of a gated product).
+struct GemmMaps {
+  CUtensorMap a, b, sfa, sfb, b2, sfb2;
+};
+
+template <int BN, bool MX, int ACC, bool PAIR, bool F8 = false, int EPI = kEpiPlain>
+__global__ void __launch_bounds__(Cfg<BN, MX, ACC, PAIR, F8, EPI>::kThreads, 1)
+    fp4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                    const __grid_constant__ CUtensorMap tmSFA, const __grid_constant__ CUtensorMap tmSFB,
+                    const __grid_constant__ CUtensorMap tmB2, const __grid_constant__ CUtensorMap tmSFB2,
+                    const GemmArgs p) {
+  using C = Cfg<BN, MX, ACC, PAIR, F8, EPI>;
+  constexpr int S = C::kStages;
+  constexpr bool kGated = EPI == kEpiGated;
+  using Schedule = Sched<BN, kGated ? BN / 2 : BN>;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ uint32_t s_tmem_base;
+  const int sub = C::kP == 1 ? 0 : threadIdx.x / 192;  // pipeline of this thread
+  const int lt = C::kP == 1 ? threadIdx.x : threadIdx.x % 192;
+  const int warp = lt >> 5, lane = lt & 31;
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023)) +
+                  sub * C::kSubBytes;
+  uint8_t* misc = smem + S * C::kStageBytes;
+  uint64_t* full = reinterpret_cast<uint64_t*>(misc);
+  uint64_t* empty = full + S;
+  uint64_t* acc_full = empty + S;
+  uint64_t* acc_empty = acc_full + ACC;
+  uint64_t* drain = acc_empty + ACC;
+  uint64_t* sf_full = drain + 1;                // [kSFSlots]: stage scale factors are in TMEM slot i
+  uint64_t* cp_drain = sf_full + C::kSFSlots;   // the copier warps' last copies have completed
+  // [S]: a stage's scale factors have landed.  With a separate copier they complete on
+  // their own barrier (and are issued first), so that the copier warps move them into TMEM
+  // while the stage's operand tiles are still arriving; otherwise they complete on full.
+  uint64_t* sf_landed = cp_drain + 1;
+  volatile int* s_abort = reinterpret_cast<volatile int*>(sf_landed + S);
+  volatile int* s_epi_fail = s_abort + 1;
+  volatile int* s_last = s_abort + 2;  // stream-K: this pipeline completes the current tile
+  int* s_mt = reinterpret_cast<int*>(misc + 1024);
+  int* s_off = s_mt + (kMaxGroups + 1);
+  int* s_pt = PAIR ? s_off + (kMaxGroups + 1) : nullptr;
+  // A CTA pair (cluster of two) shares one 256 x 256 tile: rank 0, the leader, issues the
+  // MMAs and scale-factor copies for both; each CTA loads its own 128 rows of A, its half
+  // of B's rows, its A scales and all of the tile's B scales, and stores its 128 rows.
+  const uint32_t rank = PAIR ? cluster_rank() : 0u;
+  const bool leader = rank == 0;
+  const int vb = PAIR ? static_cast<int>(blockIdx.x >> 1) : static_cast<int>(blockIdx.x) * C::kP + sub;
+  const int vg = PAIR ? static_cast<int>(gridDim.x >> 1) : static_cast<int>(gridDim.x) * C::kP;
+  constexpr int kMTile = PAIR ? 256 : 128;
+  const int sub_row = static_cast<int>(rank) * 128;
+
+  // prologue (overlaps the tail of the previous kernel under programmatic launch)
+  if (lt == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+      mbar_init(&sf_landed[s], 1);
+    }
+    for (int a = 0; a < ACC; ++a) {
+      mbar_init(&acc_full[a], 1);
+      mbar_init(&acc_empty[a], (PAIR ? 2 : 1) * C::kEpiWarps);  // a pair: both CTAs' epilogue warps
+    }
+    mbar_init(drain, 1);
+    for (int i = 0; i < C::kSFSlots; ++i) mbar_init(&sf_full[i], C::kSepCp ? C::kCopiers : 1);
+    mbar_init(cp_drain, C::kSepCp ? C::kCopiers : 1);
+    *s_abort = 0;
+    *s_epi_fail = 0;
+    *s_last = 0;
+    fence_mbar_init();
+  }
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_desc(&tmA);
+    tma_prefetch_desc(&tmB);
+    if (kGated) tma_prefetch_desc(&tmB2);
+    if (PAIR) {
+      tma_prefetch_desc(&tmSFA);
+      tma_prefetch_desc(&tmSFB);
+    }
+  }
+  if (sub == 0 && warp == 1) {  // one allocation for all pipelines of the CTA
+    if constexpr (PAIR) {       // the same columns in both CTAs of the pair
+      tmem_alloc_pair(&s_tmem_base, C::kTmemAlloc);
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(&s_tmem_base, C::kTmemAlloc);
+      tmem_relinquish();
+    }
+  }
+  // the next kernel on the stream may launch now; it waits for this grid to complete
+  allow_dependents();
+  if (p.mode == kModeGrouped && warp == 2) {
+    wait_prior_grids();  // the offsets may come from the previous kernel
+    // m-tile prefix per group (= scale row-block prefix of the grouped A layout)
+    const int E = p.num_groups;
+    // (CTA pairs: also the prefix of 256-row tiles, by which they enumerate tiles)
+    int carry = 0, carry2 = 0;
+    for (int base = 0; base < E; base += 32) {
+      const int e = base + lane;
+      int cnt = 0, cnt2 = 0;
+      if (e < E) {
+        const int lo = p.offsets[e], hi = p.offsets[e + 1];
+        s_off[e] = lo;
+        cnt = (hi - lo + 127) / 128;
+        cnt2 = (hi - lo + 255) / 256;
+      }
+      int incl = cnt, incl2 = cnt2;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int t = __shfl_up_sync(0xFFFFFFFFu, incl, d);
+        const int t2 = __shfl_up_sync(0xFFFFFFFFu, incl2, d);
+        if (lane >= d) {
+          incl += t;
+          incl2 += t2;
+        }
+      }
+      if (e < E) {
+        s_mt[e] = carry + incl - cnt;
+        if (PAIR) s_pt[e] = carry2 + incl2 - cnt2;
+      }
+      carry += __shfl_sync(0xFFFFFFFFu, incl, 31);
+      carry2 += __shfl_sync(0xFFFFFFFFu, incl2, 31);
+    }
+    if (lane == 0) {
+      s_mt[E] = carry;
+      if (PAIR) s_pt[E] = carry2;
+      s_off[E] = p.offsets[E];
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  // a pair: the peer's barriers are initialised before this CTA's loads and arrivals reach them
+  if constexpr (PAIR) cluster_sync_all();
+  tc_fence_after();
+  const uint32_t tmem = s_tmem_base + sub * C::kTmemCols;
+  const uint32_t sf_col0 = ACC * BN;
+  // copies one stage's scale-factor atoms (A's, then B's row-blocks) into a TMEM slot
+  auto copy_stage_sf = [&](uint32_t st, uint32_t sfa_t, int kb) {
+    const uint32_t sfb_t = sfa_t + C::kSFACols;
+    const int atoms = min(C::kAtomsKT, p.sf_atoms_k - kb * C::kAtomsKT);
+    for (int a = 0; a < atoms; ++a) tc_cp_sf_atom(sfa_t + a * 4, smem_desc_sf(st + C::kABytes + C::kBBytes + a * 512));
+#pragma unroll
+    for (int rb = 0; rb < C::kNRB; ++rb)
+      for (int a = 0; a < atoms; ++a)
+        tc_cp_sf_atom(sfb_t + (a * C::kNRB + rb) * 4,
+                      smem_desc_sf(st + C::kABytes + C::kBBytes + C::kSFABytes + (rb * C::kAtomsKT + a) * 512));
+  };
+
+  if constexpr (C::kLong) {  // warps 0..3 issue, warps 4..11 finish: whole warpgroups
+    static_assert(C::kThreads == 384, "three warpgroups");
+    if (warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kIssueRegs));
+    else asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kEpiRegs));
+  }
+  if (warp == 0) {
+    if (lane == 0) {
+      // ------------------------------------------------------------ producer
+      // swapped decode: the weights (A here) are read once -> evict first; the small
+      // activations (B) are re-read by every CTA -> keep
+      // otherwise both operands are re-read by other tiles -> keep (the output is stored
+      // with the streaming hint, so that it does not push them out of L2)
+      const uint64_t pol_a = p.transposed ? l2_policy_evict_first() : l2_policy_evict_last();
+      const uint64_t pol_b = l2_policy_evict_last();
+      // Loads of one stage: the A box and A scales ("a" side), the B box and B scales.
+      auto load_side = [&](int st_idx, const Work& w, int kb, bool side_a) {
+        uint8_t* st = smem + st_idx * C::kStageBytes;
+        const int atoms = min(C::kAtomsKT, p.sf_atoms_k - kb * C::kAtomsKT);
+        const uint32_t sf_bytes = static_cast<uint32_t>(atoms) * 512u;
+        const int64_t koff = static_cast<int64_t>(kb) * C::kAtomsKT * 512;
+        if constexpr (PAIR) {
+          // every box in full (out-of-range rows read as zero), so that the leader can
+          // expect a fixed byte count from both CTAs on its own barriers
+          const uint32_t c_full = cluster_addr(smem_u32(&full[st_idx]), 0);
+          const uint32_t c_sf = cluster_addr(smem_u32(&sf_landed[st_idx]), 0);
+          if (side_a) {
+            tma_load_2d_pair(st + C::kABytes + C::kBBytes, &tmSFA, c_sf, 0,
+                             static_cast<int>((w.sfa_rb * p.sfa_rb_bytes + koff) / 256), pol_a);
+            tma_load_2d_pair(st, &tmA, c_full, kb * 128, w.a_row, pol_a);
+          } else {
+#pragma unroll
+            for (int rb = 0; rb < C::kNRB; ++rb)
+              tma_load_2d_pair(st + C::kABytes + C::kBBytes + C::kSFABytes + rb * C::kAtomsKT * 512,
+                               kGated && rb ? &tmSFB2 : &tmSFB, c_sf, 0,
+                               static_cast<int>((w.sfb_off + (kGated ? 0 : rb) * p.sfb_rb_bytes + koff) / 256), pol_b);
+            // gated: the leader holds the tile's gate rows, the other CTA its up rows
+            tma_load_2d_pair(st + C::kABytes, kGated && !leader ? &tmB2 : &tmB, c_full, kb * 128, w.b_row, pol_b);
+          }
+          (void)sf_bytes;
+          return;
+        }
+        uint64_t* sf_bar = C::kSepCp ? &sf_landed[st_idx] : &full[st_idx];
+        if (side_a) {
+          bulk_load(st + C::kABytes + C::kBBytes, p.sfa + w.sfa_rb * p.sfa_rb_bytes + koff, sf_bytes, sf_bar, pol_a);
+          tma_load_2d(st, &tmA, &full[st_idx], kb * 128, w.a_row, pol_a);
+        } else {
+          if constexpr (kGated) {
+            bulk_load(st + C::kABytes + C::kBBytes + C::kSFABytes, p.sfb + w.sfb_off + koff, sf_bytes, sf_bar, pol_b);
+            bulk_load(st + C::kABytes + C::kBBytes + C::kSFABytes + C::kAtomsKT * 512, p.sfb2 + w.sfb_off + koff,
+                      sf_bytes, sf_bar, pol_b);
+            tma_load_2d(st + C::kABytes, &tmB, &full[st_idx], kb * 128, w.b_row, pol_b);
+            tma_load_2d(st + C::kABytes + C::kBBytes / 2, &tmB2, &full[st_idx], kb * 128, w.b_row, pol_b);
+            return;
+          }
+          const int rb0 = w.n0 / 128;
+#pragma unroll
+          for (int rb = 0; rb < C::kNRB; ++rb)
+            if (rb0 + rb < p.sfb_rbs)
+              bulk_load(st + C::kABytes + C::kBBytes + C::kSFABytes + rb * C::kAtomsKT * 512,
+                        p.sfb + w.sfb_off + rb * p.sfb_rb_bytes + koff, sf_bytes, sf_bar, pol_b);
+          tma_load_2d(st + C::kABytes, &tmB, &full[st_idx], kb * 128, w.b_row, pol_b);
+        }
+      };
+      auto stage_sf_bytes = [&](const Work& w, int kb) -> uint32_t {
+        const int atoms = min(C::kAtomsKT, p.sf_atoms_k - kb * C::kAtomsKT);
+        const uint32_t sf_bytes = static_cast<uint32_t>(atoms) * 512u;
+        if (kGated) return sf_bytes * 3;
+        const int rb0 = w.n0 / 128;
+        int nrb = 0;
+#pragma unroll
+        for (int rb = 0; rb < C::kNRB; ++rb) nrb += (rb0 + rb < p.sfb_rbs) ? 1 : 0;
+        return sf_bytes * (1 + nrb);
+      };
+      // With an independent operand, the first ring-full of stages loads only that side,
+      // then waits for the preceding kernel, then issues the other side of those stages.
+      const bool early = p.indep != 0;
+      const bool early_a = p.indep == 1;
+      int npend = 0;
+      bool replayed = !early;
+      auto replay = [&]() {
+        wait_prior_grids();
+        Schedule rs(p, s_mt, s_off, vb, vg, kMTile, sub_row, s_pt);
+        Work rw;
+        int j = 0;
+        while (j < npend && rs.next(rw))
+          for (int kb = rw.kb0; kb < rw.kb1 && j < npend; ++kb, ++j) load_side(j, rw, kb, !early_a);
+        replayed = true;
+      };
+      if (!early) wait_prior_grids();
+      Schedule sch(p, s_mt, s_off, vb, vg, kMTile, sub_row, s_pt);
+      Work w;
+      int stage = 0;
+      uint32_t phase = 0, issued = 0, issued_par = 0;
+      bool ok = true;
+      // operand bytes a stage's tensor copies complete: a 4-bit operand of the mixed-format
+      // MMA counts its packed bytes (half its footprint in shared memory)
+      uint32_t ab_tx = C::kABytes + C::kBBytes;
+      if constexpr (F8)
+        ab_tx = ((p.f8_fmt & 7u) == kFmtE2M1 ? C::kABytes / 2 : C::kABytes) +
+                (((p.f8_fmt >> 3) & 7u) == kFmtE2M1 ? C::kBBytes / 2 : C::kBBytes);
+      while (ok && sch.next(w)) {
+        for (int kb = w.kb0; kb < w.kb1; ++kb) {
+          if (!mbar_wait(&empty[stage], phase ^ 1, s_abort)) {
+            latch_timeout(s_abort, p.status);
+            ok = false;
+            break;
+          }
+          if constexpr (PAIR) {
+            if (leader) {  // the leader's barriers count the boxes of both CTAs
+              mbar_arrive_expect_tx(&sf_landed[stage], 2 * (C::kSFABytes + C::kSFBBytes));
+              mbar_arrive_expect_tx(&full[stage], 2 * ab_tx);
+            }
+          } else if constexpr (C::kSepCp) {
+            mbar_arrive_expect_tx(&sf_landed[stage], stage_sf_bytes(w, kb));
+            mbar_arrive_expect_tx(&full[stage], ab_tx);
+          } else {
+            mbar_arrive_expect_tx(&full[stage], C::kABytes + C::kBBytes + stage_sf_bytes(w, kb));
+          }
+          if (!replayed) {
+            load_side(stage, w, kb, early_a);
+            if (++npend == S) replay();
+          } else {
+            load_side(stage, w, kb, true);
+            load_side(stage, w, kb, false);
+          }
+          issued |= 1u << stage;
+          issued_par = (issued_par & ~(1u << stage)) | (phase << stage);
+          if (++stage == S) {
+            stage = 0;
+            phase ^= 1;
+          }
+        }
+      }
+      if (ok && !replayed) replay();
+      // let every issued copy land before the CTA's shared memory goes away (a pair's
+      // leader waits for both CTAs' boxes: they complete on its barriers)
+      if (*s_abort && leader) {
+        for (int s = 0; s < S; ++s)
+          if (issued & (1u << s)) {
+            volatile int no_abort = 0;
+            mbar_wait(&full[s], (issued_par >> s) & 1u, &no_abort);
+            if (C::kSepCp) mbar_wait(&sf_landed[s], (issued_par >> s) & 1u, &no_abort);
+          }
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0 && leader) {
+      // ------------------------------------------------------------ MMA issuer
+      Schedule sch(p, s_mt, s_off, vb, vg, kMTile, sub_row, s_pt);
+      const uint32_t smem_base = smem_u32(smem);
+      Work w;
+      int stage = 0, iter = 0, nstage = 0;
+      uint32_t phase = 0, slot = 0;
+      bool ok = true;
+      while (ok && sch.next(w)) {
+        const int acc = iter % ACC;
+        if (!mbar_wait(&acc_empty[acc], ((iter / ACC) & 1) ^ 1, s_abort)) {
+          latch_timeout(s_abort, p.status);
+          break;
+        }
+        tc_fence_after();
+        const uint32_t d_tmem = tmem + acc * BN;
+        for (int kb = w.kb0; kb < w.kb1; ++kb) {
+          if (!mbar_wait(&full[stage], phase, s_abort)) {
+            latch_timeout(s_abort, p.status);
+            ok = false;
+            break;
+          }
+          const uint32_t st = smem_base + stage * C::kStageBytes;
+          const uint32_t sfa_t = tmem + sf_col0 + slot * C::kSFSlot;
+          const uint32_t sfb_t = sfa_t + C::kSFACols;
+          if constexpr (C::kSepCp) {
+            // the copier warps have put this stage's scale factors into the slot
+            if (!mbar_wait(&sf_full[slot], (nstage / C::kSFSlots) & 1, s_abort)) {
+              latch_timeout(s_abort, p.status);
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+          } else {
+            tc_fence_after();
+            copy_stage_sf(st, sfa_t, kb);
+          }
+          ++nstage;
+          const int krem = p.K - kb * (F8 ? 128 : 256);
+          const int nk = F8 ? (krem >= 128 ? 4 : (krem + 31) / 32) : (krem >= 256 ? 4 : (krem + 63) / 64);
+          const uint64_t adesc = smem_desc_sw128(st);
+          const uint64_t bdesc = smem_desc_sw128(st + C::kABytes);
+          if constexpr (F8) {
+            // four K = 32 MMAs over the stage's 128-byte rows (one byte per element of
+            // either format); MMA k reads byte k of each row's 32-bit scale word
+            for (int k = 0; k < nk; ++k) {
+              const uint32_t sfid = static_cast<uint32_t>(k);
+              const uint32_t idesc = mma_idesc_f8(BN, p.f8_fmt & 7u, (p.f8_fmt >> 3) & 7u, sfid, sfid, kMTile);
+              const uint32_t accum = (kb > w.kb0 || k > 0) ? 1u : 0u;
+              if constexpr (PAIR)
+                tc_mma_mxf8f6f4_pair(d_tmem, adesc + 2 * k, bdesc + 2 * k, idesc, sfa_t | (sfid << 30),
+                                     sfb_t | (sfid << 30), accum);
+              else
+                tc_mma_mxf8f6f4(d_tmem, adesc + 2 * k, bdesc + 2 * k, idesc, sfa_t | (sfid << 30),
+                                sfb_t | (sfid << 30), accum);
+            }
+          } else {
+          for (int k = 0; k < nk; ++k) {
+            const uint32_t a_idx = MX ? (k >> 1) : k;
+            const uint32_t sfid = MX ? (k & 1) * 2 : 0;
+            const uint32_t idesc = mma_idesc(BN, MX, sfid, sfid, kMTile);
+            const uint32_t accum = (kb > w.kb0 || k > 0) ? 1u : 0u;
+            const uint32_t ta = (sfa_t + a_idx * 4) | (sfid << 30);
+            const uint32_t tb = (sfb_t + a_idx * C::kNRB * 4) | (sfid << 30);
+            if constexpr (PAIR && MX)
+              tc_mma_mxfp4_pair(d_tmem, adesc + 2 * k, bdesc + 2 * k, idesc, ta, tb, accum);
+            else if constexpr (PAIR)
+              tc_mma_nvfp4_pair(d_tmem, adesc + 2 * k, bdesc + 2 * k, idesc, ta, tb, accum);
+            else if constexpr (MX)
+              tc_mma_mxfp4(d_tmem, adesc + 2 * k, bdesc + 2 * k, idesc, ta, tb, accum);
+            else
+              tc_mma_nvfp4(d_tmem, adesc + 2 * k, bdesc + 2 * k, idesc, ta, tb, accum);
+          }
+          }
+          if constexpr (PAIR)
+            tc_commit_pair_mc(&empty[stage], 3);  // frees the stage in both CTAs
+          else
+            tc_commit(&empty[stage]);
+          if (++slot == C::kSFSlots) slot = 0;
+          if (++stage == S) {
+            stage = 0;
+            phase ^= 1;
+          }
+        }
+        if (!ok) break;
+        if constexpr (PAIR)
+          tc_commit_pair_mc(&acc_full[acc], 3);  // both CTAs' epilogues
+        else
+          tc_commit(&acc_full[acc]);
+        ++iter;
+      }
+      // make sure no MMA still writes TMEM when it is freed
+      if constexpr (PAIR)
+        tc_commit_pair(drain);
+      else
+        tc_commit(drain);
+      volatile int no_abort = 0;
+      mbar_wait(drain, 0, &no_abort);
+    }
+  } else if (C::kSepCp && warp >= C::kCopyWarp0 && warp < C::kCopyWarp0 + C::kCopiers) {
+    // 0: A's atoms; 1 + rb: B's row-block rb.  Two copiers for three sets: the first takes
+    // A's atoms and half of the second row-block's, the second the rest.
+    const int cw = warp - C::kCopyWarp0;
+    if (lane == 0 && leader) {
+      // ------------------------------------------------------------ scale-factor copier
+      // Stage n's atoms go to TMEM slot n % kSFSlots once they have landed and the
+      // MMAs of stage n - kSFSlots (the slot's previous user) have completed; each slot's
+      // copies are committed to sf_full[slot] for the MMA thread.
+      Schedule sch(p, s_mt, s_off, vb, vg, kMTile, sub_row, s_pt);
+      const uint32_t smem_base = smem_u32(smem);
+      Work w;
+      int stage = 0, n = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      while (ok && sch.next(w)) {
+        for (int kb = w.kb0; kb < w.kb1; ++kb) {
+          if (!mbar_wait(&sf_landed[stage], phase, s_abort)) {
+            latch_timeout(s_abort, p.status);
+            ok = false;
+            break;
+          }
+          if (n >= C::kSFSlots) {
+            const int prev = n - C::kSFSlots;
+            if (!mbar_wait(&empty[prev % S], (prev / S) & 1, s_abort)) {
+              latch_timeout(s_abort, p.status);
+              ok = false;
+              break;
+            }
+          }
+          tc_fence_after();
+          const uint32_t sl = n % C::kSFSlots;
+          {
+            const uint32_t st = smem_base + stage * C::kStageBytes;
+            const uint32_t sfa_t = tmem + sf_col0 + sl * C::kSFSlot;
+            const int atoms = min(C::kAtomsKT, p.sf_atoms_k - kb * C::kAtomsKT);
+            auto cp = [&](uint32_t taddr, uint64_t sdesc) {
+              if constexpr (PAIR)
+                tc_cp_sf_atom_pair(taddr, sdesc);
+              else
+                tc_cp_sf_atom(taddr, sdesc);
+            };
+            if (cw == 0) {
+              for (int a = 0; a < atoms; ++a) cp(sfa_t + a * 4, smem_desc_sf(st + C::kABytes + C::kBBytes + a * 512));
+            }
+            if (C::kLong && C::kNRB == 2) {
+              // row-block 0's atoms, and the second half of row-block 1's, on the second copier
+              const uint32_t sb = st + C::kABytes + C::kBBytes + C::kSFABytes;
+              const int mid = (atoms + 1) / 2;
+              if (cw == 1)
+                for (int a = 0; a < atoms; ++a) cp(sfa_t + C::kSFACols + a * C::kNRB * 4, smem_desc_sf(sb + a * 512));
+              for (int a = cw == 0 ? 0 : mid; a < (cw == 0 ? mid : atoms); ++a)
+                cp(sfa_t + C::kSFACols + (a * C::kNRB + 1) * 4, smem_desc_sf(sb + (C::kAtomsKT + a) * 512));
+            } else if (cw > 0) {
+              const int rb = cw - 1;
+              for (int a = 0; a < atoms; ++a)
+                cp(sfa_t + C::kSFACols + (a * C::kNRB + rb) * 4,
+                   smem_desc_sf(st + C::kABytes + C::kBBytes + C::kSFABytes + (rb * C::kAtomsKT + a) * 512));
+            }
+          }
+          if constexpr (PAIR)
+            tc_commit_pair(&sf_full[sl]);
+          else
+            tc_commit(&sf_full[sl]);
+          ++n;
+          if (++stage == S) {
+            stage = 0;
+            phase ^= 1;
+          }
+        }
+      }
+      // no copy may still write TMEM when it is freed
+      if constexpr (PAIR)
+        tc_commit_pair(cp_drain);
+      else
+        tc_commit(cp_drain);
+      volatile int no_abort = 0;
+      mbar_wait(cp_drain, 0, &no_abort);
+    }
+  } else if (warp >= C::kEpiWarp0 && warp < C::kEpiWarp0 + C::kEpiWarps) {
+    // ------------------------------------------------------------ epilogue
+    // a warp reads the TMEM lane quarter given by its warp index in the CTA, modulo 4,
+    // and (with eight epilogue warps) the column half given by its warp index over 4
+    const int q = (threadIdx.x >> 5) & 3;
+    const int rl = q * 32 + lane;     // accumulator row (TMEM lane) of this thread
+    const int et = lt - 32 * C::kEpiWarp0;  // 0 .. 32 * kEpiWarps - 1
+    constexpr int CH = C::kEpiCols;
+    const int c0 = ((warp - C::kEpiWarp0) >> 2) * CH;  // first accumulator column of this thread
+    // BF16 row-major tiles whose columns are all in range are converted into registers
+    // and TMEM is handed back to the MMA thread before the stores, so that they overlap
+    // the next tile's MMAs
+    const bool early_release = C::kSepCp && p.mode != kModeStreamK && p.out && p.out_bf16 && !p.transposed &&
+                               p.vec_store && !p.q_codes;
+    // hands an accumulator back to the MMA thread (a pair's leader counts both CTAs' warps)
+    auto release_acc = [&](int a) {
+      if constexpr (PAIR)
+        mbar_arrive_cluster(cluster_addr(smem_u32(&acc_empty[a]), 0));
+      else
+        mbar_arrive(&acc_empty[a]);
+    };
+    wait_prior_grids();               // the global scales come from earlier kernels
+    const float ga = p.ga ? *p.ga : 1.0f;
+    uint32_t tmax = 0;                // max |result| over this thread's values (amax_out)
+    Schedule sch(p, s_mt, s_off, vb, vg, kMTile, sub_row, s_pt);
+    Work w;
+    int iter = 0;
+    while (sch.next(w)) {
+      const int acc = iter % ACC;
+      const uint32_t par = (iter / ACC) & 1;
+      // the epilogue warps decide together whether to go on, so that none of them
+      // is left behind at a named barrier
+      if (et == 0 && !mbar_wait(&acc_full[acc], par, s_abort)) {
+        latch_timeout(s_abort, p.status);
+        *s_epi_fail = 1;
+      }
+      epi_sync(sub, 32 * C::kEpiWarps);
+      if (*s_epi_fail) break;
+      tc_fence_after();
+      const float gb = p.gb ? p.gb[w.group] : 1.0f;
+      const float scale = ga * gb;
+      float scale2 = 0.0f;  // the up columns' scale
+      if constexpr (kGated) scale2 = ga * (p.gb2 ? p.gb2[w.group] : 1.0f);
+      const bool row_ok = rl < w.rows_valid;
+      const int row = w.out_row0 + rl;
+      const uint32_t taddr = tmem + (static_cast<uint32_t>(q * 32) << 16) + acc * BN;
+      bool released = false;
+      if constexpr (EPI != kEpiPlain) {
+        if (C::kLong && p.mode != kModeStreamK && p.vec_store && w.n0 + C::kTileCols <= p.Nk) {
+          // whole tiles: the accumulator half goes into registers and TMEM back to the MMA
+          // thread; everything else overlaps the next tile's MMAs
+          constexpr int kOut = kGated ? CH / 2 : CH;   // output columns of this thread
+          const int oc = kGated ? c0 / 2 : c0;
+          uint32_t rr[CH];  // gated: the gate sums, then the up sums
+          if (q * 32 < w.rows_valid) {  // warp-uniform
+#pragma unroll
+            for (int b = 0; b < CH; b += 32)
+              tmem_ld32(taddr + (kGated ? (b < CH / 2 ? oc + b : BN / 2 + oc + b - CH / 2) : c0 + b), rr + b);
+            tmem_ld_wait();
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) release_acc(acc);
+          released = true;
+          if (row_ok) {
+            const int64_t at = static_cast<int64_t>(row) * p.ldo + w.n0 + oc;
+            const float* bias = p.bias ? p.bias + w.group * p.bias_group + w.n0 + oc : nullptr;
+            const float* bias2 = kGated && p.bias2 ? p.bias2 + w.group * p.bias_group + w.n0 + oc : nullptr;
+            with_act(p.act, [&](auto tag) {
+              constexpr int A = decltype(tag)::value;
+#pragma unroll
+              for (int c = 0; c < kOut; c += 16) {
+                float v[16], u[16];
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                  v[j] = __uint_as_float(rr[c + j]) * scale;
+                  if (kGated) u[j] = __uint_as_float(rr[(kGated ? CH / 2 : 0) + c + j]) * scale2;
+                }
+                if (bias) add_vec16(bias + c, v);
+                if (kGated && bias2) add_vec16(bias2 + c, u);
+                if (p.pre) store_vec16(p.pre, p.out_bf16, at + c, v);
+                if (kGated && p.pre2) store_vec16(p.pre2, p.out_bf16, at + c, u);
+#pragma unroll
+                for (int j = 0; j < 16; ++j) v[j] = kGated ? act_value<A>(v[j]) * u[j] : act_value<A>(v[j]);
+                if (!kGated && p.res) {
+                  float r[16];
+                  if (p.vec_res) load_vec16(p.res, p.res_bf16, at + c, r);
+                  else load_vec16_any(p.res, p.res_bf16, at + c, r);
+#pragma unroll
+                  for (int j = 0; j < 16; ++j) v[j] += r[j];
+                }
+                if (p.out) store_vec16(p.out, p.out_bf16, at + c, v);
+                if (p.q_codes) epi_quantize16(p, row, w.n0 + oc + c, v);
+                if (p.amax_out) {
+#pragma unroll
+                  for (int j = 0; j < 16; ++j) tmax = max(tmax, __float_as_uint(v[j]) & 0x7FFFFFFFu);
+                }
+              }
+            });
+          }
+        } else if (p.mode != kModeStreamK) {
+          // ragged or unaligned tiles and small-N tiles: finished as they are read
+          constexpr int kOut = kGated ? CH / 2 : CH;
+          const int oc = kGated ? c0 / 2 : c0;
+          if (q * 32 < w.rows_valid) {  // warp-uniform
+#pragma unroll 1
+            for (int c = oc; c < oc + kOut; c += 16) {
+              uint32_t rg[16], ru[16];
+              tmem_ld16(taddr + c, rg);
+              if constexpr (kGated) tmem_ld16(taddr + BN / 2 + c, ru);
+              tmem_ld_wait();
+              const int col = w.n0 + c;
+              if (!row_ok || col >= p.Nk) continue;
+              float v[16], u[16];
+#pragma unroll
+              for (int j = 0; j < 16; ++j) {
+                v[j] = __uint_as_float(rg[j]) * scale;
+                u[j] = kGated ? __uint_as_float(ru[j]) * scale2 : 0.0f;
+              }
+              epi_finish16<kGated>(p, row, col, w.group, v, u, tmax);
+            }
+          }
+        } else if (q * 32 < w.rows_valid) {
+          // stream-K: partial sums to the workspace
+          constexpr int CW = CH >= 32 ? 32 : CH;
+#pragma unroll 1
+          for (int cw = c0; cw < c0 + CH; cw += CW) {
+            uint32_t rr[CW];
+            if constexpr (CW == 32) tmem_ld32(taddr + cw, rr);
+            else tmem_ld16(taddr + cw, *reinterpret_cast<uint32_t(*)[16]>(rr));
+            tmem_ld_wait();
+            const int half = kGated && cw >= BN / 2 ? 1 : 0;
+            float* dst = p.ws + (static_cast<int64_t>(half) * p.Mk + row) * p.Nk;
+#pragma unroll
+            for (int h = 0; h < CW; h += 16) {
+              const int col = w.n0 + cw + h - half * (BN / 2);
+              if (!row_ok || col >= p.Nk) continue;
+              if ((p.Nk & 3) == 0 && col + 16 <= p.Nk) {
+#pragma unroll
+                for (int j = 0; j < 16; j += 4)
+                  red_add_v4(dst + col + j, __uint_as_float(rr[h + j]), __uint_as_float(rr[h + j + 1]),
+                             __uint_as_float(rr[h + j + 2]), __uint_as_float(rr[h + j + 3]));
+              } else {
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+                  if (col + j < p.Nk) atomicAdd(dst + col + j, __uint_as_float(rr[h + j]));
+              }
+            }
+          }
+        }
+      } else
+      if (q * 32 < w.rows_valid && early_release && w.n0 + BN <= p.Nk) {  // warp-uniform
+        uint32_t pk[CH / 2];  // this thread's columns [c0, c0 + CH) as scaled BF16 pairs
+        // 32-column TMEM loads, one wait per load: the hand-back of the accumulator
+        // waits for few TMEM round trips
+        constexpr int kLdBatch = CH >= 32 ? 32 : CH;
+        static_assert(CH % kLdBatch == 0 && kLdBatch % 16 == 0, "TMEM load batches");
+#pragma unroll
+        for (int cb = 0; cb < CH; cb += kLdBatch) {
+          uint32_t rr[kLdBatch];
+          if constexpr (kLdBatch % 32 == 0) {
+#pragma unroll
+            for (int h = 0; h < kLdBatch; h += 32) tmem_ld32(taddr + c0 + cb + h, rr + h);
+          } else {
+            tmem_ld16(taddr + c0 + cb, *reinterpret_cast<uint32_t(*)[16]>(rr));
+          }
+          tmem_ld_wait();
+#pragma unroll
+          for (int cw = 0; cw < kLdBatch; cw += 16) {
+            float v[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(rr[cw + j]) * scale;
+            if (p.bias || p.act) epi_bias_act(p, row, w.n0 + c0 + cb + cw, v);
+            if (p.amax_out && row_ok) {
+#pragma unroll
+              for (int j = 0; j < 16; ++j) tmax = max(tmax, __float_as_uint(v[j]) & 0x7FFFFFFFu);
+            }
+#pragma unroll
+            for (int j = 0; j < 16; j += 2) pk[(cb + cw + j) / 2] = pack_bf16x2(v[j], v[j + 1]);
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) release_acc(acc);
+        released = true;
+        if (row_ok) {
+          __nv_bfloat16* orow = reinterpret_cast<__nv_bfloat16*>(p.out) + static_cast<int64_t>(row) * p.ldo;
+#pragma unroll
+          for (int c = 0; c < CH; c += 8)  // streaming stores: the output is not read back here
+            __stcs(reinterpret_cast<uint4*>(orow + w.n0 + c0 + c),
+                   make_uint4(pk[c / 2], pk[c / 2 + 1], pk[c / 2 + 2], pk[c / 2 + 3]));
+        }
+      } else if (q * 32 < w.rows_valid) {  // warp-uniform: warps without a valid row skip TMEM
+        // up to 64 columns per TMEM round trip (32 with eight epilogue warps), one wait
+        constexpr int CW = C::kSepCp ? 32 : CH >= 64 ? 64 : CH;
+#pragma unroll 1
+        for (int cw = c0; cw < c0 + CH; cw += CW) {
+          uint32_t rr[CW / 16][16];
+#pragma unroll
+          for (int h = 0; h < CW / 16; ++h) tmem_ld16(taddr + cw + h * 16, rr[h]);
+          tmem_ld_wait();
+#pragma unroll
+        for (int h = 0; h < CW / 16; ++h) {
+          const int c = cw + h * 16;
+          const uint32_t (&r)[16] = rr[h];
+          const int col = w.n0 + c;
+          if (!row_ok || col >= p.Nk) continue;
+          if (p.mode == kModeStreamK) {
+            float* dst = p.ws + static_cast<int64_t>(row) * p.Nk + col;
+            if ((p.Nk & 3) == 0 && col + 16 <= p.Nk) {
+#pragma unroll
+              for (int j = 0; j < 16; j += 4)
+                red_add_v4(dst + j, __uint_as_float(r[j]), __uint_as_float(r[j + 1]), __uint_as_float(r[j + 2]),
+                           __uint_as_float(r[j + 3]));
+            } else {
+              for (int j = 0; j < 16 && col + j < p.Nk; ++j) atomicAdd(dst + j, __uint_as_float(r[j]));
+            }
+          } else {
+            float v[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(r[j]) * scale;
+            epi_row16(p, row, col, v, tmax);
+          }
+        }
+        }
+      }
+      if (!released) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) release_acc(acc);
+      }
+      ++iter;
+      if (p.mode == kModeStreamK) {
+        // The pipeline whose partial sums complete the tile's K range writes the tile:
+        // every pipeline publishes its reductions (fence), then adds the K steps it
+        // covered to the tile's counter; the one that brings it to num_kb reads the
+        // sums back from L2, scales, converts, stores, and clears sums and counter.
+        __threadfence();
+        epi_sync(sub, 32 * C::kEpiWarps);
+        if (et == 0) {
+          __threadfence();
+          const int covered = w.kb1 - w.kb0;
+          const int before = atomicAdd(p.tile_cnt + w.tile, covered);
+          *s_last = before + covered == p.num_kb ? 1 : 0;
+        }
+        epi_sync(sub, 32 * C::kEpiWarps);
+        if (*s_last) {
+          __threadfence();
+          if constexpr (EPI != kEpiPlain) {
+            if (row_ok) {
+              constexpr int kOut = kGated ? CH / 2 : CH;
+              const int oc = kGated ? c0 / 2 : c0;
+#pragma unroll 1
+              for (int c = oc; c < oc + kOut; c += 16) {
+                const int col = w.n0 + c;
+                if (col >= p.Nk) break;
+                float v[16], u[16];
+                take_sums16(p.ws + static_cast<int64_t>(row) * p.Nk, col, p.Nk, scale, v);
+                if constexpr (kGated) {
+                  take_sums16(p.ws + (static_cast<int64_t>(p.Mk) + row) * p.Nk, col, p.Nk, scale2, u);
+                } else {
+#pragma unroll
+                  for (int j = 0; j < 16; ++j) u[j] = 0.0f;
+                }
+                epi_finish16<kGated>(p, row, col, w.group, v, u, tmax);
+              }
+            }
+          } else
+          if (row_ok) {
+            float* src = p.ws + static_cast<int64_t>(row) * p.Nk;
+            for (int c = c0; c < c0 + CH; c += 16) {
+              const int col = w.n0 + c;
+              if (col >= p.Nk) break;
+              float v[16];
+              if ((p.Nk & 3) == 0 && col + 16 <= p.Nk) {
+#pragma unroll
+                for (int j = 0; j < 16; j += 4) {
+                  const float4 t = __ldcg(reinterpret_cast<const float4*>(src + col + j));
+                  __stcg(reinterpret_cast<float4*>(src + col + j), make_float4(0.f, 0.f, 0.f, 0.f));
+                  v[j] = t.x * scale;
+                  v[j + 1] = t.y * scale;
+                  v[j + 2] = t.z * scale;
+                  v[j + 3] = t.w * scale;
+                }
+              } else {
+                for (int j = 0; j < 16; ++j) {
+                  v[j] = 0.0f;
+                  if (col + j < p.Nk) {
+                    v[j] = __ldcg(src + col + j) * scale;
+                    __stcg(src + col + j, 0.0f);
+                  }
+                }
+              }
+              epi_row16(p, row, col, v, tmax);
+            }
+          }
+          if (et == 0) p.tile_cnt[w.tile] = 0;
+        }
+      }
+    }
+    if (p.amax_out) {  // one atomic per warp: non-negative float bits order as integers
+      tmax = __reduce_max_sync(0xFFFFFFFFu, tmax);
+      if (lane == 0 && tmax) atomicMax(p.amax_out, tmax);
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  // a pair: neither CTA frees TMEM or leaves (its shared memory is the peer's operand and
+  // barrier target) before both are done
+  if constexpr (PAIR) cluster_sync_all();
+  tc_fence_after();
+  if (sub == 0 && warp == 1) {
+    __syncwarp();
+    if constexpr (PAIR)
+      tmem_dealloc_pair(s_tmem_base, C::kTmemAlloc);
+    else
+      tmem_dealloc(s_tmem_base, C::kTmemAlloc);
+  }
+}
+
+template <int BN, bool MX, int ACC, bool PAIR, bool F8 = false, int EPI = kEpiPlain>
+static cudaError_t run(const GemmMaps& tm, const GemmArgs& a, int64_t units, cudaStream_t st) {
+  using C = Cfg<BN, MX, ACC, PAIR, F8, EPI>;
+  auto kern = fp4_gemm_kernel<BN, MX, ACC, PAIR, F8, EPI>;
+  // the shared-memory opt-in is per device; set it once per (kernel, device)
+  static bool attr_done[64] = {false};
+  int dev = 0;
+  cudaGetDevice(&dev);
+  cudaError_t e = cudaSuccess;
+  if (dev < 0 || dev >= 64 || !attr_done[dev]) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+    if (e != cudaSuccess) return e;
+    if constexpr (C::kLong) {
+      // the warpgroups' shares of the registers must fit what the launch allocates: a
+      // setmaxnreg.inc beyond it would wait for ever
+      cudaFuncAttributes fa;
+      e = cudaFuncGetAttributes(&fa, kern);
+      if (e != cudaSuccess) return e;
+      if (fa.numRegs != C::kLaunchRegs) return cudaErrorInvalidConfiguration;
+    }
+    if (dev >= 0 && dev < 64) attr_done[dev] = true;
+  }
+  // programmatic dependent launch: the prologue (barriers, TMEM, descriptor prefetch,
+  // and loads of an operand the caller marked as ready) overlaps the previous kernel on
+  // the stream; everything else waits for it
+  cudaLaunchConfig_t cfg = {};
+  cfg.blockDim = dim3(C::kThreads);
+  cfg.dynamicSmemBytes = C::kSmemBytes;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int grid = 0;
+  if constexpr (PAIR) {
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = 2;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.numAttrs = 2;
+    // persistent: as many pairs as can be resident at once (asked once per device)
+    static int max_pairs[64] = {0};
+    int pairs = (dev >= 0 && dev < 64) ? max_pairs[dev] : 0;
+    if (pairs <= 0) {
+      cfg.gridDim = dim3(2 * static_cast<unsigned>(num_sms() / 2));
+      e = cudaOccupancyMaxActiveClusters(&pairs, kern, &cfg);
+      if (e != cudaSuccess) return e;
+      if (pairs <= 0) return cudaErrorInvalidConfiguration;
+      if (dev >= 0 && dev < 64) max_pairs[dev] = pairs;
+    }
+    // (grouped schedules count their tiles on the device: every pair)
+    grid = 2 * static_cast<int>(a.mode == kModeGrouped ? pairs : std::max<int64_t>(1, std::min<int64_t>(units, pairs)));
+  } else {
+    grid = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>((units + C::kP - 1) / C::kP, num_sms())));
+    if (a.mode == kModeGrouped) grid = num_sms();
+  }
+  cfg.gridDim = dim3(grid);
+  return cudaLaunchKernelEx(&cfg, kern, tm.a, tm.b, tm.sfa, tm.sfb, tm.b2, tm.sfb2, a);
+}
+
+}  // namespace fp4

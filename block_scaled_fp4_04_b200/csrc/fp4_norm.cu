@@ -1,0 +1,541 @@
+// fp4_norm.cu -- layer norm over the columns of a row-major [rows, cols] tensor, forward and
+// backward, and the column sums that end a weight gradient.  Memory-bound: every row is read
+// once and kept in registers between the reductions.
+//
+//   forward   mean = sum x / n, var = sum (x - mean)^2 / n (two passes over the registers: no
+//             difference of large squares), rstd = 1 / sqrt(var + eps),
+//             y = (x - mean) rstd w + b
+//   backward  xh = (x - mean) rstd, a = dy w,
+//             dx = rstd (a - mean(a) - xh mean(a xh)) + dres, dw = sum_r dy xh, db = sum_r dy
+//
+// All sums are FP32.  Sums over a row go through a fixed tree, sums over rows through a fixed
+// split of the rows into partial sums that a second kernel adds in order: no atomics, the
+// same bits every time.
+#include "fp4_ops.h"
+#include "fp4_rows.cuh"
+
+namespace fp4 {
+
+struct LnArgs {
+  const void* x;
+  int64_t rows;
+  int n;
+  const float *w, *b;
+  float eps;
+  void* y;
+  int y_bf16;
+  float *mean, *rstd;
+  RowCodes q;
+  unsigned* amax;
+  unsigned* status;
+};
+
+// Sum over the WPR warps of one row; every thread of the row gets it.  Rows of one warp need
+// no shared memory; others meet on the named barrier `bar`.
+template <int WPR>
+__device__ __forceinline__ float row_sum(float v, float* s, int wr, int lane, int bar) {
+  v = warp_sum(v);
+  if constexpr (WPR > 1) {
+    if (lane == 0) s[wr] = v;
+    asm volatile("bar.sync %0, %1;" ::"r"(bar), "r"(WPR * 32) : "memory");
+    v = 0.0f;
+#pragma unroll
+    for (int i = 0; i < WPR; ++i) v += s[i];
+  }
+  return v;
+}
+
+// WPR warps per row, C chunks of V elements per thread held in registers; C = 0: rows of any
+// length, read again for every pass.
+template <typename T, int V, int WPR, int C, int FMT>
+__global__ void __launch_bounds__((WPR < 4 ? 4 : WPR) * 32) ln_forward_kernel(const LnArgs p) {
+  constexpr int kWarps = WPR < 4 ? 4 : WPR;
+  constexpr int kRows = kWarps / WPR;  // rows per CTA
+  constexpr int kCh = C > 0 ? C : 1;
+  __shared__ float s_red[2][kRows][WPR];
+  rows_allow_dependents();
+  rows_wait_prior();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int group = warp / WPR, wr = warp % WPR, bar = 1 + group;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + group;
+  const bool row_ok = row < p.rows;
+  const T* x = static_cast<const T*>(p.x) + (row_ok ? row : 0) * p.n;
+  const int first = (wr * 32 + lane) * V;      // this thread's first element
+  constexpr int kStep = WPR * 32 * V;
+  const int loops = C > 0 ? C : (p.n + kStep - 1) / kStep;
+
+  RowVec<T, V> raw[kCh];
+  auto load = [&](int j, RowVec<T, V>& r) {
+    const int col = first + j * kStep;
+    if (row_ok && col < p.n) r.load(x + col);
+    else r.zero();
+  };
+  if constexpr (C > 0) {
+#pragma unroll
+    for (int j = 0; j < C; ++j) load(j, raw[j]);
+  }
+  // f(chunk, values, whether they exist)
+  auto each = [&](auto&& f) {
+    if constexpr (C > 0) {
+#pragma unroll
+      for (int j = 0; j < C; ++j) {
+        float v[V];
+        raw[j].unpack(v);
+        f(first + j * kStep, v, row_ok && first + j * kStep < p.n);
+      }
+    } else {
+      for (int j = 0; j < loops; ++j) {
+        float v[V];
+        load(j, raw[0]);
+        raw[0].unpack(v);
+        f(first + j * kStep, v, row_ok && first + j * kStep < p.n);
+      }
+    }
+  };
+  const float inv_n = 1.0f / static_cast<float>(p.n);
+  float s = 0.0f;
+  each([&](int, const float (&v)[V], bool) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) s += v[i];  // missing elements are zero
+  });
+  const float mean = row_sum<WPR>(s, s_red[0][group], wr, lane, bar) * inv_n;
+  float ss = 0.0f;
+  each([&](int, const float (&v)[V], bool ok) {
+    if (ok) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const float d = v[i] - mean;
+        ss += d * d;
+      }
+    }
+  });
+  const float var = row_sum<WPR>(ss, s_red[1][group], wr, lane, bar) * inv_n;
+  const float rstd = 1.0f / sqrtf(var + p.eps);
+  if (row_ok && wr == 0 && lane == 0) {
+    if (p.mean) p.mean[row] = mean;
+    if (p.rstd) p.rstd[row] = rstd;
+  }
+  float g = 1.0f;
+  if constexpr (FMT == kCodesNv) g = *p.q.g;
+  uint32_t m = 0;
+  bool bad = false;
+  each([&](int col, const float (&v)[V], bool ok) {
+    float o[V];
+    if (ok) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) o[i] = (v[i] - mean) * rstd;
+      if (p.w) {
+        float w[V];
+        load_params<V>(p.w + col, w);
+#pragma unroll
+        for (int i = 0; i < V; ++i) o[i] *= w[i];
+      }
+      if (p.b) {
+        float b[V];
+        load_params<V>(p.b + col, b);
+#pragma unroll
+        for (int i = 0; i < V; ++i) o[i] += b[i];
+      }
+      if (p.y) store_row_vec<V>(p.y, p.y_bf16, row * p.n + col, o);
+      if (p.amax) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) m = max(m, abs_bits_of(o[i]));
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) o[i] = 0.0f;
+    }
+    if constexpr (FMT != kCodesNone) bad |= encode_row_vec<FMT, V>(p.q, g, row, col, ok, o);
+  });
+  if (p.amax) {
+    m = __reduce_max_sync(0xFFFFFFFFu, m);
+    if (lane == 0 && m) atomicMax(p.amax, m);
+  }
+  if (FMT != kCodesNone && bad) atomicOr(p.status, kStatusNonFinite);
+}
+
+template <typename T, int V, int WPR, int C, int FMT>
+static cudaError_t run_ln(const LnArgs& a, cudaStream_t st) {
+  constexpr int kWarps = WPR < 4 ? 4 : WPR, kRows = kWarps / WPR;
+  return launch_rows(ln_forward_kernel<T, V, WPR, C, FMT>, dim3(static_cast<unsigned>((a.rows + kRows - 1) / kRows)),
+                     kWarps * 32, 0, st, a);
+}
+
+// Warps per row by the row's length, so that a thread holds at most four chunks.
+template <typename T, int V, int FMT>
+static cudaError_t pick_ln(const LnArgs& a, cudaStream_t st) {
+  const int nch = (a.n + V - 1) / V;
+  if (nch <= 32) return run_ln<T, V, 1, 1, FMT>(a, st);
+  if (nch <= 64) return run_ln<T, V, 1, 2, FMT>(a, st);
+  if (nch <= 128) return run_ln<T, V, 1, 4, FMT>(a, st);
+  if (nch <= 512) return run_ln<T, V, 4, 4, FMT>(a, st);
+  if (nch <= 1024) return run_ln<T, V, 8, 4, FMT>(a, st);
+  if (nch <= 2048) return run_ln<T, V, 16, 4, FMT>(a, st);
+  return run_ln<T, V, 16, 0, FMT>(a, st);
+}
+
+static bool aligned16_rows(const void* p) { return !p || (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
+template <typename T>
+static cudaError_t pick_ln_vec(const LayerNormProblem& p, const LnArgs& a, cudaStream_t st) {
+  constexpr int V = 16 / sizeof(T);
+  // whole 16-byte words of x and of the parameters; y rows are then aligned too
+  const bool vec = a.n % V == 0 && aligned16_rows(a.x) && aligned16_rows(a.y) && aligned16_rows(a.w) && aligned16_rows(a.b);
+  if (p.q.fmt == kCodesNv) return vec ? pick_ln<T, V, kCodesNv>(a, st) : cudaErrorInvalidValue;
+  if (p.q.fmt == kCodesMx) return vec ? pick_ln<T, V, kCodesMx>(a, st) : cudaErrorInvalidValue;
+  return vec ? pick_ln<T, V, kCodesNone>(a, st) : pick_ln<T, 1, kCodesNone>(a, st);
+}
+
+cudaError_t launch_layernorm(const LayerNormProblem& p, unsigned* status, cudaStream_t st) {
+  LnArgs a{};
+  a.x = p.x;
+  a.rows = p.rows;
+  a.n = static_cast<int>(p.cols);
+  a.w = p.weight;
+  a.b = p.bias;
+  a.eps = p.eps;
+  a.y = p.y;
+  a.y_bf16 = p.y_bf16;
+  a.mean = p.mean;
+  a.rstd = p.rstd;
+  a.q = RowCodes{p.q.codes, p.q.scales, p.q.g, p.cols, (p.cols / (p.q.fmt == kCodesMx ? 32 : 16) + 3) / 4};
+  a.amax = reinterpret_cast<unsigned*>(p.amax_out);
+  a.status = status;
+  return p.bf16 ? pick_ln_vec<__nv_bfloat16>(p, a, st) : pick_ln_vec<float>(p, a, st);
+}
+
+// ------------------------------------------------------------------ backward
+struct LnGradArgs {
+  const void *dy, *x, *dres;
+  int64_t rows;
+  int n;
+  const float *w, *mean, *rstd;
+  void* dx;
+  int dx_bf16;
+  float* part;  // [grid][2][n] partial sums of dy xh and dy, or null
+};
+
+// A CTA takes rows blockIdx.x * kRows + group, + gridDim.x * kRows, ... and keeps the sums of
+// its columns in registers over all of them.
+template <typename T, int V, int WPR, int C>
+__global__ void __launch_bounds__((WPR < 8 ? 8 : WPR) * 32) ln_backward_kernel(const LnGradArgs p) {
+  constexpr int kWarps = WPR < 8 ? 8 : WPR;
+  constexpr int kRows = kWarps / WPR;
+  constexpr int kStep = WPR * 32 * V;
+  __shared__ float s_red[2][2][kRows][WPR];
+  rows_allow_dependents();
+  rows_wait_prior();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int group = warp / WPR, wr = warp % WPR, bar = 1 + group;
+  const int first = (wr * 32 + lane) * V;
+  const float inv_n = 1.0f / static_cast<float>(p.n);
+  float dw[C][V], db[C][V];
+#pragma unroll
+  for (int j = 0; j < C; ++j)
+#pragma unroll
+    for (int i = 0; i < V; ++i) dw[j][i] = db[j][i] = 0.0f;
+  int par = 0;
+  for (int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + group; row < p.rows;
+       row += static_cast<int64_t>(gridDim.x) * kRows, par ^= 1) {
+    const int64_t base = row * p.n;
+    RowVec<T, V> rx[C], rd[C];
+#pragma unroll
+    for (int j = 0; j < C; ++j) {
+      const int col = first + j * kStep;
+      if (col < p.n) {
+        rx[j].load(static_cast<const T*>(p.x) + base + col);
+        rd[j].load(static_cast<const T*>(p.dy) + base + col);
+      } else {
+        rx[j].zero();
+        rd[j].zero();
+      }
+    }
+    const float mean = __ldg(p.mean + row), rstd = __ldg(p.rstd + row);
+    float s1 = 0.0f, s2 = 0.0f;
+#pragma unroll
+    for (int j = 0; j < C; ++j) {
+      const int col = first + j * kStep;
+      if (col < p.n) {
+        float x[V], d[V], w[V];
+        rx[j].unpack(x);
+        rd[j].unpack(d);
+        if (p.w) load_params<V>(p.w + col, w);
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          const float xh = (x[i] - mean) * rstd;
+          dw[j][i] += d[i] * xh;
+          db[j][i] += d[i];
+          const float a = p.w ? d[i] * w[i] : d[i];
+          s1 += a;
+          s2 += a * xh;
+        }
+      }
+    }
+    s1 = warp_sum(s1);
+    s2 = warp_sum(s2);
+    if constexpr (WPR > 1) {
+      // two buffers in turn: a warp may be one row ahead of the others, not two
+      float* r1 = s_red[par][0][group];
+      float* r2 = s_red[par][1][group];
+      if (lane == 0) {
+        r1[wr] = s1;
+        r2[wr] = s2;
+      }
+      asm volatile("bar.sync %0, %1;" ::"r"(bar), "r"(WPR * 32) : "memory");
+      s1 = s2 = 0.0f;
+#pragma unroll
+      for (int i = 0; i < WPR; ++i) {
+        s1 += r1[i];
+        s2 += r2[i];
+      }
+    }
+    const float c1 = s1 * inv_n, c2 = s2 * inv_n;
+#pragma unroll
+    for (int j = 0; j < C; ++j) {
+      const int col = first + j * kStep;
+      if (col < p.n) {
+        float x[V], d[V], w[V], o[V];
+        rx[j].unpack(x);
+        rd[j].unpack(d);
+        if (p.w) load_params<V>(p.w + col, w);
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          const float xh = (x[i] - mean) * rstd;
+          const float a = p.w ? d[i] * w[i] : d[i];
+          o[i] = rstd * (a - c1 - xh * c2);
+        }
+        if (p.dres) {
+          RowVec<T, V> rr;
+          float r[V];
+          rr.load(static_cast<const T*>(p.dres) + base + col);
+          rr.unpack(r);
+#pragma unroll
+          for (int i = 0; i < V; ++i) o[i] += r[i];
+        }
+        store_row_vec<V>(p.dx, p.dx_bf16, base + col, o);
+      }
+    }
+  }
+  if (!p.part) return;
+  // the CTA's groups of rows add up in shared memory, in the order of the groups
+  float* out = p.part + static_cast<int64_t>(blockIdx.x) * 2 * p.n;
+  if constexpr (kRows > 1) {
+    extern __shared__ float s_part[];  // [2][n]
+    for (int gi = 0; gi < kRows; ++gi) {
+      if (group == gi) {
+#pragma unroll
+        for (int j = 0; j < C; ++j)
+#pragma unroll
+          for (int i = 0; i < V; ++i) {
+            const int col = first + j * kStep + i;
+            if (col < p.n) {
+              s_part[col] = gi ? s_part[col] + dw[j][i] : dw[j][i];
+              s_part[p.n + col] = gi ? s_part[p.n + col] + db[j][i] : db[j][i];
+            }
+          }
+      }
+      __syncthreads();
+    }
+    for (int c = threadIdx.x; c < 2 * p.n; c += kWarps * 32) out[c] = s_part[c];
+  } else {
+#pragma unroll
+    for (int j = 0; j < C; ++j) {
+      const int col = first + j * kStep;
+      if (col < p.n) {
+        if constexpr (V == 1) {
+          out[col] = dw[j][0];
+          out[p.n + col] = db[j][0];
+        } else {
+#pragma unroll
+          for (int i = 0; i < V; i += 4) {
+            *reinterpret_cast<float4*>(out + col + i) = make_float4(dw[j][i], dw[j][i + 1], dw[j][i + 2], dw[j][i + 3]);
+            *reinterpret_cast<float4*>(out + p.n + col + i) =
+                make_float4(db[j][i], db[j][i + 1], db[j][i + 2], db[j][i + 3]);
+          }
+        }
+      }
+    }
+  }
+}
+
+// Rows longer than a CTA's registers: the column sums by a kernel of their own, and dx by a
+// CTA per row that reads the row twice.
+template <typename T>
+__global__ void __launch_bounds__(512) ln_backward_long_kernel(const LnGradArgs p) {
+  __shared__ float s_red[2][16];
+  rows_allow_dependents();
+  rows_wait_prior();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const float inv_n = 1.0f / static_cast<float>(p.n);
+  const int64_t base = static_cast<int64_t>(blockIdx.x) * p.n;
+  const float mean = __ldg(p.mean + blockIdx.x), rstd = __ldg(p.rstd + blockIdx.x);
+  auto value = [&](const void* t, int col) {
+    RowVec<T, 1> r;
+    float v[1];
+    r.load(static_cast<const T*>(t) + base + col);
+    r.unpack(v);
+    return v[0];
+  };
+  float s1 = 0.0f, s2 = 0.0f;
+  for (int col = threadIdx.x; col < p.n; col += 512) {
+    const float a = value(p.dy, col) * (p.w ? __ldg(p.w + col) : 1.0f);
+    s1 += a;
+    s2 += a * ((value(p.x, col) - mean) * rstd);
+  }
+  s1 = warp_sum(s1);
+  s2 = warp_sum(s2);
+  if (lane == 0) {
+    s_red[0][warp] = s1;
+    s_red[1][warp] = s2;
+  }
+  __syncthreads();
+  s1 = s2 = 0.0f;
+  for (int i = 0; i < 16; ++i) {
+    s1 += s_red[0][i];
+    s2 += s_red[1][i];
+  }
+  const float c1 = s1 * inv_n, c2 = s2 * inv_n;
+  for (int col = threadIdx.x; col < p.n; col += 512) {
+    const float a = value(p.dy, col) * (p.w ? __ldg(p.w + col) : 1.0f);
+    const float xh = (value(p.x, col) - mean) * rstd;
+    float o[1] = {rstd * (a - c1 - xh * c2)};
+    if (p.dres) o[0] += value(p.dres, col);
+    store_row_vec<1>(p.dx, p.dx_bf16, base + col, o);
+  }
+}
+
+constexpr int kLongCols = 128;  // columns per CTA of the column pass
+
+template <typename T>
+__global__ void __launch_bounds__(kLongCols) ln_columns_long_kernel(const LnGradArgs p, int64_t rows_per_part) {
+  rows_allow_dependents();
+  rows_wait_prior();
+  const int col = blockIdx.x * kLongCols + threadIdx.x;
+  if (col >= p.n) return;
+  const int64_t r0 = static_cast<int64_t>(blockIdx.y) * rows_per_part;
+  const int64_t r1 = min(p.rows, r0 + rows_per_part);
+  float dw = 0.0f, db = 0.0f;
+  for (int64_t r = r0; r < r1; ++r) {
+    RowVec<T, 1> rx, rd;
+    float x[1], d[1];
+    rx.load(static_cast<const T*>(p.x) + r * p.n + col);
+    rd.load(static_cast<const T*>(p.dy) + r * p.n + col);
+    rx.unpack(x);
+    rd.unpack(d);
+    dw += d[0] * ((x[0] - __ldg(p.mean + r)) * __ldg(p.rstd + r));
+    db += d[0];
+  }
+  float* out = p.part + static_cast<int64_t>(blockIdx.y) * 2 * p.n;
+  out[col] = dw;
+  out[p.n + col] = db;
+}
+
+// ------------------------------------------------------------------ column sums
+// 32 columns per CTA; its eight warps each add an eighth of the partial sums, in order, and
+// the eighths are added in order.
+__global__ void __launch_bounds__(256) column_sums_kernel(const float* __restrict__ part, int parts, int64_t width,
+                                                          int64_t n0, float* out0, float* out1) {
+  __shared__ float s[8][32];
+  rows_allow_dependents();
+  rows_wait_prior();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + lane;
+  float v = 0.0f;
+  if (c < width) {
+    const int p0 = parts * warp / 8, p1 = parts * (warp + 1) / 8;
+#pragma unroll 4
+    for (int q = p0; q < p1; ++q) v += part[static_cast<int64_t>(q) * width + c];
+  }
+  s[warp][lane] = v;
+  __syncthreads();
+  if (warp == 0 && c < width) {
+    v = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v += s[i][lane];
+    if (c < n0) {
+      if (out0) out0[c] = v;
+    } else if (out1) {
+      out1[c - n0] = v;
+    }
+  }
+}
+
+cudaError_t launch_column_sums(const float* part, int parts, int64_t width, int64_t n0, float* out0, float* out1,
+                               cudaStream_t st) {
+  return launch_rows(column_sums_kernel, dim3(static_cast<unsigned>((width + 31) / 32)), 256, 0, st, part, parts, width,
+                     n0, out0, out1);
+}
+
+constexpr int kLnMaxParts = 2 * 148;
+
+// CTAs of the backward kernel (and partial sums): two per SM, no more than groups of rows.
+static int ln_parts(int64_t rows) {
+  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(rows, std::min(2 * num_sms(), kLnMaxParts))));
+}
+
+size_t layernorm_grad_workspace_bytes(int64_t rows, int64_t cols) {
+  return static_cast<size_t>(std::min<int64_t>(rows, kLnMaxParts)) * 2 * cols * sizeof(float);
+}
+
+template <typename T, int V, int WPR, int C>
+static cudaError_t run_ln_grad(const LnGradArgs& a, int parts, cudaStream_t st) {
+  constexpr int kWarps = WPR < 8 ? 8 : WPR, kRows = kWarps / WPR;
+  const size_t smem = kRows > 1 && a.part ? 2 * static_cast<size_t>(a.n) * sizeof(float) : 0;
+  return launch_rows(ln_backward_kernel<T, V, WPR, C>, dim3(static_cast<unsigned>(parts)), kWarps * 32, smem, st, a);
+}
+
+// Returns false where the row is too long for the registers of a CTA.
+template <typename T, int V>
+static bool pick_ln_grad(const LnGradArgs& a, int parts, cudaStream_t st, cudaError_t* e) {
+  const int nch = (a.n + V - 1) / V;
+  constexpr int C = V == 8 ? 2 : 4;  // at most 16 columns per thread
+  if (nch <= 32) *e = run_ln_grad<T, V, 1, 1>(a, parts, st);
+  else if (nch <= 32 * C) *e = run_ln_grad<T, V, 1, C>(a, parts, st);
+  else if (nch <= 128 * C) *e = run_ln_grad<T, V, 4, C>(a, parts, st);
+  else if (nch <= 256 * C) *e = run_ln_grad<T, V, 8, C>(a, parts, st);
+  else if (nch <= 512 * C) *e = run_ln_grad<T, V, 16, C>(a, parts, st);
+  else return false;
+  return true;
+}
+
+template <typename T>
+static cudaError_t ln_grad(const LnGradArgs& a, float* dw, float* db, cudaStream_t st) {
+  constexpr int V = 16 / sizeof(T);
+  const bool vec = a.n % V == 0 && aligned16_rows(a.x) && aligned16_rows(a.dy) && aligned16_rows(a.dres) &&
+                   aligned16_rows(a.dx) && aligned16_rows(a.w);
+  int parts = ln_parts(a.rows);
+  cudaError_t e = cudaSuccess;
+  if (!(vec ? pick_ln_grad<T, V>(a, parts, st, &e) : pick_ln_grad<T, 1>(a, parts, st, &e))) {
+    // the column pass first: dx may be written in dy's place
+    if (a.part) {
+      const int tiles = (a.n + kLongCols - 1) / kLongCols;
+      parts = static_cast<int>(std::min<int64_t>(parts, std::max(1, 4 * num_sms() / tiles)));
+      const int64_t per = (a.rows + parts - 1) / parts;
+      parts = static_cast<int>((a.rows + per - 1) / per);
+      e = launch_rows(ln_columns_long_kernel<T>, dim3(static_cast<unsigned>(tiles), static_cast<unsigned>(parts)),
+                      kLongCols, 0, st, a, per);
+    }
+    if (e == cudaSuccess)
+      e = launch_rows(ln_backward_long_kernel<T>, dim3(static_cast<unsigned>(a.rows)), 512, 0, st, a);
+  }
+  if (e != cudaSuccess || !a.part) return e;
+  return launch_column_sums(a.part, parts, 2 * static_cast<int64_t>(a.n), a.n, dw, db, st);
+}
+
+cudaError_t launch_layernorm_grad(const LayerNormGradProblem& p, cudaStream_t st) {
+  LnGradArgs a{};
+  a.dy = p.dy;
+  a.x = p.x;
+  a.dres = p.dres;
+  a.rows = p.rows;
+  a.n = static_cast<int>(p.cols);
+  a.w = p.weight;
+  a.mean = p.mean;
+  a.rstd = p.rstd;
+  a.dx = p.dx;
+  a.dx_bf16 = p.dx_bf16;
+  a.part = p.dweight || p.dbias ? p.ws : nullptr;
+  return p.bf16 ? ln_grad<__nv_bfloat16>(a, p.dweight, p.dbias, st) : ln_grad<float>(a, p.dweight, p.dbias, st);
+}
+
+}  // namespace fp4

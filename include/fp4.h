@@ -250,7 +250,17 @@ fp4_status fp4_gemm_mixed(fp4_fmt a_fmt, const uint8_t* A_dev, const uint8_t* sA
                           const uint8_t* B_dev, const uint8_t* sB_dev, int64_t M, int64_t N, int64_t K,
                           void* D_dev, fp4_dtype out_dtype, void* stream);
 
-typedef enum { FP4_ACT_NONE = 0, FP4_ACT_RELU = 1 } fp4_act;
+/* Activations, computed in FP32: RELU max(x, 0); SILU x s(x) with s(x) = 1 / (1 + e^-x); GELU
+ * x Phi(x) (the normal distribution function, by erf); GELU_TANH x s(2 c (x + 0.044715 x^3)),
+ * c = sqrt(2 / pi) (the tanh form: (1 + tanh y) / 2 = s(2y)).  fp4_gemm_epilogue takes NONE
+ * and RELU, the entry points below it all of them. */
+typedef enum {
+  FP4_ACT_NONE = 0,
+  FP4_ACT_RELU = 1,
+  FP4_ACT_SILU = 2,
+  FP4_ACT_GELU = 3,
+  FP4_ACT_GELU_TANH = 4
+} fp4_act;
 size_t fp4_gemm_epilogue_workspace_size(int64_t M, int64_t N, int64_t K, fp4_fmt fmt, int rows_in_place);
 fp4_status fp4_gemm_epilogue(fp4_fmt fmt, const uint8_t* A_dev, const uint8_t* sA_dev, const float* gA_dev,
                              const uint8_t* B_dev, const uint8_t* sB_dev, const float* gB_dev,
@@ -258,6 +268,132 @@ fp4_status fp4_gemm_epilogue(fp4_fmt fmt, const uint8_t* A_dev, const uint8_t* s
                              void* D_dev, fp4_dtype out_dtype, uint8_t* Dcodes_dev, uint8_t* Dscales_dev,
                              const float* gD_dev, float* amax_out_dev, void* workspace_dev,
                              size_t workspace_bytes, void* stream);
+
+/* fp4_gemm_epilogue with any activation, a residual, and a copy of the pre-activation:
+ *   z[m, n] = gA gB sum_k ... + bias[n],   t[m, n] = act(z[m, n]) + residual[m, n]   (FP32)
+ *   residual_dev  [M, N] row-major in residual_dtype (its own type), or NULL.  It may be D
+ *           itself (same type): every element is read before it is written.
+ *   pre_dev [M, N] in out_dtype: z, which fp4_act_backward needs, or NULL.
+ * t is what D, the NVFP4 copy and amax_out get.  flags: FP4_GEMM_WEIGHTS_READY as for
+ * fp4_gemm_ex (the residual is read after the preceding kernel has finished).  Other
+ * arguments, workspace and errors as fp4_gemm_epilogue. */
+fp4_status fp4_gemm_epilogue_ex(fp4_fmt fmt, const uint8_t* A_dev, const uint8_t* sA_dev, const float* gA_dev,
+                                const uint8_t* B_dev, const uint8_t* sB_dev, const float* gB_dev,
+                                int64_t M, int64_t N, int64_t K, const float* bias_dev, fp4_act act,
+                                const void* residual_dev, fp4_dtype residual_dtype, void* D_dev,
+                                fp4_dtype out_dtype, void* pre_dev, uint8_t* Dcodes_dev,
+                                uint8_t* Dscales_dev, const float* gD_dev, float* amax_out_dev,
+                                void* workspace_dev, size_t workspace_bytes, unsigned flags, void* stream);
+
+/* Gated product of a feed-forward block, both projections in one launch:
+ *   G = gA gWg (A . Wg^T) + bias_g,  U = gA gWu (A . Wu^T) + bias_u,  H = act(G) U   (FP32)
+ *   A_dev [M, K/2] codes with scales and global scale as for fp4_gemm; Wg_dev and Wu_dev
+ *           [F, K/2] with scales fp4_scales_bytes(F, K, fmt) and global scales of their own.
+ *           (Weights stacked as one [2F, K] tensor: pass the two halves; their scales can be
+ *           halved where F % 128 == 0.)
+ *   bias_g_dev, bias_u_dev  [F] FP32 or NULL each.
+ *   H_dev   [M, F] in out_dtype, or NULL where the NVFP4 copy is wanted alone.
+ *   G_dev, U_dev  [M, F] in out_dtype: the pre-activations that fp4_act_backward needs; both
+ *           or neither.  H is computed from the unrounded sums.
+ *   Hcodes_dev / Hscales_dev / gH_dev, amax_out_dev: the NVFP4 copy of H and its maximum, as
+ *           Dcodes / Dscales / gD and amax_out of fp4_gemm_epilogue (F % 32 == 0).
+ * Any F >= 1 otherwise; K % 32 == 0; operands, H, G and U 16-byte aligned.
+ * workspace: fp4_gemm_gated_workspace_size(M, F, K, fmt, rows_in_place) bytes, rows_in_place =
+ * (Hcodes_dev != NULL || amax_out_dev != NULL); zero-filled before first use, left so.  With
+ * a workspace in use (few rows), partial sums meet by FP32 atomic additions, whose order --
+ * and so the last bits of H -- can differ from call to call, as in fp4_gemm.
+ * flags: FP4_GEMM_WEIGHTS_READY (both weights).  M <= 32 with NVFP4 operands runs the decode
+ * kernel over both weights. */
+size_t fp4_gemm_gated_workspace_size(int64_t M, int64_t F, int64_t K, fp4_fmt fmt, int rows_in_place);
+fp4_status fp4_gemm_gated(fp4_fmt fmt, const uint8_t* A_dev, const uint8_t* sA_dev, const float* gA_dev,
+                          const uint8_t* Wg_dev, const uint8_t* sWg_dev, const float* gWg_dev,
+                          const uint8_t* Wu_dev, const uint8_t* sWu_dev, const float* gWu_dev,
+                          int64_t M, int64_t F, int64_t K, const float* bias_g_dev, const float* bias_u_dev,
+                          fp4_act act, void* H_dev, fp4_dtype out_dtype, void* G_dev, void* U_dev,
+                          uint8_t* Hcodes_dev, uint8_t* Hscales_dev, const float* gH_dev, float* amax_out_dev,
+                          void* workspace_dev, size_t workspace_bytes, unsigned flags, void* stream);
+
+/* The same from BF16 activations X [M, K], quantized to NVFP4 as fp4_quantize does (tensor
+ * amax, 16-blocks), with NVFP4 weights: M <= 32 in one cooperative launch, larger M as
+ * fp4_quantize then fp4_gemm_gated.  The activations' codes, scales and global scale are
+ * written to Xcodes_dev / Xscales_dev / gX_dev, as by fp4_gemm_bf16a; workspace likewise:
+ * fp4_gemm_gated_bf16a_workspace_size bytes, zero-filled before its first use, not to be
+ * modified between calls nor shared by calls that overlap. */
+size_t fp4_gemm_gated_bf16a_workspace_size(int64_t M, int64_t F, int64_t K);
+fp4_status fp4_gemm_gated_bf16a(const void* X_dev, const uint8_t* Wg_dev, const uint8_t* sWg_dev,
+                                const float* gWg_dev, const uint8_t* Wu_dev, const uint8_t* sWu_dev,
+                                const float* gWu_dev, int64_t M, int64_t F, int64_t K, const float* bias_g_dev,
+                                const float* bias_u_dev, fp4_act act, void* H_dev, fp4_dtype out_dtype,
+                                void* G_dev, void* U_dev, uint8_t* Xcodes_dev, uint8_t* Xscales_dev,
+                                float* gX_dev, void* workspace_dev, size_t workspace_bytes, unsigned flags,
+                                void* stream);
+
+/* The gated product by experts (rows and offsets as for fp4_gemm_grouped): rows
+ * [offsets[e], offsets[e+1]) of A with expert e's weights Wg_dev + e*F*K/2, Wu_dev + e*F*K/2.
+ *   sWg_dev, sWu_dev  num_groups consecutive fp4_scales_bytes(F, K, fmt) blocks;
+ *   gWg_dev, gWu_dev  [num_groups] floats or NULL; bias_g_dev, bias_u_dev [num_groups, F] or
+ *   NULL.  Any F >= 1; num_groups <= 1024; experts without rows are skipped; no workspace. */
+fp4_status fp4_gemm_gated_grouped(fp4_fmt fmt, int num_groups, const int32_t* offsets_dev,
+                                  const uint8_t* A_dev, const uint8_t* sA_dev, const float* gA_dev,
+                                  const uint8_t* Wg_dev, const uint8_t* sWg_dev, const float* gWg_dev,
+                                  const uint8_t* Wu_dev, const uint8_t* sWu_dev, const float* gWu_dev,
+                                  int64_t total_rows, int64_t F, int64_t K, const float* bias_g_dev,
+                                  const float* bias_u_dev, fp4_act act, void* H_dev, fp4_dtype out_dtype,
+                                  void* G_dev, void* U_dev, void* stream);
+
+/* Backward pass of the activation between two products, from the gradient dH [rows, cols] of
+ * its result and the saved pre-activations (all three in in_dtype):
+ *   U_dev != NULL (gated, H = act(G) U):  dZ [rows, 2 cols] = [dH U act'(G) | dH act(G)],
+ *       one matrix: the operand of dX = dZ . [Wg; Wu] (one fp4_gemm with K = 2 cols);
+ *   U_dev == NULL (H = act(G)):           dZ [rows, cols] = dH act'(G).
+ * RELU's slope is 0 at 0.  Outputs, each optional but one of the first two:
+ *   dZ_dev in out_dtype; codes_dev / scales_dev: dZ in `fmt` blocks along its columns (NVFP4
+ *       with the caller's global scale global_dev, or MXFP4), exactly as fp4_quantize would
+ *       quantize the FP32 values (cols % 32 == 0; a non-finite value latches
+ *       FP4_ERR_NONFINITE);
+ *   dbias_dev [cols or 2 cols] FP32: dZ's column sums (from the unrounded values, in a fixed
+ *       order: the same bits every time);
+ *   amax_out_dev 1 float: max |dZ| (zeroed, then written by this call).
+ * workspace: fp4_act_backward_workspace_size(rows, cols, gated) bytes, needed for dbias only,
+ * any contents.  Matrices 16-byte aligned. */
+size_t fp4_act_backward_workspace_size(int64_t rows, int64_t cols, int gated);
+fp4_status fp4_act_backward(const void* dH_dev, const void* G_dev, const void* U_dev, int64_t rows, int64_t cols,
+                            fp4_dtype in_dtype, fp4_act act, void* dZ_dev, fp4_dtype out_dtype, float* dbias_dev,
+                            fp4_fmt fmt, uint8_t* codes_dev, uint8_t* scales_dev, const float* global_dev,
+                            float* amax_out_dev, void* workspace_dev, size_t workspace_bytes, void* stream);
+
+/* Layer norm of the rows of x [rows, cols] (in_dtype), all sums in FP32:
+ *   y = (x - mean) rstd weight + bias,  mean = sum x / cols,
+ *   rstd = 1 / sqrt(sum (x - mean)^2 / cols + eps)
+ *   weight_dev, bias_dev  [cols] FP32, or NULL (1 and 0).
+ *   y_dev   [rows, cols] in out_dtype, or NULL; codes_dev / scales_dev: or y as the A operand
+ *           of the next product (or both): `fmt` blocks along the columns, NVFP4 with the
+ *           caller's global scale global_dev or MXFP4, exactly as fp4_quantize would quantize
+ *           the FP32 y (cols % 32 == 0; a non-finite value latches FP4_ERR_NONFINITE).
+ *   mean_dev, rstd_dev  [rows] FP32, which the backward pass needs, or NULL.
+ *   amax_out_dev  1 float or NULL: max |y| (zeroed, then written by this call).
+ * eps >= 0.  x, y, codes and scales 16-byte aligned; any cols >= 1. */
+fp4_status fp4_layernorm(const void* x_dev, int64_t rows, int64_t cols, fp4_dtype in_dtype, const float* weight_dev,
+                         const float* bias_dev, float eps, void* y_dev, fp4_dtype out_dtype, float* mean_dev,
+                         float* rstd_dev, fp4_fmt fmt, uint8_t* codes_dev, uint8_t* scales_dev,
+                         const float* global_dev, float* amax_out_dev, void* stream);
+
+/* Its backward pass, from dy and x [rows, cols] (both in_dtype) and the saved mean and rstd:
+ *   xh = (x - mean) rstd,  a = dy weight,
+ *   dx = rstd (a - sum a / cols - xh (sum a xh / cols)) + dres
+ *   dweight = sum over rows of dy xh,  dbias = sum over rows of dy
+ *   dres_dev  [rows, cols] in in_dtype or NULL: the gradient that reaches x past the norm (a
+ *           residual branch).  dx_dev [rows, cols] in out_dtype; it may be dy or dres itself
+ *           where the types agree.
+ *   dweight_dev, dbias_dev  [cols] FP32 or NULL each; their sums have a fixed order.
+ * workspace: fp4_layernorm_backward_workspace_size(rows, cols) bytes, needed for dweight or
+ * dbias only, any contents, 16-byte aligned. */
+size_t fp4_layernorm_backward_workspace_size(int64_t rows, int64_t cols);
+fp4_status fp4_layernorm_backward(const void* dy_dev, const void* x_dev, int64_t rows, int64_t cols,
+                                  fp4_dtype in_dtype, const float* weight_dev, const float* mean_dev,
+                                  const float* rstd_dev, const void* dres_dev, void* dx_dev, fp4_dtype out_dtype,
+                                  float* dweight_dev, float* dbias_dev, void* workspace_dev,
+                                  size_t workspace_bytes, void* stream);
 
 /* BF16-activation GEMM (quantize-on-load): D = gX * gB * (Xq . Bq^T) where Xq is the
  * NVFP4 quantization of the bf16 activations X [M, K] (tensor amax -> gX, 16-blocks,
