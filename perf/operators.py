@@ -359,14 +359,15 @@ def _plain(s):
 _kept = {}
 
 
-def _workspace(nbytes):
-    """One zero-filled workspace for all calls, as a program keeps it."""
+def _workspace(s, nbytes):
+    """One zero-filled workspace for each problem, as a program keeps them."""
     if not nbytes:
         return None, 0
     import block_scaled_fp4_04_b200 as fp4
-    ws = _kept.setdefault("ws", fp4.Workspace())
-    buf = ws.get(nbytes)
-    return buf, buf.numel()
+    key = tuple((k, v) for k, v in sorted(s.items()) if isinstance(v, (str, int, bool)))
+    if key not in _kept:
+        _kept[key] = fp4.Workspace().get(nbytes)
+    return _kept[key], _kept[key].numel()
 
 
 def _own(s):
@@ -377,13 +378,13 @@ def _own(s):
         fp4.fp4_layernorm(s["x"], s["M"], s["N"], oc, s["w"], s["b"], EPS, s["y"], oc, s["mean"], s["rstd"])
         return {"y": s["y"], "mean": s["mean"], "rstd": s["rstd"]}
     if op == "norm_grad":
-        ws, n = _workspace(fp4.fp4_layernorm_backward_workspace_size(s["M"], s["N"]))
+        ws, n = _workspace(s, fp4.fp4_layernorm_backward_workspace_size(s["M"], s["N"]))
         fp4.fp4_layernorm_backward(s["dy"], s["x"], s["M"], s["N"], oc, s["w"], s["mean"], s["rstd"], s["dres"],
                                    s["dx"], oc, s["dw"], s["db"], ws, n)
         return {"dx": s["dx"], "dw": s["dw"], "db": s["db"]}
     act = ACTS[s["act"]]
     if op == "act_grad":
-        ws, n = _workspace(fp4.fp4_act_backward_workspace_size(s["M"], s["F"], s["gated"])) if s["bias"] else (None, 0)
+        ws, n = _workspace(s, fp4.fp4_act_backward_workspace_size(s["M"], s["F"], s["gated"])) if s["bias"] else (None, 0)
         fp4.fp4_act_backward(s["dH"], s["G"], s["U"], s["M"], s["F"], oc, act, s["dZ"], oc, s["db"], workspace=ws,
                              workspace_bytes=n)
         return {"dZ": s["dZ"], "db": s["db"]}
@@ -395,20 +396,20 @@ def _own(s):
         return {"H": s["H"]}
     if op == "out":
         a, w = s["a"], s["w"]
-        ws, n = _workspace(fp4.fp4_gemm_epilogue_workspace_size(s["M"], s["N"], s["K"], s["fmt"], False))
+        ws, n = _workspace(s, fp4.fp4_gemm_epilogue_workspace_size(s["M"], s["N"], s["K"], s["fmt"], False))
         fp4.fp4_gemm_epilogue_ex(s["fmt"], a["codes"], a["scales"], a["g"], w["codes"], w["scales"], w["g"], s["M"],
                                  s["N"], s["K"], s["bias_v"], act, s["res"], oc, s["D"], oc, s["pre"], workspace=ws,
                                  workspace_bytes=n)
         return {"D": s["D"], "pre": s["pre"]}
     wg, wu = s["wg"], s["wu"]
     if op == "gated_x":
-        ws, n = _workspace(fp4.fp4_gemm_gated_bf16a_workspace_size(s["M"], s["F"], s["K"]))
+        ws, n = _workspace(s, fp4.fp4_gemm_gated_bf16a_workspace_size(s["M"], s["F"], s["K"]))
         fp4.fp4_gemm_gated_bf16a(s["x"], wg["codes"], wg["scales"], wg["g"], wu["codes"], wu["scales"], wu["g"],
                                  s["M"], s["F"], s["K"], None, None, act, s["H"], oc, None, None, s["xc"], s["xs"],
                                  s["xg"], ws, n, fp4.GEMM_WEIGHTS_READY)
         return {"H": s["H"]}
     a = s["a"]
-    ws, n = _workspace(fp4.fp4_gemm_gated_workspace_size(s["M"], s["F"], s["K"], s["fmt"], False))
+    ws, n = _workspace(s, fp4.fp4_gemm_gated_workspace_size(s["M"], s["F"], s["K"], s["fmt"], False))
     fp4.fp4_gemm_gated(s["fmt"], a["codes"], a["scales"], a["g"], wg["codes"], wg["scales"], wg["g"], wu["codes"],
                        wu["scales"], wu["g"], s["M"], s["F"], s["K"], s["bg"], s["bu"], act, s["H"], oc, s["G"],
                        s["U"], workspace=ws, workspace_bytes=n)
