@@ -8,27 +8,58 @@
 //              one exponential, and no difference of nearly equal numbers for x << 0
 //
 // s is one exponential and one reciprocal of the special-function unit (relative errors of
-// about 2^-21 and 2^-23, far below the half step 2^-9 of a BF16 result).  For x -> -inf,
-// 1 + e^-x overflows to inf and s is 0, as it should be.
+// about 2^-21 and 2^-23, far below the half step 2^-9 of a BF16 result), both with subnormal
+// results flushed to 0, which saves their scaling steps.  For x -> -inf, 1 + e^-x overflows to
+// inf and s is 0, as it should be.
 #pragma once
 
 #include "fp4_ops.h"
 
 namespace fp4 {
 
-__device__ __forceinline__ float sigmoid_f(float x) { return __fdividef(1.0f, 1.0f + __expf(-x)); }
+constexpr float kLog2e = 1.4426950408889634f;
+
+__device__ __forceinline__ float exp2_sfu(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float rcp_sfu(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+// s(x) from y = -x log2(e)
+__device__ __forceinline__ float sigmoid_from(float y) { return rcp_sfu(1.0f + exp2_sfu(y)); }
+__device__ __forceinline__ float sigmoid_f(float x) { return sigmoid_from(x * -kLog2e); }
 
 constexpr float kGeluA = 0.044715f;
 constexpr float kGelu2C = 1.5957691216057308f;       // 2 sqrt(2 / pi)
 constexpr float kSqrtHalf = 0.70710678118654752f;
 constexpr float kInvSqrt2Pi = 0.39894228040143268f;
 
+// Phi(x), and e^(-x^2/2) for its derivative: erfc(z) = e^(-z^2) P(t), t = 1 / (1 + 0.3275911 z),
+// z = |x| / sqrt(2) >= 0, the rational approximation 7.1.26 of Abramowitz and Stegun's Handbook
+// of Mathematical Functions (error at most 1.5e-7; 2.6e-7 in all in FP32).  Half the instructions of erff, no branch,
+// and no 1 + erf of nearly -1 for x << 0.
+__device__ __forceinline__ float normal_cdf(float x, float& e) {
+  const float z = fminf(fabsf(x) * kSqrtHalf, 16.0f);  // beyond, e is 0
+  const float t = rcp_sfu(fmaf(0.3275911f, z, 1.0f));
+  e = exp2_sfu(z * z * -kLog2e);
+  float p = fmaf(t, 1.061405429f, -1.453152027f);
+  p = fmaf(t, p, 1.421413741f);
+  p = fmaf(t, p, -0.284496736f);
+  p = fmaf(t, p, 0.254829592f);
+  const float half = 0.5f * p * t * e;
+  return x >= 0.0f ? 1.0f - half : half;
+}
+
 template <int ACT>
 __device__ __forceinline__ float act_value(float x) {
-  if constexpr (ACT == kActRelu) return fmaxf(x, 0.0f);
+  if constexpr (ACT == kActRelu) return x < 0.0f ? 0.0f : x;  // a NaN stays one
   else if constexpr (ACT == kActSilu) return x * sigmoid_f(x);
-  else if constexpr (ACT == kActGelu) return 0.5f * x * (1.0f + erff(x * kSqrtHalf));
-  else if constexpr (ACT == kActGeluTanh) return x * sigmoid_f(kGelu2C * x * (1.0f + kGeluA * x * x));
+  else if constexpr (ACT == kActGelu) { float e; return x * normal_cdf(x, e); }
+  else if constexpr (ACT == kActGeluTanh) return x * sigmoid_from(x * fmaf(x * x, -kLog2e * kGelu2C * kGeluA, -kLog2e * kGelu2C));
   else return x;
 }
 
@@ -36,23 +67,24 @@ __device__ __forceinline__ float act_value(float x) {
 template <int ACT>
 __device__ __forceinline__ float act_slope(float x, float& value) {
   if constexpr (ACT == kActRelu) {
-    value = fmaxf(x, 0.0f);
+    value = x < 0.0f ? 0.0f : x;
     return x > 0.0f ? 1.0f : 0.0f;
   } else if constexpr (ACT == kActSilu) {
     const float s = sigmoid_f(x);
     value = x * s;
     return s * (1.0f + x * (1.0f - s));
   } else if constexpr (ACT == kActGelu) {
-    const float phi = 0.5f * (1.0f + erff(x * kSqrtHalf));
+    float e;
+    const float phi = normal_cdf(x, e);
     value = x * phi;
-    return phi + x * kInvSqrt2Pi * __expf(-0.5f * x * x);
+    return phi + x * kInvSqrt2Pi * e;
   } else if constexpr (ACT == kActGeluTanh) {
     // beyond |x| = 64 the sigmoid is 0 or 1: clamping keeps 0 times a large product from
     // becoming 0 times infinity
     const float c = fminf(fmaxf(x, -64.0f), 64.0f), c2 = c * c;
     const float s = sigmoid_f(kGelu2C * c * (1.0f + kGeluA * c2));
     value = x * s;
-    return s * (1.0f + c * (1.0f - s) * kGelu2C * (1.0f + 3.0f * kGeluA * c2));
+    return fmaf(0.0f, x, s * (1.0f + c * (1.0f - s) * kGelu2C * (1.0f + 3.0f * kGeluA * c2)));  // a NaN stays one
   } else {
     value = x;
     return 1.0f;

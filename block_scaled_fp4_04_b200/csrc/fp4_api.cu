@@ -776,7 +776,7 @@ fp4_status fp4_layernorm_backward(const void* dy, const void* x, int64_t rows, i
   p.dweight = dweight;
   p.dbias = dbias;
   p.ws = static_cast<float*>(workspace);
-  const cudaError_t e = launch_layernorm_grad(p, static_cast<cudaStream_t>(stream));
+  const cudaError_t e = launch_layernorm_grad(p, status, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? FP4_OK : cuda_fail(e, "layer norm backward launch");
 }
 

@@ -131,6 +131,8 @@ int launch_gated(const GatedProblem& g, unsigned* status, cudaStream_t st, const
   const int esz = g.out_bf16 ? 2 : 4;
   auto al = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; };
   a.vec_store = (g.F * esz) % 16 == 0 && al(g.H) && al(g.G) && al(g.U);
+  auto al32 = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31) == 0; };
+  a.sectors = (g.F * esz) % 32 == 0 && al32(g.H) && al32(g.G) && al32(g.U);
   a.mode = pl.mode;
   a.tiles_m = pl.tiles_m;
   a.tiles_n = pl.tiles_n;
@@ -139,6 +141,8 @@ int launch_gated(const GatedProblem& g, unsigned* status, cudaStream_t st, const
   a.status = status;
   a.bias = g.bias_g;
   a.bias2 = g.bias_u;
+  // whole tiles start at multiples of 128 columns, experts at multiples of F
+  a.vec_bias = al(g.bias_g) && al(g.bias_u) && (!grouped || g.F % 4 == 0);
   a.act = g.act;
   a.pre = g.G;
   a.pre2 = g.U;

@@ -397,10 +397,11 @@ int launch_gemm_full(const GemmProblemFull& g, unsigned* status, cudaStream_t st
   if (g.full) {
     a.res = g.full->res;
     a.res_bf16 = g.full->res_bf16;
-    const int rsz = a.res_bf16 ? 2 : 4;
-    a.vec_res = (g.N * rsz) % 16 == 0 && (reinterpret_cast<uintptr_t>(a.res) & 15) == 0;
     a.pre = g.full->pre;
-    a.vec_store = a.vec_store && (reinterpret_cast<uintptr_t>(a.pre) & 15) == 0;
+    auto al32 = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31) == 0; };
+    a.sectors = (g.N * esz) % 32 == 0 && al32(g.D) && al32(a.pre) &&
+                (!a.res || ((g.N * (a.res_bf16 ? 2 : 4)) % 32 == 0 && al32(a.res)));
+    a.vec_bias = (reinterpret_cast<uintptr_t>(a.bias) & 15) == 0;
     e = dispatch_full(pl, g.mx, tm, a, st);
   } else {
     e = g.mx ? dispatch<true>(pl, tm, a, st) : dispatch<false>(pl, tm, a, st);

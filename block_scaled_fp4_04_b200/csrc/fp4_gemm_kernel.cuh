@@ -54,7 +54,9 @@ struct GemmArgs {
   uint32_t f8_fmt;     // kind::mxf8f6f4: A's format | B's format << 3 (E4M3 0, E2M1 5)
   // kEpiFull, kEpiGated
   const void* res;       // [M, N] added after the activation, or null
-  int res_bf16, vec_res;
+  int res_bf16;
+  int vec_bias;          // biases are 16-byte aligned
+  int sectors;           // rows of the output, its copies and the residual start at 32-byte sectors
   void* pre;             // kEpiFull: the pre-activation; kEpiGated: G; [M, N] in the output type, or null
   void* pre2;            // kEpiGated: U
   const uint8_t* sfb2;   // kEpiGated: the up operand's scales, global scale, bias
@@ -207,24 +209,18 @@ struct Cfg {
   // scale factors into TMEM, so that these copies are not serialised behind the MMA
   // thread's own MMAs: one for A's atoms and one per 128-row block of B's.
   static constexpr bool kSepCp = kP == 1;
-  // The longer epilogues hold a whole accumulator half (128 FP32 values per thread) in
-  // registers: two copiers instead of three leave 12 warps, and 168 registers per thread.
   static constexpr bool kLong = kSepCp && EPI != kEpiPlain;
-  static constexpr int kCopiers = !kSepCp ? 0 : kLong ? 2 : 1 + (BN >= 128 ? BN / 128 : 1);
+  // (long epilogues: 20 warps of 96 registers; the MMA thread copies the second row-block's)
+  static constexpr int kCopiers = !kSepCp ? 0 : 1 + (BN >= 128 ? BN / 128 : 1);
   // One-pipeline kernels run two epilogue warps per TMEM lane quarter, one per column
   // half: twice the TMEM read and store rate, and half a row of packed BF16 per thread
   // is few enough registers to hold the tile while TMEM is already handed back.
+  // The long epilogues hold their sums in FP32 while TMEM is handed back: four warps per
+  // quarter, 64 sums per thread and as many more warps to hide their arithmetic and loads.
   static constexpr int kEpiWarps = kSepCp ? 8 : 4;
   static constexpr int kEpiCols = BN * 4 / kEpiWarps;  // accumulator columns per epilogue thread
   static constexpr int kTileCols = EPI == kEpiGated ? BN / 2 : BN;  // output columns of a tile
-  // Registers per thread of a long epilogue's launch (384 threads), and what its warpgroups
-  // take: 128 threads of loads, MMAs and copies, 256 of epilogue.
-  static constexpr int kLaunchRegs = 168, kIssueRegs = 64, kEpiRegs = 216;
-  static_assert(128 * kIssueRegs + 256 * kEpiRegs <= 384 * kLaunchRegs, "register split");
   static constexpr int kThreads = kSepCp ? 64 + 32 * kEpiWarps + 32 * kCopiers : 192 * kP;
-  // first epilogue / copier warp: the long epilogues' warps are two whole warpgroups
-  static constexpr int kEpiWarp0 = kLong ? 4 : 2;
-  static constexpr int kCopyWarp0 = kLong ? 2 : 2 + kEpiWarps;
   static constexpr int kAtomsKT = F8 ? 1 : MX ? 2 : 4;  // scale atoms per stage (256 K; 128 K for F8)
   static constexpr int kNRB = BN >= 128 ? BN / 128 : 1;  // B scale row-blocks per tile
   static constexpr int kABytes = 128 * 128;
@@ -406,14 +402,26 @@ __device__ __forceinline__ void take_sums16(float* row, int col, int n, float sc
   }
 }
 
-// 16 consecutive elements at offset `at` of a BF16 or FP32 matrix, 16-byte aligned.
+// One 32-byte sector, 32-byte aligned.
+__device__ __forceinline__ void st_sector(void* p, const uint32_t (&w)[8]) {
+  asm volatile("st.global.L1::no_allocate.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(w[0]), "r"(w[1]),
+               "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+__device__ __forceinline__ void ld_sector(const void* p, uint32_t* w) {
+  asm volatile("ld.global.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+               : "l"(p)
+               : "memory");
+}
+
+// 16 consecutive elements at offset `at` of a BF16 or FP32 matrix, 32-byte aligned.
 __device__ __forceinline__ void store_vec16(void* out, int bf16, int64_t at, const float (&v)[16]) {
   if (bf16) {
-    uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(out) + at);
+    uint32_t w[8];
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
-      __stcs(dst + j, make_uint4(pack_bf16x2(v[8 * j], v[8 * j + 1]), pack_bf16x2(v[8 * j + 2], v[8 * j + 3]),
-                                 pack_bf16x2(v[8 * j + 4], v[8 * j + 5]), pack_bf16x2(v[8 * j + 6], v[8 * j + 7])));
+    for (int j = 0; j < 8; ++j) w[j] = pack_bf16x2(v[2 * j], v[2 * j + 1]);
+    st_sector(static_cast<__nv_bfloat16*>(out) + at, w);
   } else {
     float4* dst = reinterpret_cast<float4*>(static_cast<float*>(out) + at);
 #pragma unroll
@@ -421,43 +429,112 @@ __device__ __forceinline__ void store_vec16(void* out, int bf16, int64_t at, con
   }
 }
 
-__device__ __forceinline__ void load_vec16(const void* in, int bf16, int64_t at, float (&v)[16]) {
-  if (bf16) {
-    const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(in) + at);
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const uint4 t = src[h];
-      const uint32_t w4[4] = {t.x, t.y, t.z, t.w};
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        v[8 * h + 2 * j] = __uint_as_float(w4[j] << 16);
-        v[8 * h + 2 * j + 1] = __uint_as_float(w4[j] & 0xFFFF0000u);
-      }
-    }
+// v[j] += b[j], 8 FP32 parameters (every row of the tile reads the same ones).
+__device__ __forceinline__ void add_vec8(const float* b, int vec, float (&v)[8]) {
+  if (vec) {
+    const float4 x = __ldg(reinterpret_cast<const float4*>(b)), y = __ldg(reinterpret_cast<const float4*>(b) + 1);
+    v[0] = __fadd_rn(v[0], x.x);
+    v[1] = __fadd_rn(v[1], x.y);
+    v[2] = __fadd_rn(v[2], x.z);
+    v[3] = __fadd_rn(v[3], x.w);
+    v[4] = __fadd_rn(v[4], y.x);
+    v[5] = __fadd_rn(v[5], y.y);
+    v[6] = __fadd_rn(v[6], y.z);
+    v[7] = __fadd_rn(v[7], y.w);
   } else {
-    const float4* src = reinterpret_cast<const float4*>(static_cast<const float*>(in) + at);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float4 t = src[j];
-      v[4 * j] = t.x;
-      v[4 * j + 1] = t.y;
-      v[4 * j + 2] = t.z;
-      v[4 * j + 3] = t.w;
-    }
+    for (int j = 0; j < 8; ++j) v[j] = __fadd_rn(v[j], __ldg(b + j));
   }
 }
 
-// The same at any alignment.
-__device__ __forceinline__ void load_vec16_any(const void* in, int bf16, int64_t at, float (&v)[16]) {
-#pragma unroll
-  for (int j = 0; j < 16; ++j)
-    v[j] = bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(in)[at + j]) : static_cast<const float*>(in)[at + j];
+// 8 consecutive elements at offset `at` of a BF16 or FP32 matrix, 16-byte aligned.
+__device__ __forceinline__ void store_vec8(void* out, int bf16, int64_t at, const float (&v)[8]) {
+  if (bf16) {
+    __stcs(reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(out) + at),
+           make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])));
+  } else {
+    float4* dst = reinterpret_cast<float4*>(static_cast<float*>(out) + at);
+    __stcs(dst, make_float4(v[0], v[1], v[2], v[3]));
+    __stcs(dst + 1, make_float4(v[4], v[5], v[6], v[7]));
+  }
 }
 
-// v += 16 FP32 parameters (every row of the tile reads the same ones).
-__device__ __forceinline__ void add_vec16(const float* b, float (&v)[16]) {
+// 16 elements of the residual at offset `at`, as they lie in memory: words 0..7 (BF16) or
+// 0..15 (FP32).
+__device__ __forceinline__ void load_res16(const GemmArgs& p, int64_t at, uint32_t (&w)[16]) {
+  if (p.res_bf16) {
+    ld_sector(static_cast<const __nv_bfloat16*>(p.res) + at, w);
+  } else {
+    ld_sector(static_cast<const float*>(p.res) + at, w);
+    ld_sector(static_cast<const float*>(p.res) + at + 8, w + 8);
+  }
+}
+
+// The long epilogues' whole tiles: OUT consecutive columns of one row whose sums are in
+// registers (gated: rr holds the gate sums, then the up sums).  Every row is read and written in
+// whole 32-byte sectors: a thread's 16-byte pieces of its own row, half a sector each, slowed the
+// whole kernel down (8192 x 4096 x 4096 gated with G and U: 216 us against 189).
+template <int ACT, bool GATED, int OUT>
+__device__ __forceinline__ void epi_rows(const GemmArgs& p, int row, int col0, int group, float scale, float scale2,
+                                         const uint32_t (&rr)[GATED ? 2 * OUT : OUT], uint32_t& tmax) {
+  const int64_t at = static_cast<int64_t>(row) * p.ldo + col0;
+  const float* bias = p.bias ? p.bias + group * p.bias_group + col0 : nullptr;
+  const float* bias2 = GATED && p.bias2 ? p.bias2 + group * p.bias_group + col0 : nullptr;
+  uint32_t res[16];  // the next 16 residual elements, loaded one step ahead
+  if (!GATED && p.res) load_res16(p, at, res);
 #pragma unroll
-  for (int j = 0; j < 16; ++j) v[j] = __fadd_rn(v[j], __ldg(b + j));
+  for (int c = 0; c < OUT; c += 16) {
+    float z[16];
+    uint32_t pw[8], pw2[8];
+#pragma unroll
+    for (int h = 0; h < 16; h += 8) {
+      float v[8], u[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        v[j] = __uint_as_float(rr[c + h + j]) * scale;
+        if (GATED) u[j] = __uint_as_float(rr[(GATED ? OUT : 0) + c + h + j]) * scale2;
+      }
+      if (bias) add_vec8(bias + c + h, p.vec_bias, v);
+      if (GATED && bias2) add_vec8(bias2 + c + h, p.vec_bias, u);
+      if (p.pre) {
+        if (p.out_bf16) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            pw[h / 2 + j] = pack_bf16x2(v[2 * j], v[2 * j + 1]);
+            if (GATED) pw2[h / 2 + j] = pack_bf16x2(u[2 * j], u[2 * j + 1]);
+          }
+        } else {
+          store_vec8(p.pre, p.out_bf16, at + c + h, v);
+          if (GATED) store_vec8(p.pre2, p.out_bf16, at + c + h, u);
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) z[h + j] = GATED ? act_value<ACT>(v[j]) * u[j] : act_value<ACT>(v[j]);
+    }
+    if (p.pre && p.out_bf16) {
+      st_sector(static_cast<__nv_bfloat16*>(p.pre) + at + c, pw);
+      if (GATED) st_sector(static_cast<__nv_bfloat16*>(p.pre2) + at + c, pw2);
+    }
+    if (!GATED && p.res) {
+      if (p.res_bf16) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          z[2 * j] += __uint_as_float(res[j] << 16);
+          z[2 * j + 1] += __uint_as_float(res[j] & 0xFFFF0000u);
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 16; ++j) z[j] += __uint_as_float(res[j]);
+      }
+      if (c + 16 < OUT) load_res16(p, at + c + 16, res);
+    }
+    if (p.out) store_vec16(p.out, p.out_bf16, at + c, z);
+    if (p.q_codes) epi_quantize16(p, row, col0 + c, z);
+    if (p.amax_out) {
+#pragma unroll
+      for (int j = 0; j < 16; ++j) tmax = max(tmax, __float_as_uint(z[j]) & 0x7FFFFFFFu);
+    }
+  }
 }
 
 // Offset in the output of kernel row `row`, column `col`.
@@ -469,7 +546,15 @@ __device__ __forceinline__ int64_t out_offset(const GemmArgs& p, int row, int co
 // output is (`out` in the output's type); columns past the matrix are left out.
 __device__ __forceinline__ void store_like_out(const GemmArgs& p, void* out, int row, int col, const float (&v)[16]) {
   if (!p.transposed && p.vec_store && col + 16 <= p.Nk) {
-    store_vec16(out, p.out_bf16, out_offset(p, row, col), v);
+    float a[8], b[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      a[j] = v[j];
+      b[j] = v[8 + j];
+    }
+    const int64_t at = out_offset(p, row, col);
+    store_vec8(out, p.out_bf16, at, a);
+    store_vec8(out, p.out_bf16, at + 8, b);
     return;
   }
 #pragma unroll
@@ -680,11 +765,6 @@ __global__ void __launch_bounds__(Cfg<BN, MX, ACC, PAIR, F8, EPI>::kThreads, 1)
                       smem_desc_sf(st + C::kABytes + C::kBBytes + C::kSFABytes + (rb * C::kAtomsKT + a) * 512));
   };
 
-  if constexpr (C::kLong) {  // warps 0..3 issue, warps 4..11 finish: whole warpgroups
-    static_assert(C::kThreads == 384, "three warpgroups");
-    if (warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kIssueRegs));
-    else asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kEpiRegs));
-  }
   if (warp == 0) {
     if (lane == 0) {
       // ------------------------------------------------------------ producer
@@ -858,6 +938,23 @@ __global__ void __launch_bounds__(Cfg<BN, MX, ACC, PAIR, F8, EPI>::kThreads, 1)
               ok = false;
               break;
             }
+            if constexpr (false) {
+              // the second row-block's atoms: copied here, in order before this stage's MMAs
+              if (!mbar_wait(&sf_landed[stage], phase, s_abort)) {
+                latch_timeout(s_abort, p.status);
+                ok = false;
+                break;
+              }
+              tc_fence_after();
+              const int atoms = min(C::kAtomsKT, p.sf_atoms_k - kb * C::kAtomsKT);
+              for (int a = 0; a < atoms; ++a) {
+                const uint64_t sd = smem_desc_sf(st + C::kABytes + C::kBBytes + C::kSFABytes + (C::kAtomsKT + a) * 512);
+                if constexpr (PAIR)
+                  tc_cp_sf_atom_pair(sfb_t + (a * C::kNRB + 1) * 4, sd);
+                else
+                  tc_cp_sf_atom(sfb_t + (a * C::kNRB + 1) * 4, sd);
+              }
+            }
             tc_fence_after();
           } else {
             tc_fence_after();
@@ -925,10 +1022,8 @@ __global__ void __launch_bounds__(Cfg<BN, MX, ACC, PAIR, F8, EPI>::kThreads, 1)
       volatile int no_abort = 0;
       mbar_wait(drain, 0, &no_abort);
     }
-  } else if (C::kSepCp && warp >= C::kCopyWarp0 && warp < C::kCopyWarp0 + C::kCopiers) {
-    // 0: A's atoms; 1 + rb: B's row-block rb.  Two copiers for three sets: the first takes
-    // A's atoms and half of the second row-block's, the second the rest.
-    const int cw = warp - C::kCopyWarp0;
+  } else if (C::kSepCp && warp >= 2 + C::kEpiWarps) {
+    const int cw = warp - 2 - C::kEpiWarps;  // 0: A's atoms; 1 + rb: B's row-block rb
     if (lane == 0 && leader) {
       // ------------------------------------------------------------ scale-factor copier
       // Stage n's atoms go to TMEM slot n % kSFSlots once they have landed and the
@@ -969,16 +1064,7 @@ __global__ void __launch_bounds__(Cfg<BN, MX, ACC, PAIR, F8, EPI>::kThreads, 1)
             };
             if (cw == 0) {
               for (int a = 0; a < atoms; ++a) cp(sfa_t + a * 4, smem_desc_sf(st + C::kABytes + C::kBBytes + a * 512));
-            }
-            if (C::kLong && C::kNRB == 2) {
-              // row-block 0's atoms, and the second half of row-block 1's, on the second copier
-              const uint32_t sb = st + C::kABytes + C::kBBytes + C::kSFABytes;
-              const int mid = (atoms + 1) / 2;
-              if (cw == 1)
-                for (int a = 0; a < atoms; ++a) cp(sfa_t + C::kSFACols + a * C::kNRB * 4, smem_desc_sf(sb + a * 512));
-              for (int a = cw == 0 ? 0 : mid; a < (cw == 0 ? mid : atoms); ++a)
-                cp(sfa_t + C::kSFACols + (a * C::kNRB + 1) * 4, smem_desc_sf(sb + (C::kAtomsKT + a) * 512));
-            } else if (cw > 0) {
+            } else {
               const int rb = cw - 1;
               for (int a = 0; a < atoms; ++a)
                 cp(sfa_t + C::kSFACols + (a * C::kNRB + rb) * 4,
@@ -1004,15 +1090,15 @@ __global__ void __launch_bounds__(Cfg<BN, MX, ACC, PAIR, F8, EPI>::kThreads, 1)
       volatile int no_abort = 0;
       mbar_wait(cp_drain, 0, &no_abort);
     }
-  } else if (warp >= C::kEpiWarp0 && warp < C::kEpiWarp0 + C::kEpiWarps) {
+  } else if (warp >= 2 && warp < 2 + C::kEpiWarps) {
     // ------------------------------------------------------------ epilogue
     // a warp reads the TMEM lane quarter given by its warp index in the CTA, modulo 4,
     // and (with eight epilogue warps) the column half given by its warp index over 4
     const int q = (threadIdx.x >> 5) & 3;
     const int rl = q * 32 + lane;     // accumulator row (TMEM lane) of this thread
-    const int et = lt - 32 * C::kEpiWarp0;  // 0 .. 32 * kEpiWarps - 1
+    const int et = lt - 32 * 2;  // 0 .. 32 * kEpiWarps - 1
     constexpr int CH = C::kEpiCols;
-    const int c0 = ((warp - C::kEpiWarp0) >> 2) * CH;  // first accumulator column of this thread
+    const int c0 = ((warp - 2) >> 2) * CH;  // first accumulator column of this thread
     // BF16 row-major tiles whose columns are all in range are converted into registers
     // and TMEM is handed back to the MMA thread before the stores, so that they overlap
     // the next tile's MMAs
@@ -1052,7 +1138,7 @@ __global__ void __launch_bounds__(Cfg<BN, MX, ACC, PAIR, F8, EPI>::kThreads, 1)
       const uint32_t taddr = tmem + (static_cast<uint32_t>(q * 32) << 16) + acc * BN;
       bool released = false;
       if constexpr (EPI != kEpiPlain) {
-        if (C::kLong && p.mode != kModeStreamK && p.vec_store && w.n0 + C::kTileCols <= p.Nk) {
+        if (C::kLong && p.mode != kModeStreamK && p.sectors && w.n0 + C::kTileCols <= p.Nk) {
           // whole tiles: the accumulator half goes into registers and TMEM back to the MMA
           // thread; everything else overlaps the next tile's MMAs
           constexpr int kOut = kGated ? CH / 2 : CH;   // output columns of this thread
@@ -1068,42 +1154,10 @@ __global__ void __launch_bounds__(Cfg<BN, MX, ACC, PAIR, F8, EPI>::kThreads, 1)
           __syncwarp();
           if (lane == 0) release_acc(acc);
           released = true;
-          if (row_ok) {
-            const int64_t at = static_cast<int64_t>(row) * p.ldo + w.n0 + oc;
-            const float* bias = p.bias ? p.bias + w.group * p.bias_group + w.n0 + oc : nullptr;
-            const float* bias2 = kGated && p.bias2 ? p.bias2 + w.group * p.bias_group + w.n0 + oc : nullptr;
+          if (row_ok)
             with_act(p.act, [&](auto tag) {
-              constexpr int A = decltype(tag)::value;
-#pragma unroll
-              for (int c = 0; c < kOut; c += 16) {
-                float v[16], u[16];
-#pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                  v[j] = __uint_as_float(rr[c + j]) * scale;
-                  if (kGated) u[j] = __uint_as_float(rr[(kGated ? CH / 2 : 0) + c + j]) * scale2;
-                }
-                if (bias) add_vec16(bias + c, v);
-                if (kGated && bias2) add_vec16(bias2 + c, u);
-                if (p.pre) store_vec16(p.pre, p.out_bf16, at + c, v);
-                if (kGated && p.pre2) store_vec16(p.pre2, p.out_bf16, at + c, u);
-#pragma unroll
-                for (int j = 0; j < 16; ++j) v[j] = kGated ? act_value<A>(v[j]) * u[j] : act_value<A>(v[j]);
-                if (!kGated && p.res) {
-                  float r[16];
-                  if (p.vec_res) load_vec16(p.res, p.res_bf16, at + c, r);
-                  else load_vec16_any(p.res, p.res_bf16, at + c, r);
-#pragma unroll
-                  for (int j = 0; j < 16; ++j) v[j] += r[j];
-                }
-                if (p.out) store_vec16(p.out, p.out_bf16, at + c, v);
-                if (p.q_codes) epi_quantize16(p, row, w.n0 + oc + c, v);
-                if (p.amax_out) {
-#pragma unroll
-                  for (int j = 0; j < 16; ++j) tmax = max(tmax, __float_as_uint(v[j]) & 0x7FFFFFFFu);
-                }
-              }
+              epi_rows<decltype(tag)::value, kGated, kOut>(p, row, w.n0 + oc, w.group, scale, scale2, rr, tmax);
             });
-          }
         } else if (p.mode != kModeStreamK) {
           // ragged or unaligned tiles and small-N tiles: finished as they are read
           constexpr int kOut = kGated ? CH / 2 : CH;
@@ -1337,14 +1391,6 @@ static cudaError_t run(const GemmMaps& tm, const GemmArgs& a, int64_t units, cud
   if (dev < 0 || dev >= 64 || !attr_done[dev]) {
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
     if (e != cudaSuccess) return e;
-    if constexpr (C::kLong) {
-      // the warpgroups' shares of the registers must fit what the launch allocates: a
-      // setmaxnreg.inc beyond it would wait for ever
-      cudaFuncAttributes fa;
-      e = cudaFuncGetAttributes(&fa, kern);
-      if (e != cudaSuccess) return e;
-      if (fa.numRegs != C::kLaunchRegs) return cudaErrorInvalidConfiguration;
-    }
     if (dev >= 0 && dev < 64) attr_done[dev] = true;
   }
   // programmatic dependent launch: the prologue (barriers, TMEM, descriptor prefetch,

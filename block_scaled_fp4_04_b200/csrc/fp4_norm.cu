@@ -154,6 +154,226 @@ __global__ void __launch_bounds__((WPR < 4 ? 4 : WPR) * 32) ln_forward_kernel(co
   if (FMT != kCodesNone && bad) atomicOr(p.status, kStatusNonFinite);
 }
 
+// ------------------------------------------------------------------ rows through a ring
+// With many rows: one CTA per SM whose groups of WPR warps walk over rows of their own.  Each
+// group has a ring of row slots in shared memory that bulk copies fill several rows ahead, so
+// that the loads in flight do not depend on how far its arithmetic is, and a thread keeps the
+// parameters of its columns in registers from row to row.  A group's first thread refills a
+// slot after the row sum's barrier, by when every thread has read the slot.
+constexpr int kRingWarps = 16;
+constexpr int kRingSlots = 8;                       // at most, per group
+constexpr size_t kRingBytes = 200 * 1024;           // shared memory for the slots of a CTA
+constexpr int kRingHeader = 1024;                   // barriers, row sums
+
+struct RingPlan {
+  int slots;      // per group
+  size_t smem;
+  int grid;
+};
+static RingPlan ring_plan(int groups, size_t slot_bytes, int64_t rows) {
+  RingPlan r{};
+  r.slots = static_cast<int>(std::min<size_t>(kRingSlots, kRingBytes / (groups * slot_bytes)));
+  r.smem = kRingHeader + static_cast<size_t>(r.slots) * groups * slot_bytes;
+  r.grid = static_cast<int>(std::min<int64_t>(num_sms(), (rows + groups - 1) / groups));
+  return r;
+}
+
+struct Ring {
+  uint64_t* full;          // [slots] of this group
+  uint8_t* slot0;          // this group's slots
+  uint32_t slot_bytes;
+  int slots;
+  volatile int* abort;
+  unsigned* status;
+  int at;                  // slot of the current row
+  uint32_t phase;
+  // Waits for the current row.  After a timeout (latched) the group goes on with what is there,
+  // so that its barriers still match; the outputs are then unspecified.
+  __device__ __forceinline__ void wait() {
+    if (!mbar_wait(&full[at], phase, abort) && !*abort) {
+      *abort = 1;
+      atomicOr(status, kStatusTimeout);
+    }
+  }
+  __device__ __forceinline__ const uint8_t* row() const { return slot0 + static_cast<size_t>(at) * slot_bytes; }
+  __device__ __forceinline__ void next() {
+    if (++at == slots) {
+      at = 0;
+      phase ^= 1;
+    }
+  }
+};
+
+template <typename T, int V>
+__device__ __forceinline__ void ring_read(RowVec<T, V>& r, const uint8_t* row, int col) {
+  const uint4 t = *reinterpret_cast<const uint4*>(row + static_cast<size_t>(col) * sizeof(T));
+  r.w[0] = t.x;
+  r.w[1] = t.y;
+  r.w[2] = t.z;
+  r.w[3] = t.w;
+}
+
+template <typename T, int V, int WPR, int C, int FMT>
+__global__ void __launch_bounds__(kRingWarps * 32, 1) ln_forward_ring_kernel(const LnArgs p, int slots) {
+  constexpr int G = kRingWarps / WPR;
+  constexpr int kStep = WPR * 32 * V;
+  extern __shared__ __align__(128) uint8_t s_ring[];
+  __shared__ float s_red[2][G][WPR];
+  __shared__ volatile int s_abort;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int group = warp / WPR, wr = warp % WPR, bar = 1 + group;
+  const int first = (wr * 32 + lane) * V;
+  const uint32_t row_bytes = static_cast<uint32_t>(p.n) * sizeof(T);
+  Ring ring{reinterpret_cast<uint64_t*>(s_ring) + group * kRingSlots,
+            s_ring + kRingHeader + static_cast<size_t>(group) * slots * row_bytes, row_bytes, slots, &s_abort, p.status, 0, 0};
+  if (threadIdx.x == 0) {
+    s_abort = 0;
+    for (int i = 0; i < G * kRingSlots; ++i) mbar_init(reinterpret_cast<uint64_t*>(s_ring) + i, 1);
+    fence_mbar_init();
+  }
+  __syncthreads();
+  rows_allow_dependents();
+  rows_wait_prior();
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * G;
+  int64_t row = static_cast<int64_t>(blockIdx.x) * G + group;
+  const bool loader = wr == 0 && lane == 0;
+  const uint64_t pol = l2_policy_evict_first();
+  auto load_row = [&](int slot, int64_t r) {
+    mbar_arrive_expect_tx(&ring.full[slot], row_bytes);
+    bulk_load(ring.slot0 + static_cast<size_t>(slot) * row_bytes, static_cast<const T*>(p.x) + r * p.n, row_bytes,
+              &ring.full[slot], pol);
+  };
+  if (loader)
+    for (int i = 0; i < slots && row + i * stride < p.rows; ++i) load_row(i, row + i * stride);
+  float w[C][V], b[C][V];
+#pragma unroll
+  for (int j = 0; j < C; ++j) {
+    const int col = first + j * kStep;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      w[j][i] = 1.0f;
+      b[j][i] = 0.0f;
+    }
+    if (col < p.n) {
+      if (p.w) load_params<V>(p.w + col, w[j]);
+      if (p.b) load_params<V>(p.b + col, b[j]);
+    }
+  }
+  const float inv_n = 1.0f / static_cast<float>(p.n);
+  float g = 1.0f;
+  if constexpr (FMT == kCodesNv) g = *p.q.g;
+  uint32_t m = 0;
+  bool bad = false;
+  for (; row < p.rows; row += stride) {
+    ring.wait();
+    RowVec<T, V> raw[C];
+#pragma unroll
+    for (int j = 0; j < C; ++j) {
+      const int col = first + j * kStep;
+      if (col < p.n) ring_read<T, V>(raw[j], ring.row(), col);
+      else raw[j].zero();
+    }
+    float s = 0.0f;
+#pragma unroll
+    for (int j = 0; j < C; ++j) {
+      float v[V];
+      raw[j].unpack(v);
+#pragma unroll
+      for (int i = 0; i < V; ++i) s += v[i];
+    }
+    const float mean = row_sum<WPR>(s, s_red[0][group], wr, lane, bar) * inv_n;
+    if constexpr (WPR == 1) __syncwarp();
+    if (loader && row + slots * stride < p.rows) load_row(ring.at, row + slots * stride);
+    ring.next();
+    float ss = 0.0f;
+#pragma unroll
+    for (int j = 0; j < C; ++j)
+      if (first + j * kStep < p.n) {
+        float v[V];
+        raw[j].unpack(v);
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          const float d = v[i] - mean;
+          ss += d * d;
+        }
+      }
+    const float var = row_sum<WPR>(ss, s_red[1][group], wr, lane, bar) * inv_n;
+    const float rstd = 1.0f / sqrtf(var + p.eps);
+    if (loader) {
+      if (p.mean) p.mean[row] = mean;
+      if (p.rstd) p.rstd[row] = rstd;
+    }
+#pragma unroll
+    for (int j = 0; j < C; ++j) {
+      const int col = first + j * kStep;
+      const bool ok = col < p.n;
+      float v[V], o[V];
+      raw[j].unpack(v);
+#pragma unroll
+      for (int i = 0; i < V; ++i) o[i] = ok ? fmaf((v[i] - mean) * rstd, w[j][i], b[j][i]) : 0.0f;
+      if (ok) {
+        if (p.y) store_row_vec<V>(p.y, p.y_bf16, row * p.n + col, o);
+        if (p.amax) {
+#pragma unroll
+          for (int i = 0; i < V; ++i) m = max(m, abs_bits_of(o[i]));
+        }
+      }
+      if constexpr (FMT != kCodesNone) bad |= encode_row_vec<FMT, V>(p.q, g, row, col, ok, o);
+    }
+  }
+  if (p.amax) {
+    m = __reduce_max_sync(0xFFFFFFFFu, m);
+    if (lane == 0 && m) atomicMax(p.amax, m);
+  }
+  if (FMT != kCodesNone && bad) atomicOr(p.status, kStatusNonFinite);
+  if (s_abort && loader) {  // copies still in flight land before the shared memory goes away
+    volatile int no_abort = 0;
+    for (int i = 0; i < slots; ++i) mbar_wait(&ring.full[i], ring.phase ^ (i < ring.at ? 1u : 0u), &no_abort);
+  }
+}
+
+template <typename K>
+static cudaError_t ring_attr(K kern, bool (&done)[64]) {
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev >= 0 && dev < 64 && done[dev]) return cudaSuccess;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             static_cast<int>(kRingHeader + kRingBytes));
+  if (e == cudaSuccess && dev >= 0 && dev < 64) done[dev] = true;
+  return e;
+}
+
+template <typename T, int V, int WPR, int C, int FMT>
+static cudaError_t run_ln_ring(const LnArgs& a, cudaStream_t st) {
+  static bool done[64] = {false};
+  const cudaError_t e = ring_attr(ln_forward_ring_kernel<T, V, WPR, C, FMT>, done);
+  if (e != cudaSuccess) return e;
+  const RingPlan r = ring_plan(kRingWarps / WPR, static_cast<size_t>(a.n) * sizeof(T), a.rows);
+  return launch_rows(ln_forward_ring_kernel<T, V, WPR, C, FMT>, dim3(static_cast<unsigned>(r.grid)), kRingWarps * 32,
+                     r.smem, st, a, r.slots);
+}
+
+// Rows and lengths the ring serves: groups whose lanes are well filled, several rows for every
+// group in the grid.
+template <typename T, int V, int FMT>
+static bool pick_ln_ring(const LnArgs& a, cudaStream_t st, cudaError_t* e) {
+  if constexpr (V == 1) {
+    return false;
+  } else {
+    const int nch = (a.n + V - 1) / V;
+    if (a.rows < 8 * static_cast<int64_t>(num_sms()) || nch < 96 || nch > 2048) return false;
+    if (nch <= 128) *e = run_ln_ring<T, V, 2, 2, FMT>(a, st);
+    else if (nch <= 256) *e = run_ln_ring<T, V, 2, 4, FMT>(a, st);
+    else if (nch <= 384) *e = run_ln_ring<T, V, 4, 3, FMT>(a, st);
+    else if (nch <= 512) *e = run_ln_ring<T, V, 4, 4, FMT>(a, st);
+    else if (nch <= 768) *e = run_ln_ring<T, V, 8, 3, FMT>(a, st);
+    else if (nch <= 1024) *e = run_ln_ring<T, V, 8, 4, FMT>(a, st);
+    else if (nch <= 1536) *e = run_ln_ring<T, V, 16, 3, FMT>(a, st);
+    else *e = run_ln_ring<T, V, 16, 4, FMT>(a, st);
+    return true;
+  }
+}
+
 template <typename T, int V, int WPR, int C, int FMT>
 static cudaError_t run_ln(const LnArgs& a, cudaStream_t st) {
   constexpr int kWarps = WPR < 4 ? 4 : WPR, kRows = kWarps / WPR;
@@ -164,6 +384,8 @@ static cudaError_t run_ln(const LnArgs& a, cudaStream_t st) {
 // Warps per row by the row's length, so that a thread holds at most four chunks.
 template <typename T, int V, int FMT>
 static cudaError_t pick_ln(const LnArgs& a, cudaStream_t st) {
+  cudaError_t e = cudaSuccess;
+  if (pick_ln_ring<T, V, FMT>(a, st, &e)) return e;
   const int nch = (a.n + V - 1) / V;
   if (nch <= 32) return run_ln<T, V, 1, 1, FMT>(a, st);
   if (nch <= 64) return run_ln<T, V, 1, 2, FMT>(a, st);
@@ -358,6 +580,208 @@ __global__ void __launch_bounds__((WPR < 8 ? 8 : WPR) * 32) ln_backward_kernel(c
   }
 }
 
+// The same through a ring of rows (x, dy and the residual's gradient side by side in a slot).
+template <typename T, int V, int WPR, int C, bool RES>
+__global__ void __launch_bounds__(kRingWarps * 32, 1) ln_backward_ring_kernel(const LnGradArgs p, int slots, unsigned* status) {
+  constexpr int G = kRingWarps / WPR;
+  constexpr int kStep = WPR * 32 * V;
+  extern __shared__ __align__(128) uint8_t s_ring[];
+  __shared__ float s_red[2][2][G][WPR];
+  __shared__ volatile int s_abort;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int group = warp / WPR, wr = warp % WPR, bar = 1 + group;
+  const int first = (wr * 32 + lane) * V;
+  const uint32_t row_bytes = static_cast<uint32_t>(p.n) * sizeof(T);
+  const uint32_t slot_bytes = row_bytes * (RES ? 3 : 2);
+  Ring ring{reinterpret_cast<uint64_t*>(s_ring) + group * kRingSlots,
+            s_ring + kRingHeader + static_cast<size_t>(group) * slots * slot_bytes, slot_bytes, slots, &s_abort, status, 0, 0};
+  if (threadIdx.x == 0) {
+    s_abort = 0;
+    for (int i = 0; i < G * kRingSlots; ++i) mbar_init(reinterpret_cast<uint64_t*>(s_ring) + i, 1);
+    fence_mbar_init();
+  }
+  __syncthreads();
+  rows_allow_dependents();
+  rows_wait_prior();
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * G;
+  int64_t row = static_cast<int64_t>(blockIdx.x) * G + group;
+  const bool loader = wr == 0 && lane == 0;
+  const uint64_t pol = l2_policy_evict_first();
+  auto load_row = [&](int slot, int64_t r) {
+    uint8_t* dst = ring.slot0 + static_cast<size_t>(slot) * slot_bytes;
+    uint64_t* full = &ring.full[slot];
+    mbar_arrive_expect_tx(full, slot_bytes);
+    bulk_load(dst, static_cast<const T*>(p.x) + r * p.n, row_bytes, full, pol);
+    bulk_load(dst + row_bytes, static_cast<const T*>(p.dy) + r * p.n, row_bytes, full, pol);
+    if (RES) bulk_load(dst + 2 * row_bytes, static_cast<const T*>(p.dres) + r * p.n, row_bytes, full, pol);
+  };
+  if (loader)
+    for (int i = 0; i < slots && row + i * stride < p.rows; ++i) load_row(i, row + i * stride);
+  float w[C][V], dw[C][V], db[C][V];
+#pragma unroll
+  for (int j = 0; j < C; ++j) {
+    const int col = first + j * kStep;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      w[j][i] = 1.0f;
+      dw[j][i] = db[j][i] = 0.0f;
+    }
+    if (p.w && col < p.n) load_params<V>(p.w + col, w[j]);
+  }
+  const float inv_n = 1.0f / static_cast<float>(p.n);
+  float mean_n = 0.0f, rstd_n = 0.0f;
+  if (row < p.rows) {
+    mean_n = __ldg(p.mean + row);
+    rstd_n = __ldg(p.rstd + row);
+  }
+  for (int par = 0; row < p.rows; row += stride, par ^= 1) {
+    const float mean = mean_n, rstd = rstd_n;
+    if (row + stride < p.rows) {  // the next row's, a row ahead
+      mean_n = __ldg(p.mean + row + stride);
+      rstd_n = __ldg(p.rstd + row + stride);
+    }
+    ring.wait();
+    RowVec<T, V> rx[C], rd[C], rr[RES ? C : 1];
+    float s1 = 0.0f, s2 = 0.0f;
+#pragma unroll
+    for (int j = 0; j < C; ++j) {
+      const int col = first + j * kStep;
+      if (col < p.n) {
+        ring_read<T, V>(rx[j], ring.row(), col);
+        ring_read<T, V>(rd[j], ring.row() + row_bytes, col);
+        if constexpr (RES) ring_read<T, V>(rr[j], ring.row() + 2 * row_bytes, col);
+        float x[V], d[V];
+        rx[j].unpack(x);
+        rd[j].unpack(d);
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          const float xh = (x[i] - mean) * rstd;
+          dw[j][i] += d[i] * xh;
+          db[j][i] += d[i];
+          const float a = d[i] * w[j][i];
+          s1 += a;
+          s2 += a * xh;
+        }
+      }
+    }
+    s1 = warp_sum(s1);
+    s2 = warp_sum(s2);
+    if constexpr (WPR > 1) {
+      float* r1 = s_red[par][0][group];
+      float* r2 = s_red[par][1][group];
+      if (lane == 0) {
+        r1[wr] = s1;
+        r2[wr] = s2;
+      }
+      asm volatile("bar.sync %0, %1;" ::"r"(bar), "r"(WPR * 32) : "memory");
+      s1 = s2 = 0.0f;
+#pragma unroll
+      for (int i = 0; i < WPR; ++i) {
+        s1 += r1[i];
+        s2 += r2[i];
+      }
+    } else {
+      __syncwarp();
+    }
+    if (loader && row + slots * stride < p.rows) load_row(ring.at, row + slots * stride);
+    ring.next();
+    const float c1 = s1 * inv_n, c2 = s2 * inv_n;
+#pragma unroll
+    for (int j = 0; j < C; ++j) {
+      const int col = first + j * kStep;
+      if (col < p.n) {
+        float x[V], d[V], o[V];
+        rx[j].unpack(x);
+        rd[j].unpack(d);
+#pragma unroll
+        for (int i = 0; i < V; ++i) o[i] = rstd * (d[i] * w[j][i] - c1 - (x[i] - mean) * rstd * c2);
+        if constexpr (RES) {
+          float r[V];
+          rr[j].unpack(r);
+#pragma unroll
+          for (int i = 0; i < V; ++i) o[i] += r[i];
+        }
+        store_row_vec<V>(p.dx, p.dx_bf16, row * p.n + col, o);
+      }
+    }
+  }
+  if (s_abort && loader) {  // copies still in flight land before the shared memory is used again
+    volatile int no_abort = 0;
+    for (int i = 0; i < slots; ++i) mbar_wait(&ring.full[i], ring.phase ^ (i < ring.at ? 1u : 0u), &no_abort);
+  }
+  if (!p.part) return;
+  // the groups' sums add up in shared memory, in the order of the groups
+  float* out = p.part + static_cast<int64_t>(blockIdx.x) * 2 * p.n;
+  if constexpr (G > 1) {
+    float* s_part = reinterpret_cast<float*>(s_ring);  // [2][n]: within the ring, which is done with
+    __syncthreads();
+    for (int gi = 0; gi < G; ++gi) {
+      if (group == gi) {
+#pragma unroll
+        for (int j = 0; j < C; ++j)
+#pragma unroll
+          for (int i = 0; i < V; ++i) {
+            const int col = first + j * kStep + i;
+            if (col < p.n) {
+              s_part[col] = gi ? s_part[col] + dw[j][i] : dw[j][i];
+              s_part[p.n + col] = gi ? s_part[p.n + col] + db[j][i] : db[j][i];
+            }
+          }
+      }
+      __syncthreads();
+    }
+    for (int c = threadIdx.x; c < 2 * p.n; c += kRingWarps * 32) out[c] = s_part[c];
+  } else {
+#pragma unroll
+    for (int j = 0; j < C; ++j) {
+      const int col = first + j * kStep;
+      if (col < p.n) {
+#pragma unroll
+        for (int i = 0; i < V; i += 4) {
+          *reinterpret_cast<float4*>(out + col + i) = make_float4(dw[j][i], dw[j][i + 1], dw[j][i + 2], dw[j][i + 3]);
+          *reinterpret_cast<float4*>(out + p.n + col + i) =
+              make_float4(db[j][i], db[j][i + 1], db[j][i + 2], db[j][i + 3]);
+        }
+      }
+    }
+  }
+}
+
+template <typename T, int V, int WPR, int C, bool RES>
+static cudaError_t run_ln_grad_ring(const LnGradArgs& a, int* parts, unsigned* status, cudaStream_t st) {
+  static bool done[64] = {false};
+  const cudaError_t e = ring_attr(ln_backward_ring_kernel<T, V, WPR, C, RES>, done);
+  if (e != cudaSuccess) return e;
+  const RingPlan r = ring_plan(kRingWarps / WPR, static_cast<size_t>(a.n) * sizeof(T) * (RES ? 3 : 2), a.rows);
+  *parts = r.grid;
+  return launch_rows(ln_backward_ring_kernel<T, V, WPR, C, RES>, dim3(static_cast<unsigned>(r.grid)), kRingWarps * 32,
+                     r.smem, st, a, r.slots, status);
+}
+
+template <typename T, int V, bool RES>
+static bool pick_ln_grad_ring(const LnGradArgs& a, int* parts, unsigned* status, cudaStream_t st, cudaError_t* e) {
+  const int nch = (a.n + V - 1) / V;
+  if (a.rows < 8 * static_cast<int64_t>(num_sms()) || nch < 96) return false;
+  if constexpr (V == 8) {  // two chunks of 8 columns per thread at most
+    if (nch <= 128) *e = run_ln_grad_ring<T, V, 2, 2, RES>(a, parts, status, st);
+    else if (nch <= 256) *e = run_ln_grad_ring<T, V, 4, 2, RES>(a, parts, status, st);
+    else if (nch <= 512) *e = run_ln_grad_ring<T, V, 8, 2, RES>(a, parts, status, st);
+    else if (nch <= 1024) *e = run_ln_grad_ring<T, V, 16, 2, RES>(a, parts, status, st);
+    else return false;
+  } else {  // four of 4 columns
+    if (nch <= 128) *e = run_ln_grad_ring<T, V, 2, 2, RES>(a, parts, status, st);
+    else if (nch <= 256) *e = run_ln_grad_ring<T, V, 2, 4, RES>(a, parts, status, st);
+    else if (nch <= 384) *e = run_ln_grad_ring<T, V, 4, 3, RES>(a, parts, status, st);
+    else if (nch <= 512) *e = run_ln_grad_ring<T, V, 4, 4, RES>(a, parts, status, st);
+    else if (nch <= 768) *e = run_ln_grad_ring<T, V, 8, 3, RES>(a, parts, status, st);
+    else if (nch <= 1024) *e = run_ln_grad_ring<T, V, 8, 4, RES>(a, parts, status, st);
+    else if (nch <= 1536) *e = run_ln_grad_ring<T, V, 16, 3, RES>(a, parts, status, st);
+    else if (nch <= 2048) *e = run_ln_grad_ring<T, V, 16, 4, RES>(a, parts, status, st);
+    else return false;
+  }
+  return true;
+}
+
 // Rows longer than a CTA's registers: the column sums by a kernel of their own, and dx by a
 // CTA per row that reads the row twice.
 template <typename T>
@@ -499,12 +923,17 @@ static bool pick_ln_grad(const LnGradArgs& a, int parts, cudaStream_t st, cudaEr
 }
 
 template <typename T>
-static cudaError_t ln_grad(const LnGradArgs& a, float* dw, float* db, cudaStream_t st) {
+static cudaError_t ln_grad(const LnGradArgs& a, float* dw, float* db, unsigned* status, cudaStream_t st) {
   constexpr int V = 16 / sizeof(T);
   const bool vec = a.n % V == 0 && aligned16_rows(a.x) && aligned16_rows(a.dy) && aligned16_rows(a.dres) &&
                    aligned16_rows(a.dx) && aligned16_rows(a.w);
   int parts = ln_parts(a.rows);
   cudaError_t e = cudaSuccess;
+  if (vec && (a.dres ? pick_ln_grad_ring<T, V, true>(a, &parts, status, st, &e)
+                     : pick_ln_grad_ring<T, V, false>(a, &parts, status, st, &e))) {
+    if (e != cudaSuccess || !a.part) return e;
+    return launch_column_sums(a.part, parts, 2 * static_cast<int64_t>(a.n), a.n, dw, db, st);
+  }
   if (!(vec ? pick_ln_grad<T, V>(a, parts, st, &e) : pick_ln_grad<T, 1>(a, parts, st, &e))) {
     // the column pass first: dx may be written in dy's place
     if (a.part) {
@@ -522,7 +951,7 @@ static cudaError_t ln_grad(const LnGradArgs& a, float* dw, float* db, cudaStream
   return launch_column_sums(a.part, parts, 2 * static_cast<int64_t>(a.n), a.n, dw, db, st);
 }
 
-cudaError_t launch_layernorm_grad(const LayerNormGradProblem& p, cudaStream_t st) {
+cudaError_t launch_layernorm_grad(const LayerNormGradProblem& p, unsigned* status, cudaStream_t st) {
   LnGradArgs a{};
   a.dy = p.dy;
   a.x = p.x;
@@ -535,7 +964,8 @@ cudaError_t launch_layernorm_grad(const LayerNormGradProblem& p, cudaStream_t st
   a.dx = p.dx;
   a.dx_bf16 = p.dx_bf16;
   a.part = p.dweight || p.dbias ? p.ws : nullptr;
-  return p.bf16 ? ln_grad<__nv_bfloat16>(a, p.dweight, p.dbias, st) : ln_grad<float>(a, p.dweight, p.dbias, st);
+  return p.bf16 ? ln_grad<__nv_bfloat16>(a, p.dweight, p.dbias, status, st)
+                : ln_grad<float>(a, p.dweight, p.dbias, status, st);
 }
 
 }  // namespace fp4

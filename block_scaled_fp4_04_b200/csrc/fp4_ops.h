@@ -53,7 +53,7 @@ struct LayerNormGradProblem {
   float* ws;
 };
 size_t layernorm_grad_workspace_bytes(int64_t rows, int64_t cols);
-cudaError_t launch_layernorm_grad(const LayerNormGradProblem& p, cudaStream_t st);
+cudaError_t launch_layernorm_grad(const LayerNormGradProblem& p, unsigned* status, cudaStream_t st);
 
 struct ActGradProblem {
   const void *dh, *g, *u;  // u null: a plain activation
