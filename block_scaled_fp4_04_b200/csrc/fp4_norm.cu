@@ -213,19 +213,33 @@ __device__ __forceinline__ void ring_read(RowVec<T, V>& r, const uint8_t* row, i
   r.w[3] = t.w;
 }
 
-template <typename T, int V, int WPR, int C, int FMT>
-__global__ void __launch_bounds__(kRingWarps * 32, 1) ln_forward_ring_kernel(const LnArgs p, int slots) {
-  constexpr int G = kRingWarps / WPR;
+// R rows at a time per group (a slot holds R consecutive rows): their chains of shuffles and
+// their one barrier overlap.  One barrier gives mean and variance: each warp takes the mean m_w
+// and the sum of squares about it of its own n_w columns, and the row's sum of squares is
+// sum_w M2_w + n_w (m_w - mean)^2 -- no difference of large squares.
+// A vector's elements as FP32 pairs: the paired FP32 instructions do two at once.
+template <typename T, int V>
+__device__ __forceinline__ void unpack2(const RowVec<T, V>& r, float2 (&v)[V / 2]) {
+  float t[V];
+  r.unpack(t);
+#pragma unroll
+  for (int i = 0; i < V / 2; ++i) v[i] = make_float2(t[2 * i], t[2 * i + 1]);
+}
+
+template <typename T, int V, int W, int WPR, int C, int R, int FMT>
+__global__ void __launch_bounds__(W * 32, 1) ln_forward_ring_kernel(const LnArgs p, int slots) {
+  constexpr int G = W / WPR;
   constexpr int kStep = WPR * 32 * V;
   extern __shared__ __align__(128) uint8_t s_ring[];
-  __shared__ float s_red[2][G][WPR];
+  __shared__ float2 s_stat[2][G][WPR][R];
   __shared__ volatile int s_abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int group = warp / WPR, wr = warp % WPR, bar = 1 + group;
   const int first = (wr * 32 + lane) * V;
   const uint32_t row_bytes = static_cast<uint32_t>(p.n) * sizeof(T);
   Ring ring{reinterpret_cast<uint64_t*>(s_ring) + group * kRingSlots,
-            s_ring + kRingHeader + static_cast<size_t>(group) * slots * row_bytes, row_bytes, slots, &s_abort, p.status, 0, 0};
+            s_ring + kRingHeader + static_cast<size_t>(group) * slots * R * row_bytes, R * row_bytes, slots, &s_abort, p.status,
+            0, 0};
   if (threadIdx.x == 0) {
     s_abort = 0;
     for (int i = 0; i < G * kRingSlots; ++i) mbar_init(reinterpret_cast<uint64_t*>(s_ring) + i, 1);
@@ -234,91 +248,158 @@ __global__ void __launch_bounds__(kRingWarps * 32, 1) ln_forward_ring_kernel(con
   __syncthreads();
   rows_allow_dependents();
   rows_wait_prior();
-  const int64_t stride = static_cast<int64_t>(gridDim.x) * G;
-  int64_t row = static_cast<int64_t>(blockIdx.x) * G + group;
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * G * R;
+  int64_t row = (static_cast<int64_t>(blockIdx.x) * G + group) * R;
   const bool loader = wr == 0 && lane == 0;
   const uint64_t pol = l2_policy_evict_first();
-  auto load_row = [&](int slot, int64_t r) {
-    mbar_arrive_expect_tx(&ring.full[slot], row_bytes);
-    bulk_load(ring.slot0 + static_cast<size_t>(slot) * row_bytes, static_cast<const T*>(p.x) + r * p.n, row_bytes,
+  auto load_rows = [&](int slot, int64_t r) {
+    const uint32_t bytes = static_cast<uint32_t>(min(static_cast<int64_t>(R), p.rows - r)) * row_bytes;
+    mbar_arrive_expect_tx(&ring.full[slot], bytes);
+    bulk_load(ring.slot0 + static_cast<size_t>(slot) * R * row_bytes, static_cast<const T*>(p.x) + r * p.n, bytes,
               &ring.full[slot], pol);
   };
   if (loader)
-    for (int i = 0; i < slots && row + i * stride < p.rows; ++i) load_row(i, row + i * stride);
-  float w[C][V], b[C][V];
+    for (int i = 0; i < slots && row + i * stride < p.rows; ++i) load_rows(i, row + i * stride);
+  float2 w[C][V / 2], b[C][V / 2];
+  int n_w = 0;  // columns of this warp
 #pragma unroll
   for (int j = 0; j < C; ++j) {
     const int col = first + j * kStep;
+    float tw[V], tb[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      w[j][i] = 1.0f;
-      b[j][i] = 0.0f;
+      tw[i] = 1.0f;
+      tb[i] = 0.0f;
     }
     if (col < p.n) {
-      if (p.w) load_params<V>(p.w + col, w[j]);
-      if (p.b) load_params<V>(p.b + col, b[j]);
+      if (p.w) load_params<V>(p.w + col, tw);
+      if (p.b) load_params<V>(p.b + col, tb);
     }
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) {
+      w[j][i] = make_float2(tw[2 * i], tw[2 * i + 1]);
+      b[j][i] = make_float2(tb[2 * i], tb[2 * i + 1]);
+    }
+    n_w += max(0, min(32 * V, p.n - (wr * 32 * V + j * kStep)));
   }
   const float inv_n = 1.0f / static_cast<float>(p.n);
+  const float inv_nw = n_w ? 1.0f / static_cast<float>(n_w) : 0.0f;
+  // columns of warp lane % WPR of the group, for combining the warps' statistics
+  constexpr int kEntries = WPR * R, kSets = kEntries > 32 ? kEntries / 32 : 1;
+  float lane_n = 0.0f;
+#pragma unroll
+  for (int j = 0; j < C; ++j)
+    lane_n += static_cast<float>(max(0, min(32 * V, p.n - ((lane % WPR) * 32 * V + j * kStep))));
+  const float lane_inv = lane_n > 0.0f ? 1.0f / lane_n : 0.0f;
   float g = 1.0f;
   if constexpr (FMT == kCodesNv) g = *p.q.g;
   uint32_t m = 0;
   bool bad = false;
-  for (; row < p.rows; row += stride) {
+  for (int par = 0; row < p.rows; row += stride, par ^= 1) {
     ring.wait();
-    RowVec<T, V> raw[C];
+    RowVec<T, V> raw[R][C];
+    float s[R], q[R];
 #pragma unroll
-    for (int j = 0; j < C; ++j) {
-      const int col = first + j * kStep;
-      if (col < p.n) ring_read<T, V>(raw[j], ring.row(), col);
-      else raw[j].zero();
+    for (int r = 0; r < R; ++r) {
+      float2 a[2] = {};
+#pragma unroll
+      for (int j = 0; j < C; ++j) {
+        const int col = first + j * kStep;
+        // (rows past the last one: what the slot held before; never stored)
+        if (col < p.n) ring_read<T, V>(raw[r][j], ring.row() + static_cast<size_t>(r) * row_bytes, col);
+        else raw[r][j].zero();
+        float2 v[V / 2];
+        unpack2(raw[r][j], v);
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) a[i & 1] = __fadd2_rn(a[i & 1], v[i]);
+      }
+      s[r] = (a[0].x + a[0].y) + (a[1].x + a[1].y);
     }
-    float s = 0.0f;
 #pragma unroll
-    for (int j = 0; j < C; ++j) {
-      float v[V];
-      raw[j].unpack(v);
+    for (int d = 16; d > 0; d >>= 1)
 #pragma unroll
-      for (int i = 0; i < V; ++i) s += v[i];
+      for (int r = 0; r < R; ++r) s[r] += __shfl_xor_sync(0xFFFFFFFFu, s[r], d);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const float mw = s[r] * inv_nw;
+      const float2 neg = make_float2(-mw, -mw);
+      float2 a[2] = {};
+#pragma unroll
+      for (int j = 0; j < C; ++j)
+        if (first + j * kStep < p.n) {
+          float2 v[V / 2];
+          unpack2(raw[r][j], v);
+#pragma unroll
+          for (int i = 0; i < V / 2; ++i) {
+            const float2 e = __fadd2_rn(v[i], neg);
+            a[i & 1] = __ffma2_rn(e, e, a[i & 1]);
+          }
+        }
+      q[r] = (a[0].x + a[0].y) + (a[1].x + a[1].y);
     }
-    const float mean = row_sum<WPR>(s, s_red[0][group], wr, lane, bar) * inv_n;
-    if constexpr (WPR == 1) __syncwarp();
-    if (loader && row + slots * stride < p.rows) load_row(ring.at, row + slots * stride);
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1)
+#pragma unroll
+      for (int r = 0; r < R; ++r) q[r] += __shfl_xor_sync(0xFFFFFFFFu, q[r], d);
+    if (lane == 0) {
+#pragma unroll
+      for (int r = 0; r < R; ++r) s_stat[par][group][wr][r] = make_float2(s[r], q[r]);
+    }
+    asm volatile("bar.sync %0, %1;" ::"r"(bar), "r"(WPR * 32) : "memory");
+    if (loader && row + slots * stride < p.rows) load_rows(ring.at, row + slots * stride);
     ring.next();
-    float ss = 0.0f;
+    // lane e (and e + 32, ...) holds what warp e % WPR found for row e / WPR
+    float mean[R], rstd[R];
 #pragma unroll
-    for (int j = 0; j < C; ++j)
-      if (first + j * kStep < p.n) {
-        float v[V];
-        raw[j].unpack(v);
+    for (int k = 0; k < kSets; ++k) {
+      const int e = (lane + 32 * k) % kEntries;
+      const float2 t = s_stat[par][group][e % WPR][e / WPR];
+      float sum = t.x;
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-          const float d = v[i] - mean;
-          ss += d * d;
+      for (int d = 1; d < WPR; d <<= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
+      const float mu = sum * inv_n;
+      const float dev = fmaf(t.x, lane_inv, -mu);
+      float sq = fmaf(dev * dev, lane_n, t.y);
+#pragma unroll
+      for (int d = 1; d < WPR; d <<= 1) sq += __shfl_xor_sync(0xFFFFFFFFu, sq, d);
+      const float rs = 1.0f / sqrtf(sq * inv_n + p.eps);
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+        if (r * WPR / 32 == k) {
+          mean[r] = __shfl_sync(0xFFFFFFFFu, mu, r * WPR % 32);
+          rstd[r] = __shfl_sync(0xFFFFFFFFu, rs, r * WPR % 32);
         }
-      }
-    const float var = row_sum<WPR>(ss, s_red[1][group], wr, lane, bar) * inv_n;
-    const float rstd = 1.0f / sqrtf(var + p.eps);
-    if (loader) {
-      if (p.mean) p.mean[row] = mean;
-      if (p.rstd) p.rstd[row] = rstd;
     }
 #pragma unroll
-    for (int j = 0; j < C; ++j) {
-      const int col = first + j * kStep;
-      const bool ok = col < p.n;
-      float v[V], o[V];
-      raw[j].unpack(v);
-#pragma unroll
-      for (int i = 0; i < V; ++i) o[i] = ok ? fmaf((v[i] - mean) * rstd, w[j][i], b[j][i]) : 0.0f;
-      if (ok) {
-        if (p.y) store_row_vec<V>(p.y, p.y_bf16, row * p.n + col, o);
-        if (p.amax) {
-#pragma unroll
-          for (int i = 0; i < V; ++i) m = max(m, abs_bits_of(o[i]));
-        }
+    for (int r = 0; r < R; ++r) {
+      const bool row_ok = row + r < p.rows;
+      if (loader && row_ok) {
+        if (p.mean) p.mean[row + r] = mean[r];
+        if (p.rstd) p.rstd[row + r] = rstd[r];
       }
-      if constexpr (FMT != kCodesNone) bad |= encode_row_vec<FMT, V>(p.q, g, row, col, ok, o);
+#pragma unroll
+      for (int j = 0; j < C; ++j) {
+        const int col = first + j * kStep;
+        const bool ok = row_ok && col < p.n;
+        float2 v[V / 2];
+        float o[V];
+        unpack2(raw[r][j], v);
+        const float2 neg = make_float2(-mean[r], -mean[r]), rs = make_float2(rstd[r], rstd[r]);
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) {
+          const float2 y = __ffma2_rn(__fmul2_rn(__fadd2_rn(v[i], neg), rs), w[j][i], b[j][i]);
+          o[2 * i] = ok ? y.x : 0.0f;
+          o[2 * i + 1] = ok ? y.y : 0.0f;
+        }
+        if (ok) {
+          if (p.y) store_row_vec<V>(p.y, p.y_bf16, (row + r) * p.n + col, o);
+          if (p.amax) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) m = max(m, abs_bits_of(o[i]));
+          }
+        }
+        if constexpr (FMT != kCodesNone) bad |= encode_row_vec<FMT, V>(p.q, g, row + r, col, ok, o);
+      }
     }
   }
   if (p.amax) {
@@ -343,33 +424,38 @@ static cudaError_t ring_attr(K kern, bool (&done)[64]) {
   return e;
 }
 
-template <typename T, int V, int WPR, int C, int FMT>
+template <typename T, int V, int W, int WPR, int C, int R, int FMT>
 static cudaError_t run_ln_ring(const LnArgs& a, cudaStream_t st) {
+  constexpr int G = W / WPR;
   static bool done[64] = {false};
-  const cudaError_t e = ring_attr(ln_forward_ring_kernel<T, V, WPR, C, FMT>, done);
+  const cudaError_t e = ring_attr(ln_forward_ring_kernel<T, V, W, WPR, C, R, FMT>, done);
   if (e != cudaSuccess) return e;
-  const RingPlan r = ring_plan(kRingWarps / WPR, static_cast<size_t>(a.n) * sizeof(T), a.rows);
-  return launch_rows(ln_forward_ring_kernel<T, V, WPR, C, FMT>, dim3(static_cast<unsigned>(r.grid)), kRingWarps * 32,
+  const RingPlan r = ring_plan(G, static_cast<size_t>(a.n) * sizeof(T) * R, (a.rows + R - 1) / R);
+  return launch_rows(ln_forward_ring_kernel<T, V, W, WPR, C, R, FMT>, dim3(static_cast<unsigned>(r.grid)), W * 32,
                      r.smem, st, a, r.slots);
 }
 
-// Rows and lengths the ring serves: groups whose lanes are well filled, several rows for every
-// group in the grid.
+// Rows and lengths the ring serves: BF16 rows that fill their groups' lanes, several steps for
+// every group in the grid.  Measured against a CTA per row (us): 8192 x 8192 BF16 48.8 / 60.8,
+// 16384 x 4096 48.9 / 56.4, 16384 x 2880 36.8 / 43.2, 32768 x 1024 27.9 / 28.1, 2400 x 4096
+// 10.7 / 11.4, but 1200 x 4096 6.4 / 6.1.  FP32 has half the arithmetic per byte and does not
+// need it: 4096 x 8192 49.7 / 43.6, 8192 x 2880 35.0 / 32.4.
 template <typename T, int V, int FMT>
 static bool pick_ln_ring(const LnArgs& a, cudaStream_t st, cudaError_t* e) {
-  if constexpr (V == 1) {
+  if constexpr (V != 8) {
     return false;
   } else {
     const int nch = (a.n + V - 1) / V;
-    if (a.rows < 8 * static_cast<int64_t>(num_sms()) || nch < 96 || nch > 2048) return false;
-    if (nch <= 128) *e = run_ln_ring<T, V, 2, 2, FMT>(a, st);
-    else if (nch <= 256) *e = run_ln_ring<T, V, 2, 4, FMT>(a, st);
-    else if (nch <= 384) *e = run_ln_ring<T, V, 4, 3, FMT>(a, st);
-    else if (nch <= 512) *e = run_ln_ring<T, V, 4, 4, FMT>(a, st);
-    else if (nch <= 768) *e = run_ln_ring<T, V, 8, 3, FMT>(a, st);
-    else if (nch <= 1024) *e = run_ln_ring<T, V, 8, 4, FMT>(a, st);
-    else if (nch <= 1536) *e = run_ln_ring<T, V, 16, 3, FMT>(a, st);
-    else *e = run_ln_ring<T, V, 16, 4, FMT>(a, st);
+    if (a.rows < 16 * static_cast<int64_t>(num_sms()) || nch < 96 || nch > 2048) return false;
+    if (nch <= 128) *e = run_ln_ring<T, V, 16, 2, 2, 2, FMT>(a, st);
+    else if (nch <= 192) *e = run_ln_ring<T, V, 16, 2, 3, 2, FMT>(a, st);
+    else if (nch <= 256) *e = run_ln_ring<T, V, 16, 4, 2, 2, FMT>(a, st);
+    else if (nch <= 384) *e = run_ln_ring<T, V, 16, 4, 3, 2, FMT>(a, st);
+    else if (nch <= 512) *e = run_ln_ring<T, V, 16, 8, 2, 2, FMT>(a, st);
+    else if (nch <= 768) *e = run_ln_ring<T, V, 16, 8, 3, 2, FMT>(a, st);
+    else if (nch <= 1024) *e = run_ln_ring<T, V, 16, 16, 2, 2, FMT>(a, st);
+    else if (nch <= 1536) *e = run_ln_ring<T, V, 16, 16, 3, 2, FMT>(a, st);
+    else *e = run_ln_ring<T, V, 16, 16, 4, 1, FMT>(a, st);
     return true;
   }
 }
@@ -581,7 +667,8 @@ __global__ void __launch_bounds__((WPR < 8 ? 8 : WPR) * 32) ln_backward_kernel(c
 }
 
 // The same through a ring of rows (x, dy and the residual's gradient side by side in a slot).
-template <typename T, int V, int WPR, int C, bool RES>
+// SUMS: the column sums too (else p.part is ignored).
+template <typename T, int V, int WPR, int C, bool RES, bool SUMS>
 __global__ void __launch_bounds__(kRingWarps * 32, 1) ln_backward_ring_kernel(const LnGradArgs p, int slots, unsigned* status) {
   constexpr int G = kRingWarps / WPR;
   constexpr int kStep = WPR * 32 * V;
@@ -656,8 +743,10 @@ __global__ void __launch_bounds__(kRingWarps * 32, 1) ln_backward_ring_kernel(co
 #pragma unroll
         for (int i = 0; i < V; ++i) {
           const float xh = (x[i] - mean) * rstd;
-          dw[j][i] += d[i] * xh;
-          db[j][i] += d[i];
+          if constexpr (SUMS) {
+            dw[j][i] += d[i] * xh;
+            db[j][i] += d[i];
+          }
           const float a = d[i] * w[j][i];
           s1 += a;
           s2 += a * xh;
@@ -709,52 +798,47 @@ __global__ void __launch_bounds__(kRingWarps * 32, 1) ln_backward_ring_kernel(co
     volatile int no_abort = 0;
     for (int i = 0; i < slots; ++i) mbar_wait(&ring.full[i], ring.phase ^ (i < ring.at ? 1u : 0u), &no_abort);
   }
+  if constexpr (!SUMS) return;
   if (!p.part) return;
-  // the groups' sums add up in shared memory, in the order of the groups
+  // The groups' sums meet in shared memory (within the ring, which is done with), each thread's
+  // element k a row apart, padded so that both the writes and the sums by columns are free of
+  // bank conflicts; they add up in the order of the groups.
   float* out = p.part + static_cast<int64_t>(blockIdx.x) * 2 * p.n;
-  if constexpr (G > 1) {
-    float* s_part = reinterpret_cast<float*>(s_ring);  // [2][n]: within the ring, which is done with
-    __syncthreads();
+  constexpr int kLine = WPR * 32 + 32 / V, kPlane = C * V * kLine;
+  static_assert(sizeof(float) * 2 * G * kPlane <= kRingBytes, "the groups' sums fit the ring");
+  float* s_part = reinterpret_cast<float*>(s_ring);
+  __syncthreads();
+#pragma unroll
+  for (int j = 0; j < C; ++j)
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      float* at = s_part + 2 * group * kPlane + (j * V + i) * kLine + wr * 32 + lane;
+      at[0] = dw[j][i];
+      at[kPlane] = db[j][i];
+    }
+  __syncthreads();
+  for (int c = threadIdx.x; c < p.n; c += kRingWarps * 32) {
+    const float* at = s_part + ((c / kStep) * V + c % V) * kLine + c % kStep / V;
+    float vw = 0.0f, vb = 0.0f;
+#pragma unroll
     for (int gi = 0; gi < G; ++gi) {
-      if (group == gi) {
-#pragma unroll
-        for (int j = 0; j < C; ++j)
-#pragma unroll
-          for (int i = 0; i < V; ++i) {
-            const int col = first + j * kStep + i;
-            if (col < p.n) {
-              s_part[col] = gi ? s_part[col] + dw[j][i] : dw[j][i];
-              s_part[p.n + col] = gi ? s_part[p.n + col] + db[j][i] : db[j][i];
-            }
-          }
-      }
-      __syncthreads();
+      vw += at[2 * gi * kPlane];
+      vb += at[(2 * gi + 1) * kPlane];
     }
-    for (int c = threadIdx.x; c < 2 * p.n; c += kRingWarps * 32) out[c] = s_part[c];
-  } else {
-#pragma unroll
-    for (int j = 0; j < C; ++j) {
-      const int col = first + j * kStep;
-      if (col < p.n) {
-#pragma unroll
-        for (int i = 0; i < V; i += 4) {
-          *reinterpret_cast<float4*>(out + col + i) = make_float4(dw[j][i], dw[j][i + 1], dw[j][i + 2], dw[j][i + 3]);
-          *reinterpret_cast<float4*>(out + p.n + col + i) =
-              make_float4(db[j][i], db[j][i + 1], db[j][i + 2], db[j][i + 3]);
-        }
-      }
-    }
+    out[c] = vw;
+    out[p.n + c] = vb;
   }
 }
 
-template <typename T, int V, int WPR, int C, bool RES>
+template <typename T, int V, int WPR, int C, bool RES, bool SUMS = true>
 static cudaError_t run_ln_grad_ring(const LnGradArgs& a, int* parts, unsigned* status, cudaStream_t st) {
   static bool done[64] = {false};
-  const cudaError_t e = ring_attr(ln_backward_ring_kernel<T, V, WPR, C, RES>, done);
+  const cudaError_t e = ring_attr(ln_backward_ring_kernel<T, V, WPR, C, RES, SUMS>, done);
   if (e != cudaSuccess) return e;
-  const RingPlan r = ring_plan(kRingWarps / WPR, static_cast<size_t>(a.n) * sizeof(T) * (RES ? 3 : 2), a.rows);
+  RingPlan r = ring_plan(kRingWarps / WPR, static_cast<size_t>(a.n) * sizeof(T) * (RES ? 3 : 2), a.rows);
+  r.smem = kRingHeader + kRingBytes;  // the groups' sums may take more than the slots
   *parts = r.grid;
-  return launch_rows(ln_backward_ring_kernel<T, V, WPR, C, RES>, dim3(static_cast<unsigned>(r.grid)), kRingWarps * 32,
+  return launch_rows(ln_backward_ring_kernel<T, V, WPR, C, RES, SUMS>, dim3(static_cast<unsigned>(r.grid)), kRingWarps * 32,
                      r.smem, st, a, r.slots, status);
 }
 
@@ -828,30 +912,53 @@ __global__ void __launch_bounds__(512) ln_backward_long_kernel(const LnGradArgs 
   }
 }
 
-constexpr int kLongCols = 128;  // columns per CTA of the column pass
+constexpr int kLongWarps = 8;
 
-template <typename T>
-__global__ void __launch_bounds__(kLongCols) ln_columns_long_kernel(const LnGradArgs p, int64_t rows_per_part) {
+// A CTA takes 32 V columns and a slab of rows; warp w the slab's rows w, w + 8, ...
+template <typename T, int V>
+__global__ void __launch_bounds__(kLongWarps * 32) ln_columns_long_kernel(const LnGradArgs p, int64_t rows_per_part) {
+  __shared__ float s_sum[kLongWarps][2][V][32];
   rows_allow_dependents();
   rows_wait_prior();
-  const int col = blockIdx.x * kLongCols + threadIdx.x;
-  if (col >= p.n) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int col = (blockIdx.x * 32 + lane) * V;
   const int64_t r0 = static_cast<int64_t>(blockIdx.y) * rows_per_part;
   const int64_t r1 = min(p.rows, r0 + rows_per_part);
-  float dw = 0.0f, db = 0.0f;
-  for (int64_t r = r0; r < r1; ++r) {
-    RowVec<T, 1> rx, rd;
-    float x[1], d[1];
-    rx.load(static_cast<const T*>(p.x) + r * p.n + col);
-    rd.load(static_cast<const T*>(p.dy) + r * p.n + col);
-    rx.unpack(x);
-    rd.unpack(d);
-    dw += d[0] * ((x[0] - __ldg(p.mean + r)) * __ldg(p.rstd + r));
-    db += d[0];
+  float dw[V], db[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) dw[i] = db[i] = 0.0f;
+  if (col < p.n) {
+#pragma unroll 4
+    for (int64_t r = r0 + warp; r < r1; r += kLongWarps) {
+      RowVec<T, V> rx, rd;
+      float x[V], d[V];
+      rx.load(static_cast<const T*>(p.x) + r * p.n + col);
+      rd.load(static_cast<const T*>(p.dy) + r * p.n + col);
+      const float mean = __ldg(p.mean + r), rstd = __ldg(p.rstd + r);
+      rx.unpack(x);
+      rd.unpack(d);
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        dw[i] += d[i] * ((x[i] - mean) * rstd);
+        db[i] += d[i];
+      }
+    }
   }
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    s_sum[warp][0][i][lane] = dw[i];
+    s_sum[warp][1][i][lane] = db[i];
+  }
+  __syncthreads();
   float* out = p.part + static_cast<int64_t>(blockIdx.y) * 2 * p.n;
-  out[col] = dw;
-  out[p.n + col] = db;
+  for (int t = threadIdx.x; t < 2 * 32 * V; t += kLongWarps * 32) {
+    const int h = t / (32 * V), k = t % (32 * V), c = blockIdx.x * 32 * V + k;
+    if (c >= p.n) continue;
+    float v = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kLongWarps; ++w) v += s_sum[w][h][k % V][k / V];
+    out[static_cast<int64_t>(h) * p.n + c] = v;
+  }
 }
 
 // ------------------------------------------------------------------ column sums
@@ -913,6 +1020,16 @@ template <typename T, int V>
 static bool pick_ln_grad(const LnGradArgs& a, int parts, cudaStream_t st, cudaError_t* e) {
   const int nch = (a.n + V - 1) / V;
   constexpr int C = V == 8 ? 2 : 4;  // at most 16 columns per thread
+  if constexpr (V == 1) {
+    if (nch > 2048 && nch <= 4096) {
+      *e = run_ln_grad<T, V, 16, 8>(a, parts, st);
+      return true;
+    }
+    if (nch > 4096 && nch <= 8192) {
+      *e = run_ln_grad<T, V, 16, 16>(a, parts, st);
+      return true;
+    }
+  }
   if (nch <= 32) *e = run_ln_grad<T, V, 1, 1>(a, parts, st);
   else if (nch <= 32 * C) *e = run_ln_grad<T, V, 1, C>(a, parts, st);
   else if (nch <= 128 * C) *e = run_ln_grad<T, V, 4, C>(a, parts, st);
@@ -937,15 +1054,23 @@ static cudaError_t ln_grad(const LnGradArgs& a, float* dw, float* db, unsigned* 
   if (!(vec ? pick_ln_grad<T, V>(a, parts, st, &e) : pick_ln_grad<T, 1>(a, parts, st, &e))) {
     // the column pass first: dx may be written in dy's place
     if (a.part) {
-      const int tiles = (a.n + kLongCols - 1) / kLongCols;
-      parts = static_cast<int>(std::min<int64_t>(parts, std::max(1, 4 * num_sms() / tiles)));
+      const int cols = 32 * (vec ? V : 1), tiles = (a.n + cols - 1) / cols;
+      parts = static_cast<int>(std::min<int64_t>(parts, std::max(1, 8 * num_sms() / tiles)));
       const int64_t per = (a.rows + parts - 1) / parts;
       parts = static_cast<int>((a.rows + per - 1) / per);
-      e = launch_rows(ln_columns_long_kernel<T>, dim3(static_cast<unsigned>(tiles), static_cast<unsigned>(parts)),
-                      kLongCols, 0, st, a, per);
+      const dim3 grid(static_cast<unsigned>(tiles), static_cast<unsigned>(parts));
+      e = vec ? launch_rows(ln_columns_long_kernel<T, V>, grid, kLongWarps * 32, 0, st, a, per)
+              : launch_rows(ln_columns_long_kernel<T, 1>, grid, kLongWarps * 32, 0, st, a, per);
     }
-    if (e == cudaSuccess)
-      e = launch_rows(ln_backward_long_kernel<T>, dim3(static_cast<unsigned>(a.rows)), 512, 0, st, a);
+    if (e == cudaSuccess) {
+      int ctas = 0;
+      // up to 2048 words: the ring without the sums; longer or unaligned rows are read twice
+      if (vec && a.n / V <= 2048 && a.rows >= 2 * static_cast<int64_t>(num_sms()))
+        e = a.dres ? run_ln_grad_ring<T, V, 16, 4, true, false>(a, &ctas, status, st)
+                   : run_ln_grad_ring<T, V, 16, 4, false, false>(a, &ctas, status, st);
+      else
+        e = launch_rows(ln_backward_long_kernel<T>, dim3(static_cast<unsigned>(a.rows)), 512, 0, st, a);
+    }
   }
   if (e != cudaSuccess || !a.part) return e;
   return launch_column_sums(a.part, parts, 2 * static_cast<int64_t>(a.n), a.n, dw, db, st);

@@ -53,7 +53,8 @@ def _ln_error(x, w, y, mean, rstd, var, n):
 LN_SHAPES = [(1, 1), (3, 7), (5, 32), (130, 256), (2, 513), (7, 1000), (16, 2880), (33, 8192), (9, 5760), (3, 16384),
              (2, 28672), (4, 12289), (300, 64), (1, 20011),
              # enough rows for the rings
-             (1187, 800), (1200, 1032), (1500, 2048), (1184, 2880), (1190, 5760), (1185, 8192)]
+             (2387, 800), (2400, 1032), (2500, 2048), (2370, 2880), (2369, 5760), (2371, 4096), (2368, 8192),
+             (2369, 16384)]
 
 
 @pytest.mark.parametrize("rows,n", LN_SHAPES)
@@ -95,7 +96,7 @@ def test_layernorm_of_constant_and_shifted_rows():
 
 @pytest.mark.parametrize("fmt", [fp4.NVFP4, fp4.MXFP4])
 @pytest.mark.parametrize("rows,n", [(1, 32), (130, 288), (128, 1024), (37, 2880), (5, 8192), (3, 20000),
-                                    (1190, 2880), (1200, 1024)])
+                                    (2400, 2880), (2371, 1024)])
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 def test_layernorm_codes(fmt, rows, n, dtype):
     """The codes are those of quantizing the FP32 y that the same call stores; pads are 0."""
@@ -141,7 +142,7 @@ def _ln_grad64(dy, x, w, mean, rstd, dres):
 @pytest.mark.parametrize("rows,n", [(1, 1), (3, 7), (700, 32), (130, 256), (513, 513), (7, 1000), (301, 2880), (33, 8192),
                                     (5, 16384), (2, 28672), (600, 64), (3, 12289), (149, 5760),
                                     (1187, 800), (1200, 1032), (1500, 2048), (1184, 2880), (1190, 5760),
-                                    (1185, 8192)])
+                                    (1185, 8192), (300, 16384), (700, 2881), (20, 5003), (300, 16400)])
 @pytest.mark.parametrize("dtype,out", [(torch.float32, torch.float32), (torch.bfloat16, torch.bfloat16),
                                        (torch.bfloat16, torch.float32)])
 @pytest.mark.parametrize("res", [True, False])
