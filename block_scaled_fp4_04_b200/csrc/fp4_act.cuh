@@ -43,7 +43,7 @@ constexpr float kInvSqrt2Pi = 0.39894228040143268f;
 // of Mathematical Functions (error at most 1.5e-7; 2.6e-7 in all in FP32).  Half the instructions of erff, no branch,
 // and no 1 + erf of nearly -1 for x << 0.
 __device__ __forceinline__ float normal_cdf(float x, float& e) {
-  const float z = fminf(fabsf(x) * kSqrtHalf, 16.0f);  // beyond, e is 0
+  const float z = fabsf(x) * kSqrtHalf;
   const float t = rcp_sfu(fmaf(0.3275911f, z, 1.0f));
   e = exp2_sfu(z * z * -kLog2e);
   float p = fmaf(t, 1.061405429f, -1.453152027f);
@@ -88,6 +88,35 @@ __device__ __forceinline__ float act_slope(float x, float& value) {
   } else {
     value = x;
     return 1.0f;
+  }
+}
+
+// Two values at once: the paired FP32 instructions do the arithmetic around the special
+// functions, which take one value each.
+__device__ __forceinline__ float2 pair(float v) { return make_float2(v, v); }
+template <int ACT>
+__device__ __forceinline__ float2 act_value2(float2 x) {
+  if constexpr (ACT == kActSilu || ACT == kActGeluTanh) {
+    float2 y;
+    if constexpr (ACT == kActSilu) y = __fmul2_rn(x, pair(-kLog2e));
+    else y = __fmul2_rn(x, __ffma2_rn(__fmul2_rn(x, x), pair(-kLog2e * kGelu2C * kGeluA), pair(-kLog2e * kGelu2C)));
+    const float2 d = __fadd2_rn(make_float2(exp2_sfu(y.x), exp2_sfu(y.y)), pair(1.0f));
+    return __fmul2_rn(x, make_float2(rcp_sfu(d.x), rcp_sfu(d.y)));
+  } else if constexpr (ACT == kActGelu) {  // as normal_cdf
+    const float2 z = make_float2(fabsf(x.x), fabsf(x.y));
+    const float2 d = __ffma2_rn(z, pair(0.3275911f * kSqrtHalf), pair(1.0f));
+    const float2 t = make_float2(rcp_sfu(d.x), rcp_sfu(d.y));
+    const float2 y = __fmul2_rn(__fmul2_rn(x, x), pair(-0.5f * kLog2e));
+    const float2 e = make_float2(exp2_sfu(y.x), exp2_sfu(y.y));
+    float2 p = __ffma2_rn(t, pair(0.5f * 1.061405429f), pair(0.5f * -1.453152027f));
+    p = __ffma2_rn(t, p, pair(0.5f * 1.421413741f));
+    p = __ffma2_rn(t, p, pair(0.5f * -0.284496736f));
+    p = __ffma2_rn(t, p, pair(0.5f * 0.254829592f));
+    const float2 half = __fmul2_rn(__fmul2_rn(p, t), e);
+    const float2 rest = __ffma2_rn(half, pair(-1.0f), pair(1.0f));
+    return __fmul2_rn(x, make_float2(x.x < 0.0f ? half.x : rest.x, x.y < 0.0f ? half.y : rest.y));
+  } else {
+    return make_float2(act_value<ACT>(x.x), act_value<ACT>(x.y));
   }
 }
 

@@ -52,7 +52,7 @@ __global__ void __launch_bounds__(kAgWarps * 32) act_grad_kernel(const ActGradAr
   if constexpr (FMT == kCodesNv) gs = *p.q.g;
   uint32_t m = 0;
   bool bad = false;
-  with_act(p.act, [&](auto tag) {
+  with_act(p.act, [&](auto tag) __attribute__((always_inline)) {
     constexpr int A = decltype(tag)::value;
     for (int64_t r = r0 + warp; r < r1; r += kAgWarps * U) {
       RowVec<T, V> rd[U], rg[U], ru[U];

@@ -187,7 +187,7 @@ __device__ __forceinline__ void d_finish(const DecodeArgs& p, int row, float sca
       if (GATED && p.pre2) d_store_to(p, p.pre2, row, j, u[j]);
     }
   }
-  with_act(p.act, [&](auto tag) {
+  with_act(p.act, [&](auto tag) __attribute__((always_inline)) {
     constexpr int A = decltype(tag)::value;
 #pragma unroll
     for (int j = 0; j < BN; ++j) v[j] = GATED ? act_value<A>(v[j]) * u[j] : act_value<A>(v[j]);

@@ -141,8 +141,7 @@ int launch_gated(const GatedProblem& g, unsigned* status, cudaStream_t st, const
   a.status = status;
   a.bias = g.bias_g;
   a.bias2 = g.bias_u;
-  // whole tiles start at multiples of 128 columns, experts at multiples of F
-  a.vec_bias = al(g.bias_g) && al(g.bias_u) && (!grouped || g.F % 4 == 0);
+  a.bias_any = g.bias_g || g.bias_u;
   a.act = g.act;
   a.pre = g.G;
   a.pre2 = g.U;

@@ -401,7 +401,7 @@ int launch_gemm_full(const GemmProblemFull& g, unsigned* status, cudaStream_t st
     auto al32 = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31) == 0; };
     a.sectors = (g.N * esz) % 32 == 0 && al32(g.D) && al32(a.pre) &&
                 (!a.res || ((g.N * (a.res_bf16 ? 2 : 4)) % 32 == 0 && al32(a.res)));
-    a.vec_bias = (reinterpret_cast<uintptr_t>(a.bias) & 15) == 0;
+    a.bias_any = a.bias != nullptr;
     e = dispatch_full(pl, g.mx, tm, a, st);
   } else {
     e = g.mx ? dispatch<true>(pl, tm, a, st) : dispatch<false>(pl, tm, a, st);

@@ -55,7 +55,7 @@ struct GemmArgs {
   // kEpiFull, kEpiGated
   const void* res;       // [M, N] added after the activation, or null
   int res_bf16;
-  int vec_bias;          // biases are 16-byte aligned
+  int bias_any;          // a bias is given
   int sectors;           // rows of the output, its copies and the residual start at 32-byte sectors
   void* pre;             // kEpiFull: the pre-activation; kEpiGated: G; [M, N] in the output type, or null
   void* pre2;            // kEpiGated: U
@@ -209,15 +209,16 @@ struct Cfg {
   // scale factors into TMEM, so that these copies are not serialised behind the MMA
   // thread's own MMAs: one for A's atoms and one per 128-row block of B's.
   static constexpr bool kSepCp = kP == 1;
-  static constexpr bool kLong = kSepCp && EPI != kEpiPlain;
-  // (long epilogues: 20 warps of 96 registers; the MMA thread copies the second row-block's)
-  static constexpr int kCopiers = !kSepCp ? 0 : 1 + (BN >= 128 ? BN / 128 : 1);
+  static constexpr int kCopiers = kSepCp ? 1 + (BN >= 128 ? BN / 128 : 1) : 0;
   // One-pipeline kernels run two epilogue warps per TMEM lane quarter, one per column
   // half: twice the TMEM read and store rate, and half a row of packed BF16 per thread
   // is few enough registers to hold the tile while TMEM is already handed back.
-  // The long epilogues hold their sums in FP32 while TMEM is handed back: four warps per
-  // quarter, 64 sums per thread and as many more warps to hide their arithmetic and loads.
-  static constexpr int kEpiWarps = kSepCp ? 8 : 4;
+  // The long epilogues have too much arithmetic for that: four warps per quarter, which take 32
+  // sums at a time and hold the last 32 (half of the tile) while TMEM is handed back.  Measured
+  // on tiles of one K step (8192 x 8192 outputs, BF16): SILU 88 us with eight warps that held all
+  // their 128 sums at 128 registers, 83 us so, with bias, GELU, residual and pre-activation 276 / 175.
+  static constexpr bool kLong = kSepCp && EPI != kEpiPlain;
+  static constexpr int kEpiWarps = kLong ? 16 : kSepCp ? 8 : 4;
   static constexpr int kEpiCols = BN * 4 / kEpiWarps;  // accumulator columns per epilogue thread
   static constexpr int kTileCols = EPI == kEpiGated ? BN / 2 : BN;  // output columns of a tile
   static constexpr int kThreads = kSepCp ? 64 + 32 * kEpiWarps + 32 * kCopiers : 192 * kP;
@@ -232,7 +233,9 @@ struct Cfg {
   static constexpr int kStageBytes = (kABytes + kBBytes + kSFABytes + kSFBBytes + 1023) / 1024 * 1024;
   // grouped schedules use 128-wide tiles only, so multi-pipeline kernels skip the group tables
   static constexpr int kGroupBytes = kP == 1 ? (PAIR ? 3 : 2) * (kMaxGroups + 1) * 4 : 0;
-  static constexpr int kMiscBytes = 1024 /*barriers, flags*/ + kGroupBytes;
+  // long epilogues: two tiles' biases (gated: gate's and up's)
+  static constexpr int kBiasOff = (1024 /*barriers, flags*/ + kGroupBytes + 15) / 16 * 16;
+  static constexpr int kMiscBytes = kLong ? kBiasOff + 2 * BN * 4 : 1024 + kGroupBytes;
   // the opt-in limit per block, less the alignment slack and the static shared memory
   static constexpr int kSmemLimit = 227 * 1024 - 1024 - 256;
   static constexpr int kStagesFit = (kSmemLimit / kP - kMiscBytes) / kStageBytes;
@@ -402,6 +405,8 @@ __device__ __forceinline__ void take_sums16(float* row, int col, int n, float sc
   }
 }
 
+__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+
 // One 32-byte sector, 32-byte aligned.
 __device__ __forceinline__ void st_sector(void* p, const uint32_t (&w)[8]) {
   asm volatile("st.global.L1::no_allocate.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(w[0]), "r"(w[1]),
@@ -429,24 +434,6 @@ __device__ __forceinline__ void store_vec16(void* out, int bf16, int64_t at, con
   }
 }
 
-// v[j] += b[j], 8 FP32 parameters (every row of the tile reads the same ones).
-__device__ __forceinline__ void add_vec8(const float* b, int vec, float (&v)[8]) {
-  if (vec) {
-    const float4 x = __ldg(reinterpret_cast<const float4*>(b)), y = __ldg(reinterpret_cast<const float4*>(b) + 1);
-    v[0] = __fadd_rn(v[0], x.x);
-    v[1] = __fadd_rn(v[1], x.y);
-    v[2] = __fadd_rn(v[2], x.z);
-    v[3] = __fadd_rn(v[3], x.w);
-    v[4] = __fadd_rn(v[4], y.x);
-    v[5] = __fadd_rn(v[5], y.y);
-    v[6] = __fadd_rn(v[6], y.z);
-    v[7] = __fadd_rn(v[7], y.w);
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = __fadd_rn(v[j], __ldg(b + j));
-  }
-}
-
 // 8 consecutive elements at offset `at` of a BF16 or FP32 matrix, 16-byte aligned.
 __device__ __forceinline__ void store_vec8(void* out, int bf16, int64_t at, const float (&v)[8]) {
   if (bf16) {
@@ -470,70 +457,108 @@ __device__ __forceinline__ void load_res16(const GemmArgs& p, int64_t at, uint32
   }
 }
 
-// The long epilogues' whole tiles: OUT consecutive columns of one row whose sums are in
-// registers (gated: rr holds the gate sums, then the up sums).  Every row is read and written in
-// whole 32-byte sectors: a thread's 16-byte pieces of its own row, half a sector each, slowed the
-// whole kernel down (8192 x 4096 x 4096 gated with G and U: 216 us against 189).
-template <int ACT, bool GATED, int OUT>
-__device__ __forceinline__ void epi_rows(const GemmArgs& p, int row, int col0, int group, float scale, float scale2,
-                                         const uint32_t (&rr)[GATED ? 2 * OUT : OUT], uint32_t& tmax) {
-  const int64_t at = static_cast<int64_t>(row) * p.ldo + col0;
-  const float* bias = p.bias ? p.bias + group * p.bias_group + col0 : nullptr;
-  const float* bias2 = GATED && p.bias2 ? p.bias2 + group * p.bias_group + col0 : nullptr;
-  uint32_t res[16];  // the next 16 residual elements, loaded one step ahead
-  if (!GATED && p.res) load_res16(p, at, res);
+// Stores 8 values; BF16 in two calls (h = 0, 8) that fill one 32-byte sector of w.
+template <bool BF16>
+__device__ __forceinline__ void put8(void* out, int64_t at, int h, uint32_t (&w)[8], const float2 (&v)[4]) {
+  if constexpr (BF16) {
 #pragma unroll
-  for (int c = 0; c < OUT; c += 16) {
-    float z[16];
-    uint32_t pw[8], pw2[8];
+    for (int j = 0; j < 4; ++j) w[h / 2 + j] = pack_bf16x2(v[j].x, v[j].y);
+    if (h == 8) st_sector(static_cast<__nv_bfloat16*>(out) + at, w);
+  } else {
+    uint32_t f[8];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      f[2 * j] = __float_as_uint(v[j].x);
+      f[2 * j + 1] = __float_as_uint(v[j].y);
+    }
+    st_sector(static_cast<float*>(out) + at + h, f);
+  }
+}
+
+// 8 sums of a product, scaled, plus the bias (in shared memory, or null).
+__device__ __forceinline__ void linear8(const uint32_t* sums, float scale, const float* bias, float2 (&v)[4]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    v[j] = __fmul2_rn(make_float2(__uint_as_float(sums[2 * j]), __uint_as_float(sums[2 * j + 1])), pair(scale));
+  if (bias) {
+    const float4 x = reinterpret_cast<const float4*>(bias)[0], y = reinterpret_cast<const float4*>(bias)[1];
+    v[0] = __fadd2_rn(v[0], make_float2(x.x, x.y));
+    v[1] = __fadd2_rn(v[1], make_float2(x.z, x.w));
+    v[2] = __fadd2_rn(v[2], make_float2(y.x, y.y));
+    v[3] = __fadd2_rn(v[3], make_float2(y.z, y.w));
+  }
+}
+
+// The long epilogues' whole tiles: 16 consecutive columns of one row whose sums are in registers
+// (gated: 16 gate sums, then 16 up sums).  Every row is read and written in whole 32-byte
+// sectors: a thread's 16-byte pieces of its own row, half a sector each, slowed the whole kernel
+// down (8192 x 4096 x 4096 gated with G and U: 216 us against 189).  Copies of the
+// pre-activations are made in passes of their own: the sums are scaled again rather than kept
+// twice.
+template <int ACT, bool GATED, bool BF16>
+__device__ __forceinline__ void epi_rows(const GemmArgs& p, int row, int col, const float* bias, const float* bias2,
+                                         float scale, float scale2, uint32_t* sums, uint32_t& tmax) {
+  const int64_t at = static_cast<int64_t>(row) * p.ldo + col;
+  uint32_t w[8], res[16];
+  if (!GATED && p.res) load_res16(p, at, res);
+  if (p.pre) {
 #pragma unroll
     for (int h = 0; h < 16; h += 8) {
-      float v[8], u[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        v[j] = __uint_as_float(rr[c + h + j]) * scale;
-        if (GATED) u[j] = __uint_as_float(rr[(GATED ? OUT : 0) + c + h + j]) * scale2;
-      }
-      if (bias) add_vec8(bias + c + h, p.vec_bias, v);
-      if (GATED && bias2) add_vec8(bias2 + c + h, p.vec_bias, u);
-      if (p.pre) {
-        if (p.out_bf16) {
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            pw[h / 2 + j] = pack_bf16x2(v[2 * j], v[2 * j + 1]);
-            if (GATED) pw2[h / 2 + j] = pack_bf16x2(u[2 * j], u[2 * j + 1]);
-          }
-        } else {
-          store_vec8(p.pre, p.out_bf16, at + c + h, v);
-          if (GATED) store_vec8(p.pre2, p.out_bf16, at + c + h, u);
-        }
-      }
-#pragma unroll
-      for (int j = 0; j < 8; ++j) z[h + j] = GATED ? act_value<ACT>(v[j]) * u[j] : act_value<ACT>(v[j]);
+      float2 v[4];
+      linear8(sums + h, scale, bias ? bias + h : nullptr, v);
+      put8<BF16>(p.pre, at, h, w, v);
     }
-    if (p.pre && p.out_bf16) {
-      st_sector(static_cast<__nv_bfloat16*>(p.pre) + at + c, pw);
-      if (GATED) st_sector(static_cast<__nv_bfloat16*>(p.pre2) + at + c, pw2);
+    if constexpr (GATED) {
+#pragma unroll
+      for (int h = 0; h < 16; h += 8) {
+        float2 v[4];
+        linear8(sums + 16 + h, scale2, bias2 ? bias2 + h : nullptr, v);
+        put8<BF16>(p.pre2, at, h, w, v);
+      }
     }
-    if (!GATED && p.res) {
+  }
+#pragma unroll
+  for (int h = 0; h < 16; h += 8) {
+    float2 v[4];
+    linear8(sums + h, scale, bias ? bias + h : nullptr, v);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = act_value2<ACT>(v[j]);
+    if constexpr (GATED) {
+      float2 u[4];
+      linear8(sums + 16 + h, scale2, bias2 ? bias2 + h : nullptr, u);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] = __fmul2_rn(v[j], u[j]);
+    } else if (p.res) {
       if (p.res_bf16) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          z[2 * j] += __uint_as_float(res[j] << 16);
-          z[2 * j + 1] += __uint_as_float(res[j] & 0xFFFF0000u);
-        }
+        for (int j = 0; j < 4; ++j)
+          v[j] = __fadd2_rn(v[j], make_float2(__uint_as_float(res[h / 2 + j] << 16),
+                                              __uint_as_float(res[h / 2 + j] & 0xFFFF0000u)));
       } else {
 #pragma unroll
-        for (int j = 0; j < 16; ++j) z[j] += __uint_as_float(res[j]);
+        for (int j = 0; j < 4; ++j)
+          v[j] = __fadd2_rn(v[j], make_float2(__uint_as_float(res[h + 2 * j]), __uint_as_float(res[h + 2 * j + 1])));
       }
-      if (c + 16 < OUT) load_res16(p, at + c + 16, res);
     }
-    if (p.out) store_vec16(p.out, p.out_bf16, at + c, z);
-    if (p.q_codes) epi_quantize16(p, row, col0 + c, z);
+    if (p.out) put8<BF16>(p.out, at, h, w, v);
     if (p.amax_out) {
 #pragma unroll
-      for (int j = 0; j < 16; ++j) tmax = max(tmax, __float_as_uint(z[j]) & 0x7FFFFFFFu);
+      for (int j = 0; j < 4; ++j)
+        tmax = max(tmax, max(__float_as_uint(v[j].x) & 0x7FFFFFFFu, __float_as_uint(v[j].y) & 0x7FFFFFFFu));
     }
+    if (p.q_codes) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        sums[h + 2 * j] = __float_as_uint(v[j].x);
+        sums[h + 2 * j + 1] = __float_as_uint(v[j].y);
+      }
+    }
+  }
+  if (p.q_codes) {
+    float z[16];
+#pragma unroll
+    for (int j = 0; j < 16; ++j) z[j] = __uint_as_float(sums[j]);
+    epi_quantize16(p, row, col, z);
   }
 }
 
@@ -599,7 +624,7 @@ __device__ __forceinline__ void epi_finish16(const GemmArgs& p, int row, int col
   if (GATED && p.bias2) add_bias16(p, p.bias2 + group * p.bias_group, row, col, u);
   if (p.pre) store_like_out(p, p.pre, row, col, v);
   if (GATED && p.pre2) store_like_out(p, p.pre2, row, col, u);
-  with_act(p.act, [&](auto tag) {
+  with_act(p.act, [&](auto tag) __attribute__((always_inline)) {
     constexpr int A = decltype(tag)::value;
 #pragma unroll
     for (int j = 0; j < 16; ++j) v[j] = GATED ? act_value<A>(v[j]) * u[j] : act_value<A>(v[j]);
@@ -938,23 +963,6 @@ __global__ void __launch_bounds__(Cfg<BN, MX, ACC, PAIR, F8, EPI>::kThreads, 1)
               ok = false;
               break;
             }
-            if constexpr (false) {
-              // the second row-block's atoms: copied here, in order before this stage's MMAs
-              if (!mbar_wait(&sf_landed[stage], phase, s_abort)) {
-                latch_timeout(s_abort, p.status);
-                ok = false;
-                break;
-              }
-              tc_fence_after();
-              const int atoms = min(C::kAtomsKT, p.sf_atoms_k - kb * C::kAtomsKT);
-              for (int a = 0; a < atoms; ++a) {
-                const uint64_t sd = smem_desc_sf(st + C::kABytes + C::kBBytes + C::kSFABytes + (C::kAtomsKT + a) * 512);
-                if constexpr (PAIR)
-                  tc_cp_sf_atom_pair(sfb_t + (a * C::kNRB + 1) * 4, sd);
-                else
-                  tc_cp_sf_atom(sfb_t + (a * C::kNRB + 1) * 4, sd);
-              }
-            }
             tc_fence_after();
           } else {
             tc_fence_after();
@@ -1120,6 +1128,25 @@ __global__ void __launch_bounds__(Cfg<BN, MX, ACC, PAIR, F8, EPI>::kThreads, 1)
     while (sch.next(w)) {
       const int acc = iter % ACC;
       const uint32_t par = (iter / ACC) & 1;
+      if constexpr (C::kLong && !kGated) {
+        // this thread's piece of the residual comes into L2 while the tile is being multiplied
+        if (p.res && p.mode != kModeStreamK && rl < w.rows_valid && w.n0 + c0 < p.Nk) {
+          const int64_t at = static_cast<int64_t>(w.out_row0 + rl) * p.ldo + w.n0 + c0;
+          const uint8_t* r = static_cast<const uint8_t*>(p.res) + at * (p.res_bf16 ? 2 : 4);
+          prefetch_l2(r);
+          if (!p.res_bf16 && w.n0 + c0 + 32 < p.Nk) prefetch_l2(r + 128);
+        }
+      }
+      float* const s_bias = reinterpret_cast<float*>(misc + (C::kLong ? C::kBiasOff : 0)) + (iter & 1) * BN;
+      if constexpr (C::kLong) {
+        // the tile's biases, before the barrier below (two buffers: a warp may still read the
+        // last tile's, but not the one's before)
+        if (et < BN && p.bias_any) {
+          const float* b = kGated && et >= BN / 2 ? p.bias2 : p.bias;
+          const int col = w.n0 + (kGated ? et % (BN / 2) : et);
+          s_bias[et] = b && col < p.Nk ? __ldg(b + w.group * p.bias_group + col) : 0.0f;
+        }
+      }
       // the epilogue warps decide together whether to go on, so that none of them
       // is left behind at a named barrier
       if (et == 0 && !mbar_wait(&acc_full[acc], par, s_abort)) {
@@ -1139,25 +1166,40 @@ __global__ void __launch_bounds__(Cfg<BN, MX, ACC, PAIR, F8, EPI>::kThreads, 1)
       bool released = false;
       if constexpr (EPI != kEpiPlain) {
         if (C::kLong && p.mode != kModeStreamK && p.sectors && w.n0 + C::kTileCols <= p.Nk) {
-          // whole tiles: the accumulator half goes into registers and TMEM back to the MMA
-          // thread; everything else overlaps the next tile's MMAs
-          constexpr int kOut = kGated ? CH / 2 : CH;   // output columns of this thread
+          // whole tiles, 32 sums per thread at a time; the last 32 are in registers when TMEM goes
+          // back to the MMA thread, so that their work overlaps the next tile's MMAs
+          constexpr int kOut = kGated ? 16 : 32;       // output columns per step
           const int oc = kGated ? c0 / 2 : c0;
-          uint32_t rr[CH];  // gated: the gate sums, then the up sums
-          if (q * 32 < w.rows_valid) {  // warp-uniform
-#pragma unroll
-            for (int b = 0; b < CH; b += 32)
-              tmem_ld32(taddr + (kGated ? (b < CH / 2 ? oc + b : BN / 2 + oc + b - CH / 2) : c0 + b), rr + b);
+#pragma unroll 1
+          for (int b = 0; b < CH / 32; ++b) {
+            uint32_t rr[32];
+            const int o = oc + b * kOut;
+            // (warps without a valid row read TMEM all the same: the loads stay convergent)
+            if constexpr (kGated) {
+              tmem_ld16(taddr + o, *reinterpret_cast<uint32_t(*)[16]>(rr));
+              tmem_ld16(taddr + BN / 2 + o, *reinterpret_cast<uint32_t(*)[16]>(rr + 16));
+            } else {
+              tmem_ld32(taddr + o, rr);
+            }
             tmem_ld_wait();
+            if (b == CH / 32 - 1) {
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) release_acc(acc);
+            }
+            if (row_ok) {
+#pragma unroll
+              for (int c = 0; c < kOut; c += 16)
+                with_act(p.act, [&](auto tag) __attribute__((always_inline)) {
+                  constexpr int A = decltype(tag)::value;
+                  const float* b1 = p.bias ? s_bias + o + c : nullptr;
+                  const float* b2 = kGated && p.bias2 ? s_bias + BN / 2 + o + c : nullptr;
+                  if (p.out_bf16) epi_rows<A, kGated, true>(p, row, w.n0 + o + c, b1, b2, scale, scale2, rr + c, tmax);
+                  else epi_rows<A, kGated, false>(p, row, w.n0 + o + c, b1, b2, scale, scale2, rr + c, tmax);
+                });
+            }
           }
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) release_acc(acc);
           released = true;
-          if (row_ok)
-            with_act(p.act, [&](auto tag) {
-              epi_rows<decltype(tag)::value, kGated, kOut>(p, row, w.n0 + oc, w.group, scale, scale2, rr, tmax);
-            });
         } else if (p.mode != kModeStreamK) {
           // ragged or unaligned tiles and small-N tiles: finished as they are read
           constexpr int kOut = kGated ? CH / 2 : CH;
