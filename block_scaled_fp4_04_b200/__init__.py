@@ -6,11 +6,12 @@ device memory and streams.  There is no CPU fallback: if the shared library is
 missing or the device is not an sm_100 GPU, the calls raise.
 
 The functions named ``fp4_*`` mirror the C entry points of ``include/fp4.h`` one to
-one (tensors stand in for device pointers).  ``quantize`` and ``gemm`` below are
-conveniences that allocate the outputs with torch and call them.
+one (tensors stand in for device pointers).  ``quantize``, ``gemm`` and the functions
+after them are conveniences that allocate the outputs with torch and call them.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -360,14 +361,20 @@ class Quantized:
 
 
 class Workspace:
-    """Zero-filled device scratch owned by the caller, reused across calls."""
+    """Zero-filled device scratch owned by the caller, reused across calls.
+
+    A buffer that has become too small is kept: captured graphs may still replay calls
+    that use it."""
 
     def __init__(self, device=None):
         self.device = torch.device(device or "cuda")
         self.buf = torch.zeros(0, dtype=torch.uint8, device=self.device)
+        self._outgrown = []
 
     def get(self, nbytes: int) -> torch.Tensor:
         if nbytes > self.buf.numel():
+            if self.buf.numel():
+                self._outgrown.append(self.buf)
             self.buf = torch.zeros(max(nbytes, 4096), dtype=torch.uint8, device=self.device)
         return self.buf
 
@@ -418,6 +425,178 @@ def gemm_mixed(a: Quantized, b: Quantized, out_dtype=torch.bfloat16, stream=None
     oc = BF16 if out.dtype == torch.bfloat16 else F32
     fp4_gemm_mixed(a.fmt, a.codes, a.scales, b.fmt, b.codes, b.scales, M, N, K, out, oc, stream)
     return out
+
+
+# ---------------------------------------------------------------- the feed-forward block
+# These run on the inputs' device, on `stream` (default: that device's current stream), with
+# their outputs allocated on that stream.  Inputs must be dense; biases and norm parameters FP32.
+@contextlib.contextmanager
+def _on(t: torch.Tensor, stream):
+    if not t.is_cuda:
+        raise ValueError("inputs must be CUDA tensors")
+    with torch.cuda.device(t.device):
+        if stream is None:
+            yield _s(None)
+        elif isinstance(stream, int):
+            with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=t.device)):
+                yield stream
+        else:
+            with torch.cuda.stream(stream):
+                yield stream.cuda_stream
+
+
+def _dense(name, t, like, shape, dtype=None):
+    """Checks an optional operand: on like's device, contiguous, of this shape (and type)."""
+    if t is None:
+        return
+    if t.device != like.device:
+        raise ValueError(f"{name} is on {t.device}, not on {like.device}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have the shape {tuple(shape)}, got {tuple(t.shape)}")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _out_code(dtype) -> int:
+    if dtype == torch.bfloat16:
+        return BF16
+    if dtype == torch.float32:
+        return F32
+    raise TypeError(f"output type must be float32 or bfloat16, got {dtype}")
+
+
+def layernorm(x: torch.Tensor, weight=None, bias=None, eps: float = 1e-5, out_dtype=None, fmt: Optional[int] = None,
+              global_in=None, stream=None, out: Optional[torch.Tensor] = None):
+    """Layer norm of the rows of x [rows, cols]: (y, mean, rstd).  With `fmt` (NVFP4, which needs
+    the caller's `global_in`, or MXFP4) y is a Quantized tensor instead, without a copy in
+    between."""
+    if x.dim() != 2:
+        raise ValueError("x must be [rows, cols]")
+    rows, cols = x.shape
+    _dense("x", x, x, (rows, cols))
+    _dense("weight", weight, x, (cols,), torch.float32)
+    _dense("bias", bias, x, (cols,), torch.float32)
+    _dense("global_in", global_in, x, (1,), torch.float32)
+    with _on(x, stream) as s:
+        mean, rstd = (torch.empty(rows, dtype=torch.float32, device=x.device) for _ in range(2))
+        if fmt is None:
+            if out is None:
+                out = torch.empty(rows, cols, dtype=out_dtype or x.dtype, device=x.device)
+            _dense("out", out, x, (rows, cols))
+            fp4_layernorm(x, rows, cols, _dtype_code(x), weight, bias, eps, out, _out_code(out.dtype), mean, rstd, stream=s)
+            return out, mean, rstd
+        if out is not None or out_dtype is not None:
+            raise ValueError("a quantized result takes neither out nor out_dtype")
+        codes = torch.empty(rows, cols // 2, dtype=torch.uint8, device=x.device)
+        scales = torch.empty(fp4_scales_bytes(rows, cols, fmt), dtype=torch.uint8, device=x.device)
+        fp4_layernorm(x, rows, cols, _dtype_code(x), weight, bias, eps, None, F32, mean, rstd, fmt, codes, scales,
+                      global_in, stream=s)
+        g = global_in if fmt == NVFP4 else torch.ones(1, dtype=torch.float32, device=x.device)
+        return Quantized(codes, scales, g, rows, cols, fmt), mean, rstd
+
+
+def layernorm_backward(dy: torch.Tensor, x: torch.Tensor, weight, mean, rstd, dres=None, out_dtype=None, stream=None):
+    """(dx, dweight, dbias) of layernorm; `dres` (x's type) is added to dx."""
+    if x.dim() != 2:
+        raise ValueError("x must be [rows, cols]")
+    rows, cols = x.shape
+    _dense("x", x, x, (rows, cols))
+    _dense("dy", dy, x, (rows, cols), x.dtype)
+    _dense("dres", dres, x, (rows, cols), x.dtype)
+    _dense("weight", weight, x, (cols,), torch.float32)
+    for name, t in (("mean", mean), ("rstd", rstd)):
+        _dense(name, t, x, (rows,), torch.float32)
+    with _on(x, stream) as s:
+        dx = torch.empty(rows, cols, dtype=out_dtype or x.dtype, device=x.device)
+        dw, db = (torch.empty(cols, dtype=torch.float32, device=x.device) for _ in range(2))
+        ws = torch.empty(fp4_layernorm_backward_workspace_size(rows, cols), dtype=torch.uint8, device=x.device)
+        fp4_layernorm_backward(dy, x, rows, cols, _dtype_code(x), weight, mean, rstd, dres, dx, _out_code(dx.dtype), dw,
+                               db, ws, ws.numel(), s)
+    return dx, dw, db
+
+
+def gemm_gated(a: Quantized, wg: Quantized, wu: Quantized, act: int = ACT_SILU, bias_g=None, bias_u=None,
+               out_dtype=torch.bfloat16, save: bool = False, quantized_out: Optional[torch.Tensor] = None,
+               workspace: Optional[Workspace] = None, stream=None):
+    """H = act(A . Wg^T + bias_g) * (A . Wu^T + bias_u) [M, F] in one launch; (H, G, U) with
+    `save`, which the backward pass needs.  `quantized_out`: the FP32 global scale [1] of an
+    NVFP4 result, returned as a Quantized tensor in H's place."""
+    if not (a.fmt == wg.fmt == wu.fmt) or not (a.cols == wg.cols == wu.cols) or wg.rows != wu.rows:
+        raise ValueError("a, wg and wu must agree in format and columns, wg and wu in rows")
+    M, F, K, like = a.rows, wg.rows, a.cols, a.codes
+    for name, q in (("wg", wg), ("wu", wu)):
+        _dense(f"{name}.codes", q.codes, like, (F, K // 2))
+    _dense("bias_g", bias_g, like, (F,), torch.float32)
+    _dense("bias_u", bias_u, like, (F,), torch.float32)
+    _dense("quantized_out", quantized_out, like, (1,), torch.float32)
+    with _on(like, stream) as s:
+        def new(dtype=out_dtype):
+            return torch.empty(M, F, dtype=dtype, device=like.device)
+
+        H = codes = scales = None
+        if quantized_out is None:
+            H = new()
+        else:
+            codes = torch.empty(M, F // 2, dtype=torch.uint8, device=like.device)
+            scales = torch.empty(fp4_scales_bytes(M, F, NVFP4), dtype=torch.uint8, device=like.device)
+        G, U = (new(), new()) if save else (None, None)
+        nbytes = fp4_gemm_gated_workspace_size(M, F, K, a.fmt, codes is not None)
+        ws = (workspace or Workspace(like.device)).get(nbytes) if nbytes else None
+        fp4_gemm_gated(a.fmt, a.codes, a.scales, a.g, wg.codes, wg.scales, wg.g, wu.codes, wu.scales, wu.g, M, F, K,
+                       bias_g, bias_u, act, H, _out_code(out_dtype), G, U, codes, scales, quantized_out, None, ws,
+                       ws.numel() if ws is not None else 0, 0, s)
+        if codes is not None:
+            H = Quantized(codes, scales, quantized_out, M, F, NVFP4)
+    return (H, G, U) if save else H
+
+
+def gemm_epilogue(a: Quantized, b: Quantized, bias=None, act: int = ACT_NONE, residual=None, out_dtype=torch.bfloat16,
+                  save: bool = False, workspace: Optional[Workspace] = None, stream=None,
+                  out: Optional[torch.Tensor] = None):
+    """D = act(A . B^T + bias) + residual; (D, pre-activation) with `save`.  `out` may be the
+    residual itself."""
+    if a.fmt != b.fmt or a.cols != b.cols:
+        raise ValueError("a and b must agree in format and columns")
+    M, N, K, like = a.rows, b.rows, a.cols, a.codes
+    _dense("b.codes", b.codes, like, (N, K // 2))
+    _dense("bias", bias, like, (N,), torch.float32)
+    _dense("residual", residual, like, (M, N))
+    _dense("out", out, like, (M, N))
+    rc = F32 if residual is None else _out_code(residual.dtype)
+    with _on(like, stream) as s:
+        if out is None:
+            out = torch.empty(M, N, dtype=out_dtype, device=like.device)
+        pre = torch.empty_like(out) if save else None
+        nbytes = fp4_gemm_epilogue_workspace_size(M, N, K, a.fmt, False)
+        ws = (workspace or Workspace(like.device)).get(nbytes) if nbytes else None
+        fp4_gemm_epilogue_ex(a.fmt, a.codes, a.scales, a.g, b.codes, b.scales, b.g, M, N, K, bias, act, residual, rc, out,
+                             _out_code(out.dtype), pre, workspace=ws, workspace_bytes=ws.numel() if ws is not None else 0,
+                             stream=s)
+    return (out, pre) if save else out
+
+
+def act_backward(dH: torch.Tensor, G: torch.Tensor, U: Optional[torch.Tensor] = None, act: int = ACT_SILU,
+                 dbias: bool = False, out_dtype=None, stream=None):
+    """dZ of H = act(G) (U) from dH: [rows, cols], or with U [rows, 2 cols] = [dG | dU]; (dZ,
+    its column sums) with `dbias`."""
+    if dH.dim() != 2:
+        raise ValueError("dH must be [rows, cols]")
+    rows, cols = dH.shape
+    _dense("dH", dH, dH, (rows, cols))
+    _dense("G", G, dH, (rows, cols), dH.dtype)
+    _dense("U", U, dH, (rows, cols), dH.dtype)
+    width = cols if U is None else 2 * cols
+    with _on(dH, stream) as s:
+        dZ = torch.empty(rows, width, dtype=out_dtype or dH.dtype, device=dH.device)
+        db = ws = None
+        if dbias:
+            db = torch.empty(width, dtype=torch.float32, device=dH.device)
+            ws = torch.empty(fp4_act_backward_workspace_size(rows, cols, U is not None), dtype=torch.uint8, device=dH.device)
+        fp4_act_backward(dH, G, U, rows, cols, _dtype_code(dH), act, dZ, _out_code(dZ.dtype), db, workspace=ws,
+                         workspace_bytes=ws.numel() if ws is not None else 0, stream=s)
+    return (dZ, db) if dbias else dZ
 
 
 def transposed(w: Quantized) -> Quantized:

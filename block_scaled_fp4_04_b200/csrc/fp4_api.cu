@@ -259,8 +259,8 @@ size_t fp4_gemm_workspace_size(int64_t M, int64_t N, int64_t K, fp4_fmt fmt) {
   return gemm_workspace_bytes(M, N, K, fmt == FP4_MXFP4);
 }
 
-static fp4_status gemm_common(const GemmProblem& g, fp4_fmt fmt, fp4_dtype out_dtype, void* stream,
-                              const GemmFull* full = nullptr) {
+// What every dense or grouped product needs of its arguments.
+static fp4_status gemm_check(const GemmProblem& g, fp4_fmt fmt, fp4_dtype out_dtype) {
   if (fmt != FP4_NVFP4 && fmt != FP4_MXFP4) return fail(FP4_ERR_INVALID_ARG, "fmt");
   if (out_dtype != FP4_F32 && out_dtype != FP4_BF16) return fail(FP4_ERR_INVALID_ARG, "out_dtype");
   if (!g.A || !g.B || !g.sA || !g.sB || (!g.D && !g.q_codes)) return fail(FP4_ERR_INVALID_ARG, "null pointer");
@@ -269,6 +269,13 @@ static fp4_status gemm_common(const GemmProblem& g, fp4_fmt fmt, fp4_dtype out_d
   if (g.M > (1ll << 31) - 256 || g.N > (1ll << 31) - 256) return fail(FP4_ERR_UNSUPPORTED, "dimension too large");
   if (!aligned16(g.A) || !aligned16(g.B) || !aligned16(g.sA) || !aligned16(g.sB) || (g.D && !aligned16(g.D)))
     return fail(FP4_ERR_INVALID_ARG, "A, B, scales and D must be 16-byte aligned");
+  return FP4_OK;
+}
+
+static fp4_status gemm_common(const GemmProblem& g, fp4_fmt fmt, fp4_dtype out_dtype, void* stream,
+                              const GemmFull* full = nullptr) {
+  const fp4_status c = gemm_check(g, fmt, out_dtype);
+  if (c != FP4_OK) return c;
   unsigned* status;
   fp4_status s = device_state(&status);
   if (s != FP4_OK) return s;
@@ -383,8 +390,14 @@ static fp4_status epilogue_common(fp4_fmt fmt, const uint8_t* A, const uint8_t* 
   g.q_scales = Dscales;
   g.q_g = gD;
   g.amax_out = amax_out;
+  if (!aligned4(amax_out)) return fail(FP4_ERR_INVALID_ARG, "amax_out alignment");
+  // every check before the first thing is enqueued
+  const fp4_status c = gemm_check(g, fmt, out_dtype);
+  if (c != FP4_OK) return c;
+  const size_t need = gemm_workspace_bytes(M, N, K, g.mx, Dcodes || amax_out);
+  if (need && (!workspace || workspace_bytes < need))
+    return fail(FP4_ERR_INVALID_ARG, "workspace too small (see fp4_gemm_epilogue_workspace_size)");
   if (amax_out) {
-    if (!aligned4(amax_out)) return fail(FP4_ERR_INVALID_ARG, "amax_out alignment");
     const cudaError_t e = cudaMemsetAsync(amax_out, 0, sizeof(float), static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "zeroing amax_out");
   }

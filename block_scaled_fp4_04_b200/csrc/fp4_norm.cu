@@ -964,7 +964,8 @@ __global__ void __launch_bounds__(kLongWarps * 32) ln_columns_long_kernel(const 
 // ------------------------------------------------------------------ column sums
 // 32 columns per CTA; its eight warps each add an eighth of the partial sums, in order, and
 // the eighths are added in order.
-__global__ void __launch_bounds__(256) column_sums_kernel(const float* __restrict__ part, int parts, int64_t width,
+// The partial sums are cleared behind it: a zero-filled workspace that other calls share stays so.
+__global__ void __launch_bounds__(256) column_sums_kernel(float* part, int parts, int64_t width,
                                                           int64_t n0, float* out0, float* out1) {
   __shared__ float s[8][32];
   rows_allow_dependents();
@@ -975,7 +976,8 @@ __global__ void __launch_bounds__(256) column_sums_kernel(const float* __restric
   if (c < width) {
     const int p0 = parts * warp / 8, p1 = parts * (warp + 1) / 8;
 #pragma unroll 4
-    for (int q = p0; q < p1; ++q) v += part[static_cast<int64_t>(q) * width + c];
+    for (int q = p0; q < p1; ++q) v += __ldcg(part + static_cast<int64_t>(q) * width + c);
+    for (int q = p0; q < p1; ++q) __stcg(part + static_cast<int64_t>(q) * width + c, 0.0f);
   }
   s[warp][lane] = v;
   __syncthreads();
@@ -991,7 +993,7 @@ __global__ void __launch_bounds__(256) column_sums_kernel(const float* __restric
   }
 }
 
-cudaError_t launch_column_sums(const float* part, int parts, int64_t width, int64_t n0, float* out0, float* out1,
+cudaError_t launch_column_sums(float* part, int parts, int64_t width, int64_t n0, float* out0, float* out1,
                                cudaStream_t st) {
   return launch_rows(column_sums_kernel, dim3(static_cast<unsigned>((width + 31) / 32)), 256, 0, st, part, parts, width,
                      n0, out0, out1);

@@ -71,8 +71,8 @@ size_t act_grad_workspace_bytes(int64_t rows, int64_t cols, int gated);
 cudaError_t launch_act_grad(const ActGradProblem& p, unsigned* status, cudaStream_t st);
 
 // out0[c] = sum_p part[p][c] for c < n0, out1[c - n0] for the rest of the `width` columns, in
-// the order of p; either output may be null.
-cudaError_t launch_column_sums(const float* part, int parts, int64_t width, int64_t n0, float* out0, float* out1,
+// the order of p; either output may be null.  Clears part.
+cudaError_t launch_column_sums(float* part, int parts, int64_t width, int64_t n0, float* out0, float* out1,
                                cudaStream_t st);
 
 // GemmProblem with the long epilogue's operands (full null: the plain epilogue).

@@ -355,7 +355,7 @@ fp4_status fp4_gemm_gated_grouped(fp4_fmt fmt, int num_groups, const int32_t* of
  *       order: the same bits every time);
  *   amax_out_dev 1 float: max |dZ| (zeroed, then written by this call).
  * workspace: fp4_act_backward_workspace_size(rows, cols, gated) bytes, needed for dbias only,
- * any contents.  Matrices 16-byte aligned. */
+ * any contents; what it uses of it is left zero-filled.  Matrices 16-byte aligned. */
 size_t fp4_act_backward_workspace_size(int64_t rows, int64_t cols, int gated);
 fp4_status fp4_act_backward(const void* dH_dev, const void* G_dev, const void* U_dev, int64_t rows, int64_t cols,
                             fp4_dtype in_dtype, fp4_act act, void* dZ_dev, fp4_dtype out_dtype, float* dbias_dev,
@@ -387,7 +387,7 @@ fp4_status fp4_layernorm(const void* x_dev, int64_t rows, int64_t cols, fp4_dtyp
  *           where the types agree.
  *   dweight_dev, dbias_dev  [cols] FP32 or NULL each; their sums have a fixed order.
  * workspace: fp4_layernorm_backward_workspace_size(rows, cols) bytes, needed for dweight or
- * dbias only, any contents, 16-byte aligned. */
+ * dbias only, any contents, 16-byte aligned; what it uses of it is left zero-filled. */
 size_t fp4_layernorm_backward_workspace_size(int64_t rows, int64_t cols);
 fp4_status fp4_layernorm_backward(const void* dy_dev, const void* x_dev, int64_t rows, int64_t cols,
                                   fp4_dtype in_dtype, const float* weight_dev, const float* mean_dev,
