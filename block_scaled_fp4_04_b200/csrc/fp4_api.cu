@@ -561,7 +561,7 @@ fp4_status fp4_gemm_gated_bf16a(const void* X, const uint8_t* Wg, const uint8_t*
     return fail(FP4_ERR_INVALID_ARG, "workspace too small (see fp4_gemm_gated_bf16a_workspace_size)");
   uint8_t* const ws = static_cast<uint8_t*>(workspace) + quant_ws_aligned();
   const size_t ws_bytes = workspace_bytes - quant_ws_aligned();
-  if (!decode_eligible(M, F, K)) {
+  if (!gated_decode_eligible(M, F, K)) {
     const fp4_status s = fp4_quantize(X, M, K, FP4_BF16, FP4_NVFP4, 16, Xcodes, Xscales, gX, nullptr, nullptr, nullptr,
                                       workspace, kQuantWorkspaceBytes, stream);
     if (s != FP4_OK) return s;

@@ -26,12 +26,17 @@ static Plan gated_plan(int64_t M, int64_t F, int64_t K, int groups) {
   pl.tiles_m = static_cast<int>((M + 127) / 128);
   const int64_t tiles = static_cast<int64_t>(pl.tiles_m) * pl.tiles_n;
   const int sms = num_sms();
-  // fewer tiles than SMs: every tile's K range is split over CTAs, where it is long enough
-  // that the partial sums' traffic stays small
-  if (tiles < sms && pl.num_kb >= 4) {
+  // Fewer tiles than SMs: a tile's K steps, about 0.5 us each, can be split over CTAs.  What that
+  // costs (partial sums of 16 bytes a thread meet in L2, then are read back) grows with the rows
+  // and tiles; in us, from: F = 256, K = 8192: 33 rows 14.9 split / 20.1 whole, 128 rows 26.9 /
+  // 21.5; F = 2880, K = 28672: 128 rows 50 / 76, 512 rows 83 / 76; F = 2880, K = 2880: 33 rows
+  // 23.6 / 11.5, 512 rows 45.6 / 13.2.
+  const double saved = 0.5 * static_cast<double>(pl.num_kb - (tiles * pl.num_kb + sms - 1) / sms);
+  const double cost = 8.0 + 0.09 * static_cast<double>(std::min<int64_t>(M, 128)) + 0.05 * static_cast<double>(tiles);
+  if (tiles < sms && saved > cost) {
     pl.mode = kModeStreamK;
     pl.units = tiles * pl.num_kb;
-    pl.ws_bytes = (static_cast<size_t>(2 * M * F) * 4 + 255) / 256 * 256 + (static_cast<size_t>(tiles) * 4 + 255) / 256 * 256;
+    pl.ws_bytes = (static_cast<size_t>(2 * M * ((F + 3) / 4 * 4)) * 4 + 255) / 256 * 256 + (static_cast<size_t>(tiles) * 4 + 255) / 256 * 256;
     return pl;
   }
   pl.mode = kModeTile;
@@ -44,20 +49,29 @@ static Plan gated_plan(int64_t M, int64_t F, int64_t K, int groups) {
   return pl;
 }
 
+// Up to 16 rows the decode kernel streams the weights faster than whole tiles with 112 rows
+// empty; from 17 rows on its 32-wide MMAs and partial sums cost more than they save (us,
+// quantized operands, decode / tiles: F = 28672, K = 8192: 1 row 48.5 / 69.5, 16 rows 52.7 / 69.8, 32
+// rows 63.6 / 58.5; F = K = 2880: 16 rows 12.4 / 11.9, 32 rows 20.1 / 11.8).
+bool gated_decode_eligible(int64_t M, int64_t F, int64_t K) { return M <= 16 && decode_eligible(M, F, K); }
+
 size_t gated_workspace_bytes(int64_t M, int64_t F, int64_t K, int mx, bool rows_in_place) {
-  if (!mx && !rows_in_place && decode_eligible(M, F, K)) return decode_gated_workspace_bytes(M, F);
+  if (!mx && !rows_in_place && gated_decode_eligible(M, F, K)) return decode_gated_workspace_bytes(M, F);
   return gated_plan(M, F, K, 0).ws_bytes;
 }
 
 template <bool MX>
 static cudaError_t dispatch_gated(const Plan& pl, const GemmMaps& tm, const GemmArgs& a, cudaStream_t st) {
+  if (pl.mode != kModeStreamK && a.sectors && a.Nk % 16 == 0)
+    return pl.pair ? run<256, MX, 1, true, false, kEpiGatedWhole>(tm, a, pl.units, st)
+                   : run<256, MX, 1, false, false, kEpiGatedWhole>(tm, a, pl.units, st);
   return pl.pair ? run<256, MX, 1, true, false, kEpiGated>(tm, a, pl.units, st)
                  : run<256, MX, 1, false, false, kEpiGated>(tm, a, pl.units, st);
 }
 
 int launch_gated(const GatedProblem& g, unsigned* status, cudaStream_t st, const char** why, cudaError_t* err) {
   const int grouped = g.num_groups > 0;
-  if (!grouped && !g.mx && !g.q_codes && !g.amax_out && decode_eligible(g.M, g.F, g.K)) {
+  if (!grouped && !g.mx && !g.q_codes && !g.amax_out && gated_decode_eligible(g.M, g.F, g.K)) {
     DecodeProblem q{};
     q.W = g.Wg;
     q.sW = g.sWg;
@@ -152,7 +166,8 @@ int launch_gated(const GatedProblem& g, unsigned* status, cudaStream_t st, const
   a.amax_out = reinterpret_cast<unsigned*>(g.amax_out);
   if (pl.mode == kModeStreamK) {
     a.ws = static_cast<float*>(g.ws);
-    a.tile_cnt = reinterpret_cast<int*>(static_cast<uint8_t*>(g.ws) + (static_cast<size_t>(2 * g.M * g.F) * 4 + 255) / 256 * 256);
+    a.ws_ld = static_cast<int>((g.F + 3) / 4 * 4);
+    a.tile_cnt = reinterpret_cast<int*>(static_cast<uint8_t*>(g.ws) + (static_cast<size_t>(2 * g.M * a.ws_ld) * 4 + 255) / 256 * 256);
   }
   if (grouped) {
     a.num_groups = g.num_groups;

@@ -236,7 +236,8 @@ Plan make_plan(int64_t M, int64_t N, int64_t K, int groups, int mx, bool row_maj
   if (tiles < 2 * sms && pl.num_kb >= 4 && (pl.swap || (2 * tiles < sms && pl.num_kb >= 16))) {
     pl.mode = kModeStreamK;
     pl.units = tiles * pl.num_kb;
-    pl.ws_bytes = (static_cast<size_t>(M * N) * 4 + 255) / 256 * 256 + (static_cast<size_t>(tiles) * 4 + 255) / 256 * 256;
+    // (rows of whole float4s, as the long epilogue keeps them)
+    pl.ws_bytes = (static_cast<size_t>(M * ((N + 3) / 4 * 4)) * 4 + 255) / 256 * 256 + (static_cast<size_t>(tiles) * 4 + 255) / 256 * 256;
   } else {
     pl.mode = kModeTile;
     pl.units = tiles;
@@ -382,7 +383,8 @@ int launch_gemm_full(const GemmProblemFull& g, unsigned* status, cudaStream_t st
   a.amax_out = reinterpret_cast<unsigned*>(g.amax_out);
   if (pl.mode == kModeStreamK) {
     a.ws = static_cast<float*>(g.ws);
-    a.tile_cnt = reinterpret_cast<int*>(static_cast<uint8_t*>(g.ws) + (static_cast<size_t>(g.M * g.N) * 4 + 255) / 256 * 256);
+    a.ws_ld = static_cast<int>(g.full && !pl.swap ? (g.N + 3) / 4 * 4 : g.N);
+    a.tile_cnt = reinterpret_cast<int*>(static_cast<uint8_t*>(g.ws) + (static_cast<size_t>(g.M * a.ws_ld) * 4 + 255) / 256 * 256);
   }
   if (grouped) {
     a.num_groups = g.num_groups;

@@ -6,6 +6,11 @@ namespace fp4 {
 
 template <bool MX>
 static cudaError_t dispatch_full_t(const Plan& pl, const GemmMaps& tm, const GemmArgs& a, cudaStream_t st) {
+  if (pl.BN >= 128 && pl.mode != kModeStreamK && a.sectors && a.Nk % 16 == 0) {
+    if (pl.BN == 128) return run<128, MX, 2, false, false, kEpiFullWhole>(tm, a, pl.units, st);
+    return pl.pair ? run<256, MX, 1, true, false, kEpiFullWhole>(tm, a, pl.units, st)
+                   : run<256, MX, 1, false, false, kEpiFullWhole>(tm, a, pl.units, st);
+  }
   switch (pl.BN) {
     case 16: return run<16, MX, 2, false, false, kEpiFull>(tm, a, pl.units, st);
     case 32: return run<32, MX, 2, false, false, kEpiFull>(tm, a, pl.units, st);

@@ -56,6 +56,7 @@ struct GemmArgs {
   const void* res;       // [M, N] added after the activation, or null
   int res_bf16;
   int bias_any;          // a bias is given
+  int ws_ld;             // floats per row of partial sums, a multiple of 4
   int sectors;           // rows of the output, its copies and the residual start at 32-byte sectors
   void* pre;             // kEpiFull: the pre-activation; kEpiGated: G; [M, N] in the output type, or null
   void* pre2;            // kEpiGated: U
@@ -200,7 +201,8 @@ constexpr int pipes_per_cta() { return BN <= 32 ? FP4_SMALL_N_PIPES : BN <= 64 ?
 // memory, an E8M0 scale per 32): a stage holds 128 K elements, one scale atom per row-block.
 template <int BN, bool MX, int ACC, bool PAIR = false, bool F8 = false, int EPI = kEpiPlain>
 struct Cfg {
-  static_assert(EPI != kEpiGated || BN == 256, "gated tiles: 128 gate and 128 up columns");
+  static constexpr bool kGated = EPI == kEpiGated || EPI == kEpiGatedWhole;
+  static_assert(!kGated || BN == 256, "gated tiles: 128 gate and 128 up columns");
   static_assert(EPI == kEpiPlain || !F8, "mixed-format products have the plain epilogue");
   static_assert(!F8 || MX, "mixed-format MMAs: E8M0 scales");
   static_assert(!PAIR || (BN == 256 && ACC == 1), "CTA pairs run 256 x 256 tiles");
@@ -220,7 +222,7 @@ struct Cfg {
   static constexpr bool kLong = kSepCp && EPI != kEpiPlain;
   static constexpr int kEpiWarps = kLong ? 16 : kSepCp ? 8 : 4;
   static constexpr int kEpiCols = BN * 4 / kEpiWarps;  // accumulator columns per epilogue thread
-  static constexpr int kTileCols = EPI == kEpiGated ? BN / 2 : BN;  // output columns of a tile
+  static constexpr int kTileCols = kGated ? BN / 2 : BN;  // output columns of a tile
   static constexpr int kThreads = kSepCp ? 64 + 32 * kEpiWarps + 32 * kCopiers : 192 * kP;
   static constexpr int kAtomsKT = F8 ? 1 : MX ? 2 : 4;  // scale atoms per stage (256 K; 128 K for F8)
   static constexpr int kNRB = BN >= 128 ? BN / 128 : 1;  // B scale row-blocks per tile
@@ -380,6 +382,24 @@ __device__ __forceinline__ void epi_row16(const GemmArgs& p, int row, int col, f
   }
 }
 
+// Reads 16 summed partials of one row (columns [col, col + 16)) of rows padded to whole float4s,
+// and clears them.
+__device__ __forceinline__ void take_raw16(float* row, int col, int n, uint32_t* v) {
+#pragma unroll
+  for (int j = 0; j < 16; j += 4) {
+    float4* at = reinterpret_cast<float4*>(row + col + j);
+    float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (col + j < n) {
+      t = __ldcg(at);
+      __stcg(at, make_float4(0.f, 0.f, 0.f, 0.f));
+    }
+    v[j] = __float_as_uint(t.x);
+    v[j + 1] = __float_as_uint(t.y);
+    v[j + 2] = __float_as_uint(t.z);
+    v[j + 3] = __float_as_uint(t.w);
+  }
+}
+
 // Reads 16 summed partials of one row (columns [col, col + 16) of n), clears them, scales.
 __device__ __forceinline__ void take_sums16(float* row, int col, int n, float scale, float (&v)[16]) {
   if ((n & 3) == 0 && col + 16 <= n) {
@@ -420,20 +440,6 @@ __device__ __forceinline__ void ld_sector(const void* p, uint32_t* w) {
                : "memory");
 }
 
-// 16 consecutive elements at offset `at` of a BF16 or FP32 matrix, 32-byte aligned.
-__device__ __forceinline__ void store_vec16(void* out, int bf16, int64_t at, const float (&v)[16]) {
-  if (bf16) {
-    uint32_t w[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) w[j] = pack_bf16x2(v[2 * j], v[2 * j + 1]);
-    st_sector(static_cast<__nv_bfloat16*>(out) + at, w);
-  } else {
-    float4* dst = reinterpret_cast<float4*>(static_cast<float*>(out) + at);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) __stcs(dst + j, make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]));
-  }
-}
-
 // 8 consecutive elements at offset `at` of a BF16 or FP32 matrix, 16-byte aligned.
 __device__ __forceinline__ void store_vec8(void* out, int bf16, int64_t at, const float (&v)[8]) {
   if (bf16) {
@@ -446,119 +452,194 @@ __device__ __forceinline__ void store_vec8(void* out, int bf16, int64_t at, cons
   }
 }
 
-// 16 elements of the residual at offset `at`, as they lie in memory: words 0..7 (BF16) or
-// 0..15 (FP32).
-__device__ __forceinline__ void load_res16(const GemmArgs& p, int64_t at, uint32_t (&w)[16]) {
-  if (p.res_bf16) {
-    ld_sector(static_cast<const __nv_bfloat16*>(p.res) + at, w);
-  } else {
-    ld_sector(static_cast<const float*>(p.res) + at, w);
-    ld_sector(static_cast<const float*>(p.res) + at + 8, w + 8);
-  }
-}
+// Where a warp of the long epilogues is: 32 rows from row0 (the first `rows` of them exist), this
+// lane's row being row0 + lane, and `cols` (at most 16) columns from col.
+struct EpiSpot {
+  int row0, rows, lane;
+  int col, cols;
+  bool direct;   // whole sectors: each lane reads and writes its own row
+  __device__ __forceinline__ bool row_ok() const { return lane < rows; }
+};
 
-// Stores 8 values; BF16 in two calls (h = 0, 8) that fill one 32-byte sector of w.
-template <bool BF16>
-__device__ __forceinline__ void put8(void* out, int64_t at, int h, uint32_t (&w)[8], const float2 (&v)[4]) {
-  if constexpr (BF16) {
+// Transposes 8 x 8 words over groups of 8 lanes (its own inverse): word k of lane i becomes
+// word i of lane k.
+__device__ __forceinline__ void transpose8(uint32_t (&w)[8], int lane) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) w[h / 2 + j] = pack_bf16x2(v[j].x, v[j].y);
-    if (h == 8) st_sector(static_cast<__nv_bfloat16*>(out) + at, w);
-  } else {
-    uint32_t f[8];
+  for (int d = 1; d < 8; d <<= 1) {
+    const bool up = lane & d;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      f[2 * j] = __float_as_uint(v[j].x);
-      f[2 * j + 1] = __float_as_uint(v[j].y);
-    }
-    st_sector(static_cast<float*>(out) + at + h, f);
-  }
-}
-
-// 8 sums of a product, scaled, plus the bias (in shared memory, or null).
-__device__ __forceinline__ void linear8(const uint32_t* sums, float scale, const float* bias, float2 (&v)[4]) {
-#pragma unroll
-  for (int j = 0; j < 4; ++j)
-    v[j] = __fmul2_rn(make_float2(__uint_as_float(sums[2 * j]), __uint_as_float(sums[2 * j + 1])), pair(scale));
-  if (bias) {
-    const float4 x = reinterpret_cast<const float4*>(bias)[0], y = reinterpret_cast<const float4*>(bias)[1];
-    v[0] = __fadd2_rn(v[0], make_float2(x.x, x.y));
-    v[1] = __fadd2_rn(v[1], make_float2(x.z, x.w));
-    v[2] = __fadd2_rn(v[2], make_float2(y.x, y.y));
-    v[3] = __fadd2_rn(v[3], make_float2(y.z, y.w));
-  }
-}
-
-// The long epilogues' whole tiles: 16 consecutive columns of one row whose sums are in registers
-// (gated: 16 gate sums, then 16 up sums).  Every row is read and written in whole 32-byte
-// sectors: a thread's 16-byte pieces of its own row, half a sector each, slowed the whole kernel
-// down (8192 x 4096 x 4096 gated with G and U: 216 us against 189).  Copies of the
-// pre-activations are made in passes of their own: the sums are scaled again rather than kept
-// twice.
-template <int ACT, bool GATED, bool BF16>
-__device__ __forceinline__ void epi_rows(const GemmArgs& p, int row, int col, const float* bias, const float* bias2,
-                                         float scale, float scale2, uint32_t* sums, uint32_t& tmax) {
-  const int64_t at = static_cast<int64_t>(row) * p.ldo + col;
-  uint32_t w[8], res[16];
-  if (!GATED && p.res) load_res16(p, at, res);
-  if (p.pre) {
-#pragma unroll
-    for (int h = 0; h < 16; h += 8) {
-      float2 v[4];
-      linear8(sums + h, scale, bias ? bias + h : nullptr, v);
-      put8<BF16>(p.pre, at, h, w, v);
-    }
-    if constexpr (GATED) {
-#pragma unroll
-      for (int h = 0; h < 16; h += 8) {
-        float2 v[4];
-        linear8(sums + 16 + h, scale2, bias2 ? bias2 + h : nullptr, v);
-        put8<BF16>(p.pre2, at, h, w, v);
+    for (int k = 0; k < 8; ++k)
+      if ((k & d) == 0) {
+        const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, up ? w[k] : w[k | d], d);
+        if (up) w[k] = got;
+        else w[k | d] = got;
       }
-    }
   }
+}
+
+// Eight words of every lane's row, from element column `col` on (16 BF16 or 8 FP32 elements, of
+// which `cols` exist), to or from the matrix.  Where all exist and rows start at 32-byte sectors
+// (s.direct; known at compile time in the WHOLE kernels) each lane reads and writes whole sectors
+// of its own row: 16-byte pieces, half a sector each, slowed the whole kernel down (8192 x 4096 x
+// 4096 gated with G and U: 216 us against 189).  Else the words are transposed over 8 lanes, which
+// then hold a run of one row each time, so that neighbouring lanes touch neighbouring words (8192 x
+// 4097 x 4096 gated: 199 us, 441 with every lane's elements stored one by one).
+template <bool BF16, bool WHOLE>
+__device__ __forceinline__ void put_words(const GemmArgs& p, const EpiSpot& s, void* out, int col, int cols, uint32_t (&w)[8]) {
+  if (WHOLE || s.direct) {
+    if (s.row_ok()) {
+      const int64_t at = static_cast<int64_t>(s.row0 + s.lane) * p.ldo + col;
+      st_sector(static_cast<uint8_t*>(out) + at * (BF16 ? 2 : 4), w);
+    }
+    return;
+  }
+  if constexpr (WHOLE) return;
+  uint32_t x[8];
 #pragma unroll
-  for (int h = 0; h < 16; h += 8) {
-    float2 v[4];
-    linear8(sums + h, scale, bias ? bias + h : nullptr, v);
+  for (int j = 0; j < 8; ++j) x[j] = w[j];
+  transpose8(x, s.lane);
+  const int i = s.lane & 7, r0 = s.lane & ~7;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) v[j] = act_value2<ACT>(v[j]);
-    if constexpr (GATED) {
-      float2 u[4];
-      linear8(sums + 16 + h, scale2, bias2 ? bias2 + h : nullptr, u);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) v[j] = __fmul2_rn(v[j], u[j]);
-    } else if (p.res) {
-      if (p.res_bf16) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          v[j] = __fadd2_rn(v[j], make_float2(__uint_as_float(res[h / 2 + j] << 16),
-                                              __uint_as_float(res[h / 2 + j] & 0xFFFF0000u)));
+  for (int j = 0; j < 8; ++j) {
+    if (r0 + j >= s.rows) continue;
+    const int64_t at = static_cast<int64_t>(s.row0 + r0 + j) * p.ldo + col + (BF16 ? 2 * i : i);
+    if constexpr (BF16) {
+      uint16_t* dst = static_cast<uint16_t*>(out) + at;
+      if (2 * i + 1 < cols && (at & 1) == 0) {
+        *reinterpret_cast<uint32_t*>(dst) = x[j];
       } else {
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          v[j] = __fadd2_rn(v[j], make_float2(__uint_as_float(res[h + 2 * j]), __uint_as_float(res[h + 2 * j + 1])));
+        if (2 * i < cols) dst[0] = static_cast<uint16_t>(x[j]);
+        if (2 * i + 1 < cols) dst[1] = static_cast<uint16_t>(x[j] >> 16);
       }
+    } else {
+      if (i < cols) static_cast<uint32_t*>(out)[at] = x[j];
     }
-    if (p.out) put8<BF16>(p.out, at, h, w, v);
-    if (p.amax_out) {
+  }
+}
+
+template <bool BF16, bool WHOLE>
+__device__ __forceinline__ void get_words(const GemmArgs& p, const EpiSpot& s, const void* in, int col, int cols, uint32_t (&w)[8]) {
+  if (WHOLE || s.direct) {
+    const int64_t at = static_cast<int64_t>(s.row0 + s.lane) * p.ldo + col;
+    if (s.row_ok()) ld_sector(static_cast<const uint8_t*>(in) + at * (BF16 ? 2 : 4), w);
+    return;
+  }
+  if constexpr (WHOLE) return;
+  const int i = s.lane & 7, r0 = s.lane & ~7;
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        tmax = max(tmax, max(__float_as_uint(v[j].x) & 0x7FFFFFFFu, __float_as_uint(v[j].y) & 0x7FFFFFFFu));
+  for (int j = 0; j < 8; ++j) {
+    w[j] = 0;
+    if (r0 + j >= s.rows) continue;
+    const int64_t at = static_cast<int64_t>(s.row0 + r0 + j) * p.ldo + col + (BF16 ? 2 * i : i);
+    if constexpr (BF16) {
+      const uint16_t* src = static_cast<const uint16_t*>(in) + at;
+      if (2 * i + 1 < cols && (at & 1) == 0) {
+        w[j] = *reinterpret_cast<const uint32_t*>(src);
+      } else {
+        if (2 * i < cols) w[j] = src[0];
+        if (2 * i + 1 < cols) w[j] |= static_cast<uint32_t>(src[1]) << 16;
+      }
+    } else {
+      if (i < cols) w[j] = static_cast<const uint32_t*>(in)[at];
     }
-    if (p.q_codes) {
+  }
+  transpose8(w, s.lane);
+}
+
+// Stores 16 values of a row.
+template <bool WHOLE>
+__device__ __forceinline__ void put16(const GemmArgs& p, const EpiSpot& s, void* out, const float2 (&v)[8]) {
+  uint32_t w[8];
+  if (p.out_bf16) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) w[j] = pack_bf16x2(v[j].x, v[j].y);
+    put_words<true, WHOLE>(p, s, out, s.col, s.cols, w);
+  } else {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        sums[h + 2 * j] = __float_as_uint(v[j].x);
-        sums[h + 2 * j + 1] = __float_as_uint(v[j].y);
+        w[2 * j] = __float_as_uint(v[4 * h + j].x);
+        w[2 * j + 1] = __float_as_uint(v[4 * h + j].y);
+      }
+      put_words<false, WHOLE>(p, s, out, s.col + 8 * h, s.cols - 8 * h, w);
+    }
+  }
+}
+
+// 16 sums of a product, scaled, plus the bias (in shared memory, or null).
+__device__ __forceinline__ void linear16(const uint32_t* sums, float scale, const float* bias, float2 (&v)[8]) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    v[j] = __fmul2_rn(make_float2(__uint_as_float(sums[2 * j]), __uint_as_float(sums[2 * j + 1])), pair(scale));
+  if (bias) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float4 x = reinterpret_cast<const float4*>(bias)[j];
+      v[2 * j] = __fadd2_rn(v[2 * j], make_float2(x.x, x.y));
+      v[2 * j + 1] = __fadd2_rn(v[2 * j + 1], make_float2(x.z, x.w));
+    }
+  }
+}
+
+// The long epilogues: 16 consecutive columns of a warp's 32 rows, one row per lane, whose sums
+// are in registers (gated: 16 gate sums, then 16 up sums).  Only the activation itself is in a
+// switch: a copy of the whole per activation took minutes to compile and spilled.  All lanes take
+// part.
+template <bool GATED, bool WHOLE>
+__device__ __forceinline__ void epi_rows(const GemmArgs& p, const EpiSpot& s, const float* bias, const float* bias2,
+                                         float scale, float scale2, const uint32_t* sums, uint32_t& tmax) {
+  uint32_t res[8], res2[8];
+  if (!GATED && p.res) {
+    if (p.res_bf16) {
+      get_words<true, WHOLE>(p, s, p.res, s.col, s.cols, res);
+    } else {
+      get_words<false, WHOLE>(p, s, p.res, s.col, s.cols, res);
+      get_words<false, WHOLE>(p, s, p.res, s.col + 8, s.cols - 8, res2);
+    }
+  }
+  float2 v[8];
+  linear16(sums, scale, bias, v);
+  if (p.pre) put16<WHOLE>(p, s, p.pre, v);
+  with_act(p.act, [&](auto tag) __attribute__((always_inline)) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = act_value2<decltype(tag)::value>(v[j]);
+  });
+  if constexpr (GATED) {
+    float2 u[8];
+    linear16(sums + 16, scale2, bias2, u);
+    if (p.pre2) put16<WHOLE>(p, s, p.pre2, u);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = __fmul2_rn(v[j], u[j]);
+  } else if (p.res) {
+    if (p.res_bf16) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        v[j] = __fadd2_rn(v[j], make_float2(__uint_as_float(res[j] << 16), __uint_as_float(res[j] & 0xFFFF0000u)));
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        v[j] = __fadd2_rn(v[j], make_float2(__uint_as_float(res[2 * j]), __uint_as_float(res[2 * j + 1])));
+        v[4 + j] = __fadd2_rn(v[4 + j], make_float2(__uint_as_float(res2[2 * j]), __uint_as_float(res2[2 * j + 1])));
       }
     }
   }
-  if (p.q_codes) {
+  if (p.out) put16<WHOLE>(p, s, p.out, v);
+  if (p.amax_out && s.row_ok()) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if (WHOLE || 2 * j < s.cols) tmax = max(tmax, __float_as_uint(v[j].x) & 0x7FFFFFFFu);
+      if (WHOLE || 2 * j + 1 < s.cols) tmax = max(tmax, __float_as_uint(v[j].y) & 0x7FFFFFFFu);
+    }
+  }
+  if (p.q_codes && s.row_ok()) {
     float z[16];
 #pragma unroll
-    for (int j = 0; j < 16; ++j) z[j] = __uint_as_float(sums[j]);
-    epi_quantize16(p, row, col, z);
+    for (int j = 0; j < 8; ++j) {
+      z[2 * j] = v[j].x;
+      z[2 * j + 1] = v[j].y;
+    }
+    epi_quantize16(p, s.row0 + s.lane, s.col, z);
   }
 }
 
@@ -614,29 +695,17 @@ __device__ __forceinline__ void add_bias16(const GemmArgs& p, const float* bias,
   }
 }
 
-// Finishes 16 consecutive kernel columns of one kernel row in the long epilogues (values
-// already multiplied by their global scales): biases, copies of the pre-activations,
-// activation, product with u (gated) or residual, output, NVFP4 copy, maximum.
-template <bool GATED>
-__device__ __forceinline__ void epi_finish16(const GemmArgs& p, int row, int col, int group, float (&v)[16],
-                                             float (&u)[16], uint32_t& tmax) {
-  if (p.bias) add_bias16(p, p.bias + group * p.bias_group, row, col, v);
-  if (GATED && p.bias2) add_bias16(p, p.bias2 + group * p.bias_group, row, col, u);
+// kEpiFull on small-N tiles: finishes 16 consecutive kernel columns of one kernel row (values
+// already multiplied by the global scales).
+__device__ __forceinline__ void epi_finish16(const GemmArgs& p, int row, int col, float (&v)[16]) {
+  if (p.bias) add_bias16(p, p.bias, row, col, v);
   if (p.pre) store_like_out(p, p.pre, row, col, v);
-  if (GATED && p.pre2) store_like_out(p, p.pre2, row, col, u);
   with_act(p.act, [&](auto tag) __attribute__((always_inline)) {
-    constexpr int A = decltype(tag)::value;
 #pragma unroll
-    for (int j = 0; j < 16; ++j) v[j] = GATED ? act_value<A>(v[j]) * u[j] : act_value<A>(v[j]);
+    for (int j = 0; j < 16; ++j) v[j] = act_value<decltype(tag)::value>(v[j]);
   });
-  if (!GATED && p.res) add_residual16(p, row, col, v);
+  if (p.res) add_residual16(p, row, col, v);
   if (p.out) store_like_out(p, p.out, row, col, v);
-  if (p.q_codes) epi_quantize16(p, row, col, v);
-  if (p.amax_out) {
-#pragma unroll
-    for (int j = 0; j < 16; ++j)
-      if (col + j < p.Nk) tmax = max(tmax, __float_as_uint(v[j]) & 0x7FFFFFFFu);
-  }
 }
 
 // Named barrier among the epilogue threads of one pipeline.
@@ -657,7 +726,7 @@ __global__ void __launch_bounds__(Cfg<BN, MX, ACC, PAIR, F8, EPI>::kThreads, 1)
                     const GemmArgs p) {
   using C = Cfg<BN, MX, ACC, PAIR, F8, EPI>;
   constexpr int S = C::kStages;
-  constexpr bool kGated = EPI == kEpiGated;
+  constexpr bool kGated = C::kGated, kWhole = EPI == kEpiFullWhole || EPI == kEpiGatedWhole;
   using Schedule = Sched<BN, kGated ? BN / 2 : BN>;
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint32_t s_tmem_base;
@@ -1165,88 +1234,126 @@ __global__ void __launch_bounds__(Cfg<BN, MX, ACC, PAIR, F8, EPI>::kThreads, 1)
       const uint32_t taddr = tmem + (static_cast<uint32_t>(q * 32) << 16) + acc * BN;
       bool released = false;
       if constexpr (EPI != kEpiPlain) {
-        if (C::kLong && p.mode != kModeStreamK && p.sectors && w.n0 + C::kTileCols <= p.Nk) {
-          // whole tiles, 32 sums per thread at a time; the last 32 are in registers when TMEM goes
-          // back to the MMA thread, so that their work overlaps the next tile's MMAs
-          constexpr int kOut = kGated ? 16 : 32;       // output columns per step
-          const int oc = kGated ? c0 / 2 : c0;
+        if constexpr (C::kLong) {
+          const int rows = max(0, min(32, w.rows_valid - q * 32));  // of this warp
+          bool finish = true;
+          if (!kWhole && p.mode == kModeStreamK) {
+            // Partial sums to the workspace (rows of ws_ld floats; gated: G's, then U's).  The
+            // pipeline whose sums complete the tile's K range finishes it (as below).
 #pragma unroll 1
-          for (int b = 0; b < CH / 32; ++b) {
-            uint32_t rr[32];
-            const int o = oc + b * kOut;
-            // (warps without a valid row read TMEM all the same: the loads stay convergent)
-            if constexpr (kGated) {
-              tmem_ld16(taddr + o, *reinterpret_cast<uint32_t(*)[16]>(rr));
-              tmem_ld16(taddr + BN / 2 + o, *reinterpret_cast<uint32_t(*)[16]>(rr + 16));
-            } else {
-              tmem_ld32(taddr + o, rr);
-            }
-            tmem_ld_wait();
-            if (b == CH / 32 - 1) {
-              tc_fence_before();
-              __syncwarp();
-              if (lane == 0) release_acc(acc);
-            }
-            if (row_ok) {
+            for (int cw = c0; cw < c0 + CH; cw += 32) {
+              uint32_t rr[32];
+              tmem_ld32(taddr + cw, rr);
+              tmem_ld_wait();
+              const int half = kGated && cw >= BN / 2 ? 1 : 0;
+              const int col = w.n0 + cw - half * (BN / 2);
+              float* dst = p.ws + (static_cast<int64_t>(half) * p.Mk + row) * p.ws_ld + col;
 #pragma unroll
-              for (int c = 0; c < kOut; c += 16)
-                with_act(p.act, [&](auto tag) __attribute__((always_inline)) {
-                  constexpr int A = decltype(tag)::value;
-                  const float* b1 = p.bias ? s_bias + o + c : nullptr;
-                  const float* b2 = kGated && p.bias2 ? s_bias + BN / 2 + o + c : nullptr;
-                  if (p.out_bf16) epi_rows<A, kGated, true>(p, row, w.n0 + o + c, b1, b2, scale, scale2, rr + c, tmax);
-                  else epi_rows<A, kGated, false>(p, row, w.n0 + o + c, b1, b2, scale, scale2, rr + c, tmax);
-                });
+              for (int j = 0; j < 32; j += 4)
+                if (row_ok && col + j < p.ws_ld)
+                  red_add_v4(dst + j, __uint_as_float(rr[j]), __uint_as_float(rr[j + 1]), __uint_as_float(rr[j + 2]),
+                             __uint_as_float(rr[j + 3]));
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) release_acc(acc);
+            __threadfence();
+            epi_sync(sub, 32 * C::kEpiWarps);
+            if (et == 0) {
+              __threadfence();
+              const int covered = w.kb1 - w.kb0;
+              const int before = atomicAdd(p.tile_cnt + w.tile, covered);
+              *s_last = before + covered == p.num_kb ? 1 : 0;
+            }
+            epi_sync(sub, 32 * C::kEpiWarps);
+            finish = *s_last;
+            if (finish) {
+              __threadfence();
+              if (et == 0) p.tile_cnt[w.tile] = 0;
             }
           }
-          released = true;
-        } else if (p.mode != kModeStreamK) {
-          // ragged or unaligned tiles and small-N tiles: finished as they are read
-          constexpr int kOut = kGated ? CH / 2 : CH;
+          // 32 sums per thread at a time; the last 32 are in registers when TMEM goes back to the
+          // MMA thread, so that their work overlaps the next tile's MMAs
+          constexpr int kOut = kGated ? 16 : 32;  // output columns per step
           const int oc = kGated ? c0 / 2 : c0;
+          if (finish) {
+#pragma unroll 1
+            for (int b = 0; b < CH / 32; ++b) {
+              uint32_t rr[32];
+              const int o = oc + b * kOut;
+              if (!kWhole && p.mode == kModeStreamK) {
+                if (row_ok) {
+                  float* src = p.ws + static_cast<int64_t>(row) * p.ws_ld;
+                  take_raw16(src, w.n0 + o, p.ws_ld, rr);
+                  take_raw16(kGated ? src + static_cast<int64_t>(p.Mk) * p.ws_ld : src, w.n0 + o + (kGated ? 0 : 16),
+                             p.ws_ld, rr + 16);
+                }
+              } else {
+                // (One site of these loads: copies of it, per activation or per kind of tile,
+                // spill whatever the register budget.  Warps without a valid row read TMEM all
+                // the same: the loads stay convergent.)
+                if constexpr (kGated) {
+                  tmem_ld16(taddr + o, *reinterpret_cast<uint32_t(*)[16]>(rr));
+                  tmem_ld16(taddr + BN / 2 + o, *reinterpret_cast<uint32_t(*)[16]>(rr + 16));
+                } else {
+                  tmem_ld32(taddr + o, rr);
+                }
+                tmem_ld_wait();
+                if (b == CH / 32 - 1) {
+                  tc_fence_before();
+                  __syncwarp();
+                  if (lane == 0) release_acc(acc);
+                }
+              }
+#pragma unroll
+              for (int c = 0; c < kOut; c += 16) {
+                const int col = w.n0 + o + c, cols = min(16, p.Nk - col);  // (whole: 16, or none)
+                if (rows > 0 && cols > 0) {  // warp-uniform
+                  const EpiSpot spot{row - lane, rows, lane, col, cols, p.sectors && cols == 16};
+                  const float* b1 = p.bias ? s_bias + o + c : nullptr;
+                  const float* b2 = kGated && p.bias2 ? s_bias + BN / 2 + o + c : nullptr;
+                  epi_rows<kGated, kWhole>(p, spot, b1, b2, scale, scale2, rr + c, tmax);
+                }
+              }
+            }
+          }
+          ++iter;
+          continue;
+        } else if (p.mode != kModeStreamK) {
+          // small-N tiles: finished as they are read
           if (q * 32 < w.rows_valid) {  // warp-uniform
 #pragma unroll 1
-            for (int c = oc; c < oc + kOut; c += 16) {
-              uint32_t rg[16], ru[16];
+            for (int c = c0; c < c0 + CH; c += 16) {
+              uint32_t rg[16];
               tmem_ld16(taddr + c, rg);
-              if constexpr (kGated) tmem_ld16(taddr + BN / 2 + c, ru);
               tmem_ld_wait();
               const int col = w.n0 + c;
               if (!row_ok || col >= p.Nk) continue;
-              float v[16], u[16];
+              float v[16];
 #pragma unroll
-              for (int j = 0; j < 16; ++j) {
-                v[j] = __uint_as_float(rg[j]) * scale;
-                u[j] = kGated ? __uint_as_float(ru[j]) * scale2 : 0.0f;
-              }
-              epi_finish16<kGated>(p, row, col, w.group, v, u, tmax);
+              for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(rg[j]) * scale;
+              epi_finish16(p, row, col, v);
             }
           }
         } else if (q * 32 < w.rows_valid) {
-          // stream-K: partial sums to the workspace
-          constexpr int CW = CH >= 32 ? 32 : CH;
+          // small-N tiles, stream-K: partial sums to the workspace
 #pragma unroll 1
-          for (int cw = c0; cw < c0 + CH; cw += CW) {
-            uint32_t rr[CW];
-            if constexpr (CW == 32) tmem_ld32(taddr + cw, rr);
-            else tmem_ld16(taddr + cw, *reinterpret_cast<uint32_t(*)[16]>(rr));
+          for (int c = c0; c < c0 + CH; c += 16) {
+            uint32_t rr[16];
+            tmem_ld16(taddr + c, rr);
             tmem_ld_wait();
-            const int half = kGated && cw >= BN / 2 ? 1 : 0;
-            float* dst = p.ws + (static_cast<int64_t>(half) * p.Mk + row) * p.Nk;
+            const int col = w.n0 + c;
+            if (!row_ok || col >= p.Nk) continue;
+            float* dst = p.ws + static_cast<int64_t>(row) * p.Nk + col;
+            if ((p.Nk & 3) == 0 && col + 16 <= p.Nk) {
 #pragma unroll
-            for (int h = 0; h < CW; h += 16) {
-              const int col = w.n0 + cw + h - half * (BN / 2);
-              if (!row_ok || col >= p.Nk) continue;
-              if ((p.Nk & 3) == 0 && col + 16 <= p.Nk) {
+              for (int j = 0; j < 16; j += 4)
+                red_add_v4(dst + j, __uint_as_float(rr[j]), __uint_as_float(rr[j + 1]), __uint_as_float(rr[j + 2]),
+                           __uint_as_float(rr[j + 3]));
+            } else {
 #pragma unroll
-                for (int j = 0; j < 16; j += 4)
-                  red_add_v4(dst + col + j, __uint_as_float(rr[h + j]), __uint_as_float(rr[h + j + 1]),
-                             __uint_as_float(rr[h + j + 2]), __uint_as_float(rr[h + j + 3]));
-              } else {
-#pragma unroll
-                for (int j = 0; j < 16; ++j)
-                  if (col + j < p.Nk) atomicAdd(dst + col + j, __uint_as_float(rr[h + j]));
-              }
+              for (int j = 0; j < 16; ++j)
+                if (col + j < p.Nk) atomicAdd(dst + j, __uint_as_float(rr[j]));
             }
           }
         }
@@ -1350,21 +1457,13 @@ __global__ void __launch_bounds__(Cfg<BN, MX, ACC, PAIR, F8, EPI>::kThreads, 1)
           __threadfence();
           if constexpr (EPI != kEpiPlain) {
             if (row_ok) {
-              constexpr int kOut = kGated ? CH / 2 : CH;
-              const int oc = kGated ? c0 / 2 : c0;
 #pragma unroll 1
-              for (int c = oc; c < oc + kOut; c += 16) {
+              for (int c = c0; c < c0 + CH; c += 16) {
                 const int col = w.n0 + c;
                 if (col >= p.Nk) break;
-                float v[16], u[16];
+                float v[16];
                 take_sums16(p.ws + static_cast<int64_t>(row) * p.Nk, col, p.Nk, scale, v);
-                if constexpr (kGated) {
-                  take_sums16(p.ws + (static_cast<int64_t>(p.Mk) + row) * p.Nk, col, p.Nk, scale2, u);
-                } else {
-#pragma unroll
-                  for (int j = 0; j < 16; ++j) u[j] = 0.0f;
-                }
-                epi_finish16<kGated>(p, row, col, w.group, v, u, tmax);
+                epi_finish16(p, row, col, v);
               }
             }
           } else

@@ -302,7 +302,7 @@ fp4_status fp4_gemm_epilogue_ex(fp4_fmt fmt, const uint8_t* A_dev, const uint8_t
  * (Hcodes_dev != NULL || amax_out_dev != NULL); zero-filled before first use, left so.  With
  * a workspace in use (few rows), partial sums meet by FP32 atomic additions, whose order --
  * and so the last bits of H -- can differ from call to call, as in fp4_gemm.
- * flags: FP4_GEMM_WEIGHTS_READY (both weights).  M <= 32 with NVFP4 operands runs the decode
+ * flags: FP4_GEMM_WEIGHTS_READY (both weights).  M <= 16 with NVFP4 operands runs the decode
  * kernel over both weights. */
 size_t fp4_gemm_gated_workspace_size(int64_t M, int64_t F, int64_t K, fp4_fmt fmt, int rows_in_place);
 fp4_status fp4_gemm_gated(fp4_fmt fmt, const uint8_t* A_dev, const uint8_t* sA_dev, const float* gA_dev,
@@ -314,7 +314,7 @@ fp4_status fp4_gemm_gated(fp4_fmt fmt, const uint8_t* A_dev, const uint8_t* sA_d
                           void* workspace_dev, size_t workspace_bytes, unsigned flags, void* stream);
 
 /* The same from BF16 activations X [M, K], quantized to NVFP4 as fp4_quantize does (tensor
- * amax, 16-blocks), with NVFP4 weights: M <= 32 in one cooperative launch, larger M as
+ * amax, 16-blocks), with NVFP4 weights: M <= 16 in one cooperative launch, larger M as
  * fp4_quantize then fp4_gemm_gated.  The activations' codes, scales and global scale are
  * written to Xcodes_dev / Xscales_dev / gX_dev, as by fp4_gemm_bf16a; workspace likewise:
  * fp4_gemm_gated_bf16a_workspace_size bytes, zero-filled before its first use, not to be
