@@ -30,24 +30,32 @@ struct ActGradArgs {
 
 constexpr int kAgWarps = 8;
 
-// A CTA takes 32 V columns and a slab of rows; warp w the slab's rows w, w + 8, ...
+// Words of a row per lane: several where a word is a single element or a pair, so that a row's
+// address is worked out once for as many bytes.
+template <int V>
+__host__ __device__ constexpr int ag_words() { return V == 1 ? 4 : V == 2 ? 2 : 1; }
+
+// A CTA takes 32 J V columns (J words a lane, 32 V columns apart) and a slab of rows; warp w the
+// slab's rows w, w + 8, ...
 template <typename T, int V, bool GATED, int FMT>
 __global__ void __launch_bounds__(kAgWarps * 32) act_grad_kernel(const ActGradArgs p) {
   constexpr int kHalves = GATED ? 2 : 1;
-  constexpr int U = V == 1 ? 4 : 2;  // rows in flight per warp
-  __shared__ float s_sum[kAgWarps][kHalves][32 * V];
+  constexpr int U = 2;  // rows in flight per warp
+  constexpr int J = ag_words<V>();
+  __shared__ float s_sum[kAgWarps][kHalves][32 * V * J];
   rows_allow_dependents();
   rows_wait_prior();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int col = (blockIdx.x * 32 + lane) * V;
-  const bool col_ok = col < p.n;
+  const int col0 = (blockIdx.x * 32 * J + lane) * V;
   const int64_t r0 = static_cast<int64_t>(blockIdx.y) * p.rows_per;
   const int64_t r1 = min(p.rows, r0 + p.rows_per);
-  float acc[kHalves][V];
+  float acc[kHalves][J][V];
 #pragma unroll
   for (int h = 0; h < kHalves; ++h)
 #pragma unroll
-    for (int i = 0; i < V; ++i) acc[h][i] = 0.0f;
+    for (int j = 0; j < J; ++j)
+#pragma unroll
+      for (int i = 0; i < V; ++i) acc[h][j][i] = 0.0f;
   float gs = 1.0f;
   if constexpr (FMT == kCodesNv) gs = *p.q.g;
   uint32_t m = 0;
@@ -55,51 +63,60 @@ __global__ void __launch_bounds__(kAgWarps * 32) act_grad_kernel(const ActGradAr
   with_act(p.act, [&](auto tag) __attribute__((always_inline)) {
     constexpr int A = decltype(tag)::value;
     for (int64_t r = r0 + warp; r < r1; r += kAgWarps * U) {
-      RowVec<T, V> rd[U], rg[U], ru[U];
+      RowVec<T, V> rd[U][J], rg[U][J], ru[U][J];
 #pragma unroll
       for (int k = 0; k < U; ++k) {
         const int64_t rr = r + k * kAgWarps;
-        rd[k].zero();
-        rg[k].zero();
-        ru[k].zero();
-        if (col_ok && rr < r1) {
-          rd[k].load(static_cast<const T*>(p.dh) + rr * p.n + col);
-          rg[k].load(static_cast<const T*>(p.g) + rr * p.n + col);
-          if constexpr (GATED) ru[k].load(static_cast<const T*>(p.u) + rr * p.n + col);
+        const int64_t at = rr * p.n + col0;
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+          rd[k][j].zero();
+          rg[k][j].zero();
+          ru[k][j].zero();
+          if (col0 + j * 32 * V < p.n && rr < r1) {
+            rd[k][j].load(static_cast<const T*>(p.dh) + at + j * 32 * V);
+            rg[k][j].load(static_cast<const T*>(p.g) + at + j * 32 * V);
+            if constexpr (GATED) ru[k][j].load(static_cast<const T*>(p.u) + at + j * 32 * V);
+          }
         }
       }
 #pragma unroll
       for (int k = 0; k < U; ++k) {
         const int64_t rr = r + k * kAgWarps;
         if (rr >= r1) break;  // warp-uniform
-        float d[V], g[V], u[V], z[kHalves][V];
-        rd[k].unpack(d);
-        rg[k].unpack(g);
-        ru[k].unpack(u);
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-          float value;
-          const float slope = act_slope<A>(g[i], value);
-          if constexpr (GATED) {
-            z[0][i] = d[i] * u[i] * slope;
-            z[1][i] = d[i] * value;
-          } else {
-            z[0][i] = d[i] * slope;
-          }
-        }
+        for (int j = 0; j < J; ++j) {
+          const int col = col0 + j * 32 * V;
+          const bool col_ok = col < p.n;
+          float d[V], g[V], u[V], z[kHalves][V];
+          rd[k][j].unpack(d);
+          rg[k][j].unpack(g);
+          ru[k][j].unpack(u);
 #pragma unroll
-        for (int h = 0; h < kHalves; ++h) {
-          const int64_t zc = static_cast<int64_t>(h) * p.n + col;
-          if (col_ok) {
-            if (p.dz) store_row_vec<V>(p.dz, p.dz_bf16, rr * p.ldz + zc, z[h]);
-#pragma unroll
-            for (int i = 0; i < V; ++i) acc[h][i] += z[h][i];
-            if (p.amax) {
-#pragma unroll
-              for (int i = 0; i < V; ++i) m = max(m, abs_bits_of(z[h][i]));
+          for (int i = 0; i < V; ++i) {
+            float value;
+            const float slope = act_slope<A>(g[i], value);
+            if constexpr (GATED) {
+              z[0][i] = d[i] * u[i] * slope;
+              z[1][i] = d[i] * value;
+            } else {
+              z[0][i] = d[i] * slope;
             }
           }
-          if constexpr (FMT != kCodesNone) bad |= encode_row_vec<FMT, V>(p.q, gs, rr, zc, col_ok, z[h]);
+#pragma unroll
+          for (int h = 0; h < kHalves; ++h) {
+            const int64_t zc = static_cast<int64_t>(h) * p.n + col;
+            if (col_ok) {
+              if (p.dz) store_row_vec<V>(p.dz, p.dz_bf16, rr * p.ldz + zc, z[h]);
+#pragma unroll
+              for (int i = 0; i < V; ++i) acc[h][j][i] += z[h][i];
+              if (p.amax) {
+#pragma unroll
+                for (int i = 0; i < V; ++i) m = max(m, abs_bits_of(z[h][i]));
+              }
+            }
+            if constexpr (FMT != kCodesNone) bad |= encode_row_vec<FMT, V>(p.q, gs, rr, zc, col_ok, z[h]);
+          }
         }
       }
     }
@@ -113,15 +130,18 @@ __global__ void __launch_bounds__(kAgWarps * 32) act_grad_kernel(const ActGradAr
 #pragma unroll
   for (int h = 0; h < kHalves; ++h)
 #pragma unroll
-    for (int i = 0; i < V; ++i) s_sum[warp][h][i * 32 + lane] = acc[h][i];
+    for (int j = 0; j < J; ++j)
+#pragma unroll
+      for (int i = 0; i < V; ++i) s_sum[warp][h][(j * V + i) * 32 + lane] = acc[h][j][i];
   __syncthreads();
-  for (int t = threadIdx.x; t < kHalves * 32 * V; t += kAgWarps * 32) {
-    const int h = t / (32 * V), k = t % (32 * V);  // element k % V of lane k / V
-    const int c = blockIdx.x * 32 * V + k;
+  for (int t = threadIdx.x; t < kHalves * 32 * V * J; t += kAgWarps * 32) {
+    const int h = t / (32 * V * J), k = t % (32 * V * J);  // column k of the CTA's: element k % V of a lane's word
+    const int c = blockIdx.x * 32 * V * J + k;
     if (c >= p.n) continue;
+    const int j = k / (32 * V), l = k % (32 * V) / V, i = k % V;
     float v = 0.0f;
 #pragma unroll
-    for (int w = 0; w < kAgWarps; ++w) v += s_sum[w][h][(k % V) * 32 + k / V];
+    for (int w = 0; w < kAgWarps; ++w) v += s_sum[w][h][(j * V + i) * 32 + l];
     p.part[static_cast<int64_t>(blockIdx.y) * p.ldz + static_cast<int64_t>(h) * p.n + c] = v;
   }
 }
@@ -142,7 +162,8 @@ static cudaError_t run_ag(ActGradArgs a, cudaStream_t st) {
   // the slabs of a launch are grid.y, at most 65535
   per = std::max(per, (a.rows + 65534) / 65535);
   a.rows_per = per;
-  const dim3 grid(static_cast<unsigned>((a.n + 32 * V - 1) / (32 * V)), static_cast<unsigned>((a.rows + per - 1) / per));
+  constexpr int kCols = 32 * V * ag_words<V>();
+  const dim3 grid(static_cast<unsigned>((a.n + kCols - 1) / kCols), static_cast<unsigned>((a.rows + per - 1) / per));
   return a.u ? launch_rows(act_grad_kernel<T, V, true, FMT>, grid, kAgWarps * 32, 0, st, a)
              : launch_rows(act_grad_kernel<T, V, false, FMT>, grid, kAgWarps * 32, 0, st, a);
 }
@@ -154,7 +175,8 @@ static cudaError_t pick_ag(const ActGradArgs& a, int fmt, cudaStream_t st) {
   const bool vec = a.n % V == 0 && al(a.dh) && al(a.g) && al(a.u) && al(a.dz);
   if (fmt == kCodesNv) return vec ? run_ag<T, V, kCodesNv>(a, st) : cudaErrorInvalidValue;
   if (fmt == kCodesMx) return vec ? run_ag<T, V, kCodesMx>(a, st) : cudaErrorInvalidValue;
-  return vec ? run_ag<T, V, kCodesNone>(a, st) : run_ag<T, 1, kCodesNone>(a, st);
+  if (vec) return run_ag<T, V, kCodesNone>(a, st);
+  return a.n % 2 == 0 ? run_ag<T, 2, kCodesNone>(a, st) : run_ag<T, 1, kCodesNone>(a, st);
 }
 
 cudaError_t launch_act_grad(const ActGradProblem& p, unsigned* status, cudaStream_t st) {

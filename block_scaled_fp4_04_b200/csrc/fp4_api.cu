@@ -394,7 +394,8 @@ static fp4_status epilogue_common(fp4_fmt fmt, const uint8_t* A, const uint8_t* 
   // every check before the first thing is enqueued
   const fp4_status c = gemm_check(g, fmt, out_dtype);
   if (c != FP4_OK) return c;
-  const size_t need = gemm_workspace_bytes(M, N, K, g.mx, Dcodes || amax_out);
+  const size_t need = full ? gemm_full_workspace_bytes(M, N, K, g.mx, Dcodes || amax_out)
+                           : gemm_workspace_bytes(M, N, K, g.mx, Dcodes || amax_out);
   if (need && (!workspace || workspace_bytes < need))
     return fail(FP4_ERR_INVALID_ARG, "workspace too small (see fp4_gemm_epilogue_workspace_size)");
   if (amax_out) {
@@ -795,7 +796,7 @@ fp4_status fp4_layernorm_backward(const void* dy, const void* x, int64_t rows, i
 
 size_t fp4_gemm_epilogue_workspace_size(int64_t M, int64_t N, int64_t K, fp4_fmt fmt, int rows_in_place) {
   if (M <= 0 || N <= 0 || K <= 0) return 0;
-  return gemm_workspace_bytes(M, N, K, fmt == FP4_MXFP4, rows_in_place != 0);
+  return gemm_full_workspace_bytes(M, N, K, fmt == FP4_MXFP4, rows_in_place != 0);
 }
 
 size_t fp4_gemm_bf16a_workspace_size(int64_t M, int64_t N, int64_t K) {

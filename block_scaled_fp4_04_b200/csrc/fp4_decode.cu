@@ -1056,11 +1056,9 @@ static int launch_decode_any(const DecodeProblem& q, const DecodeExtra* x, unsig
     a.pre2 = x->pre2;
   }
   if (gated && q.X)
-    e = BN == 16 ? run_decode<16, true, kEpiGated>(tw, tx, tw2, a, grid, st)
-                 : run_decode<32, true, kEpiGated>(tw, tx, tw2, a, grid, st);
+    e = run_decode<16, true, kEpiGated>(tw, tx, tw2, a, grid, st);
   else if (gated)
-    e = BN == 16 ? run_decode<16, false, kEpiGated>(tw, tx, tw2, a, grid, st)
-                 : run_decode<32, false, kEpiGated>(tw, tx, tw2, a, grid, st);
+    e = run_decode<16, false, kEpiGated>(tw, tx, tw2, a, grid, st);
   else if (x)
     e = BN == 16 ? run_decode<16, false, kEpiFull>(tw, tx, tw2, a, grid, st)
                  : run_decode<32, false, kEpiFull>(tw, tx, tw2, a, grid, st);
@@ -1083,6 +1081,10 @@ int launch_decode_extra(const DecodeProblem& q, const DecodeExtra& x, unsigned* 
                         const char** why, cudaError_t* err) {
   if (!x.W2 && q.X) {  // the long epilogue takes quantized activations only
     *why = "BF16 activations with a residual or a pre-activation";
+    return 1;
+  }
+  if (x.W2 && !gated_decode_eligible(q.M, q.N, q.K)) {
+    *why = "gated decode kernel: 1 <= M <= 16";
     return 1;
   }
   return launch_decode_any(q, &x, status, st, why, err);

@@ -10,7 +10,7 @@
 namespace fp4 {
 
 // A tile is 128 (a CTA pair: 256) rows by 128 output columns.
-static Plan gated_plan(int64_t M, int64_t F, int64_t K, int groups) {
+static Plan gated_plan(int64_t M, int64_t F, int64_t K, int groups, int mx) {
   Plan pl{};
   pl.num_kb = static_cast<int>((K + 255) / 256);
   pl.BN = 256;
@@ -20,7 +20,10 @@ static Plan gated_plan(int64_t M, int64_t F, int64_t K, int groups) {
   pl.tiles_n = static_cast<int>((F + 127) / 128);
   if (groups) {
     pl.mode = kModeGrouped;
-    pl.pair = M >= 1280 * static_cast<int64_t>(groups);
+    // CTA pairs for many rows per expert, as the plain grouped product's; with MXFP4's half as
+    // many scale copies single CTAs are faster throughout (us, pairs / singles: 32 experts x 2048
+    // rows x 2880 x 2880 732 / 695, 8 x 4096 x 4096 x 4096 589 / 549, 4 x 2048 x 8192 x 8192 568 / 507)
+    pl.pair = !mx && M >= 1280 * static_cast<int64_t>(groups);
     return pl;
   }
   pl.tiles_m = static_cast<int>((M + 127) / 128);
@@ -41,6 +44,7 @@ static Plan gated_plan(int64_t M, int64_t F, int64_t K, int groups) {
   }
   pl.mode = kModeTile;
   pl.units = tiles;
+  // (NVFP4 4096 x 8192 x 8192: pairs 251 us, singles 293; MXFP4 245 both)
   if (M >= 256 && tiles >= sms) {
     pl.pair = true;
     pl.tiles_m = static_cast<int>((M + 255) / 256);
@@ -57,7 +61,7 @@ bool gated_decode_eligible(int64_t M, int64_t F, int64_t K) { return M <= 16 && 
 
 size_t gated_workspace_bytes(int64_t M, int64_t F, int64_t K, int mx, bool rows_in_place) {
   if (!mx && !rows_in_place && gated_decode_eligible(M, F, K)) return decode_gated_workspace_bytes(M, F);
-  return gated_plan(M, F, K, 0).ws_bytes;
+  return gated_plan(M, F, K, 0, mx).ws_bytes;
 }
 
 template <bool MX>
@@ -98,7 +102,7 @@ int launch_gated(const GatedProblem& g, unsigned* status, cudaStream_t st, const
     x.pre2 = g.U;
     return launch_decode_extra(q, x, status, st, why, err);
   }
-  const Plan pl = gated_plan(g.M, g.F, g.K, g.num_groups);
+  const Plan pl = gated_plan(g.M, g.F, g.K, g.num_groups, g.mx);
   if (g.ws_bytes < pl.ws_bytes || (pl.ws_bytes && !g.ws)) {
     *why = "workspace too small (see fp4_gemm_gated_workspace_size)";
     return 1;

@@ -236,8 +236,7 @@ Plan make_plan(int64_t M, int64_t N, int64_t K, int groups, int mx, bool row_maj
   if (tiles < 2 * sms && pl.num_kb >= 4 && (pl.swap || (2 * tiles < sms && pl.num_kb >= 16))) {
     pl.mode = kModeStreamK;
     pl.units = tiles * pl.num_kb;
-    // (rows of whole float4s, as the long epilogue keeps them)
-    pl.ws_bytes = (static_cast<size_t>(M * ((N + 3) / 4 * 4)) * 4 + 255) / 256 * 256 + (static_cast<size_t>(tiles) * 4 + 255) / 256 * 256;
+    pl.ws_bytes = (static_cast<size_t>(M * N) * 4 + 255) / 256 * 256 + (static_cast<size_t>(tiles) * 4 + 255) / 256 * 256;
   } else {
     pl.mode = kModeTile;
     pl.units = tiles;
@@ -256,6 +255,17 @@ Plan make_plan(int64_t M, int64_t N, int64_t K, int groups, int mx, bool row_maj
 size_t gemm_workspace_bytes(int64_t M, int64_t N, int64_t K, int mx, bool fp4_out) {
   if (!mx && !fp4_out && decode_eligible(M, N, K)) return decode_workspace_bytes(M, N);
   return make_plan(M, N, K, 0, mx, fp4_out).ws_bytes;
+}
+
+// The long epilogue keeps its partial sums in rows of whole float4s.
+static size_t full_ws_bytes(const Plan& pl, int64_t M) {
+  if (pl.mode != kModeStreamK || pl.swap) return pl.ws_bytes;
+  return pl.ws_bytes + static_cast<size_t>(M) * 3 * 4 + 256;  // at most three floats more per row
+}
+
+size_t gemm_full_workspace_bytes(int64_t M, int64_t N, int64_t K, int mx, bool fp4_out) {
+  if (!mx && !fp4_out && decode_eligible(M, N, K)) return decode_workspace_bytes(M, N);
+  return full_ws_bytes(make_plan(M, N, K, 0, mx, fp4_out), M);
 }
 
 // the quantize workspace (tensor amax), then the GEMM's
@@ -312,7 +322,8 @@ int launch_gemm_full(const GemmProblemFull& g, unsigned* status, cudaStream_t st
   }
   // the NVFP4 copy of the result is written by rows: keep the operands in place
   const Plan pl = make_plan(g.M, g.N, g.K, g.num_groups, g.mx, g.q_codes != nullptr || g.amax_out != nullptr);
-  if (g.ws_bytes < pl.ws_bytes || (pl.ws_bytes && !g.ws)) {
+  const size_t need = g.full ? full_ws_bytes(pl, g.M) : pl.ws_bytes;
+  if (g.ws_bytes < need || (need && !g.ws)) {
     *why = "workspace too small (see fp4_gemm_workspace_size)";
     return 1;
   }

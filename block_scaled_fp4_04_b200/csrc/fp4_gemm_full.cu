@@ -11,9 +11,11 @@ static cudaError_t dispatch_full_t(const Plan& pl, const GemmMaps& tm, const Gem
     return pl.pair ? run<256, MX, 1, true, false, kEpiFullWhole>(tm, a, pl.units, st)
                    : run<256, MX, 1, false, false, kEpiFullWhole>(tm, a, pl.units, st);
   }
+  if constexpr (MX) {  // (up to 32 rows of NVFP4 take the decode kernel)
+    if (pl.BN == 16) return run<16, MX, 2, false, false, kEpiFull>(tm, a, pl.units, st);
+    if (pl.BN == 32) return run<32, MX, 2, false, false, kEpiFull>(tm, a, pl.units, st);
+  }
   switch (pl.BN) {
-    case 16: return run<16, MX, 2, false, false, kEpiFull>(tm, a, pl.units, st);
-    case 32: return run<32, MX, 2, false, false, kEpiFull>(tm, a, pl.units, st);
     case 64: return run<64, MX, 2, false, false, kEpiFull>(tm, a, pl.units, st);
     case 128: return run<128, MX, 2, false, false, kEpiFull>(tm, a, pl.units, st);
     default:

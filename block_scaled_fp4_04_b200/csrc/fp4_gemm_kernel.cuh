@@ -440,18 +440,6 @@ __device__ __forceinline__ void ld_sector(const void* p, uint32_t* w) {
                : "memory");
 }
 
-// 8 consecutive elements at offset `at` of a BF16 or FP32 matrix, 16-byte aligned.
-__device__ __forceinline__ void store_vec8(void* out, int bf16, int64_t at, const float (&v)[8]) {
-  if (bf16) {
-    __stcs(reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(out) + at),
-           make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])));
-  } else {
-    float4* dst = reinterpret_cast<float4*>(static_cast<float*>(out) + at);
-    __stcs(dst, make_float4(v[0], v[1], v[2], v[3]));
-    __stcs(dst + 1, make_float4(v[4], v[5], v[6], v[7]));
-  }
-}
-
 // Where a warp of the long epilogues is: 32 rows from row0 (the first `rows` of them exist), this
 // lane's row being row0 + lane, and `cols` (at most 16) columns from col.
 struct EpiSpot {
@@ -643,69 +631,38 @@ __device__ __forceinline__ void epi_rows(const GemmArgs& p, const EpiSpot& s, co
   }
 }
 
-// Offset in the output of kernel row `row`, column `col`.
-__device__ __forceinline__ int64_t out_offset(const GemmArgs& p, int row, int col) {
-  return p.transposed ? static_cast<int64_t>(col) * p.ldo + row : static_cast<int64_t>(row) * p.ldo + col;
-}
-
-// Stores 16 values of kernel row `row`, columns [col, col + 16), to a matrix laid out as the
-// output is (`out` in the output's type); columns past the matrix are left out.
-__device__ __forceinline__ void store_like_out(const GemmArgs& p, void* out, int row, int col, const float (&v)[16]) {
-  if (!p.transposed && p.vec_store && col + 16 <= p.Nk) {
-    float a[8], b[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      a[j] = v[j];
-      b[j] = v[8 + j];
-    }
-    const int64_t at = out_offset(p, row, col);
-    store_vec8(out, p.out_bf16, at, a);
-    store_vec8(out, p.out_bf16, at + 8, b);
-    return;
-  }
-#pragma unroll
-  for (int j = 0; j < 16; ++j)
-    if (col + j < p.Nk) {
-      const int64_t off = out_offset(p, row, col + j);
-      if (p.out_bf16) static_cast<__nv_bfloat16*>(out)[off] = __float2bfloat16_rn(v[j]);
-      else static_cast<float*>(out)[off] = v[j];
-    }
-}
-
-// Adds 16 elements of the residual (same rows and columns as the output, its own type).
-__device__ __forceinline__ void add_residual16(const GemmArgs& p, int row, int col, float (&v)[16]) {
-#pragma unroll
-  for (int j = 0; j < 16; ++j)
-    if (col + j < p.Nk) {
-      const int64_t off = out_offset(p, row, col + j);
-      v[j] += p.res_bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(p.res)[off]) : static_cast<const float*>(p.res)[off];
-    }
-}
-
-// Bias of 16 kernel columns (swapped operands: of the kernel row, which is the output column).
-__device__ __forceinline__ void add_bias16(const GemmArgs& p, const float* bias, int row, int col, float (&v)[16]) {
-  if (p.transposed) {
-    const float b = __ldg(bias + row);
+// kEpiFull on small-N tiles, whose operands are swapped (kernel rows are output columns, so that
+// neighbouring lanes touch neighbouring elements): finishes 16 consecutive kernel columns, i.e.
+// output rows, of kernel row `row` (values already multiplied by the global scales).
+__device__ __forceinline__ void epi_finish16(const GemmArgs& p, int row, int col, float (&v)[16]) {
+  if (p.bias) {
+    const float b = __ldg(p.bias + row);
 #pragma unroll
     for (int j = 0; j < 16; ++j) v[j] = __fadd_rn(v[j], b);
-  } else {
+  }
+  auto put = [&](void* out) {
 #pragma unroll
     for (int j = 0; j < 16; ++j)
-      if (col + j < p.Nk) v[j] = __fadd_rn(v[j], __ldg(bias + col + j));
-  }
-}
-
-// kEpiFull on small-N tiles: finishes 16 consecutive kernel columns of one kernel row (values
-// already multiplied by the global scales).
-__device__ __forceinline__ void epi_finish16(const GemmArgs& p, int row, int col, float (&v)[16]) {
-  if (p.bias) add_bias16(p, p.bias, row, col, v);
-  if (p.pre) store_like_out(p, p.pre, row, col, v);
+      if (col + j < p.Nk) {
+        const int64_t at = static_cast<int64_t>(col + j) * p.ldo + row;
+        if (p.out_bf16) static_cast<__nv_bfloat16*>(out)[at] = __float2bfloat16_rn(v[j]);
+        else static_cast<float*>(out)[at] = v[j];
+      }
+  };
+  if (p.pre) put(p.pre);
   with_act(p.act, [&](auto tag) __attribute__((always_inline)) {
 #pragma unroll
     for (int j = 0; j < 16; ++j) v[j] = act_value<decltype(tag)::value>(v[j]);
   });
-  if (p.res) add_residual16(p, row, col, v);
-  if (p.out) store_like_out(p, p.out, row, col, v);
+  if (p.res) {
+#pragma unroll
+    for (int j = 0; j < 16; ++j)
+      if (col + j < p.Nk) {
+        const int64_t at = static_cast<int64_t>(col + j) * p.ldo + row;
+        v[j] += p.res_bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(p.res)[at]) : static_cast<const float*>(p.res)[at];
+      }
+  }
+  put(p.out);
 }
 
 // Named barrier among the epilogue threads of one pipeline.

@@ -87,6 +87,7 @@ struct GemmFull {
 struct GemmProblemFull : GemmProblem {
   const GemmFull* full;
 };
+size_t gemm_full_workspace_bytes(int64_t M, int64_t N, int64_t K, int mx, bool fp4_out);
 int launch_gemm_full(const GemmProblemFull& g, unsigned* status, cudaStream_t st, const char** why, cudaError_t* err);
 
 // The decode kernel with the long epilogue, or with a second weight (a gated product: W and

@@ -17,10 +17,11 @@ __device__ __forceinline__ void rows_allow_dependents() { asm volatile("griddepc
 __device__ __forceinline__ void rows_wait_prior() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // V consecutive elements of a row as they lie in memory: one 16-byte word (V = 8 BF16 or 4
-// FP32) or a single element (V = 1, for rows whose start is not 16-byte aligned).
+// FP32), or, for rows that do not start at 16 bytes, a pair (V = 2: even lengths) or a single
+// element.
 template <typename T, int V>
 struct RowVec {
-  static constexpr int kWords = V == 1 ? 1 : 4;
+  static constexpr int kWords = V == 1 ? 1 : V * static_cast<int>(sizeof(T)) / 4;
   uint32_t w[kWords];
   __device__ __forceinline__ void zero() {
 #pragma unroll
@@ -32,6 +33,12 @@ struct RowVec {
     if constexpr (V == 1) {
       if constexpr (sizeof(T) == 4) w[0] = *reinterpret_cast<const unsigned*>(p);
       else w[0] = *reinterpret_cast<const unsigned short*>(p);
+    } else if constexpr (V == 2 && sizeof(T) == 2) {
+      w[0] = *reinterpret_cast<const unsigned*>(p);
+    } else if constexpr (V == 2) {
+      const uint2 t = *reinterpret_cast<const uint2*>(p);
+      w[0] = t.x;
+      w[1] = t.y;
     } else {
       static_assert(V * sizeof(T) == 16, "one 16-byte word");
       asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
@@ -73,7 +80,10 @@ __device__ __forceinline__ void store_row_vec(void* out, int out_bf16, int64_t o
     for (int i = 0; i < V / 2; ++i) w[i] = rows_pack_bf16x2(v[2 * i], v[2 * i + 1]);
     __nv_bfloat16* p = static_cast<__nv_bfloat16*>(out) + off;
     if constexpr (V == 8) __stcs(reinterpret_cast<uint4*>(p), make_uint4(w[0], w[1], w[2], w[3]));
-    else __stcs(reinterpret_cast<uint2*>(p), make_uint2(w[0], w[1]));
+    else if constexpr (V == 4) __stcs(reinterpret_cast<uint2*>(p), make_uint2(w[0], w[1]));
+    else __stcs(reinterpret_cast<unsigned*>(p), w[0]);
+  } else if constexpr (V == 2) {
+    __stcs(reinterpret_cast<float2*>(static_cast<float*>(out) + off), make_float2(v[0], v[1]));
   } else {
     float4* p = reinterpret_cast<float4*>(static_cast<float*>(out) + off);
 #pragma unroll
@@ -86,6 +96,10 @@ template <int V>
 __device__ __forceinline__ void load_params(const float* p, float (&v)[V]) {
   if constexpr (V == 1) {
     v[0] = __ldg(p);
+  } else if constexpr (V == 2) {
+    const float2 f = __ldg(reinterpret_cast<const float2*>(p));
+    v[0] = f.x;
+    v[1] = f.y;
   } else {
 #pragma unroll
     for (int i = 0; i < V; i += 4) {

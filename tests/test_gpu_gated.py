@@ -148,7 +148,8 @@ def test_gemm_gated_bf16a(m, f, k, out, act, save):
     ([0, 0, 7], 129, 256, fp4.NVFP4),
     ([128, 256, 300, 17, 0, 64], 384, 2880, fp4.MXFP4),
     ([1300, 1400], 256, 512, fp4.NVFP4),           # CTA pairs
-    ([1500, 0, 2400], 333, 96, fp4.MXFP4),         # CTA pairs, ragged columns
+    ([1500, 0, 2400], 333, 96, fp4.NVFP4),         # CTA pairs, ragged columns
+    ([1500, 0, 2400], 336, 96, fp4.MXFP4),         # many rows, whole sectors
 ])
 @pytest.mark.parametrize("out,save", [(torch.bfloat16, False), (torch.float32, True)])
 def test_gemm_gated_grouped(counts, f, k, fmt, out, save):

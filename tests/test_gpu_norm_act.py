@@ -51,7 +51,7 @@ def _ln_error(x, w, y, mean, rstd, var, n):
 
 
 LN_SHAPES = [(1, 1), (3, 7), (5, 32), (130, 256), (2, 513), (7, 1000), (16, 2880), (33, 8192), (9, 5760), (3, 16384),
-             (2, 28672), (4, 12289), (300, 64), (1, 20011),
+             (2, 28672), (4, 12289), (300, 64), (1, 20011), (9, 1002), (5, 4098), (3, 8190),
              # enough rows for the rings
              (2387, 800), (2400, 1032), (2500, 2048), (2370, 2880), (2369, 5760), (2371, 4096), (2368, 8192),
              (2369, 16384)]
@@ -142,7 +142,8 @@ def _ln_grad64(dy, x, w, mean, rstd, dres):
 @pytest.mark.parametrize("rows,n", [(1, 1), (3, 7), (700, 32), (130, 256), (513, 513), (7, 1000), (301, 2880), (33, 8192),
                                     (5, 16384), (2, 28672), (600, 64), (3, 12289), (149, 5760),
                                     (1187, 800), (1200, 1032), (1500, 2048), (1184, 2880), (1190, 5760),
-                                    (1185, 8192), (300, 16384), (700, 2881), (20, 5003), (300, 16400)])
+                                    (1185, 8192), (300, 16384), (700, 2881), (20, 5003), (300, 16400),
+                                    (400, 1002), (7, 4098), (6, 8190), (5, 16386), (70, 250)])
 @pytest.mark.parametrize("dtype,out", [(torch.float32, torch.float32), (torch.bfloat16, torch.bfloat16),
                                        (torch.bfloat16, torch.float32)])
 @pytest.mark.parametrize("res", [True, False])
@@ -229,7 +230,7 @@ def _act_grad64(dh, g, u, act):
 @pytest.mark.parametrize("dtype,out", [(torch.float32, torch.float32), (torch.bfloat16, torch.bfloat16),
                                        (torch.bfloat16, torch.float32)])
 @pytest.mark.parametrize("rows,n,gated", [(1, 1, True), (3, 33, False), (130, 256, True), (70, 2880, False), (9, 28672, True),
-                                          (513, 100, True), (1000, 96, False)])
+                                          (513, 100, True), (1000, 96, False), (70, 1002, True), (33, 131, True)])
 def test_act_backward(act, dtype, out, rows, n, gated):
     dh, g = _rand((rows, n), n + rows, dtype), _rand((rows, n), n, dtype, 2.5)
     u = _rand((rows, n), rows, dtype) if gated else None
