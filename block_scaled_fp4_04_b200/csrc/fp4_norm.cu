@@ -981,20 +981,22 @@ __global__ void __launch_bounds__(kLongWarps * 32) ln_columns_long_kernel(const 
 }
 
 // ------------------------------------------------------------------ column sums
-// 32 columns per CTA; its eight warps each add an eighth of the partial sums, in order, and
-// the eighths are added in order.
-// The partial sums are cleared behind it: a zero-filled workspace that other calls share stays so.
-__global__ void __launch_bounds__(256) column_sums_kernel(float* part, int parts, int64_t width,
-                                                          int64_t n0, float* out0, float* out1) {
-  __shared__ float s[8][32];
+// 32 columns per CTA; each of its warps adds its share of the partial sums, in order, and the
+// shares are added in order.  (Sixteen warps: at the usual 148 parts a thread's ten loads are in
+// flight together.)  The partial sums are cleared behind it: a zero-filled workspace that other
+// calls share stays so.
+constexpr int kSumWarps = 16;
+__global__ void __launch_bounds__(kSumWarps * 32) column_sums_kernel(float* part, int parts, int64_t width, int64_t n0,
+                                                                     float* out0, float* out1) {
+  __shared__ float s[kSumWarps][32];
   rows_allow_dependents();
   rows_wait_prior();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + lane;
   float v = 0.0f;
   if (c < width) {
-    const int p0 = parts * warp / 8, p1 = parts * (warp + 1) / 8;
-#pragma unroll 4
+    const int p0 = parts * warp / kSumWarps, p1 = parts * (warp + 1) / kSumWarps;
+#pragma unroll 10
     for (int q = p0; q < p1; ++q) v += __ldcg(part + static_cast<int64_t>(q) * width + c);
     for (int q = p0; q < p1; ++q) __stcg(part + static_cast<int64_t>(q) * width + c, 0.0f);
   }
@@ -1003,7 +1005,7 @@ __global__ void __launch_bounds__(256) column_sums_kernel(float* part, int parts
   if (warp == 0 && c < width) {
     v = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v += s[i][lane];
+    for (int i = 0; i < kSumWarps; ++i) v += s[i][lane];
     if (c < n0) {
       if (out0) out0[c] = v;
     } else if (out1) {
@@ -1014,8 +1016,8 @@ __global__ void __launch_bounds__(256) column_sums_kernel(float* part, int parts
 
 cudaError_t launch_column_sums(float* part, int parts, int64_t width, int64_t n0, float* out0, float* out1,
                                cudaStream_t st) {
-  return launch_rows(column_sums_kernel, dim3(static_cast<unsigned>((width + 31) / 32)), 256, 0, st, part, parts, width,
-                     n0, out0, out1);
+  return launch_rows(column_sums_kernel, dim3(static_cast<unsigned>((width + 31) / 32)), kSumWarps * 32, 0, st, part,
+                     parts, width, n0, out0, out1);
 }
 
 constexpr int kLnMaxParts = 2 * 148;
