@@ -217,8 +217,9 @@ struct Cfg {
   // is few enough registers to hold the tile while TMEM is already handed back.
   // The long epilogues have too much arithmetic for that: four warps per quarter, which take 32
   // sums at a time and hold the last 32 (half of the tile) while TMEM is handed back.  Measured
-  // on tiles of one K step (8192 x 8192 outputs, BF16): SILU 88 us with eight warps that held all
-  // their 128 sums at 128 registers, 83 us so, with bias, GELU, residual and pre-activation 276 / 175.
+  // on tiles of one K step (8192 x 8192 outputs, BF16) with bias, GELU, residual and pre-activation:
+  // 276 us with eight warps that held all their 128 sums at 128 registers, 159 us so.  SILU alone
+  // gains nothing by it (88 / 98 us): the switch over the activation takes what the warps give.
   static constexpr bool kLong = kSepCp && EPI != kEpiPlain;
   static constexpr int kEpiWarps = kLong ? 16 : kSepCp ? 8 : 4;
   static constexpr int kEpiCols = BN * 4 / kEpiWarps;  // accumulator columns per epilogue thread
