@@ -471,7 +471,7 @@ def layernorm(x: torch.Tensor, weight=None, bias=None, eps: float = 1e-5, out_dt
               global_in=None, stream=None, out: Optional[torch.Tensor] = None):
     """Layer norm of the rows of x [rows, cols]: (y, mean, rstd).  With `fmt` (NVFP4, which needs
     the caller's `global_in`, or MXFP4) y is a Quantized tensor instead, without a copy in
-    between."""
+    between.  `out` may be x itself."""
     if x.dim() != 2:
         raise ValueError("x must be [rows, cols]")
     rows, cols = x.shape

@@ -720,6 +720,7 @@ fp4_status fp4_layernorm(const void* x, int64_t rows, int64_t cols, fp4_dtype in
   if (!dtype_ok(in_dtype) || !dtype_ok(out_dtype)) return fail(FP4_ERR_INVALID_ARG, "in_dtype / out_dtype");
   if (!(eps >= 0.0f) || eps > 3.4e38f) return fail(FP4_ERR_INVALID_ARG, "eps must be finite and not negative");
   if (!aligned16(x) || !aligned16(y)) return fail(FP4_ERR_INVALID_ARG, "x and y must be 16-byte aligned");
+  if (y == x && in_dtype != out_dtype) return fail(FP4_ERR_INVALID_ARG, "y in x's place needs x's type");
   if (!aligned4(weight) || !aligned4(bias) || !aligned4(mean) || !aligned4(rstd) || !aligned4(amax_out))
     return fail(FP4_ERR_INVALID_ARG, "weight / bias / mean / rstd / amax_out alignment");
   CodesOut q;

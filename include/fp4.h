@@ -328,7 +328,8 @@ fp4_status fp4_gemm_gated_bf16a(const void* X_dev, const uint8_t* Wg_dev, const 
                                 float* gX_dev, void* workspace_dev, size_t workspace_bytes, unsigned flags,
                                 void* stream);
 
-/* The gated product by experts (rows and offsets as for fp4_gemm_grouped): rows
+/* The gated product by experts (rows and offsets as for fp4_gemm_grouped, but the last offset
+ * may stay below total_rows: rows behind it are left as they were): rows
  * [offsets[e], offsets[e+1]) of A with expert e's weights Wg_dev + e*F*K/2, Wu_dev + e*F*K/2.
  *   sWg_dev, sWu_dev  num_groups consecutive fp4_scales_bytes(F, K, fmt) blocks;
  *   gWg_dev, gWu_dev  [num_groups] floats or NULL; bias_g_dev, bias_u_dev [num_groups, F] or
@@ -366,13 +367,15 @@ fp4_status fp4_act_backward(const void* dH_dev, const void* G_dev, const void* U
  *   y = (x - mean) rstd weight + bias,  mean = sum x / cols,
  *   rstd = 1 / sqrt(sum (x - mean)^2 / cols + eps)
  *   weight_dev, bias_dev  [cols] FP32, or NULL (1 and 0).
- *   y_dev   [rows, cols] in out_dtype, or NULL; codes_dev / scales_dev: or y as the A operand
+ *   y_dev   [rows, cols] in out_dtype (it may be x itself where the types agree, if no backward
+ *           pass needs x), or NULL; codes_dev / scales_dev: or y as the A operand
  *           of the next product (or both): `fmt` blocks along the columns, NVFP4 with the
  *           caller's global scale global_dev or MXFP4, exactly as fp4_quantize would quantize
  *           the FP32 y (cols % 32 == 0; a non-finite value latches FP4_ERR_NONFINITE).
  *   mean_dev, rstd_dev  [rows] FP32, which the backward pass needs, or NULL.
  *   amax_out_dev  1 float or NULL: max |y| (zeroed, then written by this call).
- * eps >= 0.  x, y, codes and scales 16-byte aligned; any cols >= 1. */
+ * eps >= 0.  x, y, codes and scales 16-byte aligned, with codes weight and bias too; any
+ * cols >= 1. */
 fp4_status fp4_layernorm(const void* x_dev, int64_t rows, int64_t cols, fp4_dtype in_dtype, const float* weight_dev,
                          const float* bias_dev, float eps, void* y_dev, fp4_dtype out_dtype, float* mean_dev,
                          float* rstd_dev, fp4_fmt fmt, uint8_t* codes_dev, uint8_t* scales_dev,

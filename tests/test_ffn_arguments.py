@@ -35,6 +35,12 @@ def test_layernorm_refuses(kw):
     assert _call("fp4_layernorm", LN, **kw) == fp4.ERR_INVALID_ARG
 
 
+
+def test_layernorm_in_place_needs_one_type():
+    assert _call("fp4_layernorm", LN, y=16, out=fp4.BF16) == fp4.ERR_INVALID_ARG
+    assert "x's place" in fp4.fp4_last_error()
+
+
 LNB = dict(dy=16, x=32, rows=4, cols=64, dt=fp4.F32, w=16, mean=16, rstd=16, dres=48, dx=64, out=fp4.F32, dw=16, db=16,
            ws=16, wsb=1 << 20, stream=None)
 

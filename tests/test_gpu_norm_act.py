@@ -79,6 +79,18 @@ def test_layernorm(rows, n, dtype, out):
     assert fp4.fp4_get_status() == fp4.OK
 
 
+@pytest.mark.parametrize("rows,n", [(1, 1), (3, 7), (33, 8192), (300, 1002), (3, 20011), (5, 40000), (2500, 2048),
+                                    (2400, 1032), (2369, 5760), (2369, 16384)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_layernorm_in_place(rows, n, dtype):
+    x = _rand((rows, n), rows + n, dtype, 1.5, 0.7).cuda()
+    w, b = _cuda(_rand((n,), 1, std=0.5, mean=1.0), _rand((n,), 2, std=0.5))
+    y, mean, rstd = fp4.layernorm(x, w, b)
+    z, mean2, rstd2 = fp4.layernorm(x, w, b, out=x)
+    assert z.data_ptr() == x.data_ptr()
+    assert torch.equal(z, y) and torch.equal(mean, mean2) and torch.equal(rstd, rstd2)
+
+
 def test_layernorm_of_constant_and_shifted_rows():
     """A constant row has variance 0: y is the bias, rstd 1 / sqrt(eps).  A large common offset
     does not spoil the variance (two passes, no difference of squares)."""
