@@ -191,6 +191,41 @@ def test_gemm_gated_grouped(counts, f, k, fmt, out, save):
             assert_close(u[:rows * f].view(rows, f)[lo:hi], u64, eu, f"U of expert {e}")
 
 
+
+@pytest.mark.parametrize("counts,pad,f,k,fmt", [
+    ([5, 0, 130], 70, 200, 96, fp4.MXFP4),
+    ([0, 0], 40, 128, 256, fp4.NVFP4),             # no rows at all
+    ([1300, 700], 1000, 256, 512, fp4.NVFP4),      # CTA pairs
+])
+def test_gemm_gated_grouped_leaves_rows_behind_the_last_expert(counts, pad, f, k, fmt):
+    E, rows = len(counts), sum(counts)
+    total = rows + pad
+    offs = torch.tensor([0] + list(np.cumsum(counts)), dtype=torch.int32).cuda()
+    qx = gpu_quantize(random_input(total, k, 3, torch.bfloat16).cuda(), fmt, _blk(fmt))
+    scales = torch.full((fp4.fp4_scales_bytes_grouped(total, E, k, fmt),), 0x38 if fmt == fp4.NVFP4 else 127,
+                        dtype=torch.uint8, device="cuda")
+    w = [gpu_quantize(random_input(E * f, k, s, torch.float32, std=0.05, outliers=False).cuda(), fmt, _blk(fmt))
+         for s in (1, 2)]
+    ws = [torch.full((E * fp4.fp4_scales_bytes(f, k, fmt),), 0x38 if fmt == fp4.NVFP4 else 127, dtype=torch.uint8,
+                     device="cuda") for _ in w]
+
+    def run(n):
+        out = [torch.full((total * f + 8,), 7.0, device="cuda") for _ in range(3)]
+        fp4.fp4_gemm_gated_grouped(fmt, E, offs, qx.codes, scales, None, w[0].codes, ws[0], None, w[1].codes, ws[1], None,
+                                   n, f, k, None, None, fp4.ACT_SILU, out[0], fp4.F32, out[1], out[2])
+        torch.cuda.synchronize()
+        assert fp4.fp4_get_status() == fp4.OK
+        return out
+
+    # With scales of 1 the products are multiples of 1/4 and their sums stay below 2^22 of
+    # those: exact in FP32 in any order, so both calls give the same bits.
+    padded = run(total)
+    assert all((b[rows * f:] == 7.0).all() for b in padded), "a row behind the last expert's was written"
+    if rows:
+        for b, c in zip(padded, run(rows)):
+            assert torch.equal(b, c)
+
+
 EPI = [
     # m, n, k, fmt
     (1, 333, 2080, fp4.NVFP4),       # decode kernel
