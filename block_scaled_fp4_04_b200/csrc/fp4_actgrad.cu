@@ -43,8 +43,8 @@ __global__ void __launch_bounds__(kAgWarps * 32) act_grad_kernel(const ActGradAr
   constexpr int U = 2;  // rows in flight per warp
   constexpr int J = ag_words<V>();
   __shared__ float s_sum[kAgWarps][kHalves][32 * V * J];
-  rows_allow_dependents();
   rows_wait_prior();
+  rows_allow_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int col0 = (blockIdx.x * 32 * J + lane) * V;
   const int64_t r0 = static_cast<int64_t>(blockIdx.y) * p.rows_per;

@@ -108,6 +108,8 @@ struct DecodeCfg {
   static_assert(kBBox % 1024 == 0 && kStageBytes % 1024 == 0 && kSubBytes % 1024 == 0, "1024-byte alignment");
 };
 
+// Called after the wait: the next kernel may read weights without a wait of its own, if they
+// were written before this kernel, so what is older than this kernel must be finished by then.
 __device__ __forceinline__ void d_allow_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void d_wait_prior_grids() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
@@ -329,7 +331,6 @@ __global__ void __launch_bounds__(DecodeCfg<BN>::kThreads, 1)
     tmem_alloc(&s_tmem_base, C::kTmemAlloc);
     tmem_relinquish();
   }
-  d_allow_dependents();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -530,6 +531,7 @@ __global__ void __launch_bounds__(DecodeCfg<BN>::kThreads, 1)
     if constexpr (FUSED) {
       // ---------------------------------------------------------- activations
       d_wait_prior_grids();  // X may come from the kernel just before
+      d_allow_dependents();
       // zero the scale atoms: rows M..127 of every atom are padding
       for (int o = xt * 16; o < C::kBSFBytes; o += 256 * 16)
         *reinterpret_cast<uint4*>(s_bsf + o) = make_uint4(0, 0, 0, 0);
@@ -718,7 +720,10 @@ __global__ void __launch_bounds__(DecodeCfg<BN>::kThreads, 1)
       }
     }
     // ------------------------------------------------------------ epilogue
-    if (!FUSED) d_wait_prior_grids();  // the activations' global scale
+    if (!FUSED) {
+      d_wait_prior_grids();  // the activations' global scale
+      d_allow_dependents();
+    }
     const float gw = p.gw ? *p.gw : 1.0f;
     float scale;
     if constexpr (FUSED) {

@@ -289,7 +289,9 @@ __device__ __forceinline__ void red_add_v4(float* addr, float a, float b, float 
 __device__ __forceinline__ void wait_prior_grids() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // Lets the kernel launched after this one on the stream start its prologue now (it still
-// waits for this grid's completion before it reads what this grid writes).
+// waits for this grid's completion before it reads what this grid writes).  Called by warps
+// that have waited for the grids before this one: the next kernel may read weights without a
+// wait of its own, if they were written before this kernel, so what is older must be finished.
 __device__ __forceinline__ void allow_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 __device__ __forceinline__ void store_out(const GemmArgs& p, int64_t off, float v) {
@@ -758,8 +760,6 @@ __global__ void __launch_bounds__(Cfg<BN, MX, ACC, PAIR, F8, EPI>::kThreads, 1)
       tmem_relinquish();
     }
   }
-  // the next kernel on the stream may launch now; it waits for this grid to complete
-  allow_dependents();
   if (p.mode == kModeGrouped && warp == 2) {
     wait_prior_grids();  // the offsets may come from the previous kernel
     // m-tile prefix per group (= scale row-block prefix of the grouped A layout)
@@ -1147,6 +1147,7 @@ __global__ void __launch_bounds__(Cfg<BN, MX, ACC, PAIR, F8, EPI>::kThreads, 1)
         mbar_arrive(&acc_empty[a]);
     };
     wait_prior_grids();               // the global scales come from earlier kernels
+    allow_dependents();
     const float ga = p.ga ? *p.ga : 1.0f;
     uint32_t tmax = 0;                // max |result| over this thread's values (amax_out)
     Schedule sch(p, s_mt, s_off, vb, vg, kMTile, sub_row, s_pt);

@@ -53,8 +53,8 @@ __global__ void __launch_bounds__((WPR < 4 ? 4 : WPR) * 32) ln_forward_kernel(co
   constexpr int kRows = kWarps / WPR;  // rows per CTA
   constexpr int kCh = C > 0 ? C : 1;
   __shared__ float s_red[2][kRows][WPR];
-  rows_allow_dependents();
   rows_wait_prior();
+  rows_allow_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int group = warp / WPR, wr = warp % WPR, bar = 1 + group;
   const int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + group;
@@ -246,8 +246,8 @@ __global__ void __launch_bounds__(W * 32, 1) ln_forward_ring_kernel(const LnArgs
     fence_mbar_init();
   }
   __syncthreads();
-  rows_allow_dependents();
   rows_wait_prior();
+  rows_allow_dependents();
   const int64_t stride = static_cast<int64_t>(gridDim.x) * G * R;
   int64_t row = (static_cast<int64_t>(blockIdx.x) * G + group) * R;
   const bool loader = wr == 0 && lane == 0;
@@ -547,8 +547,8 @@ __global__ void __launch_bounds__((WPR < 8 ? 8 : WPR) * 32) ln_backward_kernel(c
   constexpr int kRows = kWarps / WPR;
   constexpr int kStep = WPR * 32 * V;
   __shared__ float s_red[2][2][kRows][WPR];
-  rows_allow_dependents();
   rows_wait_prior();
+  rows_allow_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int group = warp / WPR, wr = warp % WPR, bar = 1 + group;
   const int first = (wr * 32 + lane) * V;
@@ -707,8 +707,8 @@ __global__ void __launch_bounds__(kRingWarps * 32, 1) ln_backward_ring_kernel(co
     fence_mbar_init();
   }
   __syncthreads();
-  rows_allow_dependents();
   rows_wait_prior();
+  rows_allow_dependents();
   const int64_t stride = static_cast<int64_t>(gridDim.x) * G;
   int64_t row = static_cast<int64_t>(blockIdx.x) * G + group;
   const bool loader = wr == 0 && lane == 0;
@@ -890,8 +890,8 @@ static bool pick_ln_grad_ring(const LnGradArgs& a, int* parts, unsigned* status,
 template <typename T>
 __global__ void __launch_bounds__(512) ln_backward_long_kernel(const LnGradArgs p) {
   __shared__ float s_red[2][16];
-  rows_allow_dependents();
   rows_wait_prior();
+  rows_allow_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const float inv_n = 1.0f / static_cast<float>(p.n);
   const int64_t base = static_cast<int64_t>(blockIdx.x) * p.n;
@@ -937,8 +937,8 @@ constexpr int kLongWarps = 8;
 template <typename T, int V>
 __global__ void __launch_bounds__(kLongWarps * 32) ln_columns_long_kernel(const LnGradArgs p, int64_t rows_per_part) {
   __shared__ float s_sum[kLongWarps][2][V][32];
-  rows_allow_dependents();
   rows_wait_prior();
+  rows_allow_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int col = (blockIdx.x * 32 + lane) * V;
   const int64_t r0 = static_cast<int64_t>(blockIdx.y) * rows_per_part;
@@ -989,8 +989,8 @@ constexpr int kSumWarps = 16;
 __global__ void __launch_bounds__(kSumWarps * 32) column_sums_kernel(float* part, int parts, int64_t width, int64_t n0,
                                                                      float* out0, float* out1) {
   __shared__ float s[kSumWarps][32];
-  rows_allow_dependents();
   rows_wait_prior();
+  rows_allow_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + lane;
   float v = 0.0f;

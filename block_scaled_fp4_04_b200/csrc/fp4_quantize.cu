@@ -136,7 +136,8 @@ __device__ __forceinline__ uint32_t e8m0_floor_code(float amax_b) {
 
 // Programmatic dependent launch: let the next kernel on the stream start its prologue
 // early / wait until the previous kernel's writes are visible (no-ops without the
-// launch attribute).
+// launch attribute).  The wait comes first: the next kernel may read weights without a wait
+// of its own, if they were written before this kernel, so what is older must be finished.
 __device__ __forceinline__ void allow_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void wait_prior_grids() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
@@ -151,8 +152,8 @@ template <typename T, bool RHT = false>
 __global__ void __launch_bounds__(512) amax_kernel(const T* __restrict__ x, int64_t n, uint32_t* ws,
                                                     float* amax_out, float* g_out, unsigned* status,
                                                     uint32_t signs) {
-  allow_dependents();
   wait_prior_grids();  // x may be the output of the kernel just before
+  allow_dependents();
   constexpr int EPC = Elem<T>::kPerChunk;
   const int64_t nchunks = RHT ? 0 : n / EPC;
   const uint4* xc = reinterpret_cast<const uint4*>(x);
@@ -335,8 +336,8 @@ __global__ void __launch_bounds__(256, q1d_min_ctas<T, BLOCK, VAR, GROUPED>()) q
   extern __shared__ int s_grp[];
   int* const s_rb = s_grp;
   int* const s_off = s_grp + (GROUPED ? p.num_groups + 1 : 0);
-  allow_dependents();
   wait_prior_grids();  // g (and x, offsets) may come from the kernels just before
+  allow_dependents();
   const int E = GROUPED ? p.num_groups : 1;
   const int lane = threadIdx.x & 31;
   int rb_total = static_cast<int>((p.rows + 127) / 128);
@@ -558,8 +559,8 @@ __global__ void __cluster_dims__(kSmallCtas, 1, 1) __launch_bounds__(kSmallThrea
   __shared__ uint32_t s_warp[kSmallThreads / 32];
   __shared__ uint32_t s_cta[kSmallCtas];
 
-  allow_dependents();
   wait_prior_grids();  // x may come from the kernel just before; codes / scales may still be read by it
+  allow_dependents();
   const uint32_t rank = cluster_rank();
   const int gt = static_cast<int>(rank) * kSmallThreads + threadIdx.x;
   // zero-fill the padded scale buffer; the cluster barrier below orders these stores
@@ -824,8 +825,8 @@ __global__ void debug_encode_kernel(const float* in, int64_t n, int which, uint8
 __global__ void set_value_kernel(float* p, float v) { *p = v; }
 
 __global__ void global_scale_kernel(const float* amax, float* g, unsigned* status) {
-  allow_dependents();
   wait_prior_grids();  // the maximum may come from the kernel (or collective) just before
+  allow_dependents();
   const float a = *amax;
   if (!(abs_bits(a) < 0x7F800000u)) atomicOr(status, kStatusNonFinite);
   *g = a > 0.0f ? __fdiv_rn(a, 2688.0f) : 1.0f;  // 2688 = 6 * 448

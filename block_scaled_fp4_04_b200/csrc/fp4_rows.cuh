@@ -13,6 +13,11 @@
 
 namespace fp4 {
 
+// Programmatic dependent launch.  A kernel lets the next one start only after its own wait: a
+// product whose weights are ready reads them without waiting, as they were written before the
+// kernel just before it, and so everything older than that kernel has to be finished by then.
+// (With the calls the other way round, act_backward writing a weight's codes, layer norm, then
+// such a product read the old codes in 159 of 200 runs.)
 __device__ __forceinline__ void rows_allow_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void rows_wait_prior() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
