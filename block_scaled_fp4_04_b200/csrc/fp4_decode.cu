@@ -17,8 +17,8 @@
 //   pipelines (stream-K).  Each pipeline adds its FP32 partial tiles into a workspace;
 //   the pipeline that completes a tile's K range (a per-tile counter) scales, converts
 //   and stores it, and clears the workspace and counter behind it.
-//   With BF16 activations (fused), the eight epilogue warps first compute the tensor
-//   amax of all of X themselves (every CTA: no grid-wide communication), then quantize
+//   With BF16 activations (fused), the eight epilogue warps of each CTA first take the
+//   maximum of a share of X, which meet in slots of the workspace, then quantize
 //   the CTA's K segment straight into the shared-memory operand (128-byte swizzled, as
 //   TMA would have written it) and scale atoms; the first CTA of each segment also
 //   writes those codes and scales to the caller's buffers.  Meanwhile the producers are
@@ -57,7 +57,7 @@ struct DecodeArgs {
   float* ws;              // FP32 partial sums [N, M], zero between calls
   int* tile_cnt;          // K steps summed per weight tile, zero between calls
   int weights_ready;      // W was not written by the kernel just before this one
-  unsigned* gbar;         // fused: [0] call counter, then one 128-byte slot per CTA
+  unsigned* gbar;         // fused: [0] arrival counter, then one 128-byte slot per CTA
   unsigned* status;
   const float* bias;      // [N] added to every output row after the scale, or null
   int act;                // 0: none, 1: ReLU
@@ -361,6 +361,16 @@ __global__ void __launch_bounds__(DecodeCfg<BN>::kThreads, 1)
       int tile, k0, k1, stage = 0, issued_n = 0;
       uint32_t phase = 0, issued = 0, issued_par = 0;
       bool ok = true, x_done = !p.weights_ready;
+      // Fused: the CTAs count up when they have read all slots of the exchange below (a failed
+      // one does not), and the last one clears the slots at its end.  No fence: the add depends
+      // on the values read, the clearing on the count.  (Counted with fences by an epilogue
+      // thread after the exchange, 16 x 4096 x 2048 took 1.1 us longer; so 10.8 us, as before.)
+      bool counted = false;
+      unsigned before = 0xFFFFFFFFu;
+      auto count_cta = [&]() {
+        counted = true;
+        if (s_red[8]) asm volatile("atom.add.relaxed.gpu.global.u32 %0, [%1], 1;" : "=r"(before) : "l"(p.gbar));
+      };
       if (FUSED && kFusedPrefill == 0 && !mbar_wait(&b_ready[0], 0, s_abort)) {
         if (!*s_xfail) d_latch_timeout(s_abort, p.status);
         ok = false;
@@ -403,6 +413,7 @@ __global__ void __launch_bounds__(DecodeCfg<BN>::kThreads, 1)
               ok = false;
               break;
             }
+            if (sub == 1) count_cta();
           }
           if (!x_done && issued_n == S) {
             d_wait_prior_grids();
@@ -421,6 +432,15 @@ __global__ void __launch_bounds__(DecodeCfg<BN>::kThreads, 1)
             volatile int no_abort = 0;
             mbar_wait(&full[s], (issued_par >> s) & 1u, &no_abort);
           }
+      }
+      if (FUSED && sub == 1) {
+        volatile int no_abort = 0;
+        if (!counted && mbar_wait(&b_ready[0], 0, &no_abort)) count_cta();
+        if (before + 1 == gridDim.x) {
+          uint64_t* slots = reinterpret_cast<uint64_t*>(p.gbar + 32);
+          for (unsigned b = 0; b < gridDim.x; ++b) slots[b * 16] = 0;
+          *p.gbar = 0;
+        }
       }
     }
   } else if (warp == 1) {
@@ -578,24 +598,21 @@ __global__ void __launch_bounds__(DecodeCfg<BN>::kThreads, 1)
       if (lane == 0) s_red[xt >> 5] = m;
       named_sync(3, 256);
       // Each CTA publishes its maximum in a slot of its own (one 128-byte line each, so
-      // that the polls of all CTAs spread over many L2 lines) as one 64-bit word: the
-      // call's generation number in the high half, the maximum in the low half.  Every
-      // CTA polls all slots until each carries this call's generation.  The generation
-      // is the workspace's call counter plus one; CTA 0 stores it back once it has seen
-      // every slot (by then every CTA has read the counter), so nothing needs clearing.
+      // that the polls of all CTAs spread over many L2 lines) as one 64-bit word: a mark in
+      // the high half, the maximum in the low half.  Every CTA polls all slots until each is
+      // marked.  The last one to have seen them all clears slots and counter again (count_cta), so
+      // that the workspace is left zero-filled: other shapes have their partial sums where this
+      // one has its slots.
       uint64_t* slots = reinterpret_cast<uint64_t*>(p.gbar + 32);  // 16 words per slot
       if (xt == 0) {
         uint32_t cm = 0;
 #pragma unroll
         for (int w = 0; w < 8; ++w) cm = max(cm, s_red[w]);
-        const uint32_t gen = *reinterpret_cast<volatile unsigned*>(p.gbar) + 1u;
-        s_red[8] = gen;
-        const uint64_t word = (static_cast<uint64_t>(gen) << 32) | cm;
+        const uint64_t word = (uint64_t{1} << 32) | cm;
         if (static_cast<int>(blockIdx.x) + 1 != p.stall_plus1)
           asm volatile("st.relaxed.gpu.global.u64 [%0], %1;" ::"l"(slots + blockIdx.x * 16), "l"(word) : "memory");
       }
-      named_sync(3, 256);
-      const uint32_t gen = s_red[8];
+      named_sync(3, 256);  // (without it the polls begin earlier, get in the way, and the call takes 0.5 us longer)
       uint32_t seen = 0;
       bool got = true;
       for (int b = xt; b < static_cast<int>(gridDim.x); b += 256) {
@@ -603,11 +620,11 @@ __global__ void __launch_bounds__(DecodeCfg<BN>::kThreads, 1)
         const uint64_t t0 = globaltimer_ns();
         for (uint32_t it = 1; it < kWaitMaxIters; ++it) {
           asm volatile("ld.relaxed.gpu.global.u64 %0, [%1];" : "=l"(v) : "l"(slots + b * 16) : "memory");
-          if (static_cast<uint32_t>(v >> 32) == gen) break;
+          if (v >> 32) break;
           if ((it & 63u) == 0 && globaltimer_ns() - t0 > kWaitTimeoutNs) break;
           __nanosleep(32);
         }
-        if (static_cast<uint32_t>(v >> 32) == gen) seen = max(seen, static_cast<uint32_t>(v));
+        if (v >> 32) seen = max(seen, static_cast<uint32_t>(v));
         else got = false;
       }
       seen = __reduce_max_sync(0xFFFFFFFFu, seen);
@@ -628,7 +645,7 @@ __global__ void __launch_bounds__(DecodeCfg<BN>::kThreads, 1)
           *s_xfail = 1;
           atomicOr(p.status, kStatusTimeout);
         }
-        if (ok && blockIdx.x == 0) *reinterpret_cast<volatile unsigned*>(p.gbar) = gen;
+        s_red[8] = ok;
       }
       named_sync(3, 256);
       const uint32_t am = s_red[0];
@@ -942,7 +959,7 @@ static DecodePlan decode_plan(int64_t N, int64_t K, int bn, int weights) {
   return d;
 }
 
-// [FP32 partial sums M*N][tile counters][3 barrier words], each part 256-byte aligned
+// [FP32 partial sums M*N][tile counters][arrival counter, 128 bytes][amax slots]
 static size_t ws_partials(int64_t M, int64_t N) { return (static_cast<size_t>(M * N) * 4 + 255) / 256 * 256; }
 static size_t ws_counters(int64_t N) { return (static_cast<size_t>((N + 127) / 128) * 4 + 255) / 256 * 256; }
 

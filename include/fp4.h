@@ -317,8 +317,8 @@ fp4_status fp4_gemm_gated(fp4_fmt fmt, const uint8_t* A_dev, const uint8_t* sA_d
  * amax, 16-blocks), with NVFP4 weights: M <= 16 in one cooperative launch, larger M as
  * fp4_quantize then fp4_gemm_gated.  The activations' codes, scales and global scale are
  * written to Xcodes_dev / Xscales_dev / gX_dev, as by fp4_gemm_bf16a; workspace likewise:
- * fp4_gemm_gated_bf16a_workspace_size bytes, zero-filled before its first use, not to be
- * modified between calls nor shared by calls that overlap. */
+ * fp4_gemm_gated_bf16a_workspace_size bytes, zero-filled before its first use and left so, not
+ * to be shared by calls that overlap. */
 size_t fp4_gemm_gated_bf16a_workspace_size(int64_t M, int64_t F, int64_t K);
 fp4_status fp4_gemm_gated_bf16a(const void* X_dev, const uint8_t* Wg_dev, const uint8_t* sWg_dev,
                                 const float* gWg_dev, const uint8_t* Wu_dev, const uint8_t* sWu_dev,
@@ -411,9 +411,9 @@ fp4_status fp4_layernorm_backward(const void* dy_dev, const void* x_dev, int64_t
  *     and written out by the CTA that owns each tile.
  *   M > 32: fp4_quantize then fp4_gemm_ex, chained with programmatic dependent launch.
  * flags: FP4_GEMM_WEIGHTS_READY as for fp4_gemm_ex.  workspace: at least
- * fp4_gemm_bf16a_workspace_size(M, N, K) bytes, zero-filled before its first use; the
- * library keeps its contents consistent from call to call, so do not modify it between
- * calls, and calls sharing one workspace must not overlap. */
+ * fp4_gemm_bf16a_workspace_size(M, N, K) bytes, zero-filled before its first use; every
+ * call leaves it zero-filled again, so calls of other shapes and entry points can use it
+ * too, but calls sharing one workspace must not overlap. */
 size_t fp4_gemm_bf16a_workspace_size(int64_t M, int64_t N, int64_t K);
 fp4_status fp4_gemm_bf16a(const void* X_dev, const uint8_t* B_dev, const uint8_t* sB_dev, const float* gB_dev,
                           int64_t M, int64_t N, int64_t K, void* D_dev, fp4_dtype out_dtype,

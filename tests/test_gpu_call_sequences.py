@@ -3,7 +3,7 @@ import pytest
 import torch
 
 import block_scaled_fp4_04_b200 as fp4
-from fp4_testutil import random_input
+from fp4_testutil import gpu_quantize, random_input
 
 pytestmark = pytest.mark.gpu
 
@@ -54,3 +54,69 @@ def test_weights_written_two_kernels_before_a_product_that_may_read_them_early(m
     wrong = [r for r, d in enumerate(got) if not torch.equal(d, want[r % 2])]
     assert not wrong, f"{len(wrong)} of {len(got)} products read weights that were not there yet"
     assert fp4.fp4_get_status() == fp4.OK
+
+
+class _FromBf16:
+    """A product from BF16 activations (gated or not) with its output buffers."""
+
+    def __init__(self, m, n, k, seed, gated=False):
+        self.m, self.n, self.k, self.gated = m, n, k, gated
+        self.q = gpu_quantize(random_input(n, k, seed, torch.float32, outliers=False).cuda(), fp4.NVFP4, 16)
+        self.d = torch.empty(m, n, device="cuda")
+        self.codes = torch.empty(m, k // 2, dtype=torch.uint8, device="cuda")
+        self.scales = torch.empty(fp4.fp4_scales_bytes(m, k, fp4.NVFP4), dtype=torch.uint8, device="cuda")
+        self.g = torch.empty(1, device="cuda")
+
+    def size(self):
+        return (fp4.fp4_gemm_gated_bf16a_workspace_size if self.gated else fp4.fp4_gemm_bf16a_workspace_size)(
+            self.m, self.n, self.k)
+
+    def __call__(self, x, ws):
+        q, d = self.q, self.d
+        d.fill_(float("nan"))
+        if self.gated:
+            fp4.fp4_gemm_gated_bf16a(x, q.codes, q.scales, q.g, q.codes, q.scales, q.g, self.m, self.n, self.k, None, None,
+                                     fp4.ACT_NONE, d, fp4.F32, None, None, self.codes, self.scales, self.g, ws, ws.numel())
+        else:
+            fp4.fp4_gemm_bf16a(x, q.codes, q.scales, q.g, self.m, self.n, self.k, d, fp4.F32, self.codes, self.scales,
+                               self.g, ws, ws.numel())
+        return d.clone(), self.codes.clone(), self.scales.clone(), self.g.clone()
+
+
+@pytest.mark.parametrize("m,k,n,gated", [(16, 1024, 512, False), (5, 2048, 640, True), (32, 512, 256, False)])
+def test_one_workspace_for_products_of_other_shapes(m, k, n, gated):
+    """A second shape's partial sums end among the first one's slots and counters: each call finds
+    the workspace as the one before it left it, zero-filled."""
+    # where the first shape's slots start, in rows of the second one's sums
+    halves = 2 if gated else 1
+    wider = n * halves + (-(-n // 128) * 4 * halves + 256 + 40 * 128) // (m * 4)
+    a, b = _FromBf16(m, n, k, 1, gated), _FromBf16(m, wider, k, 2)
+    ws = torch.zeros(max(a.size(), b.size()), dtype=torch.uint8, device="cuda")
+    plain = fp4.fp4_gemm_workspace_size(m, wider, k, fp4.NVFP4)
+    for call in range(4):
+        # activations of another size each time: an old maximum would give another scale
+        x = (random_input(m, k, 10 + call, torch.float32, outliers=False) * 4.0 ** -call).to(torch.bfloat16).cuda()
+        for f in (a, b):
+            got = f(x, ws)
+            torch.cuda.synchronize()
+            assert fp4.fp4_get_status() == fp4.OK
+            assert not ws.any(), "workspace not left zero-filled"
+            want = f(x, torch.zeros(f.size(), dtype=torch.uint8, device="cuda"))
+            for p, q in zip(got[1:], want[1:]):
+                assert torch.equal(p, q)
+            check_gemm_like(got[0], want[0])
+            # (a tensor as the divisor: by a number, torch multiplies with its rounded reciprocal)
+            assert torch.equal(got[3].cpu(), x.abs().max().float().cpu().reshape(1) / torch.tensor([2688.0]))
+        d = torch.empty(m, wider, device="cuda")
+        fp4.fp4_gemm(fp4.NVFP4, b.codes, b.scales, b.g, b.q.codes, b.q.scales, b.q.g, m, wider, k, d, fp4.F32, ws, plain)
+        check_gemm_like(d, want[0])
+    x[m // 2, 7] = float("inf")  # refused on the device; the workspace is clean all the same
+    a(x, ws)
+    assert fp4.fp4_get_status() == fp4.ERR_NONFINITE and not ws.any()
+
+
+def check_gemm_like(got, want):
+    """The same products, their FP32 partial sums added in any order: sums of at most 8 parts (K <=
+    2048 in steps of 256), each within 2^-24 of the sum of magnitudes, which random signs keep
+    within 64 times the largest result."""
+    assert (got - want).abs().max() <= 2 * 8 * 2.0 ** -24 * 64 * want.abs().max()
