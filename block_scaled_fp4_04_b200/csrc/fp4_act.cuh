@@ -1,6 +1,6 @@
 // fp4_act.cuh -- activation functions and their derivatives in FP32.
 //
-//   RELU       max(x, 0)                        slope 1 where x > 0, else 0
+//   RELU       max(x, 0), NaN for a NaN         slope 1 where x > 0, else 0
 //   SILU       x s(x)                           s + x s (1 - s),  s(x) = 1 / (1 + e^-x)
 //   GELU       x Phi(x)                         Phi(x) + x phi(x)
 //   GELU_TANH  x s(2 c (x + a x^3))             s + x s (1 - s) 2 c (1 + 3 a x^2)
@@ -54,9 +54,16 @@ __device__ __forceinline__ float normal_cdf(float x, float& e) {
   return x >= 0.0f ? 1.0f - half : half;
 }
 
+// (fmaxf would turn a NaN into 0)
+__device__ __forceinline__ float relu_f(float x) {
+  float r;
+  asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(r) : "f"(x));
+  return r;
+}
+
 template <int ACT>
 __device__ __forceinline__ float act_value(float x) {
-  if constexpr (ACT == kActRelu) return x < 0.0f ? 0.0f : x;  // a NaN stays one
+  if constexpr (ACT == kActRelu) return relu_f(x);
   else if constexpr (ACT == kActSilu) return x * sigmoid_f(x);
   else if constexpr (ACT == kActGelu) { float e; return x * normal_cdf(x, e); }
   else if constexpr (ACT == kActGeluTanh) return x * sigmoid_from(x * fmaf(x * x, -kLog2e * kGelu2C * kGeluA, -kLog2e * kGelu2C));
@@ -67,7 +74,7 @@ __device__ __forceinline__ float act_value(float x) {
 template <int ACT>
 __device__ __forceinline__ float act_slope(float x, float& value) {
   if constexpr (ACT == kActRelu) {
-    value = x < 0.0f ? 0.0f : x;
+    value = relu_f(x);
     return x > 0.0f ? 1.0f : 0.0f;
   } else if constexpr (ACT == kActSilu) {
     const float s = sigmoid_f(x);

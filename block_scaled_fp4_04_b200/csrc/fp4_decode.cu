@@ -857,7 +857,7 @@ __global__ void __launch_bounds__(DecodeCfg<BN>::kThreads, 1)
             if (j < p.M) {
               float o = v[j] * scale;
               if (p.bias) o = __fadd_rn(o, bias);
-              if (p.act == 1) o = fmaxf(o, 0.0f);
+              if (p.act == kActRelu) o = relu_f(o);
               d_store(p, row, j, o);
             }
         }

@@ -343,9 +343,9 @@ __device__ __forceinline__ void epi_bias_act(const GemmArgs& p, int row, int col
         if (col + j < p.Nk) v[j] = __fadd_rn(v[j], __ldg(p.bias + col + j));
     }
   }
-  if (p.act == 1) {
+  if (p.act == kActRelu) {
 #pragma unroll
-    for (int j = 0; j < 16; ++j) v[j] = fmaxf(v[j], 0.0f);
+    for (int j = 0; j < 16; ++j) v[j] = relu_f(v[j]);
   }
 }
 

@@ -250,10 +250,10 @@ fp4_status fp4_gemm_mixed(fp4_fmt a_fmt, const uint8_t* A_dev, const uint8_t* sA
                           const uint8_t* B_dev, const uint8_t* sB_dev, int64_t M, int64_t N, int64_t K,
                           void* D_dev, fp4_dtype out_dtype, void* stream);
 
-/* Activations, computed in FP32: RELU max(x, 0); SILU x s(x) with s(x) = 1 / (1 + e^-x); GELU
- * x Phi(x) (the normal distribution function, by erf); GELU_TANH x s(2 c (x + 0.044715 x^3)),
- * c = sqrt(2 / pi) (the tanh form: (1 + tanh y) / 2 = s(2y)).  fp4_gemm_epilogue takes NONE
- * and RELU, the entry points below it all of them. */
+/* Activations, computed in FP32: RELU max(x, 0), NaN for a NaN; SILU x s(x) with s(x) =
+ * 1 / (1 + e^-x); GELU x Phi(x) (the normal distribution function, by erf); GELU_TANH
+ * x s(2 c (x + 0.044715 x^3)), c = sqrt(2 / pi) (the tanh form: (1 + tanh y) / 2 = s(2y)).
+ * fp4_gemm_epilogue takes NONE and RELU, the entry points below it all of them. */
 typedef enum {
   FP4_ACT_NONE = 0,
   FP4_ACT_RELU = 1,
@@ -347,7 +347,8 @@ fp4_status fp4_gemm_gated_grouped(fp4_fmt fmt, int num_groups, const int32_t* of
  *   U_dev != NULL (gated, H = act(G) U):  dZ [rows, 2 cols] = [dH U act'(G) | dH act(G)],
  *       one matrix: the operand of dX = dZ . [Wg; Wu] (one fp4_gemm with K = 2 cols);
  *   U_dev == NULL (H = act(G)):           dZ [rows, cols] = dH act'(G).
- * RELU's slope is 0 at 0.  Outputs, each optional but one of the first two:
+ * RELU's slope is 1 above 0, else 0 (at 0 and for a NaN too).  Outputs, each optional but one
+ * of the first two:
  *   dZ_dev in out_dtype; codes_dev / scales_dev: dZ in `fmt` blocks along its columns (NVFP4
  *       with the caller's global scale global_dev, or MXFP4), exactly as fp4_quantize would
  *       quantize the FP32 values (cols % 32 == 0; a non-finite value latches
