@@ -272,10 +272,19 @@ static fp4_status gemm_check(const GemmProblem& g, fp4_fmt fmt, fp4_dtype out_dt
   return FP4_OK;
 }
 
+// Whether the workspace stands where the kernels' widest access to it can.
+static bool workspace_aligned(const GemmProblem& g) {
+  return aligned16(g.ws) ||
+         reinterpret_cast<uintptr_t>(g.ws) %
+                 gemm_workspace_align(g.M, g.N, g.K, g.mx, g.q_codes != nullptr || g.amax_out != nullptr) ==
+             0;
+}
+
 static fp4_status gemm_common(const GemmProblem& g, fp4_fmt fmt, fp4_dtype out_dtype, void* stream,
                               const GemmFull* full = nullptr) {
   const fp4_status c = gemm_check(g, fmt, out_dtype);
   if (c != FP4_OK) return c;
+  if (!g.num_groups && !workspace_aligned(g)) return fail(FP4_ERR_INVALID_ARG, "workspace alignment");
   unsigned* status;
   fp4_status s = device_state(&status);
   if (s != FP4_OK) return s;
@@ -398,6 +407,8 @@ static fp4_status epilogue_common(fp4_fmt fmt, const uint8_t* A, const uint8_t* 
                            : gemm_workspace_bytes(M, N, K, g.mx, Dcodes || amax_out);
   if (need && (!workspace || workspace_bytes < need))
     return fail(FP4_ERR_INVALID_ARG, "workspace too small (see fp4_gemm_epilogue_workspace_size)");
+  if (full ? need && !aligned16(workspace) : !workspace_aligned(g))
+    return fail(FP4_ERR_INVALID_ARG, "workspace alignment");
   if (amax_out) {
     const cudaError_t e = cudaMemsetAsync(amax_out, 0, sizeof(float), static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "zeroing amax_out");

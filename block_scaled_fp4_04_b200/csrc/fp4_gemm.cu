@@ -257,6 +257,16 @@ size_t gemm_workspace_bytes(int64_t M, int64_t N, int64_t K, int mx, bool fp4_ou
   return make_plan(M, N, K, 0, mx, fp4_out).ws_bytes;
 }
 
+size_t gemm_workspace_align(int64_t M, int64_t N, int64_t K, int mx, bool fp4_out) {
+  int64_t row = M;  // floats per row of partial sums
+  if (mx || fp4_out || !decode_eligible(M, N, K)) {
+    const Plan pl = make_plan(M, N, K, 0, mx, fp4_out);
+    if (pl.mode != kModeStreamK) return 1;
+    row = pl.Nk;
+  }
+  return row % 4 == 0 ? 16 : 4;
+}
+
 // The long epilogue keeps its partial sums in rows of whole float4s.
 static size_t full_ws_bytes(const Plan& pl, int64_t M) {
   if (pl.mode != kModeStreamK || pl.swap) return pl.ws_bytes;

@@ -74,6 +74,10 @@ struct GemmProblem {
 
 size_t gemm_workspace_bytes(int64_t M, int64_t N, int64_t K, int mx, bool fp4_out = false);
 
+// Bytes its workspace has to be aligned to: 16 where the kernel moves partial sums in 16-byte
+// words, 4 where it moves single ones, 1 where it uses none.
+size_t gemm_workspace_align(int64_t M, int64_t N, int64_t K, int mx, bool fp4_out);
+
 size_t gemm_bf16a_workspace_bytes(int64_t M, int64_t N, int64_t K);
 
 // Encoded 2-D TMA map of a [rows, inner_bytes] uint8 matrix, boxes of box_rows x 128

@@ -186,8 +186,10 @@ fp4_status fp4_dequantize(const uint8_t* codes_dev, const uint8_t* scales_dev,
                           float* out_dev, void* stream);
 
 /* Device workspace bytes fp4_gemm needs for this shape (0 if none).  It must be
- * zero-filled before first use; every call leaves it zero-filled again.  After a call
- * that latched FP4_ERR_TIMEOUT its contents are undefined: zero it again. */
+ * 16-byte aligned (4-byte where no partial sums move in wider words; a call refuses
+ * what its accesses do not allow) and zero-filled before first use; every call leaves
+ * it zero-filled again.  After a call that latched FP4_ERR_TIMEOUT its contents are
+ * undefined: zero it again. */
 size_t fp4_gemm_workspace_size(int64_t M, int64_t N, int64_t K, fp4_fmt fmt);
 
 /* Block-scaled FP4 GEMM on the 5th-generation tensor cores ("Rubin FP4 GEMM overview"
@@ -234,8 +236,8 @@ fp4_status fp4_gemm_ex(fp4_fmt fmt, const uint8_t* A_dev, const uint8_t* sA_dev,
  *           by this call), so that the next quantization of t (fp4_global_scale, then
  *           fp4_quantize with global_in) needs no separate amax pass over it.
  * workspace: fp4_gemm_epilogue_workspace_size(M, N, K, fmt, rows_in_place) bytes with
- * rows_in_place = (Dcodes_dev != NULL || amax_out_dev != NULL), zero-filled before first
- * use (left zero-filled).  Plain (not grouped) problems only. */
+ * rows_in_place = (Dcodes_dev != NULL || amax_out_dev != NULL), aligned as fp4_gemm's and
+ * zero-filled before first use (left zero-filled).  Plain (not grouped) problems only. */
 /* Mixed-format GEMM ("Rubin FP4 GEMM overview" 3.4: weights in FP4 where they tolerate it,
  * activations kept in FP8, or the other way round): D[M, N] = A[M, K] B[N, K]^T with each
  * operand FP4_MXFP4 (E2M1 codes [rows, K/2], E8M0 scales per 32) or FP4_MXFP8 (E4M3
@@ -275,8 +277,8 @@ fp4_status fp4_gemm_epilogue(fp4_fmt fmt, const uint8_t* A_dev, const uint8_t* s
  *           itself (same type): every element is read before it is written.
  *   pre_dev [M, N] in out_dtype: z, which fp4_act_backward needs, or NULL.
  * t is what D, the NVFP4 copy and amax_out get.  flags: FP4_GEMM_WEIGHTS_READY as for
- * fp4_gemm_ex (the residual is read after the preceding kernel has finished).  Other
- * arguments, workspace and errors as fp4_gemm_epilogue. */
+ * fp4_gemm_ex (the residual is read after the preceding kernel has finished).  The workspace
+ * is 16-byte aligned.  Other arguments, its size and errors as fp4_gemm_epilogue. */
 fp4_status fp4_gemm_epilogue_ex(fp4_fmt fmt, const uint8_t* A_dev, const uint8_t* sA_dev, const float* gA_dev,
                                 const uint8_t* B_dev, const uint8_t* sB_dev, const float* gB_dev,
                                 int64_t M, int64_t N, int64_t K, const float* bias_dev, fp4_act act,
@@ -299,9 +301,9 @@ fp4_status fp4_gemm_epilogue_ex(fp4_fmt fmt, const uint8_t* A_dev, const uint8_t
  *           Dcodes / Dscales / gD and amax_out of fp4_gemm_epilogue (F % 32 == 0).
  * Any F >= 1 otherwise; K % 32 == 0; operands, H, G and U 16-byte aligned.
  * workspace: fp4_gemm_gated_workspace_size(M, F, K, fmt, rows_in_place) bytes, rows_in_place =
- * (Hcodes_dev != NULL || amax_out_dev != NULL); zero-filled before first use, left so.  With
- * a workspace in use (few rows), partial sums meet by FP32 atomic additions, whose order --
- * and so the last bits of H -- can differ from call to call, as in fp4_gemm.
+ * (Hcodes_dev != NULL || amax_out_dev != NULL); 16-byte aligned, zero-filled before first use,
+ * left so.  With a workspace in use (few rows), partial sums meet by FP32 atomic additions,
+ * whose order -- and so the last bits of H -- can differ from call to call, as in fp4_gemm.
  * flags: FP4_GEMM_WEIGHTS_READY (both weights).  M <= 16 with NVFP4 operands runs the decode
  * kernel over both weights. */
 size_t fp4_gemm_gated_workspace_size(int64_t M, int64_t F, int64_t K, fp4_fmt fmt, int rows_in_place);

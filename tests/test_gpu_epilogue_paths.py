@@ -68,3 +68,21 @@ def test_gated_keeps_a_nan(act, m):
                        bias, None, act, h, fp4.F32, workspace=ws, workspace_bytes=n)
     torch.cuda.synchronize()
     assert torch.isnan(h[:, 3]).all() and torch.isnan(h).sum() == m
+
+
+@pytest.mark.parametrize("m,n,k,fmt", [(1, 512, 2048, fp4.NVFP4), (7, 640, 4096, fp4.NVFP4), (5, 300, 2048, fp4.MXFP4),
+                                       (130, 257, 8192, fp4.NVFP4)])
+def test_partial_sums_of_odd_products_need_a_word_s_alignment(m, n, k, fmt):
+    qa, qb = _operands(m, n, k, fmt)
+    need = fp4.fp4_gemm_workspace_size(m, n, k, fmt)
+    assert need > 0
+    d, e = (torch.empty(m, n, device="cuda") for _ in range(2))
+    ws = torch.zeros(need + 16, dtype=torch.uint8, device="cuda")
+    head = (fmt, qa.codes, qa.scales, qa.g, qb.codes, qb.scales, qb.g, m, n, k)
+    fp4.fp4_gemm(*head, d, fp4.F32, ws, need)
+    fp4.fp4_gemm(*head, e, fp4.F32, ws[4:], need)
+    torch.cuda.synchronize()
+    # up to 64 parts of a sum in any order, each rounded to half a step of the sum of magnitudes,
+    # which is below 64 times the largest of these sums of random signs
+    assert (d - e).abs().max() <= 2 * 64 * 2.0 ** -24 * 64 * d.abs().max()
+    assert not ws.any() and fp4.fp4_get_status() == fp4.OK

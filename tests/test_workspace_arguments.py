@@ -1,0 +1,46 @@
+"""Workspaces that the entry points refuse on the host, before anything is enqueued (no GPU needed)."""
+import pytest
+
+import block_scaled_fp4_04_b200 as fp4
+from block_scaled_fp4_04_b200 import build as fp4_build
+
+ENOUGH = 1 << 30
+SPLIT = [                     # m, n, k, fmt of products that need a workspace with 16-byte accesses
+    (16, 512, 2048, fp4.NVFP4),   # decode kernel
+    (16, 512, 2048, fp4.MXFP4),   # operands swapped
+    (48, 640, 2048, fp4.NVFP4),   # the same, 64 columns
+    (256, 256, 8192, fp4.NVFP4),  # in place
+    (130, 260, 8192, fp4.MXFP4),
+]
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    fp4_build.build()
+
+
+@pytest.mark.parametrize("m,n,k,fmt", SPLIT)
+@pytest.mark.parametrize("ws", [2, 4, 8, 24])
+def test_products_refuse_a_misaligned_workspace(m, n, k, fmt, ws):
+    L, head = fp4.lib(), (fmt, 16, 16, 16, 16, 16, 16, m, n, k)
+    assert fp4.fp4_gemm_workspace_size(m, n, k, fmt) > 0
+    assert L.fp4_gemm(*head, 16, fp4.F32, ws, ENOUGH, None) == fp4.ERR_INVALID_ARG
+    assert L.fp4_gemm_ex(*head, 16, fp4.F32, ws, ENOUGH, 0, None) == fp4.ERR_INVALID_ARG
+    assert L.fp4_gemm_epilogue(*head, None, fp4.ACT_RELU, 16, fp4.F32, None, None, None, None, ws, ENOUGH,
+                               None) == fp4.ERR_INVALID_ARG
+    assert "alignment" in fp4.fp4_last_error()
+    for res, pre in ((None, None), (32, None), (None, 64)):
+        assert L.fp4_gemm_epilogue_ex(*head, None, fp4.ACT_RELU, res, fp4.F32, 48, fp4.F32, pre, None, None, None, None, ws,
+                                      ENOUGH, 0, None) == fp4.ERR_INVALID_ARG
+        assert "alignment" in fp4.fp4_last_error()
+
+
+@pytest.mark.parametrize("m,n,k", [(1, 512, 2048), (7, 640, 4096), (130, 257, 8192)])
+def test_odd_products_refuse_less_than_their_words(m, n, k):
+    """Partial sums that move one at a time need 4 bytes; the long epilogue pads them to 16."""
+    L, head = fp4.lib(), (fp4.NVFP4, 16, 16, 16, 16, 16, 16, m, n, k)
+    for ws in (1, 2, 18):
+        assert L.fp4_gemm(*head, 16, fp4.F32, ws, ENOUGH, None) == fp4.ERR_INVALID_ARG
+    for ws in (2, 4, 8):
+        assert L.fp4_gemm_epilogue_ex(*head, None, fp4.ACT_SILU, None, fp4.F32, 48, fp4.F32, None, None, None, None, None, ws,
+                                      ENOUGH, 0, None) == fp4.ERR_INVALID_ARG
