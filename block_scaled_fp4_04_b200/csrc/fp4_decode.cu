@@ -903,6 +903,7 @@ __global__ void __launch_bounds__(DecodeCfg<BN>::kThreads, 1)
             for (int j = 0; j < 16 && c + j < p.M; ++j) atomicAdd(wsrow + c + j, __uint_as_float(r[j]));
           }
         }
+        if (BN > 16) __syncwarp();  // the next TMEM load takes the whole warp
       }
       tc_fence_before();
       __syncwarp();

@@ -1212,6 +1212,7 @@ __global__ void __launch_bounds__(Cfg<BN, MX, ACC, PAIR, F8, EPI>::kThreads, 1)
                 if (row_ok && col + j < p.ws_ld)
                   red_add_v4(dst + j, __uint_as_float(rr[j]), __uint_as_float(rr[j + 1]), __uint_as_float(rr[j + 2]),
                              __uint_as_float(rr[j + 3]));
+              __syncwarp();  // the next TMEM load takes the whole warp
             }
             tc_fence_before();
             __syncwarp();
@@ -1274,6 +1275,7 @@ __global__ void __launch_bounds__(Cfg<BN, MX, ACC, PAIR, F8, EPI>::kThreads, 1)
                   epi_rows<kGated, kWhole>(p, spot, b1, b2, scale, scale2, rr + c, tmax);
                 }
               }
+              __syncwarp();  // the next TMEM load takes the whole warp
             }
           }
           ++iter;
@@ -1287,11 +1289,13 @@ __global__ void __launch_bounds__(Cfg<BN, MX, ACC, PAIR, F8, EPI>::kThreads, 1)
               tmem_ld16(taddr + c, rg);
               tmem_ld_wait();
               const int col = w.n0 + c;
-              if (!row_ok || col >= p.Nk) continue;
-              float v[16];
+              if (row_ok && col < p.Nk) {
+                float v[16];
 #pragma unroll
-              for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(rg[j]) * scale;
-              epi_finish16(p, row, col, v);
+                for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(rg[j]) * scale;
+                epi_finish16(p, row, col, v);
+              }
+              __syncwarp();  // the next TMEM load takes the whole warp
             }
           }
         } else if (q * 32 < w.rows_valid) {
@@ -1302,18 +1306,20 @@ __global__ void __launch_bounds__(Cfg<BN, MX, ACC, PAIR, F8, EPI>::kThreads, 1)
             tmem_ld16(taddr + c, rr);
             tmem_ld_wait();
             const int col = w.n0 + c;
-            if (!row_ok || col >= p.Nk) continue;
-            float* dst = p.ws + static_cast<int64_t>(row) * p.Nk + col;
-            if ((p.Nk & 3) == 0 && col + 16 <= p.Nk) {
+            if (row_ok && col < p.Nk) {
+              float* dst = p.ws + static_cast<int64_t>(row) * p.Nk + col;
+              if ((p.Nk & 3) == 0 && col + 16 <= p.Nk) {
 #pragma unroll
-              for (int j = 0; j < 16; j += 4)
-                red_add_v4(dst + j, __uint_as_float(rr[j]), __uint_as_float(rr[j + 1]), __uint_as_float(rr[j + 2]),
-                           __uint_as_float(rr[j + 3]));
-            } else {
+                for (int j = 0; j < 16; j += 4)
+                  red_add_v4(dst + j, __uint_as_float(rr[j]), __uint_as_float(rr[j + 1]), __uint_as_float(rr[j + 2]),
+                             __uint_as_float(rr[j + 3]));
+              } else {
 #pragma unroll
-              for (int j = 0; j < 16; ++j)
-                if (col + j < p.Nk) atomicAdd(dst + j, __uint_as_float(rr[j]));
+                for (int j = 0; j < 16; ++j)
+                  if (col + j < p.Nk) atomicAdd(dst + j, __uint_as_float(rr[j]));
+              }
             }
+            __syncwarp();  // the next TMEM load takes the whole warp
           }
         }
       } else
@@ -1339,9 +1345,10 @@ __global__ void __launch_bounds__(Cfg<BN, MX, ACC, PAIR, F8, EPI>::kThreads, 1)
 #pragma unroll
             for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(rr[cw + j]) * scale;
             if (p.bias || p.act) epi_bias_act(p, row, w.n0 + c0 + cb + cw, v);
-            if (p.amax_out && row_ok) {
+            if (p.amax_out) {  // (a mask, no branch by rows: the next TMEM load takes the whole warp)
+              const uint32_t keep = row_ok ? 0x7FFFFFFFu : 0u;
 #pragma unroll
-              for (int j = 0; j < 16; ++j) tmax = max(tmax, __float_as_uint(v[j]) & 0x7FFFFFFFu);
+              for (int j = 0; j < 16; ++j) tmax = max(tmax, __float_as_uint(v[j]) & keep);
             }
 #pragma unroll
             for (int j = 0; j < 16; j += 2) pk[(cb + cw + j) / 2] = pack_bf16x2(v[j], v[j + 1]);
@@ -1390,6 +1397,7 @@ __global__ void __launch_bounds__(Cfg<BN, MX, ACC, PAIR, F8, EPI>::kThreads, 1)
             epi_row16(p, row, col, v, tmax);
           }
         }
+          __syncwarp();  // the next TMEM loads take the whole warp
         }
       }
       if (!released) {

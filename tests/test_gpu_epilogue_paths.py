@@ -1,9 +1,12 @@
 """The product's epilogues on the paths that a plan can take: values that are no numbers, whole and
 split tiles of every width, rows that are no whole sectors."""
+import numpy as np
 import pytest
 import torch
 
 import block_scaled_fp4_04_b200 as fp4
+from ffn_testutil import (ACTS, CODE, MAX_SLOPE, act64, act_error, assert_close, assert_codes_of, codes_like, dequantized,
+                          product64)
 from fp4_testutil import gpu_quantize, random_input
 
 pytestmark = pytest.mark.gpu
@@ -86,3 +89,74 @@ def test_partial_sums_of_odd_products_need_a_word_s_alignment(m, n, k, fmt):
     # which is below 64 times the largest of these sums of random signs
     assert (d - e).abs().max() <= 2 * 64 * 2.0 ** -24 * 64 * d.abs().max()
     assert not ws.any() and fp4.fp4_get_status() == fp4.OK
+
+
+def _bias(n, seed):
+    return torch.from_numpy((np.random.default_rng(seed).standard_normal(n) * 0.7).astype(np.float32))
+
+
+def _linear64(a, b, bias):
+    """(a b^T + bias, the bound of its FP32 error: the product's, two roundings of the sum)."""
+    z, e = product64(a, b)
+    if bias is not None:
+        z = z + bias.double()
+        e = e + 2.0 ** -24 * bias.double().abs()
+    return z, e + 2.0 ** -23 * z.abs()
+
+
+def _epilogue(m, n, k, fmt, out, res, act, save, bias, split, offset=0):
+    """fp4_gemm_epilogue_ex against 64 bits; `split`: whether the plan splits K (the workspace says
+    so); outputs and residual start `offset` bytes behind their allocation."""
+    qa, qb = _operands(m, n, k, fmt)
+    b = _bias(n, 5) if bias else None
+    r = None if res is None else random_input(m, n, 6, res, outliers=False)
+    need = fp4.fp4_gemm_epilogue_workspace_size(m, n, k, fmt, False)
+    assert (need > 0) == split, "the plan no longer takes the path this case is for"
+    ws = torch.zeros(max(need, 16), dtype=torch.uint8, device="cuda")
+
+    def new(dtype):
+        pad = offset // torch.empty(0, dtype=dtype).element_size()
+        return torch.full((m * n + pad,), float("nan"), dtype=dtype, device="cuda")[pad:].view(m, n)
+
+    d, pre = new(out), new(out)
+    rd = None
+    if r is not None:
+        rd = new(res)
+        rd.copy_(r)
+
+    def call(d, rd):
+        fp4.fp4_gemm_epilogue_ex(fmt, qa.codes, qa.scales, qa.g, qb.codes, qb.scales, qb.g, m, n, k,
+                                 None if b is None else b.cuda(), ACTS[act], rd, CODE[res] if res else 0, d, CODE[out],
+                                 pre if save else None, workspace=ws, workspace_bytes=need)
+        torch.cuda.synchronize()
+        assert fp4.fp4_get_status() == fp4.OK
+        assert not ws.any(), "workspace not left zero-filled"
+
+    call(d, rd)
+    z64, ez = _linear64(dequantized(qa), dequantized(qb), b)
+    v, _ = act64(z64, act)
+    t64 = v + (r.double() if r is not None else 0.0)
+    et = (1.0 if act in ("none", "relu") else MAX_SLOPE) * ez + act_error(z64, v) + 2.0 ** -23 * t64.abs()
+    assert_close(d, t64, et, "D")
+    if save:
+        assert_close(pre, z64, ez, "pre")
+    if res == out:  # in place
+        call(rd, rd)
+        assert_close(rd, t64, et, "in place")
+
+
+EXTRAS = [(torch.bfloat16, torch.bfloat16, "none", False, True), (torch.float32, torch.float32, "gelu", True, True),
+          (torch.bfloat16, torch.float32, "silu", True, False), (torch.float32, torch.bfloat16, "relu", True, True)]
+
+
+@pytest.mark.parametrize("m,n,k,fmt,split", [
+    (48, 1000, 96, fp4.NVFP4, False),     # 64 columns of swapped operands, a warp with some of its rows
+    (33, 333, 96, fp4.MXFP4, False),
+    (50, 1001, 2048, fp4.NVFP4, True),    # split, single partial sums
+    (64, 1000, 1056, fp4.MXFP4, True),    # split, partial sums by fours
+    (20, 1001, 2048, fp4.MXFP4, True),    # 32 columns
+    (5, 333, 2048, fp4.MXFP4, True),      # 16 columns
+])
+@pytest.mark.parametrize("out,res,act,save,bias", EXTRAS)
+def test_epilogue_of_few_rows(m, n, k, fmt, split, out, res, act, save, bias):
+    _epilogue(m, n, k, fmt, out, res, act, save, bias, split)
