@@ -360,11 +360,18 @@ class Quantized:
     scalesT: Optional[torch.Tensor] = None
 
 
+def _capturing(device: torch.device) -> bool:
+    return device.type == "cuda" and torch.cuda.is_current_stream_capturing()
+
+
 class Workspace:
     """Zero-filled device scratch owned by the caller, reused across calls.
 
     A buffer that has become too small is kept: captured graphs may still replay calls
-    that use it."""
+    that use it.  While a graph is being captured the buffer does not grow: a call that
+    needs more gets a buffer of its own, zero-filled by every replay (the zero-fill of a
+    shared one would wait for the first replay, while other calls already use it).  One
+    call of each kind before the capture avoids that."""
 
     def __init__(self, device=None):
         self.device = torch.device(device or "cuda")
@@ -372,11 +379,14 @@ class Workspace:
         self._outgrown = []
 
     def get(self, nbytes: int) -> torch.Tensor:
-        if nbytes > self.buf.numel():
+        if nbytes <= self.buf.numel():
+            return self.buf
+        new = torch.zeros(max(nbytes, 4096), dtype=torch.uint8, device=self.device)
+        if not _capturing(self.device):
             if self.buf.numel():
                 self._outgrown.append(self.buf)
-            self.buf = torch.zeros(max(nbytes, 4096), dtype=torch.uint8, device=self.device)
-        return self.buf
+            self.buf = new
+        return new
 
 
 def quantize(x: torch.Tensor, fmt: int = NVFP4, block: Optional[int] = None, global_in=None,

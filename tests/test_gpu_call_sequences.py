@@ -115,6 +115,34 @@ def test_one_workspace_for_products_of_other_shapes(m, k, n, gated):
     assert fp4.fp4_get_status() == fp4.ERR_NONFINITE and not ws.any()
 
 
+def test_a_capture_that_needs_a_larger_workspace():
+    """Calls captured with a workspace that is too small, eager calls with it before and after the
+    first replay, and when the graph is gone."""
+    m, n, k = 16, 640, 2048
+    qa, qb = (gpu_quantize(random_input(r, k, s, torch.float32, outliers=False).cuda(), fp4.NVFP4, 16)
+              for r, s in ((m, 1), (n, 2)))
+    want = fp4.gemm(qa, qb, torch.float32)
+    ws = fp4.Workspace()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        junk = torch.full((1 << 20,), 255, dtype=torch.uint8, device="cuda")
+        del junk
+        d1 = fp4.gemm(qa, qb, torch.float32, ws)
+        d2 = fp4.gemm_epilogue(qa, qb, residual=d1, out_dtype=torch.float32, workspace=ws)
+    for _ in range(3):
+        check_gemm_like(fp4.gemm(qa, qb, torch.float32, ws), want)
+        d1.fill_(float("nan"))
+        graph.replay()
+        check_gemm_like(d1, want)
+        check_gemm_like(d2 / 2, want)
+    torch.cuda.synchronize()
+    del graph, d1, d2
+    torch.cuda.empty_cache()
+    check_gemm_like(fp4.gemm(qa, qb, torch.float32, ws), want)
+    torch.cuda.synchronize()
+    assert not ws.buf.any() and fp4.fp4_get_status() == fp4.OK
+
+
 def check_gemm_like(got, want):
     """The same products, their FP32 partial sums added in any order: sums of at most 8 parts (K <=
     2048 in steps of 256), each within 2^-24 of the sum of magnitudes, which random signs keep

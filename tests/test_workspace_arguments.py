@@ -1,5 +1,7 @@
-"""Workspaces that the entry points refuse on the host, before anything is enqueued (no GPU needed)."""
+"""Workspaces that the entry points refuse on the host, before anything is enqueued, and the buffers
+that a Workspace hands out (no GPU needed)."""
 import pytest
+import torch
 
 import block_scaled_fp4_04_b200 as fp4
 from block_scaled_fp4_04_b200 import build as fp4_build
@@ -44,3 +46,25 @@ def test_odd_products_refuse_less_than_their_words(m, n, k):
     for ws in (2, 4, 8):
         assert L.fp4_gemm_epilogue_ex(*head, None, fp4.ACT_SILU, None, fp4.F32, 48, fp4.F32, None, None, None, None, None, ws,
                                       ENOUGH, 0, None) == fp4.ERR_INVALID_ARG
+
+
+def test_a_workspace_does_not_grow_into_a_capture(monkeypatch):
+    """What a capture allocates is zero-filled when the graph replays, not before: calls outside the
+    graph must not be given it."""
+    ws = fp4.Workspace("cpu")
+    first = ws.get(5000)
+    monkeypatch.setattr(fp4, "_capturing", lambda device: True)
+    assert ws.get(4000).data_ptr() == first.data_ptr()  # large enough: the one buffer
+    inside = ws.get(9000)
+    assert inside.numel() >= 9000 and not inside.any()
+    assert ws.get(9000).data_ptr() != inside.data_ptr()
+    monkeypatch.undo()
+    assert ws.get(5000).data_ptr() == first.data_ptr()
+    after = ws.get(9000)
+    assert after.data_ptr() != inside.data_ptr() and ws.get(9000).data_ptr() == after.data_ptr()
+
+
+def test_a_workspace_keeps_the_buffers_it_has_outgrown():
+    ws = fp4.Workspace("cpu")
+    held = [ws.get(n).data_ptr() for n in (5000, 50000, 500000)]
+    assert len(set(held)) == 3 and [b.data_ptr() for b in ws._outgrown] == held[:2]
