@@ -368,7 +368,8 @@ class Workspace:
     """Zero-filled device scratch owned by the caller, reused across calls.
 
     A buffer that has become too small is kept: captured graphs may still replay calls
-    that use it.  While a graph is being captured the buffer does not grow: a call that
+    that use it.  Each new one has at least twice its size, so that together they are
+    smaller than the buffer in use.  While a graph is being captured the buffer does not grow: a call that
     needs more gets a buffer of its own, zero-filled by every replay (the zero-fill of a
     shared one would wait for the first replay, while other calls already use it).  One
     call of each kind before the capture avoids that."""
@@ -381,11 +382,12 @@ class Workspace:
     def get(self, nbytes: int) -> torch.Tensor:
         if nbytes <= self.buf.numel():
             return self.buf
-        new = torch.zeros(max(nbytes, 4096), dtype=torch.uint8, device=self.device)
-        if not _capturing(self.device):
-            if self.buf.numel():
-                self._outgrown.append(self.buf)
-            self.buf = new
+        if _capturing(self.device):
+            return torch.zeros(nbytes, dtype=torch.uint8, device=self.device)
+        new = torch.zeros(max(nbytes, 2 * self.buf.numel(), 4096), dtype=torch.uint8, device=self.device)
+        if self.buf.numel():
+            self._outgrown.append(self.buf)
+        self.buf = new
         return new
 
 

@@ -68,3 +68,10 @@ def test_a_workspace_keeps_the_buffers_it_has_outgrown():
     ws = fp4.Workspace("cpu")
     held = [ws.get(n).data_ptr() for n in (5000, 50000, 500000)]
     assert len(set(held)) == 3 and [b.data_ptr() for b in ws._outgrown] == held[:2]
+
+
+def test_what_a_workspace_keeps_stays_below_what_it_uses():
+    ws = fp4.Workspace("cpu")
+    for n in range(5000, 200000, 1000):
+        assert ws.get(n).numel() >= n
+    assert sum(b.numel() for b in ws._outgrown) < ws.buf.numel() < 2 * 200000
