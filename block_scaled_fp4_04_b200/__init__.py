@@ -369,10 +369,10 @@ class Workspace:
 
     A buffer that has become too small is kept: captured graphs may still replay calls
     that use it.  Each new one has at least twice its size, so that together they are
-    smaller than the buffer in use.  While a graph is being captured the buffer does not grow: a call that
-    needs more gets a buffer of its own, zero-filled by every replay (the zero-fill of a
-    shared one would wait for the first replay, while other calls already use it).  One
-    call of each kind before the capture avoids that."""
+    smaller than the buffer in use.  While a graph is being captured the buffer does not
+    grow: a call that needs more gets a buffer of its own, zero-filled by every replay (the
+    zero-fill of a shared one would wait for the first replay, while other calls already
+    use it).  One call of each kind before the capture avoids that."""
 
     def __init__(self, device=None):
         self.device = torch.device(device or "cuda")

@@ -160,3 +160,114 @@ EXTRAS = [(torch.bfloat16, torch.bfloat16, "none", False, True), (torch.float32,
 @pytest.mark.parametrize("out,res,act,save,bias", EXTRAS)
 def test_epilogue_of_few_rows(m, n, k, fmt, split, out, res, act, save, bias):
     _epilogue(m, n, k, fmt, out, res, act, save, bias, split)
+
+
+@pytest.mark.parametrize("m,n,k,fmt,split,offset", [
+    (130, 257, 8192, fp4.NVFP4, True, 0),     # split in place, rows of partial sums padded to 260
+    (130, 131, 16384, fp4.MXFP4, True, 0),
+    (130, 260, 8192, fp4.NVFP4, True, 16),
+    (2560, 2001, 64, fp4.NVFP4, False, 0),    # CTA pairs, odd rows
+    (2560, 2004, 64, fp4.MXFP4, False, 0),    # CTA pairs, rows of no whole sectors
+    (2560, 2048, 64, fp4.NVFP4, False, 16),   # CTA pairs, whole sectors that start between two
+    (129, 19001, 64, fp4.NVFP4, False, 0),    # 256-wide tiles on single CTAs, odd rows
+    (129, 19004, 64, fp4.MXFP4, False, 0),
+    (129, 19008, 64, fp4.MXFP4, False, 16),
+])
+@pytest.mark.parametrize("out,res,act,save,bias", EXTRAS)
+def test_epilogue_in_place(m, n, k, fmt, split, offset, out, res, act, save, bias):
+    _epilogue(m, n, k, fmt, out, res, act, save, bias, split, offset)
+
+
+@pytest.mark.parametrize("m,n,k,fmt,split", [(130, 288, 8192, fp4.NVFP4, True), (20, 96, 16384, fp4.MXFP4, True),
+                                             (130, 384, 512, fp4.MXFP4, False), (2560, 2080, 64, fp4.MXFP4, False)])
+def test_epilogue_to_codes(m, n, k, fmt, split):
+    """NVFP4 codes and the maximum of the result, from operands of either format, whole and split."""
+    qa, qb = _operands(m, n, k, fmt)
+    r = random_input(m, n, 3, torch.bfloat16, outliers=False).cuda()
+    need = fp4.fp4_gemm_epilogue_workspace_size(m, n, k, fmt, True)
+    assert (need > 0) == split, "the plan no longer takes the path this case is for"
+    ws = torch.zeros(max(need, 16), dtype=torch.uint8, device="cuda")
+    codes, scales = codes_like(m, n, fp4.NVFP4)
+    gd, amax = torch.tensor([0.004], device="cuda"), torch.empty(1, device="cuda")
+    d, pre = (torch.empty(m, n, device="cuda") for _ in range(2))
+    for _ in range(2):
+        fp4.fp4_gemm_epilogue_ex(fmt, qa.codes, qa.scales, qa.g, qb.codes, qb.scales, qb.g, m, n, k, None, fp4.ACT_GELU, r,
+                                 fp4.BF16, d, fp4.F32, pre, codes, scales, gd, amax, ws, need)
+        torch.cuda.synchronize()
+        assert fp4.fp4_get_status() == fp4.OK and not ws.any()
+        assert_codes_of(codes, scales, gd, d, fp4.NVFP4)
+        assert amax.item() == d.abs().max().item()
+    z64, ez = _linear64(dequantized(qa), dequantized(qb), None)
+    v, _ = act64(z64, "gelu")
+    t64 = v + r.cpu().double()
+    assert_close(pre, z64, ez, "pre")
+    assert_close(d, t64, MAX_SLOPE * ez + act_error(z64, v) + 2.0 ** -23 * t64.abs(), "D")
+
+
+GATED = [
+    (1, 257, 8192, fp4.MXFP4, True),       # split, odd F: rows of partial sums padded to 260
+    (20, 257, 8192, fp4.MXFP4, True),
+    (17, 384, 8192, fp4.NVFP4, True),      # the first row count past the decode kernel
+    (130, 131, 16384, fp4.NVFP4, True),    # split, more than one tile of rows
+    (130, 160, 16384, fp4.MXFP4, True),
+    (16, 512, 2880, fp4.MXFP4, False),     # whole tiles: too little to save
+    (33, 640, 2048, fp4.NVFP4, False),
+    (2560, 2001, 64, fp4.NVFP4, False),    # CTA pairs, odd rows
+    (2560, 2004, 64, fp4.MXFP4, False),
+    (129, 19001, 64, fp4.NVFP4, False),    # single CTAs, odd rows
+]
+
+
+@pytest.mark.parametrize("m,f,k,fmt,split", GATED)
+@pytest.mark.parametrize("out,act,bias", [(torch.float32, "silu", True), (torch.bfloat16, "gelu_tanh", False)])
+def test_gated_plans(m, f, k, fmt, split, out, act, bias):
+    qa, qg = _operands(m, f, k, fmt)
+    qu = gpu_quantize(random_input(f, k, 13, torch.float32, std=0.05, outliers=False).cuda(), fmt, _blk(fmt))
+    bg, bu = (_bias(f, 1), _bias(f, 2)) if bias else (None, None)
+    need = fp4.fp4_gemm_gated_workspace_size(m, f, k, fmt, False)
+    assert (need > 0) == split, "the plan no longer takes the path this case is for"
+    ws = torch.zeros(max(need, 16), dtype=torch.uint8, device="cuda")
+    h, g, u = (torch.full((m, f), float("nan"), dtype=out, device="cuda") for _ in range(3))
+    dev = [None if b is None else b.cuda() for b in (bg, bu)]
+    for _ in range(2):
+        fp4.fp4_gemm_gated(fmt, qa.codes, qa.scales, qa.g, qg.codes, qg.scales, qg.g, qu.codes, qu.scales, qu.g, m, f, k,
+                           dev[0], dev[1], ACTS[act], h, CODE[out], g, u, workspace=ws, workspace_bytes=need)
+        torch.cuda.synchronize()
+        assert fp4.fp4_get_status() == fp4.OK
+        assert not ws.any(), "workspace not left zero-filled"
+    a = dequantized(qa)
+    g64, eg = _linear64(a, dequantized(qg), bg)
+    u64, eu = _linear64(a, dequantized(qu), bu)
+    assert_close(g, g64, eg, "G")
+    assert_close(u, u64, eu, "U")
+    v, _ = act64(g64, act)
+    ev = MAX_SLOPE * eg + act_error(g64, v)
+    assert_close(h, v * u64, ev * u64.abs() + eu * v.abs() + ev * eu + 2.0 ** -23 * (v * u64).abs(), "H")
+
+
+@pytest.mark.parametrize("m,f,k,fmt,split", [(130, 160, 16384, fp4.NVFP4, True), (20, 96, 16384, fp4.MXFP4, True),
+                                             (1, 128, 8192, fp4.NVFP4, True), (130, 288, 512, fp4.MXFP4, False)])
+def test_gated_to_codes(m, f, k, fmt, split):
+    """NVFP4 codes and the maximum of H, from operands of either format, whole and split."""
+    qa, qg = _operands(m, f, k, fmt)
+    qu = gpu_quantize(random_input(f, k, 13, torch.float32, std=0.05, outliers=False).cuda(), fmt, _blk(fmt))
+    need = fp4.fp4_gemm_gated_workspace_size(m, f, k, fmt, True)
+    assert (need > 0) == split, "the plan no longer takes the path this case is for"
+    ws = torch.zeros(max(need, 16), dtype=torch.uint8, device="cuda")
+    gh, amax = torch.tensor([0.01], device="cuda"), torch.empty(1, device="cuda")
+    h = torch.empty(m, f, device="cuda")
+    for _ in range(2):
+        codes, scales = codes_like(m, f, fp4.NVFP4)
+        fp4.fp4_gemm_gated(fmt, qa.codes, qa.scales, qa.g, qg.codes, qg.scales, qg.g, qu.codes, qu.scales, qu.g, m, f, k,
+                           None, None, fp4.ACT_SILU, h, fp4.F32, Hcodes=codes, Hscales=scales, gH=gh, amax_out=amax,
+                           workspace=ws, workspace_bytes=need)
+        torch.cuda.synchronize()
+        assert fp4.fp4_get_status() == fp4.OK and not ws.any()
+        assert_codes_of(codes, scales, gh, h, fp4.NVFP4)
+        assert amax.item() == h.abs().max().item()
+    a = dequantized(qa)
+    g64, eg = _linear64(a, dequantized(qg), None)
+    u64, eu = _linear64(a, dequantized(qu), None)
+    v, _ = act64(g64, "silu")
+    ev = MAX_SLOPE * eg + act_error(g64, v)
+    assert_close(h, v * u64, ev * u64.abs() + eu * v.abs() + ev * eu + 2.0 ** -23 * (v * u64).abs(), "H")
