@@ -357,6 +357,7 @@ __device__ __forceinline__ void epi_quantize16(const GemmArgs& p, int row, int c
   uint32_t m = 0;
 #pragma unroll
   for (int j = 0; j < 16; ++j) m = max(m, __float_as_uint(v[j]) & 0x7FFFFFFFu);
+  if (m >= 0x7F800000u) atomicOr(p.status, kStatusNonFinite);
   uint32_t sb;
   const float mul = nvfp4_block_scale(__uint_as_float(m), g, sb);
   float a[8], b[8];

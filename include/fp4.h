@@ -228,9 +228,10 @@ fp4_status fp4_gemm_ex(fp4_fmt fmt, const uint8_t* A_dev, const uint8_t* sA_dev,
  *           codes [M, N/2], scales fp4_scales_bytes(M, N, FP4_NVFP4) in the swizzled
  *           layout, quantized exactly as fp4_quantize would quantize the FP32 t with
  *           global_in = gD_dev (the caller's global scale: t's amax is not known until
- *           the whole product is, so it cannot be computed here).  The layout's pad
- *           bytes are written as 0, as fp4_quantize writes them.  The result can feed
- *           the next fp4_gemm as its A operand directly.  Needs N % 32 == 0.
+ *           the whole product is, so it cannot be computed here); a non-finite t latches
+ *           FP4_ERR_NONFINITE.  The layout's pad bytes are written as 0, as fp4_quantize
+ *           writes them.  The result can feed the next fp4_gemm as its A operand
+ *           directly.  Needs N % 32 == 0.
  *   bias_dev [N] FP32 or NULL; act FP4_ACT_NONE or FP4_ACT_RELU.
  *   amax_out_dev: 1 float, or NULL: max |t| over the whole result (zeroed, then written
  *           by this call), so that the next quantization of t (fp4_global_scale, then

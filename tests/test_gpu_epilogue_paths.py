@@ -271,3 +271,36 @@ def test_gated_to_codes(m, f, k, fmt, split):
     v, _ = act64(g64, "silu")
     ev = MAX_SLOPE * eg + act_error(g64, v)
     assert_close(h, v * u64, ev * u64.abs() + eu * v.abs() + ev * eu + 2.0 ** -23 * (v * u64).abs(), "H")
+
+
+@pytest.mark.parametrize("m,n,k", [(16, 288, 2048), (130, 288, 8192), (2560, 2048, 64)])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+def test_codes_of_a_value_that_has_none_latch(m, n, k, bad):
+    """As fp4_quantize does; a result without codes keeps the value and latches nothing."""
+    qa, qb = _operands(m, n, k, fp4.NVFP4)
+    bias = torch.zeros(n, device="cuda")
+    ws = torch.zeros(max(16, *(size(m, n, k, fp4.NVFP4, in_place) for in_place in (True, False)
+                               for size in (fp4.fp4_gemm_epilogue_workspace_size, fp4.fp4_gemm_gated_workspace_size))),
+                     dtype=torch.uint8, device="cuda")
+    codes, scales = codes_like(m, n, fp4.NVFP4)
+    gd, d = torch.tensor([0.01], device="cuda"), torch.empty(m, n, device="cuda")
+    head = (fp4.NVFP4, qa.codes, qa.scales, qa.g, qb.codes, qb.scales, qb.g)
+    tail = dict(workspace=ws, workspace_bytes=ws.numel())
+    calls = [
+        lambda c, s: fp4.fp4_gemm_epilogue(*head, m, n, k, bias, fp4.ACT_NONE, d, fp4.F32, c, s, gd, **tail),
+        lambda c, s: fp4.fp4_gemm_epilogue_ex(*head, m, n, k, bias, fp4.ACT_NONE, d, fp4.F32, d, fp4.F32, None, c, s, gd,
+                                              **tail),
+        lambda c, s: fp4.fp4_gemm_gated(*head, qb.codes, qb.scales, qb.g, m, n, k, bias, None, fp4.ACT_NONE, d, fp4.F32,
+                                        Hcodes=c, Hscales=s, gH=gd, **tail),
+    ]
+    for value, status in ((0.0, fp4.OK), (bad, fp4.ERR_NONFINITE)):
+        bias[n - 1] = value
+        for call in calls:
+            d.zero_()
+            call(codes, scales)
+            assert fp4.fp4_get_status() == status
+            d.zero_()
+            call(None, None)
+            assert fp4.fp4_get_status() == fp4.OK
+            assert torch.isfinite(d[:, n - 1]).all() == (status == fp4.OK)
+    assert not ws.any()
