@@ -68,6 +68,7 @@ static fp4_status device_state(unsigned** status) {
 }
 
 static bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+static bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 // Test hook (fp4_debug_stall_next_decode): the CTA whose amax share the next fused decode
 // launch of this thread leaves unpublished, plus one (0: none).
@@ -105,6 +106,7 @@ fp4_status fp4_amax(const void* x, int64_t n, fp4_dtype in_dtype, float* amax_ou
   if (n <= 0) return fail(FP4_ERR_INVALID_ARG, "n must be positive");
   if (in_dtype != FP4_F32 && in_dtype != FP4_BF16) return fail(FP4_ERR_INVALID_ARG, "in_dtype");
   if (!aligned16(x) || !aligned16(workspace)) return fail(FP4_ERR_INVALID_ARG, "x and workspace must be 16-byte aligned");
+  if (!aligned4(amax_out)) return fail(FP4_ERR_INVALID_ARG, "amax_out alignment");
   if (workspace_bytes < kQuantWorkspaceBytes) return fail(FP4_ERR_INVALID_ARG, "workspace too small");
   unsigned* status;
   fp4_status s = device_state(&status);
@@ -143,6 +145,8 @@ static fp4_status quantize_common(const void* x, int64_t rows, int64_t cols, fp4
       (scalesT && !aligned16(scalesT)))
     return fail(FP4_ERR_INVALID_ARG, "x, codes and scales must be 16-byte aligned");
   if (num_groups && (num_groups > kMaxGroups || !offsets)) return fail(FP4_ERR_INVALID_ARG, "groups / offsets");
+  if (!aligned4(gout) || !aligned4(gin) || !aligned4(offsets))
+    return fail(FP4_ERR_INVALID_ARG, "global scale / offsets alignment");
   if (variant != kQuantPlain && two_d) return fail(FP4_ERR_UNSUPPORTED, "quantizer variants are 1-D only");
   if (variant == kQuantMxFloor && fmt != FP4_MXFP4) return fail(FP4_ERR_INVALID_ARG, "the E8M0 floor is for MXFP4");
   if (variant == kQuantSR && (fmt != FP4_NVFP4 || !rbits || !aligned16(rbits)))
@@ -224,6 +228,7 @@ fp4_status fp4_quantize_rht(const void* x, int64_t rows, int64_t cols, fp4_dtype
 
 fp4_status fp4_global_scale(const float* amax, float* global_out, void* stream) {
   if (!amax || !global_out) return fail(FP4_ERR_INVALID_ARG, "null pointer");
+  if (!aligned4(amax) || !aligned4(global_out)) return fail(FP4_ERR_INVALID_ARG, "amax / global_out alignment");
   unsigned* status;
   fp4_status s = device_state(&status);
   if (s != FP4_OK) return s;
@@ -244,6 +249,7 @@ fp4_status fp4_quantize_grouped(const void* x, int64_t rows, int64_t cols, fp4_d
 fp4_status fp4_dequantize(const uint8_t* codes, const uint8_t* scales, const float* global, int64_t rows,
                           int64_t cols, fp4_fmt fmt, float* out, void* stream) {
   if (!codes || !scales || !out) return fail(FP4_ERR_INVALID_ARG, "null pointer");
+  if (!aligned4(global) || !aligned4(out)) return fail(FP4_ERR_INVALID_ARG, "global / out alignment");
   if (rows <= 0 || cols <= 0 || cols % 32 != 0) return fail(FP4_ERR_INVALID_ARG, "shape");
   if (fmt != FP4_NVFP4 && fmt != FP4_MXFP4) return fail(FP4_ERR_INVALID_ARG, "fmt");
   unsigned* status;
@@ -269,6 +275,8 @@ static fp4_status gemm_check(const GemmProblem& g, fp4_fmt fmt, fp4_dtype out_dt
   if (g.M > (1ll << 31) - 256 || g.N > (1ll << 31) - 256) return fail(FP4_ERR_UNSUPPORTED, "dimension too large");
   if (!aligned16(g.A) || !aligned16(g.B) || !aligned16(g.sA) || !aligned16(g.sB) || (g.D && !aligned16(g.D)))
     return fail(FP4_ERR_INVALID_ARG, "A, B, scales and D must be 16-byte aligned");
+  if (!aligned4(g.gA) || !aligned4(g.gB) || !aligned4(g.q_g) || !aligned4(g.offsets))
+    return fail(FP4_ERR_INVALID_ARG, "global scale / offsets alignment");
   return FP4_OK;
 }
 
@@ -365,7 +373,6 @@ fp4_status fp4_gemm(fp4_fmt fmt, const uint8_t* A, const uint8_t* sA, const floa
 
 static bool act_ok(fp4_act act) { return act >= FP4_ACT_NONE && act <= FP4_ACT_GELU_TANH; }
 static bool dtype_ok(fp4_dtype t) { return t == FP4_F32 || t == FP4_BF16; }
-static bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 static fp4_status epilogue_common(fp4_fmt fmt, const uint8_t* A, const uint8_t* sA, const float* gA, const uint8_t* B,
                                   const uint8_t* sB, const float* gB, int64_t M, int64_t N, int64_t K,
@@ -476,6 +483,8 @@ static fp4_status gated_common(GatedProblem& g, fp4_fmt fmt, fp4_act act, fp4_dt
       !aligned16(g.sWu) || !aligned16(g.H) || !aligned16(g.G) || !aligned16(g.U))
     return fail(FP4_ERR_INVALID_ARG, "A, weights, scales, H, G and U must be 16-byte aligned");
   if (!aligned4(g.bias_g) || !aligned4(g.bias_u)) return fail(FP4_ERR_INVALID_ARG, "bias alignment");
+  if (!aligned4(g.gA) || !aligned4(g.gWg) || !aligned4(g.gWu) || !aligned4(g.q_g) || !aligned4(g.offsets))
+    return fail(FP4_ERR_INVALID_ARG, "global scale / offsets alignment");
   if (g.q_codes && (!g.q_scales || !g.q_g)) return fail(FP4_ERR_INVALID_ARG, "FP4 output needs Hscales and gH");
   if (g.q_codes && g.F % 32 != 0) return fail(FP4_ERR_INVALID_ARG, "FP4 output needs F % 32 == 0");
   if (g.q_codes && (!aligned16(g.q_codes) || !aligned16(g.q_scales))) return fail(FP4_ERR_INVALID_ARG, "Hcodes / Hscales alignment");
@@ -569,6 +578,7 @@ fp4_status fp4_gemm_gated_bf16a(const void* X, const uint8_t* Wg, const uint8_t*
       !aligned16(G) || !aligned16(U) || !aligned16(Xcodes) || !aligned16(Xscales) || !aligned16(workspace))
     return fail(FP4_ERR_INVALID_ARG, "buffers must be 16-byte aligned");
   if (!aligned4(bias_g) || !aligned4(bias_u)) return fail(FP4_ERR_INVALID_ARG, "bias alignment");
+  if (!aligned4(gWg) || !aligned4(gWu) || !aligned4(gX)) return fail(FP4_ERR_INVALID_ARG, "global scale alignment");
   if (workspace_bytes < fp4_gemm_gated_bf16a_workspace_size(M, F, K))
     return fail(FP4_ERR_INVALID_ARG, "workspace too small (see fp4_gemm_gated_bf16a_workspace_size)");
   uint8_t* const ws = static_cast<uint8_t*>(workspace) + quant_ws_aligned();
@@ -622,7 +632,6 @@ fp4_status fp4_gemm_gated_grouped(fp4_fmt fmt, int num_groups, const int32_t* of
                                   int64_t total_rows, int64_t F, int64_t K, const float* bias_g, const float* bias_u,
                                   fp4_act act, void* H, fp4_dtype out_dtype, void* G, void* U, void* stream) {
   if (num_groups <= 0 || num_groups > kMaxGroups || !offsets) return fail(FP4_ERR_INVALID_ARG, "groups / offsets");
-  if (!aligned4(gWg) || !aligned4(gWu)) return fail(FP4_ERR_INVALID_ARG, "global scale alignment");
   GatedProblem g{};
   g.A = A;
   g.sA = sA;
@@ -656,6 +665,7 @@ static fp4_status check_codes(fp4_fmt fmt, const uint8_t* codes, const uint8_t* 
   if (fmt == FP4_NVFP4 && !global) return fail(FP4_ERR_INVALID_ARG, "NVFP4 output needs the caller's global scale");
   if (cols % 32 != 0) return fail(FP4_ERR_INVALID_ARG, "FP4 output needs cols % 32 == 0");
   if (!aligned16(codes) || !aligned16(scales)) return fail(FP4_ERR_INVALID_ARG, "codes and scales must be 16-byte aligned");
+  if (!aligned4(global)) return fail(FP4_ERR_INVALID_ARG, "global scale alignment");
   q->fmt = fmt == FP4_MXFP4 ? 2 : 1;
   q->codes = const_cast<uint8_t*>(codes);
   q->scales = const_cast<uint8_t*>(scales);
@@ -826,6 +836,7 @@ fp4_status fp4_gemm_bf16a(const void* X, const uint8_t* B, const uint8_t* sB, co
   if (!aligned16(X) || !aligned16(B) || !aligned16(sB) || !aligned16(D) || !aligned16(Xcodes) || !aligned16(Xscales) ||
       !aligned16(workspace))
     return fail(FP4_ERR_INVALID_ARG, "buffers must be 16-byte aligned");
+  if (!aligned4(gB) || !aligned4(gX)) return fail(FP4_ERR_INVALID_ARG, "global scale alignment");
   if (workspace_bytes < gemm_bf16a_workspace_bytes(M, N, K))
     return fail(FP4_ERR_INVALID_ARG, "workspace too small (see fp4_gemm_bf16a_workspace_size)");
   const size_t qws = (kQuantWorkspaceBytes + 255) / 256 * 256;

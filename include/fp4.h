@@ -34,6 +34,7 @@
  *
  * Ownership and streams: every pointer named *_dev or documented "device" is
  * caller-owned device memory; the library allocates no device memory in any call.
+ * Global scales, maxima and offsets are 4-byte aligned; other alignments stand with the calls.
  * All work is enqueued on the caller's stream (cudaStream_t passed as void*; NULL is
  * the legacy default stream); no call synchronizes the host except
  * fp4_get_status().  Global scales stay on the device (no host round trip).
