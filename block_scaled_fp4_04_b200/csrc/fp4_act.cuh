@@ -40,8 +40,9 @@ constexpr float kInvSqrt2Pi = 0.39894228040143268f;
 
 // Phi(x), and e^(-x^2/2) for its derivative: erfc(z) = e^(-z^2) P(t), t = 1 / (1 + 0.3275911 z),
 // z = |x| / sqrt(2) >= 0, the rational approximation 7.1.26 of Abramowitz and Stegun's Handbook
-// of Mathematical Functions (error at most 1.5e-7; 2.6e-7 in all in FP32).  Half the instructions of erff, no branch,
-// and no 1 + erf of nearly -1 for x << 0.
+// of Mathematical Functions (error at most 1.5e-7; x Phi(x) / x is within 3.4e-7 over [-40, 40] in
+// all, 0.2% of Phi itself at x = -5).  Half the instructions of erff, no branch, and no 1 + erf
+// of nearly -1 for x << 0.
 __device__ __forceinline__ float normal_cdf(float x, float& e) {
   const float z = fabsf(x) * kSqrtHalf;
   const float t = rcp_sfu(fmaf(0.3275911f, z, 1.0f));

@@ -257,6 +257,8 @@ fp4_status fp4_gemm_mixed(fp4_fmt a_fmt, const uint8_t* A_dev, const uint8_t* sA
 /* Activations, computed in FP32: RELU max(x, 0), NaN for a NaN; SILU x s(x) with s(x) =
  * 1 / (1 + e^-x); GELU x Phi(x) (the normal distribution function, by erf); GELU_TANH
  * x s(2 c (x + 0.044715 x^3)), c = sqrt(2 / pi) (the tanh form: (1 + tanh y) / 2 = s(2y)).
+ * Phi is within 3.5e-7 of the exact value (an absolute error: where x << 0 and Phi is tiny
+ * itself, much of it -- 0.2% at x = -5), s within 2e-7, slopes within 2e-6.
  * fp4_gemm_epilogue takes NONE and RELU, the entry points below it all of them. */
 typedef enum {
   FP4_ACT_NONE = 0,
