@@ -220,26 +220,6 @@ fp4_status fp4_gemm_ex(fp4_fmt fmt, const uint8_t* A_dev, const uint8_t* sA_dev,
                        int64_t M, int64_t N, int64_t K, void* D_dev, fp4_dtype out_dtype,
                        void* workspace_dev, size_t workspace_bytes, unsigned flags, void* stream);
 
-/* GEMM with the epilogue that follows the scale ("Rubin FP4 GEMM overview" 3.2: the FP32
- * result is multiplied by the scale factors, the bias is added, the activation applied,
- * then it is converted to the output format, FP4 included; 4.2: C = (A.B)(sA.sB) + bias):
- *   t[m, n] = act(gA gB sum_k ... + bias[n])      (FP32: product, then + bias, then act)
- *   D_dev   [M, N] in out_dtype (BF16 round to nearest even, or FP32), or NULL;
- *   Dcodes_dev / Dscales_dev: or an NVFP4 copy of t (or both): 16-element blocks along n,
- *           codes [M, N/2], scales fp4_scales_bytes(M, N, FP4_NVFP4) in the swizzled
- *           layout, quantized exactly as fp4_quantize would quantize the FP32 t with
- *           global_in = gD_dev (the caller's global scale: t's amax is not known until
- *           the whole product is, so it cannot be computed here); a non-finite t latches
- *           FP4_ERR_NONFINITE.  The layout's pad bytes are written as 0, as fp4_quantize
- *           writes them.  The result can feed the next fp4_gemm as its A operand
- *           directly.  Needs N % 32 == 0.
- *   bias_dev [N] FP32 or NULL; act FP4_ACT_NONE or FP4_ACT_RELU.
- *   amax_out_dev: 1 float, or NULL: max |t| over the whole result (zeroed, then written
- *           by this call), so that the next quantization of t (fp4_global_scale, then
- *           fp4_quantize with global_in) needs no separate amax pass over it.
- * workspace: fp4_gemm_epilogue_workspace_size(M, N, K, fmt, rows_in_place) bytes with
- * rows_in_place = (Dcodes_dev != NULL || amax_out_dev != NULL), aligned as fp4_gemm's and
- * zero-filled before first use (left zero-filled).  Plain (not grouped) problems only. */
 /* Mixed-format GEMM ("Rubin FP4 GEMM overview" 3.4: weights in FP4 where they tolerate it,
  * activations kept in FP8, or the other way round): D[M, N] = A[M, K] B[N, K]^T with each
  * operand FP4_MXFP4 (E2M1 codes [rows, K/2], E8M0 scales per 32) or FP4_MXFP8 (E4M3
@@ -267,6 +247,27 @@ typedef enum {
   FP4_ACT_GELU = 3,
   FP4_ACT_GELU_TANH = 4
 } fp4_act;
+
+/* GEMM with the epilogue that follows the scale ("Rubin FP4 GEMM overview" 3.2: the FP32
+ * result is multiplied by the scale factors, the bias is added, the activation applied,
+ * then it is converted to the output format, FP4 included; 4.2: C = (A.B)(sA.sB) + bias):
+ *   t[m, n] = act(gA gB sum_k ... + bias[n])      (FP32: product, then + bias, then act)
+ *   D_dev   [M, N] in out_dtype (BF16 round to nearest even, or FP32), or NULL;
+ *   Dcodes_dev / Dscales_dev: or an NVFP4 copy of t (or both): 16-element blocks along n,
+ *           codes [M, N/2], scales fp4_scales_bytes(M, N, FP4_NVFP4) in the swizzled
+ *           layout, quantized exactly as fp4_quantize would quantize the FP32 t with
+ *           global_in = gD_dev (the caller's global scale: t's amax is not known until
+ *           the whole product is, so it cannot be computed here); a non-finite t latches
+ *           FP4_ERR_NONFINITE.  The layout's pad bytes are written as 0, as fp4_quantize
+ *           writes them.  The result can feed the next fp4_gemm as its A operand
+ *           directly.  Needs N % 32 == 0.
+ *   bias_dev [N] FP32 or NULL; act FP4_ACT_NONE or FP4_ACT_RELU.
+ *   amax_out_dev: 1 float, or NULL: max |t| over the whole result (zeroed, then written
+ *           by this call), so that the next quantization of t (fp4_global_scale, then
+ *           fp4_quantize with global_in) needs no separate amax pass over it.
+ * workspace: fp4_gemm_epilogue_workspace_size(M, N, K, fmt, rows_in_place) bytes with
+ * rows_in_place = (Dcodes_dev != NULL || amax_out_dev != NULL), aligned as fp4_gemm's and
+ * zero-filled before first use (left zero-filled).  Plain (not grouped) problems only. */
 size_t fp4_gemm_epilogue_workspace_size(int64_t M, int64_t N, int64_t K, fp4_fmt fmt, int rows_in_place);
 fp4_status fp4_gemm_epilogue(fp4_fmt fmt, const uint8_t* A_dev, const uint8_t* sA_dev, const float* gA_dev,
                              const uint8_t* B_dev, const uint8_t* sB_dev, const float* gB_dev,
@@ -363,7 +364,8 @@ fp4_status fp4_gemm_gated_grouped(fp4_fmt fmt, int num_groups, const int32_t* of
  *       order: the same bits every time);
  *   amax_out_dev 1 float: max |dZ| (zeroed, then written by this call).
  * workspace: fp4_act_backward_workspace_size(rows, cols, gated) bytes, needed for dbias only,
- * any contents; what it uses of it is left zero-filled.  Matrices 16-byte aligned. */
+ * 16-byte aligned, any contents, not shared by calls that overlap; what it uses of it is left
+ * zero-filled.  Matrices 16-byte aligned. */
 size_t fp4_act_backward_workspace_size(int64_t rows, int64_t cols, int gated);
 fp4_status fp4_act_backward(const void* dH_dev, const void* G_dev, const void* U_dev, int64_t rows, int64_t cols,
                             fp4_dtype in_dtype, fp4_act act, void* dZ_dev, fp4_dtype out_dtype, float* dbias_dev,
@@ -397,7 +399,8 @@ fp4_status fp4_layernorm(const void* x_dev, int64_t rows, int64_t cols, fp4_dtyp
  *           where the types agree.
  *   dweight_dev, dbias_dev  [cols] FP32 or NULL each; their sums have a fixed order.
  * workspace: fp4_layernorm_backward_workspace_size(rows, cols) bytes, needed for dweight or
- * dbias only, any contents, 16-byte aligned; what it uses of it is left zero-filled. */
+ * dbias only, any contents, 16-byte aligned, not shared by calls that overlap; what it uses of
+ * it is left zero-filled. */
 size_t fp4_layernorm_backward_workspace_size(int64_t rows, int64_t cols);
 fp4_status fp4_layernorm_backward(const void* dy_dev, const void* x_dev, int64_t rows, int64_t cols,
                                   fp4_dtype in_dtype, const float* weight_dev, const float* mean_dev,
