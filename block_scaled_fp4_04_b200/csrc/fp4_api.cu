@@ -818,7 +818,9 @@ fp4_status fp4_layernorm_backward(const void* dy, const void* x, int64_t rows, i
 
 size_t fp4_gemm_epilogue_workspace_size(int64_t M, int64_t N, int64_t K, fp4_fmt fmt, int rows_in_place) {
   if (M <= 0 || N <= 0 || K <= 0) return 0;
-  return gemm_full_workspace_bytes(M, N, K, fmt == FP4_MXFP4, rows_in_place != 0);
+  const int mx = fmt == FP4_MXFP4;  // (the plain epilogue's plan can be another one)
+  return std::max(gemm_full_workspace_bytes(M, N, K, mx, rows_in_place != 0),
+                  gemm_workspace_bytes(M, N, K, mx, rows_in_place != 0));
 }
 
 size_t fp4_gemm_bf16a_workspace_size(int64_t M, int64_t N, int64_t K) {

@@ -930,7 +930,11 @@ __global__ void __launch_bounds__(DecodeCfg<BN>::kThreads, 1)
 
 // ---------------------------------------------------------------------- host side
 constexpr int kDecodeMaxCtas = 512;  // amax slots in the workspace
-bool decode_eligible(int64_t M, int64_t N, int64_t K) { return M >= 1 && M <= 32 && N >= 1 && K >= 32; }
+// At most one segment per CTA in the grid: longer K (from 303105 on with 148 SMs) would not fit the
+// segments' buffers and takes the general kernels.
+bool decode_eligible(int64_t M, int64_t N, int64_t K) {
+  return M >= 1 && M <= 32 && N >= 1 && K >= 32 && (K + 255) / 256 <= decode_max_seg(32) * static_cast<int64_t>(num_sms());
+}
 
 struct DecodePlan {
   int nseg, seg_len, ctas_per_seg, tiles, num_kb;
@@ -947,7 +951,6 @@ static DecodePlan decode_plan(int64_t N, int64_t K, int bn, int weights) {
   int nseg = (d.num_kb + max_seg - 1) / max_seg;
   const int min_seg = 4;
   if (nseg < min_seg) nseg = d.num_kb < min_seg ? d.num_kb : min_seg;
-  if (nseg > sms) nseg = sms;
   const int max_ctas = sms < kDecodeMaxCtas ? sms : kDecodeMaxCtas;
   d.seg_len = (d.num_kb + nseg - 1) / nseg;
   d.nseg = (d.num_kb + d.seg_len - 1) / d.seg_len;

@@ -267,6 +267,10 @@ size_t gemm_workspace_align(int64_t M, int64_t N, int64_t K, int mx, bool fp4_ou
   return row % 4 == 0 ? 16 : 4;
 }
 
+// Whether the long epilogue's operands stay in place: for outputs by rows, and for the few rows of
+// NVFP4 that have a K too long for the decode kernel (its small-N kernels are for MXFP4).
+static bool full_in_place(int64_t M, int mx, bool fp4_out) { return fp4_out || (!mx && M <= 32); }
+
 // The long epilogue keeps its partial sums in rows of whole float4s.
 static size_t full_ws_bytes(const Plan& pl, int64_t M) {
   if (pl.mode != kModeStreamK || pl.swap) return pl.ws_bytes;
@@ -275,7 +279,7 @@ static size_t full_ws_bytes(const Plan& pl, int64_t M) {
 
 size_t gemm_full_workspace_bytes(int64_t M, int64_t N, int64_t K, int mx, bool fp4_out) {
   if (!mx && !fp4_out && decode_eligible(M, N, K)) return decode_workspace_bytes(M, N);
-  return full_ws_bytes(make_plan(M, N, K, 0, mx, fp4_out), M);
+  return full_ws_bytes(make_plan(M, N, K, 0, mx, full_in_place(M, mx, fp4_out)), M);
 }
 
 // the quantize workspace (tensor amax), then the GEMM's
@@ -331,7 +335,8 @@ int launch_gemm_full(const GemmProblemFull& g, unsigned* status, cudaStream_t st
     return launch_decode(q, status, st, why, err);
   }
   // the NVFP4 copy of the result is written by rows: keep the operands in place
-  const Plan pl = make_plan(g.M, g.N, g.K, g.num_groups, g.mx, g.q_codes != nullptr || g.amax_out != nullptr);
+  const bool by_rows = g.q_codes != nullptr || g.amax_out != nullptr;
+  const Plan pl = make_plan(g.M, g.N, g.K, g.num_groups, g.mx, g.full ? full_in_place(g.M, g.mx, by_rows) : by_rows);
   const size_t need = g.full ? full_ws_bytes(pl, g.M) : pl.ws_bytes;
   if (g.ws_bytes < need || (need && !g.ws)) {
     *why = "workspace too small (see fp4_gemm_workspace_size)";

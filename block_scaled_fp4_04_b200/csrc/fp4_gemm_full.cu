@@ -11,7 +11,7 @@ static cudaError_t dispatch_full_t(const Plan& pl, const GemmMaps& tm, const Gem
     return pl.pair ? run<256, MX, 1, true, false, kEpiFullWhole>(tm, a, pl.units, st)
                    : run<256, MX, 1, false, false, kEpiFullWhole>(tm, a, pl.units, st);
   }
-  if constexpr (MX) {  // (up to 32 rows of NVFP4 take the decode kernel)
+  if constexpr (MX) {  // (up to 32 rows of NVFP4 take the decode kernel, or stay in place)
     if (pl.BN == 16) return run<16, MX, 2, false, false, kEpiFull>(tm, a, pl.units, st);
     if (pl.BN == 32) return run<32, MX, 2, false, false, kEpiFull>(tm, a, pl.units, st);
   }

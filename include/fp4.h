@@ -309,8 +309,8 @@ fp4_status fp4_gemm_epilogue_ex(fp4_fmt fmt, const uint8_t* A_dev, const uint8_t
  * (Hcodes_dev != NULL || amax_out_dev != NULL); 16-byte aligned, zero-filled before first use,
  * left so.  With a workspace in use (few rows), partial sums meet by FP32 atomic additions,
  * whose order -- and so the last bits of H -- can differ from call to call, as in fp4_gemm.
- * flags: FP4_GEMM_WEIGHTS_READY (both weights).  M <= 16 with NVFP4 operands runs the decode
- * kernel over both weights. */
+ * flags: FP4_GEMM_WEIGHTS_READY (both weights).  M <= 16 with NVFP4 operands and neither a copy
+ * nor the maximum of H runs the decode kernel over both weights (K up to 2048 x SMs). */
 size_t fp4_gemm_gated_workspace_size(int64_t M, int64_t F, int64_t K, fp4_fmt fmt, int rows_in_place);
 fp4_status fp4_gemm_gated(fp4_fmt fmt, const uint8_t* A_dev, const uint8_t* sA_dev, const float* gA_dev,
                           const uint8_t* Wg_dev, const uint8_t* sWg_dev, const float* gWg_dev,

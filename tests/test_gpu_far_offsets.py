@@ -1,4 +1,5 @@
-"""Matrices of more than 2^31 elements: the last rows are those of the same call on them alone."""
+"""Matrices of more than 2^31 elements: the last rows are those of the same call on them alone.  Few
+rows with a K beyond the decode kernel's."""
 import pytest
 import torch
 
@@ -75,3 +76,43 @@ def test_products(n):
     for a, b in ((d, d2), (pre, pre2), (h, h2), (g, g2)):
         assert torch.equal(a[lo:], b)
     assert fp4.fp4_get_status() == fp4.OK
+
+
+@pytest.mark.parametrize("m,n,more", [(1, 64, 0), (16, 64, 0), (32, 64, 0), (1, 64, 32), (16, 64, 32), (32, 64, 32),
+                                      (16, 9500, 32)])  # (the last: enough tiles not to split K)
+def test_few_rows_with_the_longest_k(m, n, more):
+    """The last K that the decode kernel takes, and the first that it does not."""
+    k = 2048 * torch.cuda.get_device_properties(0).multi_processor_count + more
+    x = torch.randn(m, k, generator=torch.Generator(device="cuda").manual_seed(1), device="cuda").to(torch.bfloat16)
+    w = torch.randn(n, k, generator=torch.Generator(device="cuda").manual_seed(2), device="cuda").mul_(0.02)
+    qa, qb = fp4.quantize(x, fp4.NVFP4), fp4.quantize(w, fp4.NVFP4)
+    del w
+
+    def values(q, rows):
+        out = torch.empty(rows, k, device="cuda")
+        fp4.fp4_dequantize(q.codes, q.scales, q.g, rows, k, fp4.NVFP4, out)
+        return out
+
+    a, b = values(qa, m).double(), values(qb, n)
+    parts = (b[i:i + 1000].double() for i in range(0, n, 1000))
+    z, size = (torch.cat(t, 1) for t in zip(*((a @ p.t(), a.abs() @ p.abs().t()) for p in parts)))
+    del b
+    err = 1e-6 * size + 2.0 ** -22 * z.abs()  # the products' bound, and the scales'
+    square = 2 * err * (z.abs() + err) + 2.0 ** -23 * z * z
+    r = torch.ones(m, n, device="cuda")
+    ws = fp4.Workspace()
+    assert ((fp4.gemm(qa, qb, torch.float32, ws) - z).abs() <= err).all()
+    d, pre = fp4.gemm_epilogue(qa, qb, residual=r, out_dtype=torch.float32, save=True, workspace=ws)
+    assert ((pre - z).abs() <= err).all() and ((d - 1 - z).abs() <= err + 2.0 ** -23 * (z.abs() + 1)).all()
+    h, g, u = fp4.gemm_gated(qa, qb, qb, fp4.ACT_NONE, out_dtype=torch.float32, save=True, workspace=ws)
+    assert ((g - z).abs() <= err).all() and ((u - z).abs() <= err).all() and ((h - z * z).abs() <= square).all()
+    xc = torch.empty(m, k // 2, dtype=torch.uint8, device="cuda")
+    xs = torch.empty(fp4.fp4_scales_bytes(m, k, fp4.NVFP4), dtype=torch.uint8, device="cuda")
+    xg, d = torch.empty(1, device="cuda"), torch.empty(m, n, device="cuda")
+    buf = ws.get(max(fp4.fp4_gemm_bf16a_workspace_size(m, n, k), fp4.fp4_gemm_gated_bf16a_workspace_size(m, n, k)))
+    fp4.fp4_gemm_gated_bf16a(x, qb.codes, qb.scales, qb.g, qb.codes, qb.scales, qb.g, m, n, k, None, None, fp4.ACT_NONE, d,
+                             fp4.F32, None, None, xc, xs, xg, buf, buf.numel())
+    assert ((d - z * z).abs() <= square).all() and torch.equal(xc, qa.codes) and torch.equal(xg, qa.g)
+    fp4.fp4_gemm_bf16a(x, qb.codes, qb.scales, qb.g, m, n, k, d, fp4.F32, xc, xs, xg, buf, buf.numel())
+    assert ((d - z).abs() <= err).all() and torch.equal(xc, qa.codes) and torch.equal(xg, qa.g)
+    assert not ws.buf.any() and fp4.fp4_get_status() == fp4.OK

@@ -75,3 +75,22 @@ def test_what_a_workspace_keeps_stays_below_what_it_uses():
     for n in range(5000, 200000, 1000):
         assert ws.get(n).numel() >= n
     assert sum(b.numel() for b in ws._outgrown) < ws.buf.numel() < 2 * 200000
+
+
+SLOTS = 512 * 128  # the decode kernel's workspace ends in these
+
+
+def test_a_k_too_long_for_the_decode_kernel_takes_the_others():
+    """A CTA holds one segment of at most 2048 elements of K; a grid has one CTA per SM (148 where
+    there is no GPU to ask)."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count if torch.cuda.is_available() else 148
+    last, n = 2048 * sms, 64
+    for m in (1, 16):
+        for size in (fp4.fp4_gemm_workspace_size, lambda *a: fp4.fp4_gemm_epilogue_workspace_size(*a, False),
+                     lambda *a: fp4.fp4_gemm_gated_workspace_size(*a, False)):
+            assert size(m, n, last, fp4.NVFP4) > SLOTS
+            assert 0 < size(m, n, last + 32, fp4.NVFP4) < SLOTS
+    # whatever the epilogue's plan is, one size serves it with and without its extras
+    for m, n in ((1, 64), (16, 28672), (32, 40000)):
+        assert (fp4.fp4_gemm_epilogue_workspace_size(m, n, last + 32, fp4.NVFP4, False)
+                >= fp4.fp4_gemm_workspace_size(m, n, last + 32, fp4.NVFP4))
