@@ -69,6 +69,7 @@ static fp4_status device_state(unsigned** status) {
 
 static bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 static bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+constexpr int64_t kMaxDim = (1ll << 31) - 256;  // rows, columns and tiles are counted in 32 bits
 
 // Test hook (fp4_debug_stall_next_decode): the CTA whose amax share the next fused decode
 // launch of this thread leaves unpublished, plus one (0: none).
@@ -124,7 +125,7 @@ static fp4_status quantize_common(const void* x, int64_t rows, int64_t cols, fp4
   if (!x || !codes || !scales) return fail(FP4_ERR_INVALID_ARG, "null pointer");
   if (rows <= 0 || cols <= 0) return fail(FP4_ERR_INVALID_ARG, "rows and cols must be positive");
   if (cols % 32 != 0) return fail(FP4_ERR_INVALID_ARG, "cols must be a multiple of 32");
-  if (rows > (1ll << 31) - 256) return fail(FP4_ERR_UNSUPPORTED, "rows too large");  // row offsets are int32
+  if (rows > kMaxDim) return fail(FP4_ERR_UNSUPPORTED, "rows too large");  // row offsets are int32
   if (in_dtype != FP4_F32 && in_dtype != FP4_BF16) return fail(FP4_ERR_INVALID_ARG, "in_dtype");
   if (fmt != FP4_NVFP4 && fmt != FP4_MXFP4 && fmt != FP4_MXFP8) return fail(FP4_ERR_INVALID_ARG, "fmt");
   if (fmt == FP4_MXFP8) {
@@ -272,7 +273,8 @@ static fp4_status gemm_check(const GemmProblem& g, fp4_fmt fmt, fp4_dtype out_dt
   if (!g.A || !g.B || !g.sA || !g.sB || (!g.D && !g.q_codes)) return fail(FP4_ERR_INVALID_ARG, "null pointer");
   if (g.M <= 0 || g.N <= 0 || g.K <= 0) return fail(FP4_ERR_INVALID_ARG, "M, N, K must be positive");
   if (g.K % 32 != 0) return fail(FP4_ERR_INVALID_ARG, "K must be a multiple of 32");
-  if (g.M > (1ll << 31) - 256 || g.N > (1ll << 31) - 256) return fail(FP4_ERR_UNSUPPORTED, "dimension too large");
+  if (g.M > kMaxDim || g.N > kMaxDim || g.K > kMaxDim) return fail(FP4_ERR_UNSUPPORTED, "dimension too large");
+  if (g.num_groups > 0 && g.N > kMaxDim / g.num_groups) return fail(FP4_ERR_UNSUPPORTED, "too many weight rows");
   if (!aligned16(g.A) || !aligned16(g.B) || !aligned16(g.sA) || !aligned16(g.sB) || (g.D && !aligned16(g.D)))
     return fail(FP4_ERR_INVALID_ARG, "A, B, scales and D must be 16-byte aligned");
   if (!aligned4(g.gA) || !aligned4(g.gB) || !aligned4(g.q_g) || !aligned4(g.offsets))
@@ -315,7 +317,7 @@ fp4_status fp4_gemm_mixed(fp4_fmt a_fmt, const uint8_t* A, const uint8_t* sA, fp
   if (!A || !B || !sA || !sB || !D) return fail(FP4_ERR_INVALID_ARG, "null pointer");
   if (M <= 0 || N <= 0 || K <= 0) return fail(FP4_ERR_INVALID_ARG, "M, N, K must be positive");
   if (K % 128 != 0) return fail(FP4_ERR_INVALID_ARG, "K must be a multiple of 128");
-  if (M > (1ll << 31) - 256 || N > (1ll << 31) - 256) return fail(FP4_ERR_UNSUPPORTED, "dimension too large");
+  if (M > kMaxDim || N > kMaxDim || K > kMaxDim) return fail(FP4_ERR_UNSUPPORTED, "dimension too large");
   if (!aligned32(A) || !aligned32(B) || !aligned16(sA) || !aligned16(sB) || !aligned16(D))
     return fail(FP4_ERR_INVALID_ARG, "A and B must be 32-byte aligned, scales and D 16-byte aligned");
   unsigned* status;
@@ -476,9 +478,8 @@ static fp4_status gated_common(GatedProblem& g, fp4_fmt fmt, fp4_act act, fp4_dt
   if (g.G && (g.G == g.U || g.G == g.H || g.U == g.H)) return fail(FP4_ERR_INVALID_ARG, "H, G and U must be different buffers");
   if (g.M <= 0 || g.F <= 0 || g.K <= 0) return fail(FP4_ERR_INVALID_ARG, "M, F, K must be positive");
   if (g.K % 32 != 0) return fail(FP4_ERR_INVALID_ARG, "K must be a multiple of 32");
-  const int64_t most = (1ll << 31) - 256;
-  if (g.M > most || g.F > most || g.K > most) return fail(FP4_ERR_UNSUPPORTED, "dimension too large");
-  if (g.num_groups > 0 && g.F > most / g.num_groups) return fail(FP4_ERR_UNSUPPORTED, "too many weight rows");
+  if (g.M > kMaxDim || g.F > kMaxDim || g.K > kMaxDim) return fail(FP4_ERR_UNSUPPORTED, "dimension too large");
+  if (g.num_groups > 0 && g.F > kMaxDim / g.num_groups) return fail(FP4_ERR_UNSUPPORTED, "too many weight rows");
   if (!aligned16(g.A) || !aligned16(g.sA) || !aligned16(g.Wg) || !aligned16(g.sWg) || !aligned16(g.Wu) ||
       !aligned16(g.sWu) || !aligned16(g.H) || !aligned16(g.G) || !aligned16(g.U))
     return fail(FP4_ERR_INVALID_ARG, "A, weights, scales, H, G and U must be 16-byte aligned");
@@ -567,8 +568,7 @@ fp4_status fp4_gemm_gated_bf16a(const void* X, const uint8_t* Wg, const uint8_t*
   if (!X || !Wg || !sWg || !Wu || !sWu || !H || !Xcodes || !Xscales || !gX || !workspace)
     return fail(FP4_ERR_INVALID_ARG, "null pointer");
   if (M <= 0 || F <= 0 || K <= 0 || K % 32 != 0) return fail(FP4_ERR_INVALID_ARG, "shape (K % 32 == 0)");
-  const int64_t most = (1ll << 31) - 256;
-  if (M > most || F > most || K > most) return fail(FP4_ERR_UNSUPPORTED, "dimension too large");
+  if (M > kMaxDim || F > kMaxDim || K > kMaxDim) return fail(FP4_ERR_UNSUPPORTED, "dimension too large");
   if (!dtype_ok(out_dtype)) return fail(FP4_ERR_INVALID_ARG, "out_dtype");
   if (!act_ok(act)) return fail(FP4_ERR_INVALID_ARG, "act");
   if (flags & ~static_cast<unsigned>(FP4_GEMM_WEIGHTS_READY)) return fail(FP4_ERR_INVALID_ARG, "unknown flag");
@@ -833,6 +833,7 @@ fp4_status fp4_gemm_bf16a(const void* X, const uint8_t* B, const uint8_t* sB, co
                           void* workspace, size_t workspace_bytes, unsigned flags, void* stream) {
   if (!X || !B || !sB || !D || !Xcodes || !Xscales || !gX || !workspace) return fail(FP4_ERR_INVALID_ARG, "null pointer");
   if (M <= 0 || N <= 0 || K <= 0 || K % 32 != 0) return fail(FP4_ERR_INVALID_ARG, "shape (K % 32 == 0)");
+  if (M > kMaxDim || N > kMaxDim || K > kMaxDim) return fail(FP4_ERR_UNSUPPORTED, "dimension too large");
   if (out_dtype != FP4_F32 && out_dtype != FP4_BF16) return fail(FP4_ERR_INVALID_ARG, "out_dtype");
   if (flags & ~static_cast<unsigned>(FP4_GEMM_WEIGHTS_READY)) return fail(FP4_ERR_INVALID_ARG, "unknown flag");
   if (!aligned16(X) || !aligned16(B) || !aligned16(sB) || !aligned16(D) || !aligned16(Xcodes) || !aligned16(Xscales) ||
