@@ -94,6 +94,18 @@ def lib() -> ctypes.CDLL:
                 "fp4_layernorm": (I32, [P, I64, I64, I32, P, P, ctypes.c_float, P, I32, P, P, I32, P, P, P, P, P]),
                 "fp4_layernorm_backward_workspace_size": (SZ, [I64, I64]),
                 "fp4_layernorm_backward": (I32, [P, P, I64, I64, I32, P, P, P, P, P, I32, P, P, P, SZ, P]),
+                "fp4_moe_sort_workspace_size": (SZ, [I64, I32, I32]),
+                "fp4_moe_sort": (I32, [P, I32, I64, I32, I32, P, P, P, P, SZ, P]),
+                "fp4_moe_dispatch": (I32, [P, I64, I64, I32, I32, P, P, I32, P]),
+                "fp4_moe_dispatch_codes": (I32, [P, I64, I64, I32, I32, P, P, I32, P, I32, P, P, P, P]),
+                "fp4_moe_dispatch_i8": (I32, [P, I64, I64, I32, I32, P, P, P, P]),
+                "fp4_moe_combine": (I32, [P, I32, P, P, I64, I32, I64, P, I32, P, I32, P]),
+                "fp4_moe_combine_backward": (I32, [P, P, I32, P, P, I64, I32, I64, P, I32, P, P]),
+                "fp4_quantize_i8": (I32, [P, I64, I64, I32, P, P, P]),
+                "fp4_gemm_i8_workspace_size": (SZ, [I64, I64, I64]),
+                "fp4_gemm_i8": (I32, [P, P, P, P, I64, I64, I64, P, I32, P, I32, P, SZ, ctypes.c_uint, P]),
+                "fp4_gemm_i8_grouped_workspace_size": (SZ, [I32, I64, I64, I64]),
+                "fp4_gemm_i8_grouped": (I32, [I32, P, P, P, P, P, I64, I64, I64, P, I32, P, I32, P, SZ, P]),
                 "fp4_get_status": (I32, [P]),
                 "fp4_debug_encode": (I32, [P, I64, I32, P, P]),
                 "fp4_debug_stall_next_decode": (I32, [I32]),
@@ -327,6 +339,66 @@ def fp4_gemm_grouped(fmt, num_groups, offsets, A, sA, gA, B, sB, gB, total_rows,
     _check(lib().fp4_gemm_grouped(fmt, num_groups, _p(offsets), _p(A), _p(sA), _p(gA), _p(B), _p(sB), _p(gB),
                                   total_rows, N, K, _p(D), out_dtype, _p(workspace), workspace_bytes,
                                   _s(stream)))
+
+
+def fp4_moe_sort_workspace_size(tokens: int, topk: int, num_experts: int) -> int:
+    return int(lib().fp4_moe_sort_workspace_size(tokens, topk, num_experts))
+
+
+def fp4_moe_sort(ids, id_bytes, tokens, topk, num_experts, offsets, row_of, scale_row_of=None, workspace=None,
+                 workspace_bytes=0, stream=None):
+    _check(lib().fp4_moe_sort(_p(ids), id_bytes, tokens, topk, num_experts, _p(offsets), _p(row_of), _p(scale_row_of),
+                              _p(workspace), workspace_bytes, _s(stream)))
+
+
+def fp4_moe_dispatch(x, tokens, cols, in_dtype, topk, row_of, y, out_dtype, stream=None):
+    _check(lib().fp4_moe_dispatch(_p(x), tokens, cols, in_dtype, topk, _p(row_of), _p(y), out_dtype, _s(stream)))
+
+
+def fp4_moe_dispatch_codes(x, tokens, cols, in_dtype, topk, row_of, scale_row_of, num_experts, offsets, fmt, codes, scales,
+                           global_in=None, stream=None):
+    _check(lib().fp4_moe_dispatch_codes(_p(x), tokens, cols, in_dtype, topk, _p(row_of), _p(scale_row_of), num_experts,
+                                        _p(offsets), fmt, _p(codes), _p(scales), _p(global_in), _s(stream)))
+
+
+def fp4_moe_dispatch_i8(x, tokens, cols, in_dtype, topk, row_of, codes, row_scales, stream=None):
+    _check(lib().fp4_moe_dispatch_i8(_p(x), tokens, cols, in_dtype, topk, _p(row_of), _p(codes), _p(row_scales),
+                                     _s(stream)))
+
+
+def fp4_moe_combine(y, in_dtype, row_of, weights, tokens, topk, cols, residual, residual_dtype, out, out_dtype,
+                    stream=None):
+    _check(lib().fp4_moe_combine(_p(y), in_dtype, _p(row_of), _p(weights), tokens, topk, cols, _p(residual),
+                                 residual_dtype, _p(out), out_dtype, _s(stream)))
+
+
+def fp4_moe_combine_backward(dout, y, in_dtype, row_of, weights, tokens, topk, cols, dy, out_dtype, dweights=None,
+                             stream=None):
+    _check(lib().fp4_moe_combine_backward(_p(dout), _p(y), in_dtype, _p(row_of), _p(weights), tokens, topk, cols, _p(dy),
+                                          out_dtype, _p(dweights), _s(stream)))
+
+
+def fp4_quantize_i8(x, rows, cols, in_dtype, codes, row_scales, stream=None):
+    _check(lib().fp4_quantize_i8(_p(x), rows, cols, in_dtype, _p(codes), _p(row_scales), _s(stream)))
+
+
+def fp4_gemm_i8_workspace_size(M: int, N: int, K: int) -> int:
+    return int(lib().fp4_gemm_i8_workspace_size(M, N, K))
+
+
+def fp4_gemm_i8(A, sA, B, sB, M, N, K, bias, act, D, out_dtype, workspace=None, workspace_bytes=0, flags=0, stream=None):
+    _check(lib().fp4_gemm_i8(_p(A), _p(sA), _p(B), _p(sB), M, N, K, _p(bias), act, _p(D), out_dtype, _p(workspace),
+                             workspace_bytes, flags, _s(stream)))
+
+
+def fp4_gemm_i8_grouped_workspace_size(num_groups: int, total_rows: int, N: int, K: int) -> int:
+    return int(lib().fp4_gemm_i8_grouped_workspace_size(num_groups, total_rows, N, K))
+
+
+def fp4_gemm_i8_grouped(num_groups, offsets, A, sA, B, sB, total_rows, N, K, bias, act, D, out_dtype, workspace=None,
+                        workspace_bytes=0, stream=None):
+    _check(lib().fp4_gemm_i8_grouped(num_groups, _p(offsets), _p(A), _p(sA), _p(B), _p(sB), total_rows, N, K, _p(bias),
+                                     act, _p(D), out_dtype, _p(workspace), workspace_bytes, _s(stream)))
 
 
 def fp4_get_status(stream=None) -> int:
@@ -615,3 +687,177 @@ def transposed(w: Quantized) -> Quantized:
     """The W^T operand a 16x16 (block 256) quantization produced alongside W."""
     assert w.codesT is not None
     return Quantized(w.codesT, w.scalesT, w.g, w.cols, w.rows, w.fmt)
+
+
+# ---------------------------------------------------------------- experts, 8-bit integers
+# Devices, streams and density as for the feed-forward block above.
+@dataclass
+class Routing:
+    """Where a router's choices stand in the experts' order (moe_sort)."""
+    offsets: torch.Tensor               # int32 [num_experts + 1]
+    row_of: torch.Tensor                # int32 [tokens, topk]: a choice's row, -1 for none
+    scale_row_of: torch.Tensor          # int32 [tokens, topk]: its row in the grouped scale layout
+    num_experts: int
+
+    @property
+    def tokens(self) -> int:
+        return self.row_of.shape[0]
+
+    @property
+    def topk(self) -> int:
+        return self.row_of.shape[1]
+
+
+@dataclass
+class Int8Rows:
+    """Rows of signed 8-bit integers with one scale each (quantize_i8)."""
+    codes: torch.Tensor                 # int8 [rows, cols], weights of experts [experts, rows, cols]
+    scales: torch.Tensor                # float32 [rows] or [experts, rows]
+
+
+def moe_sort(ids: torch.Tensor, num_experts: int, stream=None) -> Routing:
+    """Rows of the choices ids [tokens, topk] (int32 or int64) in the experts' order; a number
+    outside [0, num_experts) is no expert."""
+    if ids.dim() != 2:
+        raise ValueError("ids must be [tokens, topk]")
+    if ids.dtype not in (torch.int32, torch.int64):
+        raise TypeError(f"ids must be int32 or int64, got {ids.dtype}")
+    tokens, topk = ids.shape
+    _dense("ids", ids, ids, (tokens, topk))
+    with _on(ids, stream) as s:
+        offsets = torch.empty(num_experts + 1, dtype=torch.int32, device=ids.device)
+        row_of, scale_row_of = (torch.empty(tokens, topk, dtype=torch.int32, device=ids.device) for _ in range(2))
+        nbytes = fp4_moe_sort_workspace_size(tokens, topk, num_experts)
+        # of its own: it needs no zero-fill and leaves none behind
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=ids.device) if nbytes else None
+        fp4_moe_sort(ids, ids.element_size(), tokens, topk, num_experts, offsets, row_of, scale_row_of, ws, nbytes, s)
+    return Routing(offsets, row_of, scale_row_of, num_experts)
+
+
+def _routed(r: Routing, like: torch.Tensor):
+    _dense("offsets", r.offsets, like, (r.num_experts + 1,), torch.int32)
+    for name, t in (("row_of", r.row_of), ("scale_row_of", r.scale_row_of)):
+        _dense(name, t, like, (r.tokens, r.topk), torch.int32)
+
+
+def moe_dispatch(x: torch.Tensor, routing: Routing, fmt: Optional[int] = None, global_in=None, out_dtype=None, stream=None):
+    """The rows of x [tokens, cols] in the experts' order, [tokens * topk, cols]; rows behind the
+    last expert's hold nothing.  With `fmt` (NVFP4, which needs the caller's `global_in`, or MXFP4) a
+    Quantized tensor with grouped scales instead, the A operand of the grouped products."""
+    tokens, cols = routing.tokens, x.shape[-1]
+    _dense("x", x, x, (tokens, cols))
+    _routed(routing, x)
+    _dense("global_in", global_in, x, (1,), torch.float32)
+    rows = tokens * routing.topk
+    with _on(x, stream) as s:
+        if fmt is None:
+            y = torch.empty(rows, cols, dtype=out_dtype or x.dtype, device=x.device)
+            fp4_moe_dispatch(x, tokens, cols, _dtype_code(x), routing.topk, routing.row_of, y, _out_code(y.dtype), s)
+            return y
+        if out_dtype is not None:
+            raise ValueError("a quantized result takes no out_dtype")
+        codes = torch.empty(rows, cols // 2, dtype=torch.uint8, device=x.device)
+        scales = torch.empty(fp4_scales_bytes_grouped(rows, routing.num_experts, cols, fmt), dtype=torch.uint8,
+                             device=x.device)
+        fp4_moe_dispatch_codes(x, tokens, cols, _dtype_code(x), routing.topk, routing.row_of, routing.scale_row_of,
+                               routing.num_experts, routing.offsets, fmt, codes, scales, global_in, s)
+        g = global_in if fmt == NVFP4 else torch.ones(1, dtype=torch.float32, device=x.device)
+        return Quantized(codes, scales, g, rows, cols, fmt)
+
+
+def moe_dispatch_i8(x: torch.Tensor, routing: Routing, stream=None) -> Int8Rows:
+    """The rows of x [tokens, cols] in the experts' order as 8-bit rows (cols % 16 == 0)."""
+    tokens, cols = routing.tokens, x.shape[-1]
+    _dense("x", x, x, (tokens, cols))
+    _routed(routing, x)
+    with _on(x, stream) as s:
+        codes = torch.empty(tokens * routing.topk, cols, dtype=torch.int8, device=x.device)
+        scales = torch.empty(tokens * routing.topk, dtype=torch.float32, device=x.device)
+        fp4_moe_dispatch_i8(x, tokens, cols, _dtype_code(x), routing.topk, routing.row_of, codes, scales, s)
+    return Int8Rows(codes, scales)
+
+
+def moe_combine(y: torch.Tensor, routing: Routing, weights=None, residual=None, out_dtype=None, stream=None,
+                out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """out[t] = sum over t's choices of weight * y[its row] + residual[t]; weights [tokens, topk]
+    FP32, or 1 each.  `out` may be the residual itself."""
+    tokens, cols = routing.tokens, y.shape[-1]
+    _dense("y", y, y, (tokens * routing.topk, cols))
+    _routed(routing, y)
+    _dense("weights", weights, y, (tokens, routing.topk), torch.float32)
+    _dense("residual", residual, y, (tokens, cols))
+    _dense("out", out, y, (tokens, cols))
+    rc = F32 if residual is None else _out_code(residual.dtype)
+    with _on(y, stream) as s:
+        if out is None:
+            out = torch.empty(tokens, cols, dtype=out_dtype or y.dtype, device=y.device)
+        fp4_moe_combine(y, _dtype_code(y), routing.row_of, weights, tokens, routing.topk, cols, residual, rc, out,
+                        _out_code(out.dtype), s)
+    return out
+
+
+def moe_dispatch_backward(dy: torch.Tensor, routing: Routing, out_dtype=None, stream=None) -> torch.Tensor:
+    """dx of moe_dispatch: the sum of dy over a token's rows."""
+    return moe_combine(dy, routing, out_dtype=out_dtype, stream=stream)
+
+
+def moe_combine_backward(dout: torch.Tensor, y: torch.Tensor, routing: Routing, weights=None, out_dtype=None, stream=None):
+    """(dy, dweights) of moe_combine (rows of dy behind the last expert's hold nothing); the
+    residual's gradient is dout itself."""
+    tokens, cols = routing.tokens, y.shape[-1]
+    _dense("y", y, y, (tokens * routing.topk, cols))
+    _dense("dout", dout, y, (tokens, cols), y.dtype)
+    _routed(routing, y)
+    _dense("weights", weights, y, (tokens, routing.topk), torch.float32)
+    with _on(y, stream) as s:
+        dy = torch.empty(tokens * routing.topk, cols, dtype=out_dtype or y.dtype, device=y.device)
+        dw = torch.empty(tokens, routing.topk, dtype=torch.float32, device=y.device)
+        fp4_moe_combine_backward(dout, y, _dtype_code(y), routing.row_of, weights, tokens, routing.topk, cols, dy,
+                                 _out_code(dy.dtype), dw, s)
+    return dy, dw
+
+
+def quantize_i8(x: torch.Tensor, stream=None) -> Int8Rows:
+    """Rows of x [rows, cols] (cols % 16 == 0), or of experts' weights [experts, rows, cols], as
+    8-bit integers with one scale each."""
+    if x.dim() not in (2, 3):
+        raise ValueError("x must be [rows, cols] or [experts, rows, cols]")
+    _dense("x", x, x, x.shape)
+    rows, cols = x.numel() // max(1, x.shape[-1]), x.shape[-1]
+    with _on(x, stream) as s:
+        codes = torch.empty(x.shape, dtype=torch.int8, device=x.device)
+        scales = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+        fp4_quantize_i8(x, rows, cols, _dtype_code(x), codes, scales, s)
+    return Int8Rows(codes, scales)
+
+
+def gemm_i8(a: Int8Rows, b: Int8Rows, bias=None, act: int = ACT_NONE, out_dtype=torch.bfloat16, offsets=None,
+            workspace: Optional[Workspace] = None, stream=None, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """D[M, N] = act(A . B^T + bias) in 8-bit integers.  With `offsets` (Routing.offsets) rows of A
+    sorted by expert, each with its expert's weights b [experts, N, K] and bias [experts, N]; rows of
+    D behind the last expert's are left as they were (`out`) or hold nothing."""
+    experts = () if offsets is None else (b.codes.shape[0],)
+    if a.codes.dim() != 2 or b.codes.dim() != 2 + len(experts) or a.codes.shape[1] != b.codes.shape[-1]:
+        raise ValueError("a must be [M, K] and b [N, K], with offsets [experts, N, K]")
+    (M, K), N, like = a.codes.shape, b.codes.shape[-2], a.codes
+    _dense("a.codes", a.codes, like, (M, K), torch.int8)
+    _dense("a.scales", a.scales, like, (M,), torch.float32)
+    _dense("b.codes", b.codes, like, (*experts, N, K), torch.int8)
+    _dense("b.scales", b.scales, like, (*experts, N), torch.float32)
+    _dense("bias", bias, like, (*experts, N), torch.float32)
+    _dense("out", out, like, (M, N))
+    if experts:
+        _dense("offsets", offsets, like, (experts[0] + 1,), torch.int32)
+    with _on(like, stream) as s:
+        if out is None:
+            out = torch.empty(M, N, dtype=out_dtype, device=like.device)
+        nbytes = (fp4_gemm_i8_grouped_workspace_size(experts[0], M, N, K) if experts
+                  else fp4_gemm_i8_workspace_size(M, N, K))
+        ws = (workspace or Workspace(like.device)).get(nbytes) if nbytes else None
+        size = ws.numel() if ws is not None else 0
+        if experts:
+            fp4_gemm_i8_grouped(experts[0], offsets, a.codes, a.scales, b.codes, b.scales, M, N, K, bias, act, out,
+                                _out_code(out.dtype), ws, size, s)
+        else:
+            fp4_gemm_i8(a.codes, a.scales, b.codes, b.scales, M, N, K, bias, act, out, _out_code(out.dtype), ws, size, 0, s)
+    return out

@@ -7,6 +7,7 @@
 
 #include "fp4.h"
 #include "fp4_internal.h"
+#include "fp4_moe.h"
 #include "fp4_ops.h"
 #include "fp4_ptx.cuh"
 
@@ -814,6 +815,278 @@ fp4_status fp4_layernorm_backward(const void* dy, const void* x, int64_t rows, i
   p.ws = static_cast<float*>(workspace);
   const cudaError_t e = launch_layernorm_grad(p, status, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? FP4_OK : cuda_fail(e, "layer norm backward launch");
+}
+
+// ------------------------------------------------------------------ tokens to experts and back
+constexpr int64_t kMaxSlots = 1ll << 30, kMaxMoeCols = 1ll << 24;
+
+static fp4_status check_moe(int64_t tokens, int64_t cols, int topk, fp4_dtype in_dtype, fp4_dtype out_dtype,
+                            const int32_t* row_of) {
+  if (!row_of) return fail(FP4_ERR_INVALID_ARG, "null pointer");
+  if (tokens <= 0 || cols <= 0 || topk <= 0) return fail(FP4_ERR_INVALID_ARG, "tokens, cols and topk must be positive");
+  if (topk > 1024 || tokens > kMaxSlots / topk || cols > kMaxMoeCols)
+    return fail(FP4_ERR_UNSUPPORTED, "dimension too large");
+  if (!dtype_ok(in_dtype) || !dtype_ok(out_dtype)) return fail(FP4_ERR_INVALID_ARG, "in_dtype / out_dtype");
+  if (!aligned4(row_of)) return fail(FP4_ERR_INVALID_ARG, "row_of alignment");
+  return FP4_OK;
+}
+
+size_t fp4_moe_sort_workspace_size(int64_t tokens, int topk, int num_experts) {
+  if (tokens <= 0 || topk <= 0 || num_experts <= 0 || topk > 1024 || num_experts > kMaxGroups || tokens > kMaxSlots / topk)
+    return 0;
+  return moe_sort_workspace_bytes(tokens * topk, num_experts);
+}
+
+fp4_status fp4_moe_sort(const void* ids, int id_bytes, int64_t tokens, int topk, int num_experts, int32_t* offsets,
+                        int32_t* row_of, int32_t* scale_row_of, void* workspace, size_t workspace_bytes, void* stream) {
+  const fp4_status c = check_moe(tokens, 1, topk, FP4_F32, FP4_F32, row_of);
+  if (c != FP4_OK) return c;
+  if (!ids || !offsets) return fail(FP4_ERR_INVALID_ARG, "null pointer");
+  if (id_bytes != 4 && id_bytes != 8) return fail(FP4_ERR_INVALID_ARG, "id_bytes must be 4 or 8");
+  if (num_experts <= 0 || num_experts > kMaxGroups) return fail(FP4_ERR_INVALID_ARG, "num_experts");
+  if ((reinterpret_cast<uintptr_t>(ids) & (id_bytes - 1)) || !aligned4(offsets) || !aligned4(scale_row_of))
+    return fail(FP4_ERR_INVALID_ARG, "ids / offsets / scale_row_of alignment");
+  const size_t need = moe_sort_workspace_bytes(tokens * topk, num_experts);
+  if (need && (!workspace || !aligned4(workspace) || workspace_bytes < need))
+    return fail(FP4_ERR_INVALID_ARG, "workspace too small or misaligned (see fp4_moe_sort_workspace_size)");
+  unsigned* status;
+  const fp4_status s = device_state(&status);
+  if (s != FP4_OK) return s;
+  const cudaError_t e = launch_moe_sort(ids, id_bytes, tokens * topk, num_experts, offsets, row_of, scale_row_of, workspace,
+                                        static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? FP4_OK : cuda_fail(e, "sort launch");
+}
+
+fp4_status fp4_moe_dispatch(const void* x, int64_t tokens, int64_t cols, fp4_dtype in_dtype, int topk,
+                            const int32_t* row_of, void* y, fp4_dtype out_dtype, void* stream) {
+  const fp4_status c = check_moe(tokens, cols, topk, in_dtype, out_dtype, row_of);
+  if (c != FP4_OK) return c;
+  if (!x || !y) return fail(FP4_ERR_INVALID_ARG, "null pointer");
+  if (!aligned16(x) || !aligned16(y)) return fail(FP4_ERR_INVALID_ARG, "x and y must be 16-byte aligned");
+  if (x == y) return fail(FP4_ERR_INVALID_ARG, "y must not be x");
+  unsigned* status;
+  const fp4_status s = device_state(&status);
+  if (s != FP4_OK) return s;
+  DispatchProblem p{};
+  p.x = x;
+  p.bf16 = in_dtype == FP4_BF16;
+  p.tokens = tokens;
+  p.cols = cols;
+  p.topk = topk;
+  p.row_of = row_of;
+  p.y = y;
+  p.y_bf16 = out_dtype == FP4_BF16;
+  const cudaError_t e = launch_moe_dispatch(p, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? FP4_OK : cuda_fail(e, "dispatch launch");
+}
+
+fp4_status fp4_moe_dispatch_codes(const void* x, int64_t tokens, int64_t cols, fp4_dtype in_dtype, int topk,
+                                  const int32_t* row_of, const int32_t* scale_row_of, int num_experts,
+                                  const int32_t* offsets, fp4_fmt fmt, uint8_t* codes, uint8_t* scales,
+                                  const float* global, void* stream) {
+  const fp4_status c = check_moe(tokens, cols, topk, in_dtype, FP4_F32, row_of);
+  if (c != FP4_OK) return c;
+  if (!x || !codes || !scale_row_of || !offsets) return fail(FP4_ERR_INVALID_ARG, "null pointer");
+  if (num_experts <= 0 || num_experts > kMaxGroups) return fail(FP4_ERR_INVALID_ARG, "num_experts");
+  if (!aligned16(x)) return fail(FP4_ERR_INVALID_ARG, "x must be 16-byte aligned");
+  if (!aligned4(scale_row_of) || !aligned4(offsets)) return fail(FP4_ERR_INVALID_ARG, "scale_row_of / offsets alignment");
+  DispatchCodesProblem p{};
+  const fp4_status cs = check_codes(fmt, codes, scales, global, cols, &p.q);
+  if (cs != FP4_OK) return cs;
+  unsigned* status;
+  const fp4_status s = device_state(&status);
+  if (s != FP4_OK) return s;
+  p.x = x;
+  p.bf16 = in_dtype == FP4_BF16;
+  p.tokens = tokens;
+  p.cols = cols;
+  p.topk = topk;
+  p.num_experts = num_experts;
+  p.row_of = row_of;
+  p.scale_row_of = scale_row_of;
+  p.offsets = offsets;
+  const cudaError_t e = launch_moe_dispatch_codes(p, status, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? FP4_OK : cuda_fail(e, "dispatch launch");
+}
+
+static fp4_status i8_rows(const void* x, int64_t rows, int64_t cols, fp4_dtype in_dtype, int topk, const int32_t* row_of,
+                          int8_t* codes, float* row_scales, void* stream) {
+  if (!x || !codes || !row_scales) return fail(FP4_ERR_INVALID_ARG, "null pointer");
+  if (cols % 16 != 0) return fail(FP4_ERR_INVALID_ARG, "8-bit rows need cols % 16 == 0");
+  if (!aligned16(x) || !aligned16(codes)) return fail(FP4_ERR_INVALID_ARG, "x and codes must be 16-byte aligned");
+  if (!aligned4(row_scales)) return fail(FP4_ERR_INVALID_ARG, "row_scales alignment");
+  unsigned* status;
+  const fp4_status s = device_state(&status);
+  if (s != FP4_OK) return s;
+  I8RowsProblem p{};
+  p.x = x;
+  p.bf16 = in_dtype == FP4_BF16;
+  p.rows = rows;
+  p.cols = cols;
+  p.topk = topk;
+  p.row_of = row_of;
+  p.codes = codes;
+  p.scales = row_scales;
+  const cudaError_t e = launch_quantize_i8(p, status, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? FP4_OK : cuda_fail(e, "8-bit quantize launch");
+}
+
+fp4_status fp4_moe_dispatch_i8(const void* x, int64_t tokens, int64_t cols, fp4_dtype in_dtype, int topk,
+                               const int32_t* row_of, int8_t* codes, float* row_scales, void* stream) {
+  const fp4_status c = check_moe(tokens, cols, topk, in_dtype, FP4_F32, row_of);
+  if (c != FP4_OK) return c;
+  return i8_rows(x, tokens, cols, in_dtype, topk, row_of, codes, row_scales, stream);
+}
+
+fp4_status fp4_quantize_i8(const void* x, int64_t rows, int64_t cols, fp4_dtype in_dtype, int8_t* codes,
+                           float* row_scales, void* stream) {
+  if (rows <= 0 || cols <= 0) return fail(FP4_ERR_INVALID_ARG, "rows and cols must be positive");
+  if (rows > kMaxDim || cols > kMaxDim) return fail(FP4_ERR_UNSUPPORTED, "dimension too large");
+  if (!dtype_ok(in_dtype)) return fail(FP4_ERR_INVALID_ARG, "in_dtype");
+  return i8_rows(x, rows, cols, in_dtype, 1, nullptr, codes, row_scales, stream);
+}
+
+fp4_status fp4_moe_combine(const void* y, fp4_dtype in_dtype, const int32_t* row_of, const float* weights, int64_t tokens,
+                           int topk, int64_t cols, const void* residual, fp4_dtype residual_dtype, void* out,
+                           fp4_dtype out_dtype, void* stream) {
+  const fp4_status c = check_moe(tokens, cols, topk, in_dtype, out_dtype, row_of);
+  if (c != FP4_OK) return c;
+  if (!y || !out) return fail(FP4_ERR_INVALID_ARG, "null pointer");
+  if (residual && !dtype_ok(residual_dtype)) return fail(FP4_ERR_INVALID_ARG, "residual_dtype");
+  if (!aligned16(y) || !aligned16(out) || !aligned16(residual))
+    return fail(FP4_ERR_INVALID_ARG, "y, residual and out must be 16-byte aligned");
+  if (!aligned4(weights)) return fail(FP4_ERR_INVALID_ARG, "weights alignment");
+  if (out == y) return fail(FP4_ERR_INVALID_ARG, "out must not be y");
+  if (out == residual && out_dtype != residual_dtype)
+    return fail(FP4_ERR_INVALID_ARG, "out in the residual's place needs its type");
+  unsigned* status;
+  const fp4_status s = device_state(&status);
+  if (s != FP4_OK) return s;
+  CombineProblem p{};
+  p.y = y;
+  p.bf16 = in_dtype == FP4_BF16;
+  p.row_of = row_of;
+  p.weights = weights;
+  p.tokens = tokens;
+  p.cols = cols;
+  p.topk = topk;
+  p.res = residual;
+  p.res_bf16 = residual_dtype == FP4_BF16;
+  p.out = out;
+  p.out_bf16 = out_dtype == FP4_BF16;
+  const cudaError_t e = launch_moe_combine(p, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? FP4_OK : cuda_fail(e, "combine launch");
+}
+
+fp4_status fp4_moe_combine_backward(const void* dout, const void* y, fp4_dtype in_dtype, const int32_t* row_of,
+                                    const float* weights, int64_t tokens, int topk, int64_t cols, void* dy,
+                                    fp4_dtype out_dtype, float* dweights, void* stream) {
+  const fp4_status c = check_moe(tokens, cols, topk, in_dtype, out_dtype, row_of);
+  if (c != FP4_OK) return c;
+  if (!dout || (dweights && !y)) return fail(FP4_ERR_INVALID_ARG, "null pointer");
+  if (!dy && !dweights) return fail(FP4_ERR_INVALID_ARG, "no output: dy and dweights are both NULL");
+  if (!aligned16(dout) || !aligned16(y) || !aligned16(dy))
+    return fail(FP4_ERR_INVALID_ARG, "dout, y and dy must be 16-byte aligned");
+  if (!aligned4(weights) || !aligned4(dweights)) return fail(FP4_ERR_INVALID_ARG, "weights / dweights alignment");
+  if (dy == dout) return fail(FP4_ERR_INVALID_ARG, "dy must not be dout");
+  if (dy && dy == y && in_dtype != out_dtype) return fail(FP4_ERR_INVALID_ARG, "dy in y's place needs y's type");
+  unsigned* status;
+  const fp4_status s = device_state(&status);
+  if (s != FP4_OK) return s;
+  CombineGradProblem p{};
+  p.dout = dout;
+  p.y = y;
+  p.bf16 = in_dtype == FP4_BF16;
+  p.row_of = row_of;
+  p.weights = weights;
+  p.tokens = tokens;
+  p.cols = cols;
+  p.topk = topk;
+  p.dy = dy;
+  p.dy_bf16 = out_dtype == FP4_BF16;
+  p.dweights = dweights;
+  const cudaError_t e = launch_moe_combine_grad(p, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? FP4_OK : cuda_fail(e, "combine backward launch");
+}
+
+// ------------------------------------------------------------------ products in 8-bit integers
+constexpr int64_t kMaxI8K = 131056;  // K (-128)^2 < 2^31
+
+static fp4_status gemm_i8_common(const I8Problem& p, fp4_act act, fp4_dtype out_dtype, void* stream) {
+  if (!p.A || !p.sA || !p.B || !p.sB || !p.D) return fail(FP4_ERR_INVALID_ARG, "null pointer");
+  if (p.M <= 0 || p.N <= 0 || p.K <= 0) return fail(FP4_ERR_INVALID_ARG, "M, N and K must be positive");
+  if (p.K % 16 != 0) return fail(FP4_ERR_INVALID_ARG, "K must be a multiple of 16");
+  if (p.M > kMaxDim || p.N > kMaxDim / std::max(1, p.num_groups) || p.K > kMaxI8K)
+    return fail(FP4_ERR_UNSUPPORTED, "dimension too large");
+  if (!act_ok(act)) return fail(FP4_ERR_INVALID_ARG, "act");
+  if (!dtype_ok(out_dtype)) return fail(FP4_ERR_INVALID_ARG, "out_dtype");
+  if (!aligned16(p.A) || !aligned16(p.B) || !aligned16(p.D))
+    return fail(FP4_ERR_INVALID_ARG, "A, B and D must be 16-byte aligned");
+  if (!aligned4(p.sA) || !aligned4(p.sB) || !aligned4(p.bias) || !aligned4(p.offsets))
+    return fail(FP4_ERR_INVALID_ARG, "scales / bias / offsets alignment");
+  // (the workspace's size goes by the device's SM count)
+  const size_t need = i8_workspace_bytes(p.M, p.N, p.K, p.num_groups);
+  if (need && (!p.ws || !aligned16(p.ws) || p.ws_bytes < need))
+    return fail(FP4_ERR_INVALID_ARG, "workspace too small or misaligned (see fp4_gemm_i8_workspace_size)");
+  unsigned* status;
+  const fp4_status s = device_state(&status);
+  if (s != FP4_OK) return s;
+  const char* why = "";
+  cudaError_t e = cudaSuccess;
+  const int r = launch_gemm_i8(p, status, static_cast<cudaStream_t>(stream), &why, &e);
+  if (r == 1) return fail(FP4_ERR_INVALID_ARG, why);
+  return r == 0 ? FP4_OK : cuda_fail(e, "8-bit GEMM launch");
+}
+
+size_t fp4_gemm_i8_workspace_size(int64_t M, int64_t N, int64_t K) { return i8_workspace_bytes(M, N, K, 0); }
+
+size_t fp4_gemm_i8_grouped_workspace_size(int num_groups, int64_t total_rows, int64_t N, int64_t K) {
+  return num_groups > 0 && num_groups <= kMaxGroups ? i8_workspace_bytes(total_rows, N, K, num_groups) : 0;
+}
+
+fp4_status fp4_gemm_i8(const int8_t* A, const float* sA, const int8_t* B, const float* sB, int64_t M, int64_t N, int64_t K,
+                       const float* bias, fp4_act act, void* D, fp4_dtype out_dtype, void* workspace,
+                       size_t workspace_bytes, unsigned flags, void* stream) {
+  if (flags & ~static_cast<unsigned>(FP4_GEMM_WEIGHTS_READY)) return fail(FP4_ERR_INVALID_ARG, "unknown flag");
+  I8Problem p{};
+  p.A = A;
+  p.B = B;
+  p.sA = sA;
+  p.sB = sB;
+  p.M = M;
+  p.N = N;
+  p.K = K;
+  p.bias = bias;
+  p.act = act;
+  p.D = D;
+  p.out_bf16 = out_dtype == FP4_BF16;
+  p.ws = workspace;
+  p.ws_bytes = workspace_bytes;
+  p.weights_ready = (flags & FP4_GEMM_WEIGHTS_READY) != 0;
+  return gemm_i8_common(p, act, out_dtype, stream);
+}
+
+fp4_status fp4_gemm_i8_grouped(int num_groups, const int32_t* offsets, const int8_t* A, const float* sA, const int8_t* B,
+                               const float* sB, int64_t total_rows, int64_t N, int64_t K, const float* bias, fp4_act act,
+                               void* D, fp4_dtype out_dtype, void* workspace, size_t workspace_bytes, void* stream) {
+  if (num_groups <= 0 || num_groups > kMaxGroups || !offsets) return fail(FP4_ERR_INVALID_ARG, "groups / offsets");
+  I8Problem p{};
+  p.A = A;
+  p.B = B;
+  p.sA = sA;
+  p.sB = sB;
+  p.M = total_rows;
+  p.N = N;
+  p.K = K;
+  p.bias = bias;
+  p.act = act;
+  p.D = D;
+  p.out_bf16 = out_dtype == FP4_BF16;
+  p.ws = workspace;
+  p.ws_bytes = workspace_bytes;
+  p.num_groups = num_groups;
+  p.offsets = offsets;
+  return gemm_i8_common(p, act, out_dtype, stream);
 }
 
 size_t fp4_gemm_epilogue_workspace_size(int64_t M, int64_t N, int64_t K, fp4_fmt fmt, int rows_in_place) {

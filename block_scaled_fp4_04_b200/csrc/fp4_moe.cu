@@ -1,0 +1,605 @@
+// fp4_moe.cu -- tokens to their experts and back: a stable sort of the router's (token, choice)
+// slots by expert, the copy of token rows into the experts' order (as they are, as FP4 codes in
+// the grouped scale layout, or as 8-bit rows with a scale each), the weighted sum on the way back,
+// and its gradients.  Also the 8-bit quantizer of plain rows, which is the same kernel.
+//
+// A slot s = t topk + j is token t's j-th choice; row_of[s] is its row in the experts' order, or
+// -1 where it has no expert.  All of these but the sort go by token, not by sorted row: a token's
+// row is read once, and encoded once, for all its experts.
+#include <cuda_runtime.h>
+#include <cuda_bf16.h>
+#include <cstdint>
+
+#include "fp4_codes.cuh"
+#include "fp4_moe.h"
+#include "fp4_rows.cuh"
+
+namespace fp4 {
+
+// ------------------------------------------------------------------------------------- sort
+// A counting sort that keeps the slots' order within an expert.  Each warp counts a contiguous
+// segment of slots per expert in its own shared counters; prefix sums over warps and experts turn
+// the counts into first rows; then each warp passes over its segment again and hands out rows in
+// order, 32 slots at a time: equal experts within the 32 find one another by a match, and a slot's
+// place among them is the number of lower lanes.  No atomic decides an order, so the result is the
+// same every time.
+//
+// Up to kSortOneBlock slots one block does it all (one launch).  Beyond, blocks of kSortChunk slots
+// or more first write their histograms to the workspace, and each block of a second launch sums
+// those before it.
+struct SortArgs {
+  const void* ids;
+  int64_t slots, chunk;
+  int E;
+  int blocks;
+  uint32_t* hist;  // [blocks, E], null for one block
+  int32_t *offsets, *row_of, *scale_row_of;
+};
+
+constexpr int kSortThreads = 1024;
+constexpr int64_t kSortOneBlock = 16384, kSortChunk = 4096;
+constexpr int kSortMaxBlocks = 128;
+
+template <typename ID>
+__device__ __forceinline__ int sort_key(const SortArgs& a, int64_t s, int64_t hi) {
+  if (s >= hi) return a.E;
+  const ID id = static_cast<const ID*>(a.ids)[s];
+  return id >= 0 && id < static_cast<ID>(a.E) ? static_cast<int>(id) : a.E;
+}
+
+template <typename ID>
+__global__ void __launch_bounds__(kSortThreads) moe_hist_kernel(const SortArgs a) {
+  extern __shared__ uint32_t s_cnt[];
+  rows_wait_prior();
+  rows_allow_dependents();
+  for (int e = threadIdx.x; e <= a.E; e += blockDim.x) s_cnt[e] = 0;
+  __syncthreads();
+  const int64_t lo = blockIdx.x * a.chunk, hi = min(a.slots, lo + a.chunk);
+  for (int64_t s = lo + threadIdx.x; s < hi; s += blockDim.x) atomicAdd(&s_cnt[sort_key<ID>(a, s, hi)], 1u);
+  __syncthreads();
+  for (int e = threadIdx.x; e < a.E; e += blockDim.x) a.hist[static_cast<int64_t>(blockIdx.x) * a.E + e] = s_cnt[e];
+}
+
+template <typename ID>
+__global__ void __launch_bounds__(kSortThreads, 1) moe_sort_kernel(const SortArgs a) {
+  extern __shared__ uint32_t s_mem[];
+  const int E = a.E, E1 = E + 1;  // the last counter takes the slots without an expert
+  const int warps = blockDim.x / 32, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  uint32_t* s_cnt = s_mem;              // [warps, E1]
+  uint32_t* s_all = s_cnt + warps * E1;  // [E] rows of an expert, then its first row
+  uint32_t* s_before = s_all + E;       // [E] of them in earlier blocks
+  uint32_t* s_sfirst = s_before + E;    // [E] its first row in the grouped scale layout
+  uint32_t* s_part = s_sfirst + E;      // [2, blockDim.x] (several blocks only)
+  rows_wait_prior();
+  rows_allow_dependents();
+  for (int i = threadIdx.x; i < warps * E1; i += blockDim.x) s_cnt[i] = 0;
+  const int64_t lo = blockIdx.x * a.chunk, hi = min(a.slots, lo + a.chunk);
+  const int64_t seg = ((hi - lo + warps - 1) / warps + 31) / 32 * 32;
+  const int64_t from = min(hi, lo + warp * seg), to = min(hi, from + seg);
+  uint32_t* mine = s_cnt + warp * E1;
+  __syncthreads();
+  for (int64_t s = from + lane; s < to; s += 32) atomicAdd(&mine[sort_key<ID>(a, s, to)], 1u);
+  if (a.hist) {
+    // columns of the histograms: neighbouring threads take neighbouring experts, and the blocks
+    // are shared out over as many groups of threads as there are
+    int wide = 32;
+    while (wide < E) wide *= 2;  // at most 1024
+    const int parts = blockDim.x / wide, e = threadIdx.x % wide, part = threadIdx.x / wide;
+    uint32_t before = 0, all = 0;
+    if (e < E) {
+#pragma unroll 4
+      for (int b = part; b < a.blocks; b += parts) {
+        const uint32_t c = __ldcg(a.hist + static_cast<int64_t>(b) * E + e);
+        all += c;
+        if (b < static_cast<int>(blockIdx.x)) before += c;
+      }
+    }
+    s_part[threadIdx.x] = all;
+    s_part[blockDim.x + threadIdx.x] = before;
+    __syncthreads();
+    if (part == 0 && e < E) {
+      for (int q = 1; q < parts; ++q) {
+        all += s_part[q * wide + e];
+        before += s_part[blockDim.x + q * wide + e];
+      }
+      s_all[e] = all;
+      s_before[e] = before;
+    }
+  }
+  __syncthreads();
+  // counts of an expert become the places of each warp's first row among the block's
+  for (int e = threadIdx.x; e < E; e += blockDim.x) {
+    uint32_t sum = 0;
+#pragma unroll 8
+    for (int w = 0; w < warps; ++w) {
+      const uint32_t c = s_cnt[w * E1 + e];
+      s_cnt[w * E1 + e] = sum;
+      sum += c;
+    }
+    if (!a.hist) {
+      s_all[e] = sum;
+      s_before[e] = 0;
+    }
+  }
+  __syncthreads();
+  if (warp == 0) {  // first rows: prefix sums over the experts
+    uint32_t rows = 0, blocks = 0;
+    for (int base = 0; base < E; base += 32) {
+      const int e = base + lane;
+      const uint32_t n = e < E ? s_all[e] : 0u, nb = (n + 127) / 128;
+      uint32_t in = n, inb = nb;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const uint32_t t = __shfl_up_sync(0xFFFFFFFFu, in, d), tb = __shfl_up_sync(0xFFFFFFFFu, inb, d);
+        if (lane >= d) {
+          in += t;
+          inb += tb;
+        }
+      }
+      if (e < E) {
+        const uint32_t first = rows + in - n;
+        s_all[e] = first + s_before[e];
+        s_sfirst[e] = (blocks + inb - nb) * 128 + s_before[e];
+        if (blockIdx.x == 0) a.offsets[e] = static_cast<int32_t>(first);
+      }
+      rows += __shfl_sync(0xFFFFFFFFu, in, 31);
+      blocks += __shfl_sync(0xFFFFFFFFu, inb, 31);
+    }
+    if (lane == 0 && blockIdx.x == 0) a.offsets[E] = static_cast<int32_t>(rows);
+  }
+  __syncthreads();
+  for (int64_t s0 = from; s0 < to; s0 += 32) {
+    const int64_t s = s0 + lane;
+    const int key = sort_key<ID>(a, s, to);
+    const unsigned same = __match_any_sync(0xFFFFFFFFu, key);
+    const uint32_t at = mine[key], lower = __popc(same & ((1u << lane) - 1));
+    __syncwarp();
+    if (lower == 0) mine[key] = at + __popc(same);
+    __syncwarp();
+    if (s < to) {
+      a.row_of[s] = key < E ? static_cast<int32_t>(s_all[key] + at + lower) : -1;
+      if (a.scale_row_of) a.scale_row_of[s] = key < E ? static_cast<int32_t>(s_sfirst[key] + at + lower) : -1;
+    }
+  }
+}
+
+static int sort_blocks(int64_t slots, int64_t* chunk) {
+  if (slots <= kSortOneBlock) {
+    *chunk = slots;
+    return 1;
+  }
+  *chunk = std::max(kSortChunk, (slots + kSortMaxBlocks - 1) / kSortMaxBlocks);
+  return static_cast<int>((slots + *chunk - 1) / *chunk);
+}
+
+size_t moe_sort_workspace_bytes(int64_t slots, int E) {
+  int64_t chunk;
+  const int blocks = sort_blocks(slots, &chunk);
+  return blocks == 1 ? 0 : static_cast<size_t>(blocks) * E * sizeof(uint32_t);
+}
+
+template <typename ID>
+static cudaError_t sort_typed(const SortArgs& a, cudaStream_t st) {
+  auto kern = moe_sort_kernel<ID>;
+  // one block: as many warps as segments of 32 slots, but at least one expert's column a thread
+  const int64_t want = std::max<int64_t>((std::min(a.chunk, a.slots) + 31) / 32 * 32, (std::min(a.E, 256) + 31) / 32 * 32);
+  const int threads = a.hist ? kSortThreads : static_cast<int>(std::min<int64_t>(kSortThreads, want));
+  const size_t smem = (static_cast<size_t>(threads / 32) * (a.E + 1) + 3 * a.E + (a.hist ? 2 * threads : 0)) * 4;
+  cudaError_t e = cudaSuccess;
+  if (smem > 48 * 1024) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+  }
+  if (a.hist) {
+    e = launch_rows(moe_hist_kernel<ID>, dim3(a.blocks), kSortThreads, static_cast<size_t>(a.E + 1) * 4, st, a);
+    if (e != cudaSuccess) return e;
+  }
+  return launch_rows(kern, dim3(a.blocks), threads, smem, st, a);
+}
+
+cudaError_t launch_moe_sort(const void* ids, int id_bytes, int64_t slots, int E, int32_t* offsets, int32_t* row_of,
+                            int32_t* scale_row_of, void* ws, cudaStream_t st) {
+  SortArgs a{};
+  a.ids = ids;
+  a.slots = slots;
+  a.E = E;
+  a.blocks = sort_blocks(slots, &a.chunk);
+  a.hist = a.blocks > 1 ? static_cast<uint32_t*>(ws) : nullptr;
+  a.offsets = offsets;
+  a.row_of = row_of;
+  a.scale_row_of = scale_row_of;
+  return id_bytes == 8 ? sort_typed<int64_t>(a, st) : sort_typed<int32_t>(a, st);
+}
+
+// --------------------------------------------------------------------------------- dispatch
+// Words of 16 bytes of the input (V = 8 BF16 or 4 FP32) where its rows start at 16 bytes, pairs for
+// even widths, else single elements.  (A matrix of the other type then moves 8 or 32 bytes at once,
+// which its rows' starts allow.)
+static int row_width(int64_t cols, int bf16) {
+  const int v = bf16 ? 8 : 4;
+  return cols % v == 0 ? v : cols % 2 == 0 ? 2 : 1;
+}
+
+template <int V>
+struct WordSize {
+  static constexpr int value = V;
+};
+template <typename F>
+static cudaError_t with_rows(int bf16, int v, F&& f) {
+  if (bf16) {
+    if (v == 8) return f(__nv_bfloat16{}, WordSize<8>{});
+    if (v == 2) return f(__nv_bfloat16{}, WordSize<2>{});
+    return f(__nv_bfloat16{}, WordSize<1>{});
+  }
+  if (v == 4) return f(float{}, WordSize<4>{});
+  if (v == 2) return f(float{}, WordSize<2>{});
+  return f(float{}, WordSize<1>{});
+}
+
+// Threads that take `per` words each of a row's `words`.
+static int row_threads(int64_t words, int per, int most) {
+  return static_cast<int>(std::min<int64_t>(most, std::max<int64_t>(32, ((words + per - 1) / per + 31) / 32 * 32)));
+}
+
+constexpr int kCopyWords = 4, kCopyThreads = 256;
+
+// y[row_of[t, j]] = x[t]: a block copies kCopyWords words a thread of one token's row to its
+// topk places.
+template <typename T, int V>
+__global__ void __launch_bounds__(kCopyThreads) moe_dispatch_kernel(const DispatchProblem p) {
+  rows_wait_prior();
+  rows_allow_dependents();
+  const int64_t t = blockIdx.x, words = p.cols / V;
+  const int64_t w0 = static_cast<int64_t>(blockIdx.y) * blockDim.x * kCopyWords + threadIdx.x;
+  const T* x = static_cast<const T*>(p.x) + t * p.cols;
+  const int32_t* rows = p.row_of + t * p.topk;
+  RowVec<T, V> in[kCopyWords];
+#pragma unroll
+  for (int i = 0; i < kCopyWords; ++i)
+    if (w0 + i * blockDim.x < words) in[i].load(x + (w0 + i * blockDim.x) * V);
+  for (int j = 0; j < p.topk; ++j) {
+    const int32_t row = __ldg(rows + j);
+    if (row < 0) continue;
+#pragma unroll
+    for (int i = 0; i < kCopyWords; ++i) {
+      if (w0 + i * blockDim.x >= words) continue;
+      const int64_t at = row * p.cols + (w0 + i * blockDim.x) * V;
+      if (p.y_bf16 == (sizeof(T) == 2)) {  // one type: the same bits, those of a NaN too
+        in[i].store(static_cast<T*>(p.y) + at);
+      } else {
+        float v[V];
+        in[i].unpack(v);
+        store_row_vec<V>(p.y, p.y_bf16, at, v);
+      }
+    }
+  }
+}
+
+cudaError_t launch_moe_dispatch(const DispatchProblem& p, cudaStream_t st) {
+  const int v = row_width(p.cols, p.bf16);
+  const int64_t words = p.cols / v;
+  const int threads = row_threads(words, kCopyWords, kCopyThreads);
+  const int64_t per = static_cast<int64_t>(threads) * kCopyWords;
+  const dim3 grid(static_cast<unsigned>(p.tokens), static_cast<unsigned>((words + per - 1) / per));
+  return with_rows(p.bf16, v, [&](auto t, auto n) {
+    return launch_rows(moe_dispatch_kernel<decltype(t), decltype(n)::value>, grid, threads, 0, st, p);
+  });
+}
+
+// ------------------------------------------------------------------- dispatch to FP4 codes
+// A token's row is encoded once; its codes go to row row_of[t, j], its scales to row
+// scale_row_of[t, j] of the grouped layout.  Blocks behind the tokens' write the layout's pads:
+// num_experts blocks the rows behind each expert's last, then one block per 128-row block of the
+// buffer, which clears it if it lies behind the last expert's.
+constexpr int kCodeThreads = 256;
+
+__device__ __forceinline__ void clear_scale_rows(uint8_t* scales, int64_t atoms, int64_t block, int first_row) {
+  for (int64_t i = threadIdx.x; i < atoms * 128; i += blockDim.x) {
+    const int w = static_cast<int>(i % 128);  // word w of an atom: 4 scales of row (w % 4) 32 + w / 4
+    if ((w & 3) * 32 + (w >> 2) >= first_row)
+      reinterpret_cast<uint32_t*>(scales)[(block * atoms + i / 128) * 128 + w] = 0;
+  }
+}
+
+template <typename T, int V, int FMT>
+__global__ void __launch_bounds__(kCodeThreads) moe_dispatch_codes_kernel(const DispatchCodesProblem p, unsigned* status) {
+  constexpr int BLOCK = FMT == kCodesMx ? 32 : 16;
+  rows_wait_prior();
+  rows_allow_dependents();
+  const int64_t blocks_k = p.cols / BLOCK, atoms = (blocks_k + 3) / 4;
+  const int64_t t = blockIdx.x;
+  if (t >= p.tokens) {  // pads
+    const int64_t i = t - p.tokens;
+    const int upto = i < p.num_experts ? static_cast<int>(i) : p.num_experts;  // experts to count
+    __shared__ int s_sum[kCodeThreads / 32];
+    int sum = 0;
+    for (int e = threadIdx.x; e < upto; e += blockDim.x) sum += (p.offsets[e + 1] - p.offsets[e] + 127) / 128;
+    sum = __reduce_add_sync(0xFFFFFFFFu, sum);
+    if (threadIdx.x % 32 == 0) s_sum[threadIdx.x / 32] = sum;
+    __syncthreads();
+    int64_t first = 0;
+    for (int w = 0; w < static_cast<int>(blockDim.x / 32); ++w) first += s_sum[w];
+    if (i < p.num_experts) {
+      const int n = p.offsets[i + 1] - p.offsets[i];
+      if (n % 128) clear_scale_rows(p.q.scales, atoms, first + n / 128, n % 128);
+    } else if (i - p.num_experts >= first) {
+      clear_scale_rows(p.q.scales, atoms, i - p.num_experts, 0);
+    }
+    return;
+  }
+  const float g = FMT == kCodesNv ? __ldg(p.q.g) : 1.0f;
+  const T* x = static_cast<const T*>(p.x) + t * p.cols;
+  const int64_t words = p.cols / V;
+  bool bad = false;
+  for (int64_t w0 = 0; w0 < words; w0 += blockDim.x) {  // whole warps: the block maxima need every lane
+    const int64_t w = w0 + threadIdx.x, col = w * V;
+    const bool ok = w < words;
+    RowVec<T, V> in;
+    in.zero();
+    if (ok) in.load(x + col);
+    float v[V];
+    in.unpack(v);
+    uint32_t sb;
+    const uint32_t packed = encode_vec<FMT, V>(g, v, sb, bad);
+    if (!ok) continue;
+    const int64_t k = col / BLOCK;
+    for (int j = 0; j < p.topk; ++j) {
+      const int64_t s = t * p.topk + j;
+      const int32_t row = __ldg(p.row_of + s);
+      if (row < 0) continue;
+      store_codes<V>(p.q.codes + row * (p.cols / 2) + col / 2, packed);
+      if (col % BLOCK == 0) p.q.scales[scale_at(__ldg(p.scale_row_of + s), k, atoms)] = static_cast<uint8_t>(sb);
+    }
+  }
+  if (blocks_k % 4) {  // the row's pad columns
+    const int pad = 4 - static_cast<int>(blocks_k % 4);
+    for (int i = threadIdx.x; i < pad * p.topk; i += blockDim.x) {
+      const int64_t s = t * p.topk + i / pad;
+      if (p.row_of[s] >= 0) p.q.scales[scale_at(p.scale_row_of[s], blocks_k + i % pad, atoms)] = 0;
+    }
+  }
+  if (bad) atomicOr(status, kStatusNonFinite);
+}
+
+cudaError_t launch_moe_dispatch_codes(const DispatchCodesProblem& p, unsigned* status, cudaStream_t st) {
+  const int64_t pads = p.num_experts + (p.tokens * p.topk + 127) / 128 + p.num_experts;
+  const dim3 grid(static_cast<unsigned>(p.tokens + pads));
+  const int threads = row_threads(p.cols / (p.bf16 ? 8 : 4), 1, kCodeThreads);
+  if (p.bf16)
+    return p.q.fmt == kCodesMx
+               ? launch_rows(moe_dispatch_codes_kernel<__nv_bfloat16, 8, kCodesMx>, grid, threads, 0, st, p, status)
+               : launch_rows(moe_dispatch_codes_kernel<__nv_bfloat16, 8, kCodesNv>, grid, threads, 0, st, p, status);
+  return p.q.fmt == kCodesMx ? launch_rows(moe_dispatch_codes_kernel<float, 4, kCodesMx>, grid, threads, 0, st, p, status)
+                             : launch_rows(moe_dispatch_codes_kernel<float, 4, kCodesNv>, grid, threads, 0, st, p, status);
+}
+
+// -------------------------------------------------------------------------------- 8-bit rows
+// q = rn(x (1 / s)), s = max|x| / 127 of the row, at least 2^-126 (its reciprocal is finite, so
+// that a zero stays zero), 1 for a zero row.  A block per row: its words stay in registers between
+// the maximum and the encoding (kI8Words a thread; longer rows are read again).
+constexpr int kI8Words = 4, kI8Threads = 1024;
+
+template <int V>
+__device__ __forceinline__ void store_i8(int8_t* dst, const float (&v)[V], float inv) {
+  uint32_t w[V / 4];
+#pragma unroll
+  for (int i = 0; i < V / 4; ++i) {
+    int q[4];
+#pragma unroll
+    for (int h = 0; h < 4; ++h) q[h] = __float2int_rn(__fmul_rn(v[4 * i + h], inv));
+    uint32_t hi;
+    asm("cvt.pack.sat.s8.s32.b32 %0, %1, %2, 0;" : "=r"(hi) : "r"(q[3]), "r"(q[2]));
+    asm("cvt.pack.sat.s8.s32.b32 %0, %1, %2, %3;" : "=r"(w[i]) : "r"(q[1]), "r"(q[0]), "r"(hi));
+  }
+  if constexpr (V == 8) *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
+  else *reinterpret_cast<uint32_t*>(dst) = w[0];
+}
+
+template <typename T, int V>
+__global__ void __launch_bounds__(kI8Threads) quantize_i8_kernel(const I8RowsProblem p, unsigned* status) {
+  __shared__ uint32_t s_max[kI8Threads / 32];
+  rows_wait_prior();
+  rows_allow_dependents();
+  const int64_t t = blockIdx.x, words = p.cols / V;
+  const T* x = static_cast<const T*>(p.x) + t * p.cols;
+  RowVec<T, V> in[kI8Words];
+  uint32_t m = 0;
+  auto largest = [&](const RowVec<T, V>& r) {
+    float v[V];
+    r.unpack(v);
+#pragma unroll
+    for (int i = 0; i < V; ++i) m = max(m, abs_bits_of(v[i]));
+  };
+#pragma unroll
+  for (int i = 0; i < kI8Words; ++i) {
+    in[i].zero();
+    const int64_t w = threadIdx.x + i * static_cast<int64_t>(blockDim.x);
+    if (w < words) in[i].load(x + w * V);
+  }
+#pragma unroll
+  for (int i = 0; i < kI8Words; ++i) largest(in[i]);
+  for (int64_t w = threadIdx.x + kI8Words * static_cast<int64_t>(blockDim.x); w < words; w += blockDim.x) {
+    RowVec<T, V> r;
+    r.load(x + w * V);
+    largest(r);
+  }
+  m = __reduce_max_sync(0xFFFFFFFFu, m);
+  if (blockDim.x > 32) {
+    if (threadIdx.x % 32 == 0) s_max[threadIdx.x / 32] = m;
+    __syncthreads();
+    m = threadIdx.x % 32 < blockDim.x / 32 ? s_max[threadIdx.x % 32] : 0u;
+    m = __reduce_max_sync(0xFFFFFFFFu, m);
+  }
+  if (threadIdx.x == 0 && m >= 0x7F800000u) atomicOr(status, kStatusNonFinite);
+  const float s = m ? fmaxf(__fdiv_rn(__uint_as_float(m), 127.0f), 0x1p-126f) : 1.0f;
+  const float inv = __frcp_rn(s);
+  for (int j = 0; j < p.topk; ++j) {
+    const int64_t row = p.row_of ? __ldg(p.row_of + t * p.topk + j) : t;
+    if (row < 0) continue;
+    if (threadIdx.x == 0) p.scales[row] = s;
+    int8_t* q = p.codes + row * p.cols;
+#pragma unroll
+    for (int i = 0; i < kI8Words; ++i) {
+      const int64_t w = threadIdx.x + i * static_cast<int64_t>(blockDim.x);
+      float v[V];
+      in[i].unpack(v);
+      if (w < words) store_i8<V>(q + w * V, v, inv);
+    }
+    for (int64_t w = threadIdx.x + kI8Words * static_cast<int64_t>(blockDim.x); w < words; w += blockDim.x) {
+      RowVec<T, V> r;
+      r.load(x + w * V);
+      float v[V];
+      r.unpack(v);
+      store_i8<V>(q + w * V, v, inv);
+    }
+  }
+}
+
+cudaError_t launch_quantize_i8(const I8RowsProblem& p, unsigned* status, cudaStream_t st) {
+  const int64_t words = p.cols / (p.bf16 ? 8 : 4);
+  // few rows: one word a thread, for the shortest way through a row
+  const int threads = row_threads(words, p.rows <= num_sms() ? 1 : kI8Words, kI8Threads);
+  const dim3 grid(static_cast<unsigned>(p.rows));
+  return p.bf16 ? launch_rows(quantize_i8_kernel<__nv_bfloat16, 8>, grid, threads, 0, st, p, status)
+                : launch_rows(quantize_i8_kernel<float, 4>, grid, threads, 0, st, p, status);
+}
+
+// ----------------------------------------------------------------------------------- combine
+// out[t] = sum_j w[t, j] y[row_of[t, j]] + res[t], the sum in FP32 in the order of j, rounded once.
+constexpr int kSumWords = 2, kSumThreads = 256, kSumRows = 4;
+
+template <typename T, int V>
+__global__ void __launch_bounds__(kSumThreads) moe_combine_kernel(const CombineProblem p) {
+  rows_wait_prior();
+  rows_allow_dependents();
+  const int64_t t = blockIdx.x, words = p.cols / V;
+  const int64_t w0 = static_cast<int64_t>(blockIdx.y) * blockDim.x * kSumWords + threadIdx.x;
+  const T* y = static_cast<const T*>(p.y);
+  float sum[kSumWords][V] = {};
+  for (int j0 = 0; j0 < p.topk; j0 += kSumRows) {
+    // kSumRows rows' words are asked for before the first is needed
+    RowVec<T, V> in[kSumRows][kSumWords];
+    float weight[kSumRows];
+    bool on[kSumRows];
+#pragma unroll
+    for (int j = 0; j < kSumRows; ++j) {
+      const int64_t s = t * p.topk + j0 + j;
+      const int32_t row = j0 + j < p.topk ? __ldg(p.row_of + s) : -1;
+      on[j] = row >= 0;
+      weight[j] = on[j] && p.weights ? __ldg(p.weights + s) : 1.0f;
+#pragma unroll
+      for (int i = 0; i < kSumWords; ++i)
+        if (on[j] && w0 + i * blockDim.x < words) in[j][i].load(y + row * p.cols + (w0 + i * blockDim.x) * V);
+    }
+#pragma unroll
+    for (int j = 0; j < kSumRows; ++j) {
+      if (!on[j]) continue;
+#pragma unroll
+      for (int i = 0; i < kSumWords; ++i) {
+        float v[V];
+        in[j][i].unpack(v);
+#pragma unroll
+        for (int k = 0; k < V; ++k) sum[i][k] = fmaf(weight[j], v[k], sum[i][k]);
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kSumWords; ++i) {
+    if (w0 + i * blockDim.x >= words) continue;
+    const int64_t at = t * p.cols + (w0 + i * blockDim.x) * V;
+    if (p.res) {
+      float r[V];
+      load_row_any<V>(p.res, p.res_bf16, at, r);
+#pragma unroll
+      for (int k = 0; k < V; ++k) sum[i][k] += r[k];
+    }
+    store_row_vec<V>(p.out, p.out_bf16, at, sum[i]);
+  }
+}
+
+cudaError_t launch_moe_combine(const CombineProblem& p, cudaStream_t st) {
+  const int v = row_width(p.cols, p.bf16);
+  const int64_t words = p.cols / v;
+  const int threads = row_threads(words, kSumWords, kSumThreads);
+  const int64_t per = static_cast<int64_t>(threads) * kSumWords;
+  const dim3 grid(static_cast<unsigned>(p.tokens), static_cast<unsigned>((words + per - 1) / per));
+  return with_rows(p.bf16, v, [&](auto t, auto n) {
+    return launch_rows(moe_combine_kernel<decltype(t), decltype(n)::value>, grid, threads, 0, st, p);
+  });
+}
+
+// ------------------------------------------------------------------------- its backward pass
+// dy[row_of[t, j]] = w[t, j] dout[t], dw[t, j] = <dout[t], y[row_of[t, j]]>: a block per token, so
+// that dout is read once and each dot product is summed in one place, in a fixed order.
+constexpr int kGradRows = 8, kGradThreads = 256;
+
+template <typename T, int V>
+__global__ void __launch_bounds__(kGradThreads) moe_combine_grad_kernel(const CombineGradProblem p) {
+  __shared__ float s_dot[kGradThreads / 32][kGradRows];
+  rows_wait_prior();
+  rows_allow_dependents();
+  const int64_t t = blockIdx.x, words = p.cols / V;
+  const T* dout = static_cast<const T*>(p.dout) + t * p.cols;
+  const T* y = static_cast<const T*>(p.y);
+  for (int j0 = 0; j0 < p.topk; j0 += kGradRows) {
+    int32_t row[kGradRows];
+    float weight[kGradRows], dot[kGradRows];
+#pragma unroll
+    for (int j = 0; j < kGradRows; ++j) {
+      const int64_t s = t * p.topk + j0 + j;
+      row[j] = j0 + j < p.topk ? __ldg(p.row_of + s) : -1;
+      weight[j] = row[j] >= 0 && p.weights ? __ldg(p.weights + s) : 1.0f;
+      dot[j] = 0.0f;
+    }
+    for (int64_t w = threadIdx.x; w < words; w += blockDim.x) {
+      RowVec<T, V> in;
+      in.load(dout + w * V);
+      float d[V];
+      in.unpack(d);
+#pragma unroll
+      for (int j = 0; j < kGradRows; ++j) {
+        if (row[j] < 0) continue;
+        const int64_t at = row[j] * p.cols + w * V;
+        if (p.dweights) {
+          RowVec<T, V> yr;
+          yr.load(y + at);
+          float v[V];
+          yr.unpack(v);
+#pragma unroll
+          for (int k = 0; k < V; ++k) dot[j] = fmaf(d[k], v[k], dot[j]);
+        }
+        if (p.dy) {
+          float o[V];
+#pragma unroll
+          for (int k = 0; k < V; ++k) o[k] = weight[j] * d[k];
+          store_row_vec<V>(p.dy, p.dy_bf16, at, o);
+        }
+      }
+    }
+    if (p.dweights) {
+#pragma unroll
+      for (int j = 0; j < kGradRows; ++j) {
+        const float v = warp_sum(dot[j]);
+        if (threadIdx.x % 32 == 0) s_dot[threadIdx.x / 32][j] = v;
+      }
+      __syncthreads();
+      if (threadIdx.x < kGradRows && j0 + static_cast<int>(threadIdx.x) < p.topk) {
+        float v = 0.0f;
+        for (int w = 0; w < static_cast<int>(blockDim.x / 32); ++w) v += s_dot[w][threadIdx.x];
+        p.dweights[t * p.topk + j0 + threadIdx.x] = v;
+      }
+      __syncthreads();
+    }
+  }
+}
+
+cudaError_t launch_moe_combine_grad(const CombineGradProblem& p, cudaStream_t st) {
+  const int v = row_width(p.cols, p.bf16);
+  const int threads = row_threads(p.cols / v, 2, kGradThreads);
+  const dim3 grid(static_cast<unsigned>(p.tokens));
+  return with_rows(p.bf16, v, [&](auto t, auto n) {
+    return launch_rows(moe_combine_grad_kernel<decltype(t), decltype(n)::value>, grid, threads, 0, st, p);
+  });
+}
+
+}  // namespace fp4

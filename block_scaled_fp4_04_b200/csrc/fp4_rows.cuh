@@ -51,6 +51,19 @@ struct RowVec {
                    : "l"(p));
     }
   }
+  // the same bits to another row of this type
+  __device__ __forceinline__ void store(T* p) const {
+    if constexpr (V == 1) {
+      if constexpr (sizeof(T) == 4) *reinterpret_cast<unsigned*>(p) = w[0];
+      else *reinterpret_cast<unsigned short*>(p) = static_cast<unsigned short>(w[0]);
+    } else if constexpr (V == 2 && sizeof(T) == 2) {
+      *reinterpret_cast<unsigned*>(p) = w[0];
+    } else if constexpr (V == 2) {
+      *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+    } else {
+      *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  }
   __device__ __forceinline__ void unpack(float (&v)[V]) const {
     if constexpr (sizeof(T) == 4) {
 #pragma unroll
@@ -96,6 +109,42 @@ __device__ __forceinline__ void store_row_vec(void* out, int out_bf16, int64_t o
   }
 }
 
+// V values at element offset `off` of a BF16 or FP32 matrix, aligned as for store_row_vec.
+template <int V>
+__device__ __forceinline__ void load_row_any(const void* in, int in_bf16, int64_t off, float (&v)[V]) {
+  if (in_bf16) {
+    const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(in) + off;
+    if constexpr (V == 4) {
+      const uint2 w = *reinterpret_cast<const uint2*>(p);
+      v[0] = __uint_as_float(w.x << 16);
+      v[1] = __uint_as_float(w.x & 0xFFFF0000u);
+      v[2] = __uint_as_float(w.y << 16);
+      v[3] = __uint_as_float(w.y & 0xFFFF0000u);
+    } else {
+      RowVec<__nv_bfloat16, V> r;
+      r.load(p);
+      r.unpack(v);
+    }
+  } else {
+    const float* p = static_cast<const float*>(in) + off;
+    if constexpr (V == 8) {
+      float a[4];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        RowVec<float, 4> r;
+        r.load(p + 4 * h);
+        r.unpack(a);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[4 * h + i] = a[i];
+      }
+    } else {
+      RowVec<float, V> r;
+      r.load(p);
+      r.unpack(v);
+    }
+  }
+}
+
 // V FP32 parameters (weights, biases): re-read by every row, so cached.
 template <int V>
 __device__ __forceinline__ void load_params(const float* p, float (&v)[V]) {
@@ -136,14 +185,23 @@ struct RowCodes {
   int64_t atoms;      // scale atoms per 128-row block
 };
 
-// Encodes V (4 or 8) values of columns [col, col + V) of row `row`; the lanes of a block's
-// 16 (NVFP4) or 32 (MXFP4) columns are neighbours and combine its maximum by shuffles.  Every
-// lane of the warp calls it; `ok` says whether the lane's columns exist.  The same FP32 steps
-// as the quantize kernels, so the codes are those of quantizing the values as FP32.
-// Returns whether the block holds a non-finite value.
+// Address of the scale of `row`'s k-th block in 128 x 4 atoms.
+__device__ __forceinline__ int64_t scale_at(int64_t row, int64_t k, int64_t atoms) {
+  return ((row / 128) * atoms + k / 4) * 512 + (row % 32) * 16 + ((row % 128) / 32) * 4 + k % 4;
+}
+
+template <int V>
+__device__ __forceinline__ void store_codes(uint8_t* dst, uint32_t packed) {
+  if constexpr (V == 8) *reinterpret_cast<uint32_t*>(dst) = packed;
+  else *reinterpret_cast<uint16_t*>(dst) = static_cast<uint16_t>(packed);
+}
+
+// Block scale and codes of V (4 or 8) values; the lanes of a block's 16 (NVFP4) or 32 (MXFP4)
+// columns are neighbours and combine its maximum by shuffles, so every lane of the warp calls it.
+// The same FP32 steps as the quantize kernels: the codes are those of quantizing the values as
+// FP32.  Sets `bad` where the block holds a non-finite value.
 template <int FMT, int V>
-__device__ __forceinline__ bool encode_row_vec(const RowCodes& c, float g, int64_t row, int64_t col, bool ok,
-                                               const float (&v)[V]) {
+__device__ __forceinline__ uint32_t encode_vec(float g, const float (&v)[V], uint32_t& sb, bool& bad) {
   static_assert(V == 4 || V == 8, "one 16-byte word of FP32 or BF16 input");
   constexpr int BLOCK = FMT == kCodesMx ? 32 : 16;
   uint32_t m = 0;
@@ -151,7 +209,6 @@ __device__ __forceinline__ bool encode_row_vec(const RowCodes& c, float g, int64
   for (int i = 0; i < V; ++i) m = max(m, abs_bits_of(v[i]));
 #pragma unroll
   for (int d = 1; d < BLOCK / V; d <<= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
-  uint32_t sb;
   float mul;
   if constexpr (FMT == kCodesMx) {
     sb = e8m0_code(__fdiv_rn(__uint_as_float(m), 6.0f));
@@ -162,17 +219,25 @@ __device__ __forceinline__ bool encode_row_vec(const RowCodes& c, float g, int64
   float s[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) s[i] = v[i] == 0.0f ? v[i] : __fmul_rn(v[i], mul);  // 1/denom may have overflowed
+  bad |= m >= 0x7F800000u;
+  if constexpr (V == 8) return pack8<kE2M1Hardware>(s);
+  else return pack4<kE2M1Hardware>(s);
+}
+
+// encode_vec of columns [col, col + V) of row `row`, stored; `ok` says whether the lane's columns
+// exist.  Returns whether the block holds a non-finite value.
+template <int FMT, int V>
+__device__ __forceinline__ bool encode_row_vec(const RowCodes& c, float g, int64_t row, int64_t col, bool ok,
+                                               const float (&v)[V]) {
+  constexpr int BLOCK = FMT == kCodesMx ? 32 : 16;
+  uint32_t sb;
+  bool bad = false;
+  const uint32_t packed = encode_vec<FMT, V>(g, v, sb, bad);
   if (ok) {
-    uint8_t* dst = c.codes + row * (c.cols / 2) + col / 2;
-    if constexpr (V == 8) *reinterpret_cast<uint32_t*>(dst) = pack8<kE2M1Hardware>(s);
-    else *reinterpret_cast<uint16_t*>(dst) = static_cast<uint16_t>(pack4<kE2M1Hardware>(s));
-    if (col % BLOCK == 0) {
-      const int64_t k = col / BLOCK;
-      c.scales[((row / 128) * c.atoms + k / 4) * 512 + (row % 32) * 16 + ((row % 128) / 32) * 4 + k % 4] =
-          static_cast<uint8_t>(sb);
-    }
+    store_codes<V>(c.codes + row * (c.cols / 2) + col / 2, packed);
+    if (col % BLOCK == 0) c.scales[scale_at(row, col / BLOCK, c.atoms)] = static_cast<uint8_t>(sb);
   }
-  return ok && m >= 0x7F800000u;
+  return ok && bad;
 }
 
 template <typename... KArgs, typename... Args>

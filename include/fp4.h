@@ -464,6 +464,110 @@ fp4_status fp4_gemm_grouped(fp4_fmt fmt, int num_groups, const int32_t* offsets_
                             fp4_dtype out_dtype, void* workspace_dev, size_t workspace_bytes,
                             void* stream);
 
+/* ---- Tokens to their experts and back.  A router gives every token `topk` choices: slot
+ * s = t * topk + j is token t's j-th.  All of the calls below take the slots' rows from
+ * fp4_moe_sort; tokens * topk <= 2^30, topk <= 1024, cols <= 2^24, matrices 16-byte aligned.
+ *
+ * fp4_moe_sort: rows of the slots in the experts' order, slots of one expert in their own order
+ * (the same result every time).
+ *   ids_dev      [tokens, topk] expert numbers, int32 (id_bytes 4) or int64 (8); a number outside
+ *           [0, num_experts) is no expert: the slot gets no row.  One expert twice in a token's
+ *           list is two slots.
+ *   offsets_dev  [num_experts + 1] int32: expert e's rows are [offsets[e], offsets[e + 1]), as the
+ *           grouped products and fp4_quantize_grouped take them (offsets[num_experts] rows in all,
+ *           fewer than tokens * topk where slots have no expert).
+ *   row_of_dev   [tokens, topk] int32: the slot's row, or -1.
+ *   scale_row_of_dev  [tokens, topk] int32 or NULL: its row in the grouped scale layout (each
+ *           expert's rows start a 128-row block), or -1.
+ * num_experts <= 1024.  workspace: fp4_moe_sort_workspace_size(tokens, topk, num_experts) bytes
+ * (0 up to 16384 slots), 4-byte aligned, any contents, not shared by calls that overlap. */
+size_t fp4_moe_sort_workspace_size(int64_t tokens, int topk, int num_experts);
+fp4_status fp4_moe_sort(const void* ids_dev, int id_bytes, int64_t tokens, int topk, int num_experts,
+                        int32_t* offsets_dev, int32_t* row_of_dev, int32_t* scale_row_of_dev, void* workspace_dev,
+                        size_t workspace_bytes, void* stream);
+
+/* y[row_of[t, j]] = x[t]: the tokens' rows x [tokens, cols] (in_dtype) in the experts' order, y
+ * [tokens * topk, cols] in out_dtype.  Rows behind the last expert's are left as they were. */
+fp4_status fp4_moe_dispatch(const void* x_dev, int64_t tokens, int64_t cols, fp4_dtype in_dtype, int topk,
+                            const int32_t* row_of_dev, void* y_dev, fp4_dtype out_dtype, void* stream);
+
+/* The same rows as the A operand of the grouped products: NVFP4 codes with the caller's global
+ * scale global_dev, or MXFP4; exactly what fp4_quantize_grouped writes for the dispatched rows.
+ *   codes_dev  [tokens * topk, cols / 2]: rows behind the last expert's are left as they were;
+ *   scales_dev fp4_scales_bytes_grouped(tokens * topk, num_experts, cols, fmt) bytes, all written
+ *           (pads, and the blocks behind the last expert's, with 0).
+ *   scale_row_of_dev, offsets_dev  from the same fp4_moe_sort.
+ * cols % 32 == 0.  A non-finite element of x latches FP4_ERR_NONFINITE (of any token, also of one
+ * without an expert). */
+fp4_status fp4_moe_dispatch_codes(const void* x_dev, int64_t tokens, int64_t cols, fp4_dtype in_dtype, int topk,
+                                  const int32_t* row_of_dev, const int32_t* scale_row_of_dev, int num_experts,
+                                  const int32_t* offsets_dev, fp4_fmt fmt, uint8_t* codes_dev, uint8_t* scales_dev,
+                                  const float* global_dev, void* stream);
+
+/* The same rows as fp4_quantize_i8 quantizes them: codes_dev [tokens * topk, cols], a scale each in
+ * row_scales_dev [tokens * topk]; rows behind the last expert's are left as they were.
+ * cols % 16 == 0. */
+fp4_status fp4_moe_dispatch_i8(const void* x_dev, int64_t tokens, int64_t cols, fp4_dtype in_dtype, int topk,
+                               const int32_t* row_of_dev, int8_t* codes_dev, float* row_scales_dev, void* stream);
+
+/* The way back: out[t] = sum_j weights[t, j] y[row_of[t, j]] + residual[t], the sum in FP32 in the
+ * order of j, rounded once.  Slots without an expert add nothing; a token without any gives 0 (or
+ * its residual).
+ *   y_dev   [tokens * topk, cols] in in_dtype; only the slots' rows are read.
+ *   weights_dev  [tokens, topk] FP32, or NULL: 1 each.  Without weights and residual this is the
+ *           gradient of fp4_moe_dispatch, dx[t] = sum_j dy[row_of[t, j]].
+ *   residual_dev [tokens, cols] in residual_dtype, or NULL; it may be out itself (same type).
+ *   out_dev [tokens, cols] in out_dtype; it must not overlap y. */
+fp4_status fp4_moe_combine(const void* y_dev, fp4_dtype in_dtype, const int32_t* row_of_dev, const float* weights_dev,
+                           int64_t tokens, int topk, int64_t cols, const void* residual_dev, fp4_dtype residual_dtype,
+                           void* out_dev, fp4_dtype out_dtype, void* stream);
+
+/* Its backward pass, from dout [tokens, cols] and y (both in_dtype):
+ *   dy[row_of[t, j]] = weights[t, j] dout[t],   dweights[t, j] = sum_c dout[t, c] y[row_of[t, j], c]
+ *   dy_dev  [tokens * topk, cols] in out_dtype or NULL (rows behind the last expert's are left as
+ *           they were); it may be y itself where the types agree.
+ *   dweights_dev [tokens, topk] FP32 or NULL (y is then not read and may be NULL): sums in FP32 in a
+ *           fixed order, 0 for a slot without an expert.
+ *   weights_dev  as above.  (The residual's gradient is dout itself.) */
+fp4_status fp4_moe_combine_backward(const void* dout_dev, const void* y_dev, fp4_dtype in_dtype,
+                                    const int32_t* row_of_dev, const float* weights_dev, int64_t tokens, int topk,
+                                    int64_t cols, void* dy_dev, fp4_dtype out_dtype, float* dweights_dev, void* stream);
+
+/* ---- Products in 8-bit integers with a scale for each token and each channel.
+ *
+ * fp4_quantize_i8: the rows of x [rows, cols] (in_dtype) as signed 8-bit integers with one FP32 scale
+ * each: s = max |x| / 127 of the row (at least 2^-126; 1 for a row of zeros), q = x * (1 / s) rounded
+ * to the nearest integer, ties to even, within [-127, 127] (each FP32 operation rounds once).
+ * codes_dev [rows, cols], row_scales_dev [rows].  For activations (rows are tokens) and weights
+ * (rows are output channels) alike.  cols % 16 == 0, x and codes 16-byte aligned; a non-finite
+ * element latches FP4_ERR_NONFINITE. */
+fp4_status fp4_quantize_i8(const void* x_dev, int64_t rows, int64_t cols, fp4_dtype in_dtype, int8_t* codes_dev,
+                           float* row_scales_dev, void* stream);
+
+/* D[m, n] = act(sA[m] sB[n] sum_k A[m, k] B[n, k] + bias[n]): A_dev [M, K] and B_dev [N, K] signed
+ * 8-bit, sA_dev [M] and sB_dev [N] FP32, bias_dev [N] FP32 or NULL, D_dev [M, N] in out_dtype.
+ * The sums are exact (32-bit integers), then FP32: the sum times sA[m], times sB[n], plus the bias,
+ * the activation, one rounding to the output type; the same bits every time.
+ * K % 16 == 0, K <= 131056 (sums of any 8-bit values stay within 32 bits); A, B and D 16-byte
+ * aligned.  workspace: fp4_gemm_i8_workspace_size(M, N, K) bytes, 16-byte aligned, zero-filled before
+ * first use, left so, not shared by calls that overlap (after FP4_ERR_TIMEOUT: zero it again).
+ * flags: FP4_GEMM_WEIGHTS_READY (B only: its scales and bias are read after the preceding kernel). */
+size_t fp4_gemm_i8_workspace_size(int64_t M, int64_t N, int64_t K);
+fp4_status fp4_gemm_i8(const int8_t* A_dev, const float* sA_dev, const int8_t* B_dev, const float* sB_dev, int64_t M,
+                       int64_t N, int64_t K, const float* bias_dev, fp4_act act, void* D_dev, fp4_dtype out_dtype,
+                       void* workspace_dev, size_t workspace_bytes, unsigned flags, void* stream);
+
+/* By experts: rows [offsets[e], offsets[e + 1]) of A with expert e's weights B_dev + e N K, scales
+ * sB_dev + e N and bias bias_dev + e N.  offsets_dev as for fp4_gemm_gated_grouped (the last one may
+ * stay below total_rows: rows of D behind it are left as they were; experts without rows are
+ * skipped).  num_groups <= 1024, num_groups * N <= 2^31 - 256.  Its own workspace size; otherwise as
+ * fp4_gemm_i8. */
+size_t fp4_gemm_i8_grouped_workspace_size(int num_groups, int64_t total_rows, int64_t N, int64_t K);
+fp4_status fp4_gemm_i8_grouped(int num_groups, const int32_t* offsets_dev, const int8_t* A_dev, const float* sA_dev,
+                               const int8_t* B_dev, const float* sB_dev, int64_t total_rows, int64_t N, int64_t K,
+                               const float* bias_dev, fp4_act act, void* D_dev, fp4_dtype out_dtype,
+                               void* workspace_dev, size_t workspace_bytes, void* stream);
+
 /* Reads and clears the device status word latched by earlier calls on this device
  * (after synchronizing `stream`).  Returns FP4_OK, FP4_ERR_NONFINITE or FP4_ERR_TIMEOUT
  * (the first error latched), or FP4_ERR_CUDA if the synchronization failed. */
