@@ -13,24 +13,28 @@
 //
 // Structure, one CTA (or one CTA of a pair) per SM, persistent:
 //   warp 0      loads, by TMA: per K step of 128 bytes one 128 x 128-byte box of weights and one box
-//               of BN (pair: BN / 2) tokens, both with the 128-byte swizzle, into a ring of stages
-//   warp 1      owns TMEM; one lane issues four K = 32 MMAs a stage
-//   warps 2..   epilogue, four warps (tiles up to 64 tokens) or eight (two per TMEM lane quarter,
-//               one per half of the columns); two accumulators, so that it overlaps the next tile
+//               of tokens, both with the 128-byte swizzle, into a ring of stages of one K step
+//               (pairs: two)
+//   warp 1      owns TMEM; one lane issues four K = 32 MMAs a K step
+//   warps 2..   epilogue, four warps (one per TMEM lane quarter), or eight from 64 tokens on, which
+//               share out the columns; two accumulators, so that it overlaps the next tile
+// Above 64 tokens a tile is shared by a pair of CTAs: 256 channels x up to 256 tokens, each CTA loading
+// its 128 channels and half of the tokens.  Its width is the tokens that share weights (one
+// expert's, or all) in equal parts, rounded up to 64: 530 rows are 3 x 192, not 2 x 256 and a rest.
 //
-// Schedules: whole tiles, strided over the grid; or a split, where the K steps of all tiles form one
-// sequence that is cut evenly over the grid.  A tile cut in pieces has its partial sums added up
-// in the workspace, in the slot of the CTA that starts it; the CTA whose piece completes the K
-// steps takes them from there, clears slot and counter, and finishes the tile.  No CTA waits for
-// another one.
+// Schedules: pairs take whole tiles, strided over the grid.  Single CTAs split: the K steps of all
+// tiles form one sequence that is cut evenly over the grid.  A CTA then leaves the sums of a tile that
+// it has only a piece of in the workspace (one slot for a tile that it ends, one for a tile that
+// it starts); the one whose piece completes the tile's K steps adds up the others' slots, clears
+// them, and finishes the tile.  No CTA waits for another one.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <cuda_bf16.h>
 #include <cstdint>
 
 #include "fp4_act.cuh"
+#include "fp4_i8.cuh"
 #include "fp4_moe.h"
-#include "fp4_ptx.cuh"
 
 namespace fp4 {
 namespace {
@@ -41,13 +45,15 @@ struct I8Args {
   int M, N, K, num_kb;
   void* out;
   int out_bf16;
+  int wide;            // BF16 elements that go out at once: 8, 2 or 1
   int early_w;         // weights may be read before the preceding kernel finishes
+  int weights_once;    // a weight's tokens fit one tile: it need not stay in L2
   int split;
   int tiles_w, tiles_t;  // tiles along the channels, along the tokens (dense)
   int num_groups;
   const int32_t* offsets;
-  int* cnt;            // split: K steps summed so far in each slot, zero between calls
-  int* sums;           // split: [grid][BN][128] partial sums, zero between calls
+  int* cnt;            // split: K steps done of the tile that each CTA starts, per warp; zero between calls
+  int4* sums;          // split: two slots per CTA of BN x 128 sums, zero between calls
   unsigned* status;
 };
 
@@ -55,32 +61,40 @@ struct I8Work {
   int w_row, x_row;    // first rows of the tile's boxes (of this CTA's)
   int n0, n_valid;     // this CTA's channels
   int t0, t_valid;     // the tile's tokens
+  int width;           // its MMA columns
   int group;
   int kb0, kb1;
-  int slot;            // split: the CTA that starts the tile
+  int first, last;     // split: the CTAs that hold its first and last K step
 };
 
 template <int BN, bool PAIR>
 struct I8Cfg {
-  static constexpr int kEpiWarps = BN >= 128 ? 8 : 4;
+  static constexpr int kEpiWarps = BN >= 64 ? 8 : 4;
   static constexpr int kThreads = 64 + 32 * kEpiWarps;
+  static constexpr int kSteps = PAIR ? 2 : 1;  // K steps of 128 bytes a stage
   static constexpr int kWBytes = 128 * 128;
-  static constexpr int kXRows = PAIR ? BN / 2 : BN;
-  static constexpr int kXBytes = kXRows * 128;
-  static constexpr int kStageBytes = kWBytes + kXBytes;
+  static constexpr int kXBytes = (PAIR ? BN / 2 : BN) * 128;
+  static constexpr int kStageBytes = kSteps * (kWBytes + kXBytes);
   static constexpr int kScaleOff = 1024;                        // barriers and flags before it
   static constexpr int kGroupOff = kScaleOff + 2 * BN * 4;      // two tiles' token scales
-  static constexpr int kMiscBytes = kGroupOff + 2 * (kMaxGroups + 1) * 4;
+  static constexpr int kOutOff = (kGroupOff + 2 * (kMaxGroups + 1) * 4 + 15) / 16 * 16;  // 1 KB per epilogue warp
+  static constexpr int kMiscBytes = kOutOff + 1024 * kEpiWarps;
   static constexpr int kFit = (227 * 1024 - 1024 - 256 - kMiscBytes) / kStageBytes;
   static constexpr int kStages = kFit > 12 ? 12 : kFit;
   static constexpr int kSmemBytes = kStages * kStageBytes + kMiscBytes + 1024;
   static constexpr int kTmemCols = 2 * BN;  // 32 .. 512, a power of two
   static constexpr int kChunk = BN * 4 / kEpiWarps;  // accumulator columns of an epilogue thread
-  static_assert(BN == 16 || BN == 32 || BN == 64 || BN == 128 || BN == 256, "tile width");
-  static_assert(!PAIR || BN == 256, "pairs run 256 x 256 tiles");
-  static_assert(kStageBytes % 1024 == 0, "the 128-byte swizzle's alignment");
+  static constexpr int kLoad = PAIR ? 32 : 16;  // that it takes at once
+  static_assert(32 * kEpiWarps >= BN, "a token scale per epilogue thread");
+  static_assert(PAIR ? BN == 256 : BN == 16 || BN == 32 || BN == 64, "tile width");
+  static_assert(kXBytes % 1024 == 0 && kStageBytes % 1024 == 0, "the 128-byte swizzle's alignment");
   static_assert(kStages >= 3 && kSmemBytes + 256 <= 227 * 1024, "shared memory");
   static_assert((2 * kStages + 5) * 8 + 16 <= kScaleOff, "barriers");
+};
+
+// Token rows of a pair's boxes: half of a tile's width of 64, 128, 192 or 256.
+struct I8TokenMaps {
+  CUtensorMap box[4];
 };
 
 template <int BN, bool PAIR>
@@ -89,11 +103,11 @@ struct I8Sched {
   const I8Args& p;
   const int *s_off, *s_tiles;  // by experts: row offsets, prefix of token tiles
   int vb, vg, sub_row;
-  int64_t u, end, tiles, units;
+  uint32_t u, end, units;  // (32 bits: divisions are taken for every tile, and the host sees to it that they do)
 
   __device__ I8Sched(const I8Args& a, const int* off, const int* tl, int vb_, int vg_, int sub)
       : p(a), s_off(off), s_tiles(tl), vb(vb_), vg(vg_), sub_row(sub) {
-    tiles = static_cast<int64_t>(p.tiles_w) * (p.num_groups ? s_tiles[p.num_groups] : p.tiles_t);
+    const uint32_t tiles = static_cast<uint32_t>(p.tiles_w) * (p.num_groups ? s_tiles[p.num_groups] : p.tiles_t);
     units = tiles * p.num_kb;
     u = p.split ? units * vb / vg : vb;
     end = p.split ? units * (vb + 1) / vg : tiles;
@@ -101,44 +115,43 @@ struct I8Sched {
 
   __device__ bool next(I8Work& w) {
     if (u >= end) return false;
-    int64_t tile = u;
+    uint32_t tile = u;
     w.kb0 = 0;
     w.kb1 = p.num_kb;
-    w.slot = 0;
     if (p.split) {
       tile = u / p.num_kb;
       w.kb0 = static_cast<int>(u - tile * p.num_kb);
-      w.kb1 = static_cast<int>(min(static_cast<int64_t>(p.num_kb), w.kb0 + (end - u)));
-      // the CTA c whose units [units c / vg, units (c + 1) / vg) hold the tile's first one
-      w.slot = static_cast<int>(((tile * p.num_kb + 1) * vg - 1) / units);
+      w.kb1 = static_cast<int>(min(static_cast<uint32_t>(p.num_kb), w.kb0 + (end - u)));
+      // the CTA c whose units [units c / vg, units (c + 1) / vg) hold unit x is ((x + 1) vg - 1) / units
+      w.first = static_cast<int>(((tile * p.num_kb + 1) * vg - 1) / units);
+      w.last = static_cast<int>(((tile + 1) * p.num_kb * vg - 1) / units);
       u += w.kb1 - w.kb0;
     } else {
       u += vg;
     }
-    int wt, tt, row0, row_end;
+    int wt, tt, tts, row0, row_end;
     if (p.num_groups) {
       int lo = 0, hi = p.num_groups - 1;  // the last expert whose tiles start at or before this one
       while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
-        if (static_cast<int64_t>(s_tiles[mid]) * p.tiles_w <= tile) lo = mid;
+        if (static_cast<uint32_t>(s_tiles[mid]) * p.tiles_w <= tile) lo = mid;
         else hi = mid - 1;
       }
-      const int mine = s_tiles[lo + 1] - s_tiles[lo];
-      const int64_t local = tile - static_cast<int64_t>(s_tiles[lo]) * p.tiles_w;
-      wt = static_cast<int>(local / mine);
-      tt = static_cast<int>(local % mine);
+      tts = s_tiles[lo + 1] - s_tiles[lo];
+      const uint32_t local = tile - static_cast<uint32_t>(s_tiles[lo]) * p.tiles_w;
+      wt = static_cast<int>(local / tts);
+      tt = static_cast<int>(local - wt * tts);
       w.group = lo;
       row0 = s_off[lo];
       row_end = s_off[lo + 1];
     } else {
-      // groups of eight token tiles, so that tiles that run at once share boxes in L2
-      constexpr int kBand = 8;
-      const int64_t band = static_cast<int64_t>(kBand) * p.tiles_w;
-      const int first = static_cast<int>(tile / band) * kBand;
-      const int size = min(kBand, p.tiles_t - first);
-      const int r = static_cast<int>(tile % band);
-      wt = r / size;
-      tt = first + r % size;
+      // groups of sixteen token tiles, so that tiles that run at once share boxes in L2
+      constexpr uint32_t kBand = 16;
+      const uint32_t band = tile / (kBand * p.tiles_w), first = band * kBand;
+      const uint32_t size = min(kBand, p.tiles_t - first), r = tile - first * p.tiles_w;
+      wt = static_cast<int>(r / size);
+      tt = static_cast<int>(first + r - wt * size);
+      tts = p.tiles_t;
       w.group = 0;
       row0 = 0;
       row_end = p.M;
@@ -146,12 +159,61 @@ struct I8Sched {
     w.n0 = wt * kRows + sub_row;
     w.n_valid = max(0, min(128, p.N - w.n0));
     w.w_row = w.group * p.N + w.n0;
-    w.t0 = row0 + tt * BN;
-    w.t_valid = min(BN, row_end - w.t0);
-    w.x_row = w.t0 + (PAIR ? sub_row : 0);
+    w.width = PAIR ? ((row_end - row0 + tts - 1) / tts + 63) / 64 * 64 : BN;
+    w.t0 = row0 + tt * w.width;
+    w.t_valid = min(w.width, row_end - w.t0);
+    w.x_row = w.t0 + (sub_row ? w.width / 2 : 0);
     return true;
   }
 };
+
+// Stores 16 tokens of a warp's 32 channels: v[i] holds tokens `token` + 2i and + 2i + 1 (of which
+// `tokens` exist) of channel `ch` + lane (of which `chs` exist).  FP32 rows are whole lines as they
+// are.  BF16 ones meet in the warp's 1 KB of shared memory and leave in 16-byte words where the
+// rows start at those, else in pairs or single elements.
+__device__ __forceinline__ void store_tokens16(const I8Args& p, uint16_t* stage, int64_t token, int tokens, int ch,
+                                               int chs, int lane, const float2 (&v)[8]) {
+  if (!p.out_bf16) {
+    float* out = static_cast<float*>(p.out) + token * p.N + ch + lane;
+    if (lane >= chs) return;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (2 * i < tokens) out[0] = v[i].x;
+      if (2 * i + 1 < tokens) out[p.N] = v[i].y;
+      out += 2 * static_cast<int64_t>(p.N);
+    }
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(v[i].x, v[i].y);
+    const uint32_t w = *reinterpret_cast<const uint32_t*>(&h);
+    stage[2 * i * 32 + lane] = static_cast<uint16_t>(w);
+    stage[(2 * i + 1) * 32 + lane] = static_cast<uint16_t>(w >> 16);
+  }
+  __syncwarp();
+  uint16_t* out = static_cast<uint16_t*>(p.out) + token * p.N + ch;
+  if (p.wide == 8) {
+    const int c = lane % 4 * 8;
+#pragma unroll
+    for (int t = lane / 4; t < 16; t += 8)
+      if (t < tokens && c < chs)
+        __stcs(reinterpret_cast<uint4*>(out + static_cast<int64_t>(t) * p.N + c),
+               *reinterpret_cast<const uint4*>(stage + t * 32 + c));
+  } else if (p.wide == 2) {
+    const int c = lane % 16 * 2;
+#pragma unroll
+    for (int t = lane / 16; t < 16; t += 2)
+      if (t < tokens && c < chs)
+        *reinterpret_cast<uint32_t*>(out + static_cast<int64_t>(t) * p.N + c) =
+            *reinterpret_cast<const uint32_t*>(stage + t * 32 + c);
+  } else {
+#pragma unroll
+    for (int t = 0; t < 16; ++t)
+      if (t < tokens && lane < chs) out[static_cast<int64_t>(t) * p.N + lane] = stage[t * 32 + lane];
+  }
+  __syncwarp();  // before the next 16 tokens take their place
+}
 
 __device__ __forceinline__ void i8_timeout(volatile int* abort, unsigned* status) {
   *abort = 1;
@@ -160,7 +222,7 @@ __device__ __forceinline__ void i8_timeout(volatile int* abort, unsigned* status
 
 template <int BN, bool PAIR>
 __global__ void __launch_bounds__(I8Cfg<BN, PAIR>::kThreads, 1)
-    fp4_i8_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX, const I8Args p) {
+    fp4_i8_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ I8TokenMaps tmX, const I8Args p) {
   using C = I8Cfg<BN, PAIR>;
   using Schedule = I8Sched<BN, PAIR>;
   constexpr int S = C::kStages;
@@ -175,7 +237,6 @@ __global__ void __launch_bounds__(I8Cfg<BN, PAIR>::kThreads, 1)
   uint64_t* drain = acc_empty + 2;
   volatile int* s_abort = reinterpret_cast<volatile int*>(drain + 1);
   volatile int* s_fail = s_abort + 1;
-  volatile int* s_last = s_abort + 2;
   float* s_scale = reinterpret_cast<float*>(misc + C::kScaleOff);
   int* s_off = reinterpret_cast<int*>(misc + C::kGroupOff);
   int* s_tiles = s_off + kMaxGroups + 1;
@@ -197,10 +258,9 @@ __global__ void __launch_bounds__(I8Cfg<BN, PAIR>::kThreads, 1)
     mbar_init(drain, 1);
     *s_abort = 0;
     *s_fail = 0;
-    *s_last = 0;
     fence_mbar_init();
     tma_prefetch_desc(&tmW);
-    tma_prefetch_desc(&tmX);
+    if constexpr (!PAIR) tma_prefetch_desc(&tmX.box[0]);
   }
   if (warp == 1) {
     if constexpr (PAIR) {
@@ -245,18 +305,21 @@ __global__ void __launch_bounds__(I8Cfg<BN, PAIR>::kThreads, 1)
   if (warp == 0) {
     if (lane == 0) {
       // ------------------------------------------------------------ loads
-      // weights that one band of tokens reads once need not stay in L2
-      const uint64_t pol_w = p.tiles_t == 1 ? l2_policy_evict_first() : l2_policy_evict_last();
+      const uint64_t pol_w = p.weights_once ? l2_policy_evict_first() : l2_policy_evict_last();
       const uint64_t pol_x = l2_policy_evict_last();
       auto load = [&](int stage, const I8Work& w, int kb, bool weights) {
-        uint8_t* st = smem + stage * C::kStageBytes;
-        if constexpr (PAIR) {
-          const uint32_t bar = cluster_addr(smem_u32(&full[stage]), 0);
-          if (weights) tma_load_2d_pair(st, &tmW, bar, kb * 128, w.w_row, pol_w);
-          else tma_load_2d_pair(st + C::kWBytes, &tmX, bar, kb * 128, w.x_row, pol_x);
-        } else {
-          if (weights) tma_load_2d(st, &tmW, &full[stage], kb * 128, w.w_row, pol_w);
-          else tma_load_2d(st + C::kWBytes, &tmX, &full[stage], kb * 128, w.x_row, pol_x);
+        uint8_t* st = smem + stage * C::kStageBytes + (weights ? 0 : C::kSteps * C::kWBytes);
+#pragma unroll
+        for (int h = 0; h < C::kSteps; ++h) {
+          const int x = (kb * C::kSteps + h) * 128;
+          if constexpr (PAIR) {
+            const uint32_t bar = cluster_addr(smem_u32(&full[stage]), 0);
+            if (weights) tma_load_2d_pair(st + h * C::kWBytes, &tmW, bar, x, w.w_row, pol_w);
+            else tma_load_2d_pair(st + h * C::kXBytes, &tmX.box[w.width / 64 - 1], bar, x, w.x_row, pol_x);
+          } else {
+            if (weights) tma_load_2d(st + h * C::kWBytes, &tmW, &full[stage], x, w.w_row, pol_w);
+            else tma_load_2d(st + h * C::kXBytes, &tmX.box[0], &full[stage], x, w.x_row, pol_x);
+          }
         }
       };
       // with weights that are ready, the first ring-full of stages asks for them, then waits for
@@ -286,7 +349,8 @@ __global__ void __launch_bounds__(I8Cfg<BN, PAIR>::kThreads, 1)
             break;
           }
           // a pair's leader counts the boxes of both CTAs (out-of-range rows read as zero)
-          if (leader) mbar_arrive_expect_tx(&full[stage], (PAIR ? 2 : 1) * C::kStageBytes);
+          if (leader)
+            mbar_arrive_expect_tx(&full[stage], PAIR ? C::kSteps * (2 * C::kWBytes + w.width * 128) : C::kStageBytes);
           load(stage, w, kb, true);
           if (waited) load(stage, w, kb, false);
           else if (++pending == S) tokens();
@@ -310,8 +374,6 @@ __global__ void __launch_bounds__(I8Cfg<BN, PAIR>::kThreads, 1)
   } else if (warp == 1) {
     if (lane == 0 && leader) {
       // ------------------------------------------------------------ MMAs
-      constexpr uint32_t idesc_rows = PAIR ? 256 : 128;
-      const uint32_t idesc = mma_idesc_i8(BN, idesc_rows);
       Schedule sch(p, s_off, s_tiles, vb, vg, sub_row);
       I8Work w;
       int stage = 0, iter = 0;
@@ -325,6 +387,7 @@ __global__ void __launch_bounds__(I8Cfg<BN, PAIR>::kThreads, 1)
         }
         tc_fence_after();
         const uint32_t d_tmem = tmem + acc * BN;
+        const uint32_t idesc = mma_idesc_i8(PAIR ? w.width : BN, PAIR ? 256 : 128);
         for (int kb = w.kb0; kb < w.kb1; ++kb) {
           if (!mbar_wait(&full[stage], phase, s_abort)) {
             i8_timeout(s_abort, p.status);
@@ -333,12 +396,16 @@ __global__ void __launch_bounds__(I8Cfg<BN, PAIR>::kThreads, 1)
           }
           tc_fence_after();
           const uint32_t st = smem_u32(smem) + stage * C::kStageBytes;
-          const uint64_t adesc = smem_desc_sw128(st), bdesc = smem_desc_sw128(st + C::kWBytes);
-          const int nk = min(4, (p.K - kb * 128 + 31) / 32);
-          for (int k = 0; k < nk; ++k) {
+          const uint64_t adesc = smem_desc_sw128(st), bdesc = smem_desc_sw128(st + C::kSteps * C::kWBytes);
+          const int left = (p.K - kb * C::kSteps * 128 + 31) / 32;  // MMAs up to the end of K
+#pragma unroll
+          for (int k = 0; k < 4 * C::kSteps; ++k) {
+            if (k >= left) break;
+            const uint64_t ad = adesc + (k / 4) * (C::kWBytes / 16) + 2 * (k % 4);
+            const uint64_t bd = bdesc + (k / 4) * (C::kXBytes / 16) + 2 * (k % 4);
             const uint32_t accum = kb > w.kb0 || k > 0 ? 1u : 0u;
-            if constexpr (PAIR) tc_mma_i8_pair(d_tmem, adesc + 2 * k, bdesc + 2 * k, idesc, accum);
-            else tc_mma_i8(d_tmem, adesc + 2 * k, bdesc + 2 * k, idesc, accum);
+            if constexpr (PAIR) tc_mma_i8_pair(d_tmem, ad, bd, idesc, accum);
+            else tc_mma_i8(d_tmem, ad, bd, idesc, accum);
           }
           if constexpr (PAIR) tc_commit_pair_mc(&empty[stage], 3);
           else tc_commit(&empty[stage]);
@@ -366,20 +433,30 @@ __global__ void __launch_bounds__(I8Cfg<BN, PAIR>::kThreads, 1)
     const int et = threadIdx.x - 64;
     const int c0 = ((warp - 2) >> 2) * C::kChunk;  // this thread's first column
     const int rl = q * 32 + lane;                 // its channel within the tile
+    uint16_t* stage = reinterpret_cast<uint16_t*>(misc + C::kOutOff) + (warp - 2) * 512;
     Schedule sch(p, s_off, s_tiles, vb, vg, sub_row);
-    I8Work w;
+    I8Work w, next;
+    // a tile's scales and biases are asked for one tile ahead
+    float next_x = 0.0f, next_w = 0.0f, next_b = 0.0f;
+    auto ahead = [&]() {
+      if (!sch.next(next)) return false;
+      next_x = et < next.t_valid ? __ldg(p.sx + next.t0 + et) : 0.0f;
+      if (rl < next.n_valid) {
+        const int64_t ch = static_cast<int64_t>(next.group) * p.N + next.n0 + rl;
+        next_w = __ldg(p.sw + ch);
+        if (p.bias) next_b = __ldg(p.bias + ch);
+      }
+      return true;
+    };
+    bool more = ahead();
     int iter = 0;
-    while (sch.next(w)) {
+    while (more) {
+      w = next;
       const int acc = iter & 1;
       float* xs = s_scale + acc * BN;
-      for (int c = et; c < BN; c += 32 * C::kEpiWarps) xs[c] = c < w.t_valid ? __ldg(p.sx + w.t0 + c) : 0.0f;
-      const bool ch_ok = rl < w.n_valid;
-      float sw = 0.0f, b = 0.0f;
-      if (ch_ok) {
-        const int64_t ch = static_cast<int64_t>(w.group) * p.N + w.n0 + rl;
-        sw = __ldg(p.sw + ch);
-        if (p.bias) b = __ldg(p.bias + ch);
-      }
+      if (et < BN) xs[et] = next_x;
+      const float sw = next_w, b = next_b;
+      more = ahead();
       // the warps decide together whether to go on, so that none is left at a barrier
       if (et == 0 && !mbar_wait(&acc_full[acc], (iter >> 1) & 1, s_abort)) {
         i8_timeout(s_abort, p.status);
@@ -389,49 +466,99 @@ __global__ void __launch_bounds__(I8Cfg<BN, PAIR>::kThreads, 1)
       if (*s_fail) break;
       tc_fence_after();
       const uint32_t taddr = tmem + (static_cast<uint32_t>(q * 32) << 16) + acc * BN;
-      // 16 tokens of this thread's channel
-      auto finish = [&](int c, const uint32_t (&r)[16]) {
-        float v[16];
+      // 16 tokens of this thread's channel (all lanes take part)
+      const int chs = max(0, min(32, w.n_valid - q * 32));
+      auto finish = [&](int c, const uint32_t* r) __attribute__((always_inline)) {
+        float2 z[8];
 #pragma unroll
-        for (int j = 0; j < 16; ++j) v[j] = __fmul_rn(__fmul_rn(__int2float_rn(static_cast<int>(r[j])), xs[c + j]), sw);
+        for (int j = 0; j < 8; j += 2) {
+          const float4 x = *reinterpret_cast<const float4*>(xs + c + 2 * j);
+          const int* a = reinterpret_cast<const int*>(r) + 2 * j;
+          z[j] = __fmul2_rn(make_float2(__int2float_rn(a[0]), __int2float_rn(a[1])), make_float2(x.x, x.y));
+          z[j + 1] = __fmul2_rn(make_float2(__int2float_rn(a[2]), __int2float_rn(a[3])), make_float2(x.z, x.w));
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) z[j] = __fmul2_rn(z[j], pair(sw));
         if (p.bias) {
 #pragma unroll
-          for (int j = 0; j < 16; ++j) v[j] = __fadd_rn(v[j], b);
+          for (int j = 0; j < 8; ++j) z[j] = __fadd2_rn(z[j], pair(b));
         }
         with_act(p.act, [&](auto tag) __attribute__((always_inline)) {
 #pragma unroll
-          for (int j = 0; j < 16; ++j) v[j] = act_value<decltype(tag)::value>(v[j]);
+          for (int j = 0; j < 8; ++j) z[j] = act_value2<decltype(tag)::value>(z[j]);
         });
-        if (!ch_ok) return;
-        const int64_t at = static_cast<int64_t>(w.t0 + c) * p.N + w.n0 + rl;
-        if (p.out_bf16) {
-          __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.out) + at;
-#pragma unroll
-          for (int j = 0; j < 16; ++j)
-            if (c + j < w.t_valid) o[static_cast<int64_t>(j) * p.N] = __float2bfloat16_rn(v[j]);
-        } else {
-          float* o = static_cast<float*>(p.out) + at;
-#pragma unroll
-          for (int j = 0; j < 16; ++j)
-            if (c + j < w.t_valid) o[static_cast<int64_t>(j) * p.N] = v[j];
-        }
+        store_tokens16(p, stage, w.t0 + c, w.t_valid - c, w.n0 + q * 32, chs, lane, z);
       };
-      const bool piece = w.kb1 - w.kb0 < p.num_kb;
-      int* slot = p.sums + static_cast<int64_t>(w.slot) * (BN * 128) + rl;
-#pragma unroll 1
-      for (int c = c0; c < c0 + C::kChunk; c += 16) {
-        if (c >= w.t_valid) break;  // the same for all lanes
-        uint32_t r[16];
-        tmem_ld16(taddr + c, r);
+      auto load = [&](int c, uint32_t* r) __attribute__((always_inline)) {
+        if constexpr (C::kLoad == 32) tmem_ld32(taddr + c, r);
+        else tmem_ld16(taddr + c, *reinterpret_cast<uint32_t(*)[16]>(r));
         tmem_ld_wait();
-        if (!PAIR && piece) {
+      };
+      const int c1 = min(c0 + C::kChunk, w.t_valid);
+      bool done = true;
+      const bool piece = !PAIR && w.kb1 - w.kb0 < p.num_kb;
+      // this thread's sums in the slot of CTA `who`: the one for the tile that it starts, or ends
+      auto slot = [&](int who) { return p.sums + (2 * who + (who == w.first)) * static_cast<int64_t>(BN * 32) + rl; };
+      if (piece) {
+        int4* mine = slot(vb);
+#pragma unroll 1
+        for (int c = c0; c < c1; c += C::kLoad) {  // c1 is the same for all lanes
+          int r[C::kLoad];
+          load(c, reinterpret_cast<uint32_t*>(r));
 #pragma unroll
-          for (int j = 0; j < 16; ++j)
-            if (ch_ok && c + j < w.t_valid) atomicAdd(slot + (c + j) * 128, static_cast<int>(r[j]));
-        } else {
-          finish(c, r);
+          for (int j = 0; j < C::kLoad; j += 4)
+            __stcg(mine + (c + j) / 4 * 128, make_int4(r[j], r[j + 1], r[j + 2], r[j + 3]));
         }
-        __syncwarp();  // the next TMEM load takes the whole warp
+        // every warp for itself: the warps of this number in the tile's CTAs have the same sums to add
+        // (with barriers over the CTA 64 x 8192 x 8192 took 28.8 us, so 21.8)
+        __syncwarp();
+        if (lane == 0) {
+          __threadfence();
+          int* cnt = p.cnt + w.first * C::kEpiWarps + warp - 2;
+          const int all = atomicAdd(cnt, w.kb1 - w.kb0) + w.kb1 - w.kb0;
+          done = all == p.num_kb;
+          if (done) *cnt = 0;
+        }
+        done = __shfl_sync(0xFFFFFFFFu, done, 0);
+        if (done) __threadfence();
+      }
+      if (done) {
+#pragma unroll 1
+        for (int c = c0; c < c1; c += C::kLoad) {
+          uint32_t r[C::kLoad];
+          load(c, r);
+          if (piece) {
+            constexpr int kAsk = 4, kWords = C::kLoad / 4;  // slots that are asked for at once
+            for (int who = w.first; who <= w.last; who += kAsk) {
+              int4 t[kAsk][kWords];
+#pragma unroll
+              for (int h = 0; h < kAsk; ++h) {
+                const int4* from = slot(who + h) + c / 4 * 128;
+#pragma unroll
+                for (int j = 0; j < kWords; ++j)
+                  t[h][j] = who + h <= w.last && who + h != vb ? __ldcg(from + j * 128) : make_int4(0, 0, 0, 0);
+              }
+#pragma unroll
+              for (int h = 0; h < kAsk; ++h) {
+                if (who + h > w.last) break;
+                int4* from = slot(who + h) + c / 4 * 128;
+#pragma unroll
+                for (int j = 0; j < kWords; ++j) {
+                  r[4 * j] += t[h][j].x;
+                  r[4 * j + 1] += t[h][j].y;
+                  r[4 * j + 2] += t[h][j].z;
+                  r[4 * j + 3] += t[h][j].w;
+                  __stcg(from + j * 128, make_int4(0, 0, 0, 0));
+                }
+              }
+            }
+          }
+          finish(c, r);
+          if constexpr (C::kLoad == 32) {
+            if (c + 16 < w.t_valid) finish(c + 16, r + 16);
+          }
+          __syncwarp();  // the next TMEM load takes the whole warp
+        }
       }
       tc_fence_before();
       __syncwarp();
@@ -440,32 +567,6 @@ __global__ void __launch_bounds__(I8Cfg<BN, PAIR>::kThreads, 1)
         else mbar_arrive(&acc_empty[acc]);
       }
       ++iter;
-      if (PAIR || !piece) continue;
-      // this piece's sums are out; the one that completes the tile's K steps finishes it
-      __threadfence();
-      asm volatile("bar.sync 1, %0;" ::"n"(32 * C::kEpiWarps) : "memory");
-      if (et == 0) {
-        __threadfence();
-        const int before = atomicAdd(p.cnt + w.slot, w.kb1 - w.kb0);
-        *s_last = before + (w.kb1 - w.kb0) == p.num_kb;
-      }
-      asm volatile("bar.sync 1, %0;" ::"n"(32 * C::kEpiWarps) : "memory");
-      if (!*s_last) continue;
-      __threadfence();
-      if (et == 0) p.cnt[w.slot] = 0;
-#pragma unroll 1
-      for (int c = c0; c < c0 + C::kChunk && c < w.t_valid; c += 16) {
-        uint32_t r[16];
-#pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          r[j] = 0;
-          if (ch_ok && c + j < w.t_valid) {
-            r[j] = static_cast<uint32_t>(__ldcg(slot + (c + j) * 128));
-            __stcg(slot + (c + j) * 128, 0);
-          }
-        }
-        finish(c, r);
-      }
     }
   }
 
@@ -486,39 +587,64 @@ struct I8Plan {
   int BN;
   bool pair, split;
   int64_t tiles_w, tiles_t;  // (by experts: an estimate of the token tiles, the offsets are on the device)
+  int64_t rows;              // tokens that share their weights
+  int64_t units;             // K steps of all tiles, at most
   int num_kb;
-  int grid;                  // CTAs or pairs; split: slots
+  int grid;                  // CTAs or pairs
 };
 
 I8Plan i8_plan(int64_t M, int64_t N, int64_t K, int groups) {
   I8Plan pl{};
-  const int sms = num_sms();
+  const int sms = num_sms(), pairs = sms / 2;
   const int64_t used = groups ? std::min<int64_t>(groups, M) : 1;  // experts with rows, at most
-  const int64_t rows = (M + used - 1) / used;                      // tokens that share their weights
-  pl.num_kb = static_cast<int>((K + 127) / 128);
-  auto tiles_t = [&](int bn) { return used * ((rows + bn - 1) / bn); };
-  pl.BN = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
-  if (rows > 128 && N > 128 && (N + 255) / 256 * tiles_t(256) >= sms / 4) {
-    pl.BN = 256;
-    pl.pair = true;
+  pl.rows = (M + used - 1) / used;
+  pl.pair = pl.rows > 64;
+  pl.BN = pl.rows <= 16 ? 16 : pl.rows <= 32 ? 32 : pl.rows <= 64 ? 64 : 256;
+  const int step = pl.pair ? 256 : 128;
+  pl.num_kb = static_cast<int>((K + step - 1) / step);
+  pl.tiles_w = (N + step - 1) / step;
+  int width = pl.BN;
+  if (pl.pair && !groups) {
+    // A pair's K step takes about as long as loading 320 + width rows, and all pairs wait for the
+    // last round of tiles: the width with the shortest rounds in all.  (256 x 4096 x 4096: widths
+    // 64 / 128 / 256 take 15.1 / 16.6 / 18.5 us, 1024 x 8192 x 8192 115 / 73 / 50.)
+    int64_t best = INT64_MAX;
+    for (int w = 64; w <= 256; w += 64) {
+      const int64_t tiles = pl.tiles_w * ((M + w - 1) / w), cost = (tiles + pairs - 1) / pairs * (320 + w);
+      if (cost <= best) {
+        best = cost;
+        width = w;
+      }
+    }
   }
-  pl.tiles_w = (N + (pl.pair ? 255 : 127)) / (pl.pair ? 256 : 128);
-  pl.tiles_t = tiles_t(pl.BN);
+  pl.tiles_t = used * ((pl.rows + width - 1) / width);
   const int64_t tiles = pl.tiles_w * pl.tiles_t;
-  pl.split = !pl.pair && pl.num_kb > 1 && (pl.BN <= 64 || tiles < 2 * sms);
-  pl.grid = pl.pair ? sms / 2 : sms;
-  if (!groups) pl.grid = static_cast<int>(std::min<int64_t>(pl.grid, pl.split ? tiles * pl.num_kb : tiles));
+  // (units times CTAs fit 32 bits; so many units have enough tiles without a split.  Experts' rows that
+  // fall unevenly make at most one more tile each.)
+  pl.units = (tiles + (groups ? groups * pl.tiles_w : 0)) * pl.num_kb;
+  pl.split = !pl.pair && pl.num_kb > 1 && pl.units < (1ll << 32) / (sms + 1);
+  pl.grid = pl.pair ? pairs : sms;
+  if (pl.split) {
+    // A tile's pieces are added up by one CTA, so that with many of them their sum takes longer
+    // than their K steps: about the square root of the K steps is the best number.
+    int64_t pieces = 2;
+    while ((pieces + 1) * (pieces + 1) <= pl.num_kb) ++pieces;
+    pl.grid = static_cast<int>(std::min<int64_t>(pl.grid, tiles * std::min<int64_t>(pieces, pl.num_kb)));
+  } else if (!groups) {
+    pl.grid = static_cast<int>(std::min<int64_t>(pl.grid, tiles));
+  }
   return pl;
 }
 
-constexpr size_t kCountBytes = 4096;  // the slots' counters, before their sums
+constexpr int64_t kStepMargin = 1024;   // a CTA's step past the last tile
+constexpr size_t kCountBytes = 16384;   // counters of each CTA's epilogue warps, before the slots
 
 size_t plan_workspace(const I8Plan& pl) {
-  return pl.split ? kCountBytes + static_cast<size_t>(pl.grid) * pl.BN * 128 * 4 : 0;
+  return pl.split ? kCountBytes + static_cast<size_t>(pl.grid) * 2 * pl.BN * 128 * 4 : 0;
 }
 
 template <int BN, bool PAIR>
-cudaError_t run_i8(const CUtensorMap& w, const CUtensorMap& x, const I8Args& a, int grid, cudaStream_t st) {
+cudaError_t run_i8(const CUtensorMap& w, const I8TokenMaps& x, const I8Args& a, int grid, cudaStream_t st) {
   using C = I8Cfg<BN, PAIR>;
   auto kern = fp4_i8_kernel<BN, PAIR>;
   static bool attr_done[64] = {false};
@@ -575,11 +701,22 @@ int launch_gemm_i8(const I8Problem& g, unsigned* status, cudaStream_t st, const 
     *why = "workspace too small or misaligned (see fp4_gemm_i8_workspace_size)";
     return 1;
   }
+  if (pl.units / pl.num_kb + kStepMargin > (1ll << 31)) {
+    *why = "too many tiles";
+    return 1;
+  }
   const int64_t rows_w = g.N * std::max(1, g.num_groups);
-  CUtensorMap w, x;
-  if (!make_tensor_map_u8(&w, g.B, static_cast<uint64_t>(g.K), static_cast<uint64_t>(rows_w), 128) ||
-      !make_tensor_map_u8(&x, g.A, static_cast<uint64_t>(g.K), static_cast<uint64_t>(g.M),
-                          static_cast<uint32_t>(pl.pair ? pl.BN / 2 : pl.BN))) {
+  const int64_t width = ((g.M + pl.tiles_t - 1) / pl.tiles_t + 63) / 64 * 64;  // as the kernel has it
+  CUtensorMap w;
+  I8TokenMaps x{};
+  bool ok = make_tensor_map_u8(&w, g.B, static_cast<uint64_t>(g.K), static_cast<uint64_t>(rows_w), 128);
+  for (int i = 0; ok && i < 4; ++i) {
+    // dense pairs have one width, experts' may have any
+    if (pl.pair ? !g.num_groups && width != 64 * (i + 1) : i > 0) continue;
+    ok = make_tensor_map_u8(&x.box[i], g.A, static_cast<uint64_t>(g.K), static_cast<uint64_t>(g.M),
+                            static_cast<uint32_t>(pl.pair ? 32 * (i + 1) : pl.BN));
+  }
+  if (!ok) {
     *why = "cuTensorMapEncodeTiled failed (alignment or driver)";
     return 1;
   }
@@ -594,7 +731,9 @@ int launch_gemm_i8(const I8Problem& g, unsigned* status, cudaStream_t st, const 
   a.num_kb = pl.num_kb;
   a.out = g.D;
   a.out_bf16 = g.out_bf16;
+  a.wide = g.N % 8 == 0 ? 8 : g.N % 2 == 0 ? 2 : 1;
   a.early_w = g.weights_ready && !g.num_groups;
+  a.weights_once = g.num_groups ? pl.rows <= pl.BN : pl.tiles_t == 1;
   a.split = pl.split;
   a.tiles_w = static_cast<int>(pl.tiles_w);
   a.tiles_t = static_cast<int>(pl.tiles_t);
@@ -602,14 +741,13 @@ int launch_gemm_i8(const I8Problem& g, unsigned* status, cudaStream_t st, const 
   a.offsets = g.offsets;
   if (pl.split) {
     a.cnt = static_cast<int*>(g.ws);
-    a.sums = reinterpret_cast<int*>(static_cast<uint8_t*>(g.ws) + kCountBytes);
+    a.sums = reinterpret_cast<int4*>(static_cast<uint8_t*>(g.ws) + kCountBytes);
   }
   a.status = status;
-  switch (pl.pair ? 256 : pl.BN) {
+  switch (pl.BN) {
     case 16: *err = run_i8<16, false>(w, x, a, pl.grid, st); break;
     case 32: *err = run_i8<32, false>(w, x, a, pl.grid, st); break;
     case 64: *err = run_i8<64, false>(w, x, a, pl.grid, st); break;
-    case 128: *err = run_i8<128, false>(w, x, a, pl.grid, st); break;
     default: *err = run_i8<256, true>(w, x, a, pl.grid, st); break;
   }
   return *err == cudaSuccess ? 0 : 2;

@@ -211,18 +211,6 @@ __device__ __forceinline__ void tc_mma_mxf8f6f4(uint32_t d_tmem, uint64_t adesc,
       : "memory");
 }
 
-// D (+)= A * B^T in signed 8-bit integers with 32-bit integer sums, K = 32 per instruction.
-__device__ __forceinline__ void tc_mma_i8(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
-                                          uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n\t"
-      "}\n" ::"r"(d_tmem),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-
 // ------------------------------------------------------------------ CTA pairs
 // A cluster of two CTAs on neighbouring SMs that share one MMA of M = 256 rows: CTA
 // rank 0 (the leader) issues every tcgen05 operation for both; operand tiles, scale
@@ -331,17 +319,6 @@ __device__ __forceinline__ void tc_mma_mxf8f6f4_pair(uint32_t d_tmem, uint64_t a
       : "memory");
 }
 
-__device__ __forceinline__ void tc_mma_i8_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
-                                               uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::2.kind::i8 [%0], %1, %2, %3, p;\n\t"
-      "}\n" ::"r"(d_tmem),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-
 // 32 lanes x 32-bit, 16 consecutive columns per thread.
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile(
@@ -422,12 +399,6 @@ __host__ __device__ __forceinline__ uint32_t mma_idesc_f8(int n, uint32_t a_fmt,
   d |= (static_cast<uint32_t>(m) >> 4) << 24;
   d |= (a_sf_id & 3u) << 29;
   return d;
-}
-
-// Instruction descriptor of the kind::i8 MMA: signed 8-bit A and B (1 in bits 7..9 and 10..12),
-// K-major, 32-bit integer sums (2 in bits 4..5), N / 8, M / 16.
-__host__ __device__ __forceinline__ uint32_t mma_idesc_i8(int n, int m = 128) {
-  return 2u << 4 | 1u << 7 | 1u << 10 | (static_cast<uint32_t>(n) >> 3) << 17 | (static_cast<uint32_t>(m) >> 4) << 24;
 }
 
 }  // namespace fp4
