@@ -20,25 +20,28 @@ namespace fp4 {
 // A counting sort that keeps the slots' order within an expert.  Each warp counts a contiguous
 // segment of slots per expert in its own shared counters; prefix sums over warps and experts turn
 // the counts into first rows; then each warp passes over its segment again and hands out rows in
-// order, 32 slots at a time: equal experts within the 32 find one another by a match, and a slot's
-// place among them is the number of lower lanes.  No atomic decides an order, so the result is the
+// order, 32 slots at a time: equal experts within the 32 find one another by votes on the bits of
+// their numbers (16384 slots in one block: 16.0 us; with the match instruction 18.7), and a slot's place among them is the number of
+// lower lanes.  No atomic decides an order, so the result is the
 // same every time.
 //
-// Up to kSortOneBlock slots one block does it all (one launch).  Beyond, blocks of kSortChunk slots
-// or more first write their histograms to the workspace, and each block of a second launch sums
-// those before it.
+// Up to kSortOneBlock slots one block does it all, up to kSortCluster a cluster of eight whose blocks
+// read one another's counts: one launch.  Beyond, blocks of kSortChunk slots or more first write
+// their counts to the workspace, and each block of a second launch sums those before it.  (Calls back
+// to back: 1000 slots 7.2 us by one block, 5.6 by a cluster; 16384 slots 16.0, 8.4 by a cluster, 11.7
+// by two launches; 131072 slots 19.3 by a cluster, 13.3 by two launches.)
 struct SortArgs {
   const void* ids;
   int64_t slots, chunk;
   int E;
   int blocks;
-  uint32_t* hist;  // [blocks, E], null for one block
+  uint32_t* hist;  // [blocks, E], null for one block or one cluster
   int32_t *offsets, *row_of, *scale_row_of;
 };
 
 constexpr int kSortThreads = 1024;
-constexpr int64_t kSortOneBlock = 16384, kSortChunk = 4096;
-constexpr int kSortMaxBlocks = 128;
+constexpr int64_t kSortOneBlock = 512, kSortCluster = 32768, kSortChunk = 4096;
+constexpr int kSortClusterBlocks = 8, kSortMaxBlocks = 128, kSortKeys = 16;
 
 template <typename ID>
 __device__ __forceinline__ int sort_key(const SortArgs& a, int64_t s, int64_t hi) {
@@ -77,8 +80,23 @@ __global__ void __launch_bounds__(kSortThreads, 1) moe_sort_kernel(const SortArg
   const int64_t seg = ((hi - lo + warps - 1) / warps + 31) / 32 * 32;
   const int64_t from = min(hi, lo + warp * seg), to = min(hi, from + seg);
   uint32_t* mine = s_cnt + warp * E1;
+  // a segment's numbers stay in registers between the two passes, all asked for at once, where it
+  // is that short
+  int key[kSortKeys];
+  const bool kept = seg <= 32 * kSortKeys;
+  if (kept) {
+#pragma unroll
+    for (int i = 0; i < kSortKeys; ++i) key[i] = sort_key<ID>(a, from + 32 * i + lane, to);
+  }
   __syncthreads();
-  for (int64_t s = from + lane; s < to; s += 32) atomicAdd(&mine[sort_key<ID>(a, s, to)], 1u);
+  if (kept) {
+#pragma unroll
+    for (int i = 0; i < kSortKeys; ++i)
+      if (from + 32 * i + lane < to) atomicAdd(&mine[key[i]], 1u);
+  } else {
+    for (int64_t s = from + lane; s < to; s += 32) atomicAdd(&mine[sort_key<ID>(a, s, to)], 1u);
+  }
+  const bool cluster = !a.hist && gridDim.x > 1;
   if (a.hist) {
     // columns of the histograms: neighbouring threads take neighbouring experts, and the blocks
     // are shared out over as many groups of threads as there are
@@ -121,6 +139,23 @@ __global__ void __launch_bounds__(kSortThreads, 1) moe_sort_kernel(const SortArg
       s_before[e] = 0;
     }
   }
+  if (cluster) {
+    cluster_sync_all();
+    for (int e = threadIdx.x; e < E; e += blockDim.x) {
+      uint32_t all = 0, before = 0;
+#pragma unroll
+      for (uint32_t r = 0; r < kSortClusterBlocks; ++r) {
+        uint32_t c;
+        asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(c) : "r"(cluster_addr(smem_u32(s_all + e), r)));
+        all += c;
+        if (r < blockIdx.x) before += c;
+      }
+      s_sfirst[e] = all;
+      s_before[e] = before;
+    }
+    cluster_sync_all();  // the counts have been read: they may change, and this block may end
+    for (int e = threadIdx.x; e < E; e += blockDim.x) s_all[e] = s_sfirst[e];
+  }
   __syncthreads();
   if (warp == 0) {  // first rows: prefix sums over the experts
     uint32_t rows = 0, blocks = 0;
@@ -148,18 +183,29 @@ __global__ void __launch_bounds__(kSortThreads, 1) moe_sort_kernel(const SortArg
     if (lane == 0 && blockIdx.x == 0) a.offsets[E] = static_cast<int32_t>(rows);
   }
   __syncthreads();
-  for (int64_t s0 = from; s0 < to; s0 += 32) {
-    const int64_t s = s0 + lane;
-    const int key = sort_key<ID>(a, s, to);
-    const unsigned same = __match_any_sync(0xFFFFFFFFu, key);
-    const uint32_t at = mine[key], lower = __popc(same & ((1u << lane) - 1));
+  const int bits = 32 - __clz(E);  // of the numbers up to E
+  auto place = [&](int64_t s, int k) {
+    unsigned same = 0xFFFFFFFFu;  // lanes with this expert: a vote on each bit of its number
+    for (int b = 0; b < bits; ++b) {
+      const bool one = k >> b & 1;
+      const unsigned ones = __ballot_sync(0xFFFFFFFFu, one);
+      same &= one ? ones : ~ones;
+    }
+    const uint32_t at = mine[k], lower = __popc(same & ((1u << lane) - 1));
     __syncwarp();
-    if (lower == 0) mine[key] = at + __popc(same);
+    if (lower == 0) mine[k] = at + __popc(same);
     __syncwarp();
     if (s < to) {
-      a.row_of[s] = key < E ? static_cast<int32_t>(s_all[key] + at + lower) : -1;
-      if (a.scale_row_of) a.scale_row_of[s] = key < E ? static_cast<int32_t>(s_sfirst[key] + at + lower) : -1;
+      a.row_of[s] = k < E ? static_cast<int32_t>(s_all[k] + at + lower) : -1;
+      if (a.scale_row_of) a.scale_row_of[s] = k < E ? static_cast<int32_t>(s_sfirst[k] + at + lower) : -1;
     }
+  };
+  if (kept) {
+#pragma unroll
+    for (int i = 0; i < kSortKeys; ++i)
+      if (from + 32 * i < to) place(from + 32 * i + lane, key[i]);  // (the same for the whole warp)
+  } else {
+    for (int64_t s0 = from; s0 < to; s0 += 32) place(s0 + lane, sort_key<ID>(a, s0 + lane, to));
   }
 }
 
@@ -168,6 +214,10 @@ static int sort_blocks(int64_t slots, int64_t* chunk) {
     *chunk = slots;
     return 1;
   }
+  if (slots <= kSortCluster) {
+    *chunk = (slots + kSortClusterBlocks - 1) / kSortClusterBlocks;
+    return kSortClusterBlocks;
+  }
   *chunk = std::max(kSortChunk, (slots + kSortMaxBlocks - 1) / kSortMaxBlocks);
   return static_cast<int>((slots + *chunk - 1) / *chunk);
 }
@@ -175,7 +225,7 @@ static int sort_blocks(int64_t slots, int64_t* chunk) {
 size_t moe_sort_workspace_bytes(int64_t slots, int E) {
   int64_t chunk;
   const int blocks = sort_blocks(slots, &chunk);
-  return blocks == 1 ? 0 : static_cast<size_t>(blocks) * E * sizeof(uint32_t);
+  return slots <= kSortCluster ? 0 : static_cast<size_t>(blocks) * E * sizeof(uint32_t);
 }
 
 template <typename ID>
@@ -194,7 +244,7 @@ static cudaError_t sort_typed(const SortArgs& a, cudaStream_t st) {
     e = launch_rows(moe_hist_kernel<ID>, dim3(a.blocks), kSortThreads, static_cast<size_t>(a.E + 1) * 4, st, a);
     if (e != cudaSuccess) return e;
   }
-  return launch_rows(kern, dim3(a.blocks), threads, smem, st, a);
+  return launch_rows_cluster(kern, dim3(a.blocks), threads, smem, st, a.hist ? 1 : a.blocks, a);
 }
 
 cudaError_t launch_moe_sort(const void* ids, int id_bytes, int64_t slots, int E, int32_t* offsets, int32_t* row_of,
@@ -204,7 +254,7 @@ cudaError_t launch_moe_sort(const void* ids, int id_bytes, int64_t slots, int E,
   a.slots = slots;
   a.E = E;
   a.blocks = sort_blocks(slots, &a.chunk);
-  a.hist = a.blocks > 1 ? static_cast<uint32_t*>(ws) : nullptr;
+  a.hist = slots > kSortCluster ? static_cast<uint32_t*>(ws) : nullptr;
   a.offsets = offsets;
   a.row_of = row_of;
   a.scale_row_of = scale_row_of;
@@ -241,27 +291,31 @@ static int row_threads(int64_t words, int per, int most) {
   return static_cast<int>(std::min<int64_t>(most, std::max<int64_t>(32, ((words + per - 1) / per + 31) / 32 * 32)));
 }
 
-constexpr int kCopyWords = 4, kCopyThreads = 256;
+// Words of a thread: 64 bytes of the input where it moves 16 at once, else eight.
+template <int V>
+__host__ __device__ constexpr int copy_words() { return V >= 4 ? 4 : 8; }
+constexpr int kCopyThreads = 256;
 
-// y[row_of[t, j]] = x[t]: a block copies kCopyWords words a thread of one token's row to its
-// topk places.
+// y[row_of[t, j]] = x[t]: a block copies copy_words() words a thread of one token's row to
+// its topk places.
 template <typename T, int V>
 __global__ void __launch_bounds__(kCopyThreads) moe_dispatch_kernel(const DispatchProblem p) {
+  constexpr int W = copy_words<V>();
   rows_wait_prior();
   rows_allow_dependents();
   const int64_t t = blockIdx.x, words = p.cols / V;
-  const int64_t w0 = static_cast<int64_t>(blockIdx.y) * blockDim.x * kCopyWords + threadIdx.x;
+  const int64_t w0 = static_cast<int64_t>(blockIdx.y) * blockDim.x * W + threadIdx.x;
   const T* x = static_cast<const T*>(p.x) + t * p.cols;
   const int32_t* rows = p.row_of + t * p.topk;
-  RowVec<T, V> in[kCopyWords];
+  RowVec<T, V> in[W];
 #pragma unroll
-  for (int i = 0; i < kCopyWords; ++i)
+  for (int i = 0; i < W; ++i)
     if (w0 + i * blockDim.x < words) in[i].load(x + (w0 + i * blockDim.x) * V);
   for (int j = 0; j < p.topk; ++j) {
     const int32_t row = __ldg(rows + j);
     if (row < 0) continue;
 #pragma unroll
-    for (int i = 0; i < kCopyWords; ++i) {
+    for (int i = 0; i < W; ++i) {
       if (w0 + i * blockDim.x >= words) continue;
       const int64_t at = row * p.cols + (w0 + i * blockDim.x) * V;
       if (p.y_bf16 == (sizeof(T) == 2)) {  // one type: the same bits, those of a NaN too
@@ -278,8 +332,8 @@ __global__ void __launch_bounds__(kCopyThreads) moe_dispatch_kernel(const Dispat
 cudaError_t launch_moe_dispatch(const DispatchProblem& p, cudaStream_t st) {
   const int v = row_width(p.cols, p.bf16);
   const int64_t words = p.cols / v;
-  const int threads = row_threads(words, kCopyWords, kCopyThreads);
-  const int64_t per = static_cast<int64_t>(threads) * kCopyWords;
+  const int each = v >= 4 ? 4 : 8, threads = row_threads(words, each, kCopyThreads);
+  const int64_t per = static_cast<int64_t>(threads) * each;
   const dim3 grid(static_cast<unsigned>(p.tokens), static_cast<unsigned>((words + per - 1) / per));
   return with_rows(p.bf16, v, [&](auto t, auto n) {
     return launch_rows(moe_dispatch_kernel<decltype(t), decltype(n)::value>, grid, threads, 0, st, p);
@@ -287,8 +341,8 @@ cudaError_t launch_moe_dispatch(const DispatchProblem& p, cudaStream_t st) {
 }
 
 // ------------------------------------------------------------------- dispatch to FP4 codes
-// A token's row is encoded once; its codes go to row row_of[t, j], its scales to row
-// scale_row_of[t, j] of the grouped layout.  Blocks behind the tokens' write the layout's pads:
+// A token's row is encoded once, a block a thread; its codes go to row row_of[t, j], its scales to
+// row scale_row_of[t, j] of the grouped layout.  Blocks behind the tokens' write the layout's pads:
 // num_experts blocks the rows behind each expert's last, then one block per 128-row block of the
 // buffer, which clears it if it lies behind the last expert's.
 constexpr int kCodeThreads = 256;
@@ -301,7 +355,7 @@ __device__ __forceinline__ void clear_scale_rows(uint8_t* scales, int64_t atoms,
   }
 }
 
-template <typename T, int V, int FMT>
+template <typename T, int FMT>
 __global__ void __launch_bounds__(kCodeThreads) moe_dispatch_codes_kernel(const DispatchCodesProblem p, unsigned* status) {
   constexpr int BLOCK = FMT == kCodesMx ? 32 : 16;
   rows_wait_prior();
@@ -328,34 +382,38 @@ __global__ void __launch_bounds__(kCodeThreads) moe_dispatch_codes_kernel(const 
     return;
   }
   const float g = FMT == kCodesNv ? __ldg(p.q.g) : 1.0f;
+  constexpr int V = 16 / sizeof(T), CH = BLOCK / V;  // 16-byte words of a block
   const T* x = static_cast<const T*>(p.x) + t * p.cols;
-  const int64_t words = p.cols / V;
   bool bad = false;
-  for (int64_t w0 = 0; w0 < words; w0 += blockDim.x) {  // whole warps: the block maxima need every lane
-    const int64_t w = w0 + threadIdx.x, col = w * V;
-    const bool ok = w < words;
-    RowVec<T, V> in;
-    in.zero();
-    if (ok) in.load(x + col);
-    float v[V];
-    in.unpack(v);
-    uint32_t sb;
-    const uint32_t packed = encode_vec<FMT, V>(g, v, sb, bad);
-    if (!ok) continue;
-    const int64_t k = col / BLOCK;
+  for (int64_t k0 = 0; k0 < atoms * 4; k0 += blockDim.x) {  // whole warps: neighbours share a scale word
+    const int64_t k = k0 + threadIdx.x;
+    const bool ok = k < blocks_k;
+    RowVec<T, V> in[CH];
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      in[c].zero();
+      if (ok) in[c].load(x + k * BLOCK + c * V);
+    }
+    float v[BLOCK];
+#pragma unroll
+    for (int c = 0; c < CH; ++c) in[c].unpack(*reinterpret_cast<float(*)[V]>(v + c * V));
+    uint32_t packed[BLOCK / 8], sb;
+    encode_block<FMT, BLOCK>(g, v, packed, sb, bad);
+    // the scales of four blocks, the row's pad columns (0) among them, are one word of an atom
+    uint32_t word = (ok ? sb : 0u) << (8 * (k & 3));
+    word |= __shfl_xor_sync(0xFFFFFFFFu, word, 1);
+    word |= __shfl_xor_sync(0xFFFFFFFFu, word, 2);
     for (int j = 0; j < p.topk; ++j) {
       const int64_t s = t * p.topk + j;
       const int32_t row = __ldg(p.row_of + s);
       if (row < 0) continue;
-      store_codes<V>(p.q.codes + row * (p.cols / 2) + col / 2, packed);
-      if (col % BLOCK == 0) p.q.scales[scale_at(__ldg(p.scale_row_of + s), k, atoms)] = static_cast<uint8_t>(sb);
-    }
-  }
-  if (blocks_k % 4) {  // the row's pad columns
-    const int pad = 4 - static_cast<int>(blocks_k % 4);
-    for (int i = threadIdx.x; i < pad * p.topk; i += blockDim.x) {
-      const int64_t s = t * p.topk + i / pad;
-      if (p.row_of[s] >= 0) p.q.scales[scale_at(p.scale_row_of[s], blocks_k + i % pad, atoms)] = 0;
+      if (ok) {
+        uint8_t* dst = p.q.codes + row * (p.cols / 2) + k * (BLOCK / 2);
+        if constexpr (BLOCK == 32) *reinterpret_cast<uint4*>(dst) = make_uint4(packed[0], packed[1], packed[2], packed[3]);
+        else *reinterpret_cast<uint2*>(dst) = make_uint2(packed[0], packed[1]);
+      }
+      if ((k & 3) == 0 && k < atoms * 4)
+        *reinterpret_cast<uint32_t*>(p.q.scales + scale_at(__ldg(p.scale_row_of + s), k, atoms)) = word;
     }
   }
   if (bad) atomicOr(status, kStatusNonFinite);
@@ -364,13 +422,13 @@ __global__ void __launch_bounds__(kCodeThreads) moe_dispatch_codes_kernel(const 
 cudaError_t launch_moe_dispatch_codes(const DispatchCodesProblem& p, unsigned* status, cudaStream_t st) {
   const int64_t pads = p.num_experts + (p.tokens * p.topk + 127) / 128 + p.num_experts;
   const dim3 grid(static_cast<unsigned>(p.tokens + pads));
-  const int threads = row_threads(p.cols / (p.bf16 ? 8 : 4), 1, kCodeThreads);
-  if (p.bf16)
-    return p.q.fmt == kCodesMx
-               ? launch_rows(moe_dispatch_codes_kernel<__nv_bfloat16, 8, kCodesMx>, grid, threads, 0, st, p, status)
-               : launch_rows(moe_dispatch_codes_kernel<__nv_bfloat16, 8, kCodesNv>, grid, threads, 0, st, p, status);
-  return p.q.fmt == kCodesMx ? launch_rows(moe_dispatch_codes_kernel<float, 4, kCodesMx>, grid, threads, 0, st, p, status)
-                             : launch_rows(moe_dispatch_codes_kernel<float, 4, kCodesNv>, grid, threads, 0, st, p, status);
+  const int threads = row_threads((p.cols / (p.q.fmt == kCodesMx ? 32 : 16) + 3) / 4 * 4, 1, kCodeThreads);
+  using BF = __nv_bfloat16;
+  if (p.q.fmt == kCodesMx)
+    return p.bf16 ? launch_rows(moe_dispatch_codes_kernel<BF, kCodesMx>, grid, threads, 0, st, p, status)
+                  : launch_rows(moe_dispatch_codes_kernel<float, kCodesMx>, grid, threads, 0, st, p, status);
+  return p.bf16 ? launch_rows(moe_dispatch_codes_kernel<BF, kCodesNv>, grid, threads, 0, st, p, status)
+                : launch_rows(moe_dispatch_codes_kernel<float, kCodesNv>, grid, threads, 0, st, p, status);
 }
 
 // -------------------------------------------------------------------------------- 8-bit rows
@@ -466,36 +524,41 @@ cudaError_t launch_quantize_i8(const I8RowsProblem& p, unsigned* status, cudaStr
 
 // ----------------------------------------------------------------------------------- combine
 // out[t] = sum_j w[t, j] y[row_of[t, j]] + res[t], the sum in FP32 in the order of j, rounded once.
-constexpr int kSumWords = 2, kSumThreads = 256, kSumRows = 4;
+// R rows' words (2 for up to two choices, else 4) are asked for before the first is needed, so many of
+// each that about 128 bytes a thread are under way; four blocks an SM (8192 tokens, 4 choices, 2880
+// BF16 columns: 38.0 us, 41.4 with the three that the registers would allow).
+template <int V, int R>
+__host__ __device__ constexpr int sum_words() { return V >= 4 ? 8 / R : V == 2 ? 16 / R : 6; }
+constexpr int kSumThreads = 256;
 
-template <typename T, int V>
-__global__ void __launch_bounds__(kSumThreads) moe_combine_kernel(const CombineProblem p) {
+template <typename T, int V, int R>
+__global__ void __launch_bounds__(kSumThreads, 4) moe_combine_kernel(const CombineProblem p) {
+  constexpr int W = sum_words<V, R>();
   rows_wait_prior();
   rows_allow_dependents();
   const int64_t t = blockIdx.x, words = p.cols / V;
-  const int64_t w0 = static_cast<int64_t>(blockIdx.y) * blockDim.x * kSumWords + threadIdx.x;
+  const int64_t w0 = static_cast<int64_t>(blockIdx.y) * blockDim.x * W + threadIdx.x;
   const T* y = static_cast<const T*>(p.y);
-  float sum[kSumWords][V] = {};
-  for (int j0 = 0; j0 < p.topk; j0 += kSumRows) {
-    // kSumRows rows' words are asked for before the first is needed
-    RowVec<T, V> in[kSumRows][kSumWords];
-    float weight[kSumRows];
-    bool on[kSumRows];
+  float sum[W][V] = {};
+  for (int j0 = 0; j0 < p.topk; j0 += R) {
+    RowVec<T, V> in[R][W];
+    float weight[R];
+    bool on[R];
 #pragma unroll
-    for (int j = 0; j < kSumRows; ++j) {
+    for (int j = 0; j < R; ++j) {
       const int64_t s = t * p.topk + j0 + j;
       const int32_t row = j0 + j < p.topk ? __ldg(p.row_of + s) : -1;
       on[j] = row >= 0;
       weight[j] = on[j] && p.weights ? __ldg(p.weights + s) : 1.0f;
 #pragma unroll
-      for (int i = 0; i < kSumWords; ++i)
+      for (int i = 0; i < W; ++i)
         if (on[j] && w0 + i * blockDim.x < words) in[j][i].load(y + row * p.cols + (w0 + i * blockDim.x) * V);
     }
 #pragma unroll
-    for (int j = 0; j < kSumRows; ++j) {
+    for (int j = 0; j < R; ++j) {
       if (!on[j]) continue;
 #pragma unroll
-      for (int i = 0; i < kSumWords; ++i) {
+      for (int i = 0; i < W; ++i) {
         float v[V];
         in[j][i].unpack(v);
 #pragma unroll
@@ -504,7 +567,7 @@ __global__ void __launch_bounds__(kSumThreads) moe_combine_kernel(const CombineP
     }
   }
 #pragma unroll
-  for (int i = 0; i < kSumWords; ++i) {
+  for (int i = 0; i < W; ++i) {
     if (w0 + i * blockDim.x >= words) continue;
     const int64_t at = t * p.cols + (w0 + i * blockDim.x) * V;
     if (p.res) {
@@ -517,89 +580,104 @@ __global__ void __launch_bounds__(kSumThreads) moe_combine_kernel(const CombineP
   }
 }
 
-cudaError_t launch_moe_combine(const CombineProblem& p, cudaStream_t st) {
+template <int R>
+static cudaError_t combine_rows(const CombineProblem& p, cudaStream_t st) {
   const int v = row_width(p.cols, p.bf16);
   const int64_t words = p.cols / v;
-  const int threads = row_threads(words, kSumWords, kSumThreads);
-  const int64_t per = static_cast<int64_t>(threads) * kSumWords;
+  const int each = v >= 4 ? 8 / R : v == 2 ? 16 / R : 6, threads = row_threads(words, each, kSumThreads);
+  const int64_t per = static_cast<int64_t>(threads) * each;
   const dim3 grid(static_cast<unsigned>(p.tokens), static_cast<unsigned>((words + per - 1) / per));
   return with_rows(p.bf16, v, [&](auto t, auto n) {
-    return launch_rows(moe_combine_kernel<decltype(t), decltype(n)::value>, grid, threads, 0, st, p);
+    return launch_rows(moe_combine_kernel<decltype(t), decltype(n)::value, R>, grid, threads, 0, st, p);
   });
+}
+
+cudaError_t launch_moe_combine(const CombineProblem& p, cudaStream_t st) {
+  return p.topk <= 2 && row_width(p.cols, p.bf16) >= 4 ? combine_rows<2>(p, st) : combine_rows<4>(p, st);
 }
 
 // ------------------------------------------------------------------------- its backward pass
 // dy[row_of[t, j]] = w[t, j] dout[t], dw[t, j] = <dout[t], y[row_of[t, j]]>: a block per token, so
 // that dout is read once and each dot product is summed in one place, in a fixed order.
-constexpr int kGradRows = 8, kGradThreads = 256;
+// Rows are taken R at a time (as many as there are choices, up to 8), and all their words of a column
+// are asked for before the first is needed; with R fixed at 8 and word after word it took 210 us
+// where it takes 70 (8192 tokens, 4 choices, 2880 BF16 columns).
+constexpr int kGradThreads = 256;
 
-template <typename T, int V>
-__global__ void __launch_bounds__(kGradThreads) moe_combine_grad_kernel(const CombineGradProblem p) {
-  __shared__ float s_dot[kGradThreads / 32][kGradRows];
+template <typename T, int V, int R>
+__global__ void __launch_bounds__(kGradThreads, R == 8 ? 3 : 4) moe_combine_grad_kernel(const CombineGradProblem p) {
+  __shared__ float s_dot[kGradThreads / 32][R];
   rows_wait_prior();
   rows_allow_dependents();
-  const int64_t t = blockIdx.x, words = p.cols / V;
+  const int64_t t = blockIdx.x;
+  const int words = static_cast<int>(p.cols / V);
   const T* dout = static_cast<const T*>(p.dout) + t * p.cols;
   const T* y = static_cast<const T*>(p.y);
-  for (int j0 = 0; j0 < p.topk; j0 += kGradRows) {
-    int32_t row[kGradRows];
-    float weight[kGradRows], dot[kGradRows];
+  const bool dots = p.dweights != nullptr;
+  for (int j0 = 0; j0 < p.topk; j0 += R) {
+    int32_t row[R];
+    float weight[R], dot[R];
 #pragma unroll
-    for (int j = 0; j < kGradRows; ++j) {
+    for (int j = 0; j < R; ++j) {
       const int64_t s = t * p.topk + j0 + j;
       row[j] = j0 + j < p.topk ? __ldg(p.row_of + s) : -1;
       weight[j] = row[j] >= 0 && p.weights ? __ldg(p.weights + s) : 1.0f;
       dot[j] = 0.0f;
     }
-    for (int64_t w = threadIdx.x; w < words; w += blockDim.x) {
-      RowVec<T, V> in;
+    for (int w = threadIdx.x; w < words; w += blockDim.x) {
+      RowVec<T, V> in, yr[R];
       in.load(dout + w * V);
+#pragma unroll
+      for (int j = 0; j < R; ++j) {
+        yr[j].zero();
+        if (dots && row[j] >= 0) yr[j].load(y + row[j] * p.cols + w * V);
+      }
       float d[V];
       in.unpack(d);
 #pragma unroll
-      for (int j = 0; j < kGradRows; ++j) {
-        if (row[j] < 0) continue;
-        const int64_t at = row[j] * p.cols + w * V;
-        if (p.dweights) {
-          RowVec<T, V> yr;
-          yr.load(y + at);
-          float v[V];
-          yr.unpack(v);
+      for (int j = 0; j < R; ++j) {
+        float v[V];
+        yr[j].unpack(v);
 #pragma unroll
-          for (int k = 0; k < V; ++k) dot[j] = fmaf(d[k], v[k], dot[j]);
-        }
-        if (p.dy) {
-          float o[V];
+        for (int k = 0; k < V; ++k) dot[j] = fmaf(d[k], v[k], dot[j]);
+        if (!p.dy || row[j] < 0) continue;
 #pragma unroll
-          for (int k = 0; k < V; ++k) o[k] = weight[j] * d[k];
-          store_row_vec<V>(p.dy, p.dy_bf16, at, o);
-        }
+        for (int k = 0; k < V; ++k) v[k] = weight[j] * d[k];
+        store_row_vec<V>(p.dy, p.dy_bf16, row[j] * p.cols + w * V, v);
       }
     }
-    if (p.dweights) {
+    if (dots) {
 #pragma unroll
-      for (int j = 0; j < kGradRows; ++j) {
+      for (int j = 0; j < R; ++j) {
         const float v = warp_sum(dot[j]);
         if (threadIdx.x % 32 == 0) s_dot[threadIdx.x / 32][j] = v;
       }
       __syncthreads();
-      if (threadIdx.x < kGradRows && j0 + static_cast<int>(threadIdx.x) < p.topk) {
+      if (threadIdx.x < R && j0 + static_cast<int>(threadIdx.x) < p.topk) {
+        // (a slot without an expert: 0, not 0 times what dout may hold)
         float v = 0.0f;
         for (int w = 0; w < static_cast<int>(blockDim.x / 32); ++w) v += s_dot[w][threadIdx.x];
-        p.dweights[t * p.topk + j0 + threadIdx.x] = v;
+        const int64_t s = t * p.topk + j0 + threadIdx.x;
+        p.dweights[s] = __ldg(p.row_of + s) >= 0 ? v : 0.0f;
       }
       __syncthreads();
     }
   }
 }
 
-cudaError_t launch_moe_combine_grad(const CombineGradProblem& p, cudaStream_t st) {
+template <int R>
+static cudaError_t combine_grad_rows(const CombineGradProblem& p, cudaStream_t st) {
   const int v = row_width(p.cols, p.bf16);
-  const int threads = row_threads(p.cols / v, 2, kGradThreads);
+  const int threads = row_threads(p.cols / v, v >= 4 ? 2 : 4, kGradThreads);
   const dim3 grid(static_cast<unsigned>(p.tokens));
   return with_rows(p.bf16, v, [&](auto t, auto n) {
-    return launch_rows(moe_combine_grad_kernel<decltype(t), decltype(n)::value>, grid, threads, 0, st, p);
+    return launch_rows(moe_combine_grad_kernel<decltype(t), decltype(n)::value, R>, grid, threads, 0, st, p);
   });
+}
+
+cudaError_t launch_moe_combine_grad(const CombineGradProblem& p, cudaStream_t st) {
+  if (p.topk <= 2) return combine_grad_rows<2>(p, st);
+  return p.topk <= 4 ? combine_grad_rows<4>(p, st) : combine_grad_rows<8>(p, st);
 }
 
 }  // namespace fp4

@@ -190,6 +190,17 @@ __device__ __forceinline__ int64_t scale_at(int64_t row, int64_t k, int64_t atom
   return ((row / 128) * atoms + k / 4) * 512 + (row % 32) * 16 + ((row % 128) / 32) * 4 + k % 4;
 }
 
+// Scale byte of a block whose largest magnitude has the bits m, and the elements' multiplier.
+template <int FMT>
+__device__ __forceinline__ float block_scale(uint32_t m, float g, uint32_t& sb) {
+  if constexpr (FMT == kCodesMx) {
+    sb = e8m0_code(__fdiv_rn(__uint_as_float(m), 6.0f));
+    return e8m0_inverse(sb);
+  } else {
+    return nvfp4_block_scale(__uint_as_float(m), g, sb);
+  }
+}
+
 template <int V>
 __device__ __forceinline__ void store_codes(uint8_t* dst, uint32_t packed) {
   if constexpr (V == 8) *reinterpret_cast<uint32_t*>(dst) = packed;
@@ -209,19 +220,31 @@ __device__ __forceinline__ uint32_t encode_vec(float g, const float (&v)[V], uin
   for (int i = 0; i < V; ++i) m = max(m, abs_bits_of(v[i]));
 #pragma unroll
   for (int d = 1; d < BLOCK / V; d <<= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
-  float mul;
-  if constexpr (FMT == kCodesMx) {
-    sb = e8m0_code(__fdiv_rn(__uint_as_float(m), 6.0f));
-    mul = e8m0_inverse(sb);
-  } else {
-    mul = nvfp4_block_scale(__uint_as_float(m), g, sb);
-  }
+  const float mul = block_scale<FMT>(m, g, sb);
   float s[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) s[i] = v[i] == 0.0f ? v[i] : __fmul_rn(v[i], mul);  // 1/denom may have overflowed
   bad |= m >= 0x7F800000u;
   if constexpr (V == 8) return pack8<kE2M1Hardware>(s);
   else return pack4<kE2M1Hardware>(s);
+}
+
+// The same for a whole block (16 NVFP4 or 32 MXFP4 values) in one thread.
+template <int FMT, int BLOCK>
+__device__ __forceinline__ void encode_block(float g, const float (&v)[BLOCK], uint32_t (&packed)[BLOCK / 8], uint32_t& sb,
+                                             bool& bad) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < BLOCK; ++i) m = max(m, abs_bits_of(v[i]));
+  const float mul = block_scale<FMT>(m, g, sb);
+  bad |= m >= 0x7F800000u;
+#pragma unroll
+  for (int c = 0; c < BLOCK / 8; ++c) {
+    float s[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s[i] = v[8 * c + i] == 0.0f ? v[8 * c + i] : __fmul_rn(v[8 * c + i], mul);
+    packed[c] = pack8<kE2M1Hardware>(s);
+  }
 }
 
 // encode_vec of columns [col, col + V) of row `row`, stored; `ok` says whether the lane's columns
@@ -241,19 +264,29 @@ __device__ __forceinline__ bool encode_row_vec(const RowCodes& c, float g, int64
 }
 
 template <typename... KArgs, typename... Args>
-static cudaError_t launch_rows(void (*kern)(KArgs...), dim3 grid, int threads, size_t smem, cudaStream_t st,
-                               Args... args) {
+static cudaError_t launch_rows_cluster(void (*kern)(KArgs...), dim3 grid, int threads, size_t smem, cudaStream_t st,
+                                       int cluster, Args... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kern, static_cast<KArgs>(args)...);
+}
+
+template <typename... KArgs, typename... Args>
+static cudaError_t launch_rows(void (*kern)(KArgs...), dim3 grid, int threads, size_t smem, cudaStream_t st,
+                               Args... args) {
+  return launch_rows_cluster(kern, grid, threads, smem, st, 1, args...);
 }
 
 }  // namespace fp4

@@ -480,7 +480,7 @@ fp4_status fp4_gemm_grouped(fp4_fmt fmt, int num_groups, const int32_t* offsets_
  *   scale_row_of_dev  [tokens, topk] int32 or NULL: its row in the grouped scale layout (each
  *           expert's rows start a 128-row block), or -1.
  * num_experts <= 1024.  workspace: fp4_moe_sort_workspace_size(tokens, topk, num_experts) bytes
- * (0 up to 16384 slots), 4-byte aligned, any contents, not shared by calls that overlap. */
+ * (0 up to 32768 slots), 4-byte aligned, any contents, not shared by calls that overlap. */
 size_t fp4_moe_sort_workspace_size(int64_t tokens, int topk, int num_experts);
 fp4_status fp4_moe_sort(const void* ids_dev, int id_bytes, int64_t tokens, int topk, int num_experts,
                         int32_t* offsets_dev, int32_t* row_of_dev, int32_t* scale_row_of_dev, void* workspace_dev,

@@ -27,7 +27,8 @@ def _sort(ids, experts):
 
 @pytest.mark.parametrize("tokens,topk,experts", [
     (1, 1, 1), (1, 8, 8), (3, 2, 5), (16, 4, 32), (33, 3, 7), (31, 1, 1024), (128, 8, 129), (2048, 8, 256), (4096, 4, 32),
-    (4097, 4, 33), (5000, 5, 1), (1999, 8, 1024), (16385, 1, 31), (20000, 8, 200), (131072, 8, 64), (150001, 4, 1024)])
+    (4097, 4, 33), (5000, 5, 1), (1999, 8, 1024), (16385, 1, 31), (20000, 8, 200), (131072, 8, 64), (150001, 4, 1024),
+    (512, 1, 32), (513, 1, 3), (8192, 4, 1024), (32769, 1, 16), (600000, 1, 5)])
 @pytest.mark.parametrize("drop", [0.0, 0.3])
 def test_sort(tokens, topk, experts, drop):
     ids = router_ids(tokens, topk, experts, tokens + experts, drop, torch.int64 if tokens % 2 else torch.int32)

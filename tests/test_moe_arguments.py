@@ -33,8 +33,8 @@ def test_sort_refuses(kw):
 def test_sort_sizes():
     assert _call("fp4_moe_sort", SORT, tokens=1 << 30) == fp4.ERR_UNSUPPORTED
     assert _call("fp4_moe_sort", SORT, topk=1025) == fp4.ERR_UNSUPPORTED
-    assert fp4.fp4_moe_sort_workspace_size(4096, 4, 32) == 0
-    assert 0 < fp4.fp4_moe_sort_workspace_size(4097, 4, 32) <= 128 * 32 * 4
+    assert fp4.fp4_moe_sort_workspace_size(8192, 4, 32) == 0
+    assert 0 < fp4.fp4_moe_sort_workspace_size(8193, 4, 32) <= 128 * 32 * 4
     assert fp4.fp4_moe_sort_workspace_size(1 << 27, 8, 1024) == 128 * 1024 * 4
     assert fp4.fp4_moe_sort_workspace_size(0, 4, 32) == 0
 
