@@ -262,28 +262,60 @@ cudaError_t launch_moe_sort(const void* ids, int id_bytes, int64_t slots, int E,
 }
 
 // --------------------------------------------------------------------------------- dispatch
-// Words of 16 bytes of the input (V = 8 BF16 or 4 FP32) where its rows start at 16 bytes, pairs for
-// even widths, else single elements.  (A matrix of the other type then moves 8 or 32 bytes at once,
-// which its rows' starts allow.)
-static int row_width(int64_t cols, int bf16) {
+// How rows are moved.  Words of 16 bytes of the input (V = 8 BF16 or 4 FP32) where all rows start at
+// 16 bytes (a matrix of the other type then moves 8 or 32 bytes at once, which its rows' starts
+// allow).  Other widths: the words of the matrix that is written (for the gradient, also of the one
+// that it shares rows with) still stand at 16 bytes, from some element of the row on, and the values
+// for them come from the two words of the other matrix that hold them (RowVec::load_any); the
+// elements before and behind go one by one.  Narrow rows go one by one altogether.
+enum { kByElement = 0, kByWord = 1, kByShift = 2 };
+
+static int row_way(int64_t cols, int bf16) {
   const int v = bf16 ? 8 : 4;
-  return cols % v == 0 ? v : cols % 2 == 0 ? 2 : 1;
+  return cols % v == 0 ? kByWord : cols >= 64 ? kByShift : kByElement;
 }
 
-template <int V>
-struct WordSize {
-  static constexpr int value = V;
+template <typename T, int WAY>
+__host__ __device__ constexpr int word_size() { return WAY == kByElement ? 1 : 16 / static_cast<int>(sizeof(T)); }
+
+// A row's words by its offset in the matrix: word i holds elements [first + V i, first + V (i + 1)).
+// kByShift leaves out a word more than it has to on either side, so that the words of another row
+// around the same elements, and around those behind the last word, lie within that row.
+template <int V, int WAY>
+struct RowSpan {
+  int first, words, cols;
+  __device__ __forceinline__ RowSpan(int64_t at, int64_t columns) : cols(static_cast<int>(columns)) {
+    if constexpr (WAY == kByShift) {
+      first = (static_cast<int>(-at) & (V - 1)) + V;
+      words = max(0, (cols - first) / V - 1);
+    } else {
+      first = 0;
+      words = cols / V;
+    }
+  }
+  __device__ __forceinline__ int singles() const { return cols - words * V; }  // kByShift: at most 4 V - 2
+  __device__ __forceinline__ int single(int i) const { return i < first ? i : i + words * V; }
+};
+
+// A row over several blocks of `per` words.
+static dim3 row_grid(int64_t tokens, int64_t words, int64_t per) {
+  return dim3(static_cast<unsigned>(tokens), static_cast<unsigned>((words + per - 1) / per));
+}
+
+template <int WAY>
+struct WayTag {
+  static constexpr int value = WAY;
 };
 template <typename F>
-static cudaError_t with_rows(int bf16, int v, F&& f) {
+static cudaError_t with_rows(int bf16, int way, F&& f) {
   if (bf16) {
-    if (v == 8) return f(__nv_bfloat16{}, WordSize<8>{});
-    if (v == 2) return f(__nv_bfloat16{}, WordSize<2>{});
-    return f(__nv_bfloat16{}, WordSize<1>{});
+    if (way == kByWord) return f(__nv_bfloat16{}, WayTag<kByWord>{});
+    if (way == kByShift) return f(__nv_bfloat16{}, WayTag<kByShift>{});
+    return f(__nv_bfloat16{}, WayTag<kByElement>{});
   }
-  if (v == 4) return f(float{}, WordSize<4>{});
-  if (v == 2) return f(float{}, WordSize<2>{});
-  return f(float{}, WordSize<1>{});
+  if (way == kByWord) return f(float{}, WayTag<kByWord>{});
+  if (way == kByShift) return f(float{}, WayTag<kByShift>{});
+  return f(float{}, WayTag<kByElement>{});
 }
 
 // Threads that take `per` words each of a row's `words`.
@@ -291,51 +323,66 @@ static int row_threads(int64_t words, int per, int most) {
   return static_cast<int>(std::min<int64_t>(most, std::max<int64_t>(32, ((words + per - 1) / per + 31) / 32 * 32)));
 }
 
-// Words of a thread: 64 bytes of the input where it moves 16 at once, else eight.
-template <int V>
-__host__ __device__ constexpr int copy_words() { return V >= 4 ? 4 : 8; }
-constexpr int kCopyThreads = 256;
+// y[row_of[t, j]] = x[t]: a block copies kCopyWords words a thread of one token's row to its topk
+// places.
+constexpr int kCopyWords = 4, kCopyThreads = 256;
 
-// y[row_of[t, j]] = x[t]: a block copies copy_words() words a thread of one token's row to
-// its topk places.
-template <typename T, int V>
+template <typename T, int WAY>
 __global__ void __launch_bounds__(kCopyThreads) moe_dispatch_kernel(const DispatchProblem p) {
-  constexpr int W = copy_words<V>();
+  constexpr int V = word_size<T, WAY>(), W = kCopyWords;
   rows_wait_prior();
   rows_allow_dependents();
-  const int64_t t = blockIdx.x, words = p.cols / V;
-  const int64_t w0 = static_cast<int64_t>(blockIdx.y) * blockDim.x * W + threadIdx.x;
-  const T* x = static_cast<const T*>(p.x) + t * p.cols;
+  const int64_t t = blockIdx.x, from = t * p.cols;
+  const T* x = static_cast<const T*>(p.x);
   const int32_t* rows = p.row_of + t * p.topk;
+  const bool same = p.y_bf16 == (sizeof(T) == 2);  // one type: the same bits, those of a NaN too
+  const int w0 = blockIdx.y * blockDim.x * W + threadIdx.x;
   RowVec<T, V> in[W];
+  if constexpr (WAY != kByShift) {
 #pragma unroll
-  for (int i = 0; i < W; ++i)
-    if (w0 + i * blockDim.x < words) in[i].load(x + (w0 + i * blockDim.x) * V);
+    for (int i = 0; i < W; ++i)
+      if (w0 + i * blockDim.x < p.cols / V) in[i].load(x + from + (w0 + i * blockDim.x) * V);
+  }
   for (int j = 0; j < p.topk; ++j) {
     const int32_t row = __ldg(rows + j);
     if (row < 0) continue;
+    const int64_t to = row * p.cols;
+    const RowSpan<V, WAY> span(to, p.cols);
 #pragma unroll
     for (int i = 0; i < W; ++i) {
-      if (w0 + i * blockDim.x >= words) continue;
-      const int64_t at = row * p.cols + (w0 + i * blockDim.x) * V;
-      if (p.y_bf16 == (sizeof(T) == 2)) {  // one type: the same bits, those of a NaN too
-        in[i].store(static_cast<T*>(p.y) + at);
+      const int w = w0 + i * blockDim.x, e = span.first + w * V;
+      if (w >= span.words) continue;
+      if constexpr (WAY == kByShift) in[i].load_any(x, from + e);
+      if (same) {
+        in[i].store(static_cast<T*>(p.y) + to + e);
       } else {
         float v[V];
         in[i].unpack(v);
-        store_row_vec<V>(p.y, p.y_bf16, at, v);
+        store_row_vec<V>(p.y, p.y_bf16, to + e, v);
       }
     }
+    if (WAY == kByShift && blockIdx.y == 0)
+      for (int i = threadIdx.x; i < span.singles(); i += blockDim.x) {
+        const int e = span.single(i);
+        RowVec<T, 1> one;
+        one.load(x + from + e);
+        if (same) {
+          one.store(static_cast<T*>(p.y) + to + e);
+        } else {
+          float v[1];
+          one.unpack(v);
+          store_row_vec<1>(p.y, p.y_bf16, to + e, v);
+        }
+      }
   }
 }
 
 cudaError_t launch_moe_dispatch(const DispatchProblem& p, cudaStream_t st) {
-  const int v = row_width(p.cols, p.bf16);
-  const int64_t words = p.cols / v;
-  const int each = v >= 4 ? 4 : 8, threads = row_threads(words, each, kCopyThreads);
-  const int64_t per = static_cast<int64_t>(threads) * each;
-  const dim3 grid(static_cast<unsigned>(p.tokens), static_cast<unsigned>((words + per - 1) / per));
-  return with_rows(p.bf16, v, [&](auto t, auto n) {
+  const int way = row_way(p.cols, p.bf16);
+  const int64_t words = p.cols / (way == kByElement ? 1 : p.bf16 ? 8 : 4);
+  const int threads = row_threads(words, kCopyWords, kCopyThreads);
+  const dim3 grid = row_grid(p.tokens, words, static_cast<int64_t>(threads) * kCopyWords);
+  return with_rows(p.bf16, way, [&](auto t, auto n) {
     return launch_rows(moe_dispatch_kernel<decltype(t), decltype(n)::value>, grid, threads, 0, st, p);
   });
 }
@@ -524,41 +571,73 @@ cudaError_t launch_quantize_i8(const I8RowsProblem& p, unsigned* status, cudaStr
 
 // ----------------------------------------------------------------------------------- combine
 // out[t] = sum_j w[t, j] y[row_of[t, j]] + res[t], the sum in FP32 in the order of j, rounded once.
-// R rows' words (2 for up to two choices, else 4) are asked for before the first is needed, so many of
-// each that about 128 bytes a thread are under way; four blocks an SM (8192 tokens, 4 choices, 2880
-// BF16 columns: 38.0 us, 41.4 with the three that the registers would allow).
-template <int V, int R>
-__host__ __device__ constexpr int sum_words() { return V >= 4 ? 8 / R : V == 2 ? 16 / R : 6; }
+// R rows' words (2 for up to two choices, else 4) are asked for before the first is needed, 8 in all
+// a thread; four blocks an SM with four rows (8192 tokens, 4 choices, 2880 BF16 columns: 41 us, 45
+// with the three that the registers would allow).  By shift a warp asks for 32 words of each row
+// for 31 of the sum, which leaves the registers for as many loads as by word (4095 x 2 x 8191 FP32: 86 us;
+// with both words loaded by each lane, half as many at a time, 107; 8192 columns 60).
+// Blocks that stay for many tokens and ask for the next one's row numbers ahead were slower: 16384 x 8
+// x 4096 BF16 177 us, so 165.
 constexpr int kSumThreads = 256;
 
-template <typename T, int V, int R>
-__global__ void __launch_bounds__(kSumThreads, 4) moe_combine_kernel(const CombineProblem p) {
-  constexpr int W = sum_words<V, R>();
+template <typename T, int WAY, int R>
+__global__ void __launch_bounds__(kSumThreads, R == 2 ? 3 : 4) moe_combine_kernel(const CombineProblem p) {
+  constexpr int V = word_size<T, WAY>(), W = 8 / R, LANES = WAY == kByShift ? 31 : 32;
   rows_wait_prior();
   rows_allow_dependents();
-  const int64_t t = blockIdx.x, words = p.cols / V;
-  const int64_t w0 = static_cast<int64_t>(blockIdx.y) * blockDim.x * W + threadIdx.x;
+  const int64_t t = blockIdx.x, to = t * p.cols;
   const T* y = static_cast<const T*>(p.y);
+  const RowSpan<V, WAY> span(to, p.cols);
+  if (WAY == kByShift && blockIdx.y == gridDim.y - 1) {
+    for (int i = threadIdx.x; i < span.singles(); i += blockDim.x) {
+      const int e = span.single(i);
+      float all[1] = {0.0f}, v[1];
+      for (int j = 0; j < p.topk; ++j) {
+        const int32_t row = __ldg(p.row_of + t * p.topk + j);
+        if (row < 0) continue;
+        RowVec<T, 1> one;
+        one.load(y + row * p.cols + e);
+        one.unpack(v);
+        all[0] = fmaf(p.weights ? __ldg(p.weights + t * p.topk + j) : 1.0f, v[0], all[0]);
+      }
+      if (p.res) {
+        load_row_any<1>(p.res, p.res_bf16, to + e, v);
+        all[0] += v[0];
+      }
+      store_row_vec<1>(p.out, p.out_bf16, to + e, all);
+    }
+    return;
+  }
+  const int round = blockDim.x / 32 * LANES, lane = threadIdx.x % 32;
+  const int w0 = blockIdx.y * round * W + threadIdx.x / 32 * LANES + lane;
+  const int limit = span.words + (WAY == kByShift);  // the word behind the last is asked for too
   float sum[W][V] = {};
   for (int j0 = 0; j0 < p.topk; j0 += R) {
     RowVec<T, V> in[R][W];
     float weight[R];
     bool on[R];
+    int off[R];
 #pragma unroll
     for (int j = 0; j < R; ++j) {
       const int64_t s = t * p.topk + j0 + j;
       const int32_t row = j0 + j < p.topk ? __ldg(p.row_of + s) : -1;
       on[j] = row >= 0;
+      off[j] = WAY == kByShift ? static_cast<int>(row * p.cols + span.first) & (V - 1) : 0;
       weight[j] = on[j] && p.weights ? __ldg(p.weights + s) : 1.0f;
 #pragma unroll
-      for (int i = 0; i < W; ++i)
-        if (on[j] && w0 + i * blockDim.x < words) in[j][i].load(y + row * p.cols + (w0 + i * blockDim.x) * V);
+      for (int i = 0; i < W; ++i) {
+        const int w = w0 + i * round;
+        if (!on[j] || w >= limit) continue;
+        if constexpr (WAY == kByShift) in[j][i].hold(y, row * p.cols + span.first + w * V);
+        else in[j][i].load(y + row * p.cols + w * V);
+      }
     }
 #pragma unroll
     for (int j = 0; j < R; ++j) {
       if (!on[j]) continue;
 #pragma unroll
       for (int i = 0; i < W; ++i) {
+        if constexpr (WAY == kByShift) in[j][i].shift(off[j]);
         float v[V];
         in[j][i].unpack(v);
 #pragma unroll
@@ -568,8 +647,9 @@ __global__ void __launch_bounds__(kSumThreads, 4) moe_combine_kernel(const Combi
   }
 #pragma unroll
   for (int i = 0; i < W; ++i) {
-    if (w0 + i * blockDim.x >= words) continue;
-    const int64_t at = t * p.cols + (w0 + i * blockDim.x) * V;
+    const int w = w0 + i * round;
+    if (w >= span.words || lane >= LANES) continue;
+    const int64_t at = to + span.first + w * V;
     if (p.res) {
       float r[V];
       load_row_any<V>(p.res, p.res_bf16, at, r);
@@ -582,18 +662,18 @@ __global__ void __launch_bounds__(kSumThreads, 4) moe_combine_kernel(const Combi
 
 template <int R>
 static cudaError_t combine_rows(const CombineProblem& p, cudaStream_t st) {
-  const int v = row_width(p.cols, p.bf16);
-  const int64_t words = p.cols / v;
-  const int each = v >= 4 ? 8 / R : v == 2 ? 16 / R : 6, threads = row_threads(words, each, kSumThreads);
-  const int64_t per = static_cast<int64_t>(threads) * each;
-  const dim3 grid(static_cast<unsigned>(p.tokens), static_cast<unsigned>((words + per - 1) / per));
-  return with_rows(p.bf16, v, [&](auto t, auto n) {
+  const int way = row_way(p.cols, p.bf16);
+  const int64_t words = p.cols / (way == kByElement ? 1 : p.bf16 ? 8 : 4);
+  const int threads = row_threads(words, 8 / R, kSumThreads);
+  dim3 grid = row_grid(p.tokens, words, static_cast<int64_t>(way == kByShift ? threads / 32 * 31 : threads) * (8 / R));
+  if (way == kByShift) ++grid.y;  // the single elements
+  return with_rows(p.bf16, way, [&](auto t, auto n) {
     return launch_rows(moe_combine_kernel<decltype(t), decltype(n)::value, R>, grid, threads, 0, st, p);
   });
 }
 
 cudaError_t launch_moe_combine(const CombineProblem& p, cudaStream_t st) {
-  return p.topk <= 2 && row_width(p.cols, p.bf16) >= 4 ? combine_rows<2>(p, st) : combine_rows<4>(p, st);
+  return p.topk <= 2 ? combine_rows<2>(p, st) : combine_rows<4>(p, st);
 }
 
 // ------------------------------------------------------------------------- its backward pass
@@ -604,14 +684,14 @@ cudaError_t launch_moe_combine(const CombineProblem& p, cudaStream_t st) {
 // where it takes 70 (8192 tokens, 4 choices, 2880 BF16 columns).
 constexpr int kGradThreads = 256;
 
-template <typename T, int V, int R>
+template <typename T, int WAY, int R>
 __global__ void __launch_bounds__(kGradThreads, R == 8 ? 3 : 4) moe_combine_grad_kernel(const CombineGradProblem p) {
+  constexpr int V = word_size<T, WAY>();
   __shared__ float s_dot[kGradThreads / 32][R];
   rows_wait_prior();
   rows_allow_dependents();
   const int64_t t = blockIdx.x;
-  const int words = static_cast<int>(p.cols / V);
-  const T* dout = static_cast<const T*>(p.dout) + t * p.cols;
+  const T* dout = static_cast<const T*>(p.dout);
   const T* y = static_cast<const T*>(p.y);
   const bool dots = p.dweights != nullptr;
   for (int j0 = 0; j0 < p.topk; j0 += R) {
@@ -624,26 +704,67 @@ __global__ void __launch_bounds__(kGradThreads, R == 8 ? 3 : 4) moe_combine_grad
       weight[j] = row[j] >= 0 && p.weights ? __ldg(p.weights + s) : 1.0f;
       dot[j] = 0.0f;
     }
-    for (int w = threadIdx.x; w < words; w += blockDim.x) {
-      RowVec<T, V> in, yr[R];
-      in.load(dout + w * V);
+    if constexpr (WAY == kByShift) {
+      // words at each row's own offset; dout's values for them come from L1 after the first row
+      const int64_t from = t * p.cols;
 #pragma unroll
       for (int j = 0; j < R; ++j) {
-        yr[j].zero();
-        if (dots && row[j] >= 0) yr[j].load(y + row[j] * p.cols + w * V);
+        if (row[j] < 0) continue;
+        const int64_t at = row[j] * p.cols;
+        const RowSpan<V, WAY> span(at, p.cols);
+#pragma unroll 2
+        for (int w = threadIdx.x; w < span.words; w += blockDim.x) {
+          const int e = span.first + w * V;
+          RowVec<T, V> in, yr;
+          in.load_any(dout, from + e);
+          yr.zero();
+          if (dots) yr.load(y + at + e);
+          float d[V], v[V];
+          in.unpack(d);
+          yr.unpack(v);
+#pragma unroll
+          for (int k = 0; k < V; ++k) {
+            dot[j] = fmaf(d[k], v[k], dot[j]);
+            v[k] = weight[j] * d[k];
+          }
+          if (p.dy) store_row_vec<V>(p.dy, p.dy_bf16, at + e, v);
+        }
+        for (int i = threadIdx.x; i < span.singles(); i += blockDim.x) {
+          const int e = span.single(i);
+          RowVec<T, 1> in, yr;
+          in.load(dout + from + e);
+          yr.zero();
+          if (dots) yr.load(y + at + e);
+          float d[1], v[1];
+          in.unpack(d);
+          yr.unpack(v);
+          dot[j] = fmaf(d[0], v[0], dot[j]);
+          v[0] = weight[j] * d[0];
+          if (p.dy) store_row_vec<1>(p.dy, p.dy_bf16, at + e, v);
+        }
       }
-      float d[V];
-      in.unpack(d);
+    } else {
+      for (int w = threadIdx.x; w < static_cast<int>(p.cols) / V; w += blockDim.x) {
+        RowVec<T, V> in, yr[R];
+        in.load(dout + t * p.cols + w * V);
 #pragma unroll
-      for (int j = 0; j < R; ++j) {
-        float v[V];
-        yr[j].unpack(v);
+        for (int j = 0; j < R; ++j) {
+          yr[j].zero();
+          if (dots && row[j] >= 0) yr[j].load(y + row[j] * p.cols + w * V);
+        }
+        float d[V];
+        in.unpack(d);
 #pragma unroll
-        for (int k = 0; k < V; ++k) dot[j] = fmaf(d[k], v[k], dot[j]);
-        if (!p.dy || row[j] < 0) continue;
+        for (int j = 0; j < R; ++j) {
+          float v[V];
+          yr[j].unpack(v);
 #pragma unroll
-        for (int k = 0; k < V; ++k) v[k] = weight[j] * d[k];
-        store_row_vec<V>(p.dy, p.dy_bf16, row[j] * p.cols + w * V, v);
+          for (int k = 0; k < V; ++k) dot[j] = fmaf(d[k], v[k], dot[j]);
+          if (!p.dy || row[j] < 0) continue;
+#pragma unroll
+          for (int k = 0; k < V; ++k) v[k] = weight[j] * d[k];
+          store_row_vec<V>(p.dy, p.dy_bf16, row[j] * p.cols + w * V, v);
+        }
       }
     }
     if (dots) {
@@ -667,10 +788,10 @@ __global__ void __launch_bounds__(kGradThreads, R == 8 ? 3 : 4) moe_combine_grad
 
 template <int R>
 static cudaError_t combine_grad_rows(const CombineGradProblem& p, cudaStream_t st) {
-  const int v = row_width(p.cols, p.bf16);
-  const int threads = row_threads(p.cols / v, v >= 4 ? 2 : 4, kGradThreads);
+  const int way = row_way(p.cols, p.bf16);
+  const int threads = row_threads(p.cols / (way == kByElement ? 1 : p.bf16 ? 8 : 4), 2, kGradThreads);
   const dim3 grid(static_cast<unsigned>(p.tokens));
-  return with_rows(p.bf16, v, [&](auto t, auto n) {
+  return with_rows(p.bf16, way, [&](auto t, auto n) {
     return launch_rows(moe_combine_grad_kernel<decltype(t), decltype(n)::value, R>, grid, threads, 0, st, p);
   });
 }

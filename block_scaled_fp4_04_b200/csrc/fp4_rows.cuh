@@ -26,6 +26,7 @@ __device__ __forceinline__ void rows_wait_prior() { asm volatile("griddepcontrol
 // element.
 template <typename T, int V>
 struct RowVec {
+  static constexpr int kElements = V;
   static constexpr int kWords = V == 1 ? 1 : V * static_cast<int>(sizeof(T)) / 4;
   uint32_t w[kWords];
   __device__ __forceinline__ void zero() {
@@ -50,6 +51,43 @@ struct RowVec {
                    : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
                    : "l"(p));
     }
+  }
+  // 16 bytes from any element offset of a 16-byte aligned matrix.  load_any(): by the word that holds
+  // the first of them and the next one, which has to be there too.  Or hold(), the first of the two;
+  // then shift() by all lanes of the warp, where the next lane holds the next word.
+  __device__ __forceinline__ void hold(const T* base, int64_t at) {
+    static_assert(V * sizeof(T) == 16, "one 16-byte word");
+    const uint4 a = *reinterpret_cast<const uint4*>(base + (at & ~static_cast<int64_t>(V - 1)));
+    w[0] = a.x;
+    w[1] = a.y;
+    w[2] = a.z;
+    w[3] = a.w;
+  }
+  __device__ __forceinline__ void take(const uint32_t (&x)[8], int64_t at) {
+    const int off = static_cast<int>(at) & (V - 1), words = off * static_cast<int>(sizeof(T)) / 4;
+    uint32_t u[6], v[5];
+#pragma unroll
+    for (int i = 0; i < 6; ++i) u[i] = words & 2 ? x[i + 2] : x[i];
+#pragma unroll
+    for (int i = 0; i < 5; ++i) v[i] = words & 1 ? u[i + 1] : u[i];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = sizeof(T) == 2 ? __funnelshift_r(v[i], v[i + 1], (off & 1) * 16) : v[i];
+  }
+  __device__ __forceinline__ void shift(int64_t at) {
+    uint32_t x[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[i] = w[i];
+      x[4 + i] = __shfl_down_sync(0xFFFFFFFFu, w[i], 1);
+    }
+    take(x, at);
+  }
+  __device__ __forceinline__ void load_any(const T* base, int64_t at) {
+    RowVec a, b;
+    a.hold(base, at);
+    b.hold(base, at + V);
+    const uint32_t x[8] = {a.w[0], a.w[1], a.w[2], a.w[3], b.w[0], b.w[1], b.w[2], b.w[3]};
+    take(x, at);
   }
   // the same bits to another row of this type
   __device__ __forceinline__ void store(T* p) const {

@@ -62,7 +62,7 @@ def _case(tokens, topk, experts, cols, dtype, seed=0, drop=0.25):
 
 
 SIZES = [(1, 1, 1, 16), (5, 3, 4, 8), (16, 4, 32, 2880), (33, 2, 3, 1), (70, 5, 9, 77), (64, 8, 16, 2050), (9, 2, 5, 4100),
-         (300, 1, 7, 129), (3, 2, 2, 40000)]
+         (300, 1, 7, 129), (3, 2, 2, 40000), (12, 3, 5, 65), (9, 2, 4, 63), (40, 2, 6, 8191), (7, 5, 8, 1023), (33, 4, 9, 2046)]
 
 
 @pytest.mark.parametrize("tokens,topk,experts,cols", SIZES)
