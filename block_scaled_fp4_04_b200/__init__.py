@@ -101,7 +101,7 @@ def lib() -> ctypes.CDLL:
                 "fp4_moe_dispatch_i8": (I32, [P, I64, I64, I32, I32, P, P, P, P]),
                 "fp4_moe_combine": (I32, [P, I32, P, P, I64, I32, I64, P, I32, P, I32, P]),
                 "fp4_moe_combine_backward": (I32, [P, P, I32, P, P, I64, I32, I64, P, I32, P, P]),
-                "fp4_quantize_i8": (I32, [P, I64, I64, I32, P, P, P]),
+                "fp4_quantize_i8": (I32, [P, I64, I64, I32, P, P, P, P]),
                 "fp4_gemm_i8_workspace_size": (SZ, [I64, I64, I64]),
                 "fp4_gemm_i8": (I32, [P, P, P, P, I64, I64, I64, P, I32, P, I32, P, SZ, ctypes.c_uint, P]),
                 "fp4_gemm_i8_grouped_workspace_size": (SZ, [I32, I64, I64, I64]),
@@ -378,8 +378,8 @@ def fp4_moe_combine_backward(dout, y, in_dtype, row_of, weights, tokens, topk, c
                                           out_dtype, _p(dweights), _s(stream)))
 
 
-def fp4_quantize_i8(x, rows, cols, in_dtype, codes, row_scales, stream=None):
-    _check(lib().fp4_quantize_i8(_p(x), rows, cols, in_dtype, _p(codes), _p(row_scales), _s(stream)))
+def fp4_quantize_i8(x, rows, cols, in_dtype, codes, row_scales, rows_valid=None, stream=None):
+    _check(lib().fp4_quantize_i8(_p(x), rows, cols, in_dtype, _p(codes), _p(row_scales), _p(rows_valid), _s(stream)))
 
 
 def fp4_gemm_i8_workspace_size(M: int, N: int, K: int) -> int:
@@ -817,17 +817,20 @@ def moe_combine_backward(dout: torch.Tensor, y: torch.Tensor, routing: Routing, 
     return dy, dw
 
 
-def quantize_i8(x: torch.Tensor, stream=None) -> Int8Rows:
+def quantize_i8(x: torch.Tensor, offsets: Optional[torch.Tensor] = None, stream=None) -> Int8Rows:
     """Rows of x [rows, cols] (cols % 16 == 0), or of experts' weights [experts, rows, cols], as
-    8-bit integers with one scale each."""
+    8-bit integers with one scale each.  With `offsets` (Routing.offsets) x holds rows in the
+    experts' order, and those behind the last expert's are left out."""
     if x.dim() not in (2, 3):
         raise ValueError("x must be [rows, cols] or [experts, rows, cols]")
     _dense("x", x, x, x.shape)
+    if offsets is not None:
+        _dense("offsets", offsets, x, (offsets.numel(),), torch.int32)
     rows, cols = x.numel() // max(1, x.shape[-1]), x.shape[-1]
     with _on(x, stream) as s:
         codes = torch.empty(x.shape, dtype=torch.int8, device=x.device)
         scales = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
-        fp4_quantize_i8(x, rows, cols, _dtype_code(x), codes, scales, s)
+        fp4_quantize_i8(x, rows, cols, _dtype_code(x), codes, scales, None if offsets is None else offsets[-1:], s)
     return Int8Rows(codes, scales)
 
 

@@ -910,11 +910,11 @@ fp4_status fp4_moe_dispatch_codes(const void* x, int64_t tokens, int64_t cols, f
 }
 
 static fp4_status i8_rows(const void* x, int64_t rows, int64_t cols, fp4_dtype in_dtype, int topk, const int32_t* row_of,
-                          int8_t* codes, float* row_scales, void* stream) {
+                          const int32_t* valid, int8_t* codes, float* row_scales, void* stream) {
   if (!x || !codes || !row_scales) return fail(FP4_ERR_INVALID_ARG, "null pointer");
   if (cols % 16 != 0) return fail(FP4_ERR_INVALID_ARG, "8-bit rows need cols % 16 == 0");
   if (!aligned16(x) || !aligned16(codes)) return fail(FP4_ERR_INVALID_ARG, "x and codes must be 16-byte aligned");
-  if (!aligned4(row_scales)) return fail(FP4_ERR_INVALID_ARG, "row_scales alignment");
+  if (!aligned4(row_scales) || !aligned4(valid)) return fail(FP4_ERR_INVALID_ARG, "row_scales / rows_valid alignment");
   unsigned* status;
   const fp4_status s = device_state(&status);
   if (s != FP4_OK) return s;
@@ -925,6 +925,7 @@ static fp4_status i8_rows(const void* x, int64_t rows, int64_t cols, fp4_dtype i
   p.cols = cols;
   p.topk = topk;
   p.row_of = row_of;
+  p.valid = valid;
   p.codes = codes;
   p.scales = row_scales;
   const cudaError_t e = launch_quantize_i8(p, status, static_cast<cudaStream_t>(stream));
@@ -935,15 +936,15 @@ fp4_status fp4_moe_dispatch_i8(const void* x, int64_t tokens, int64_t cols, fp4_
                                const int32_t* row_of, int8_t* codes, float* row_scales, void* stream) {
   const fp4_status c = check_moe(tokens, cols, topk, in_dtype, FP4_F32, row_of);
   if (c != FP4_OK) return c;
-  return i8_rows(x, tokens, cols, in_dtype, topk, row_of, codes, row_scales, stream);
+  return i8_rows(x, tokens, cols, in_dtype, topk, row_of, nullptr, codes, row_scales, stream);
 }
 
 fp4_status fp4_quantize_i8(const void* x, int64_t rows, int64_t cols, fp4_dtype in_dtype, int8_t* codes,
-                           float* row_scales, void* stream) {
+                           float* row_scales, const int32_t* rows_valid, void* stream) {
   if (rows <= 0 || cols <= 0) return fail(FP4_ERR_INVALID_ARG, "rows and cols must be positive");
   if (rows > kMaxDim || cols > kMaxDim) return fail(FP4_ERR_UNSUPPORTED, "dimension too large");
   if (!dtype_ok(in_dtype)) return fail(FP4_ERR_INVALID_ARG, "in_dtype");
-  return i8_rows(x, rows, cols, in_dtype, 1, nullptr, codes, row_scales, stream);
+  return i8_rows(x, rows, cols, in_dtype, 1, nullptr, rows_valid, codes, row_scales, stream);
 }
 
 fp4_status fp4_moe_combine(const void* y, fp4_dtype in_dtype, const int32_t* row_of, const float* weights, int64_t tokens,

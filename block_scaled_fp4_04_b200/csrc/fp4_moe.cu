@@ -506,6 +506,7 @@ __global__ void __launch_bounds__(kI8Threads) quantize_i8_kernel(const I8RowsPro
   rows_wait_prior();
   rows_allow_dependents();
   const int64_t t = blockIdx.x, words = p.cols / V;
+  if (p.valid && t >= __ldg(p.valid)) return;
   const T* x = static_cast<const T*>(p.x) + t * p.cols;
   RowVec<T, V> in[kI8Words];
   uint32_t m = 0;

@@ -31,13 +31,15 @@ struct DispatchCodesProblem {
 };
 cudaError_t launch_moe_dispatch_codes(const DispatchCodesProblem& p, unsigned* status, cudaStream_t st);
 
-// 8-bit rows with a scale each, in place (row_of null, topk 1) or in the experts' order.
+// 8-bit rows with a scale each, in place (row_of null, topk 1; with `valid` only that many of them)
+// or in the experts' order.
 struct I8RowsProblem {
   const void* x;
   int bf16;
   int64_t rows, cols;
   int topk;
   const int32_t* row_of;
+  const int32_t* valid;
   int8_t* codes;
   float* scales;
 };

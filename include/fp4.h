@@ -123,7 +123,9 @@ fp4_status fp4_quantize(const void* x_dev, int64_t rows, int64_t cols, fp4_dtype
  * offsets_dev[num_groups + 1] (device int32, nondecreasing, offsets[0] = 0,
  * offsets[num_groups] = rows) delimit the groups; scales are written in the grouped
  * layout (size <= fp4_scales_bytes_grouped(rows, num_groups, cols, fmt); the bytes
- * up to that bound are written, pads 0).  For NVFP4 one g covers all groups. */
+ * up to that bound are written, pads 0).  For NVFP4 one g covers all groups.  With
+ * MXFP4 or a caller's g the last offset may stay below rows (slots without an expert,
+ * fp4_moe_sort): rows behind it are not read, their codes left as they were. */
 fp4_status fp4_quantize_grouped(const void* x_dev, int64_t rows, int64_t cols, fp4_dtype in_dtype,
                                 fp4_fmt fmt, int num_groups, const int32_t* offsets_dev,
                                 uint8_t* codes_out_dev, uint8_t* scales_out_dev,
@@ -454,8 +456,9 @@ fp4_status fp4_gemm_noalloc(fp4_fmt fmt, const uint8_t* A_dev, const uint8_t* sA
  *   A_dev [total_rows, K/2] with grouped scales sA_dev (fp4_quantize_grouped; the
  *   buffer holds fp4_scales_bytes_grouped(total_rows, num_groups, K, fmt) bytes);
  *   B_dev [num_groups, N, K/2], sB_dev num_groups consecutive fp4_scales_bytes(N, K)
- *   blocks; gB_dev [num_groups] floats or NULL; offsets_dev device int32 [groups+1]
- *   with offsets[num_groups] == total_rows.  D_dev [total_rows, N].
+ *   blocks; gB_dev [num_groups] floats or NULL; offsets_dev device int32 [groups+1],
+ *   nondecreasing from 0; the last one may stay below total_rows: rows of D behind it
+ *   are left as they were.  D_dev [total_rows, N].
  * Requires K % 32 == 0, N % 128 == 0, num_groups <= 1024. */
 fp4_status fp4_gemm_grouped(fp4_fmt fmt, int num_groups, const int32_t* offsets_dev,
                             const uint8_t* A_dev, const uint8_t* sA_dev, const float* gA_dev,
@@ -540,9 +543,12 @@ fp4_status fp4_moe_combine_backward(const void* dout_dev, const void* y_dev, fp4
  * to the nearest integer, ties to even, within [-127, 127] (each FP32 operation rounds once).
  * codes_dev [rows, cols], row_scales_dev [rows].  For activations (rows are tokens) and weights
  * (rows are output channels) alike.  cols % 16 == 0, x and codes 16-byte aligned; a non-finite
- * element latches FP4_ERR_NONFINITE. */
+ * element latches FP4_ERR_NONFINITE.
+ *   rows_valid_dev  1 int32 or NULL: how many of the rows there are, where only the device knows (the
+ *           experts' rows: offsets_dev + num_experts); those behind are not read, their codes and
+ *           scales left as they were. */
 fp4_status fp4_quantize_i8(const void* x_dev, int64_t rows, int64_t cols, fp4_dtype in_dtype, int8_t* codes_dev,
-                           float* row_scales_dev, void* stream);
+                           float* row_scales_dev, const int32_t* rows_valid_dev, void* stream);
 
 /* D[m, n] = act(sA[m] sB[n] sum_k A[m, k] B[n, k] + bias[n]): A_dev [M, K] and B_dev [N, K] signed
  * 8-bit, sA_dev [M] and sB_dev [N] FP32, bias_dev [N] FP32 or NULL, D_dev [M, N] in out_dtype.

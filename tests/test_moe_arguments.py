@@ -95,11 +95,11 @@ def test_combine_backward_refuses(kw):
     assert _call("fp4_moe_combine_backward", GRAD, **kw) == fp4.ERR_INVALID_ARG
 
 
-Q8 = dict(x=16, rows=8, cols=64, dt=fp4.F32, codes=16, scales=16, stream=None)
+Q8 = dict(x=16, rows=8, cols=64, dt=fp4.F32, codes=16, scales=16, valid=16, stream=None)
 
 
 @pytest.mark.parametrize("kw", [dict(x=None), dict(codes=None), dict(scales=None), dict(rows=0), dict(cols=0), dict(cols=24),
-                                dict(dt=2), dict(x=8), dict(codes=8), dict(scales=2)])
+                                dict(dt=2), dict(x=8), dict(codes=8), dict(scales=2), dict(valid=2)])
 def test_quantize_i8_refuses(kw):
     assert _call("fp4_quantize_i8", Q8, **kw) == fp4.ERR_INVALID_ARG
 
