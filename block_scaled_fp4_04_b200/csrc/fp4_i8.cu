@@ -45,7 +45,7 @@ struct I8Args {
   int M, N, K, num_kb;
   void* out;
   int out_bf16;
-  int wide;            // BF16 elements that go out at once: 8, 2 or 1
+  int wide;            // BF16 outputs of an even width
   int early_w;         // weights may be read before the preceding kernel finishes
   int weights_once;    // a weight's tokens fit one tile: it need not stay in L2
   int split;
@@ -77,8 +77,7 @@ struct I8Cfg {
   static constexpr int kStageBytes = kSteps * (kWBytes + kXBytes);
   static constexpr int kScaleOff = 1024;                        // barriers and flags before it
   static constexpr int kGroupOff = kScaleOff + 2 * BN * 4;      // two tiles' token scales
-  static constexpr int kOutOff = (kGroupOff + 2 * (kMaxGroups + 1) * 4 + 15) / 16 * 16;  // 1 KB per epilogue warp
-  static constexpr int kMiscBytes = kOutOff + 1024 * kEpiWarps;
+  static constexpr int kMiscBytes = kGroupOff + 2 * (kMaxGroups + 1) * 4;
   static constexpr int kFit = (227 * 1024 - 1024 - 256 - kMiscBytes) / kStageBytes;
   static constexpr int kStages = kFit > 12 ? 12 : kFit;
   static constexpr int kSmemBytes = kStages * kStageBytes + kMiscBytes + 1024;
@@ -169,50 +168,39 @@ struct I8Sched {
 
 // Stores 16 tokens of a warp's 32 channels: v[i] holds tokens `token` + 2i and + 2i + 1 (of which
 // `tokens` exist) of channel `ch` + lane (of which `chs` exist).  FP32 rows are whole lines as they
-// are.  BF16 ones meet in the warp's 1 KB of shared memory and leave in 16-byte words where the
-// rows start at those, else in pairs or single elements.
-__device__ __forceinline__ void store_tokens16(const I8Args& p, uint16_t* stage, int64_t token, int tokens, int ch,
-                                               int chs, int lane, const float2 (&v)[8]) {
+// are.  BF16 ones of an even width leave in words of two channels: neighbouring lanes exchange
+// halves, so that even lanes hold even tokens.  (Meeting in shared memory for 16-byte words costs
+// bandwidth that the MMAs and their loads need: experts 32 x 16384 x 5760 x 2880 300 us under the power
+// cap, so 295; 8192 x 8192 x 256 73.5 and 66.9.)
+__device__ __forceinline__ void store_tokens16(const I8Args& p, int64_t token, int tokens, int ch, int chs, int lane,
+                                               const float2 (&v)[8]) {
+  const bool on = lane < chs;
   if (!p.out_bf16) {
     float* out = static_cast<float*>(p.out) + token * p.N + ch + lane;
-    if (lane >= chs) return;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      if (2 * i < tokens) out[0] = v[i].x;
-      if (2 * i + 1 < tokens) out[p.N] = v[i].y;
+      if (on && 2 * i < tokens) __stcs(out, v[i].x);
+      if (on && 2 * i + 1 < tokens) __stcs(out + p.N, v[i].y);
       out += 2 * static_cast<int64_t>(p.N);
     }
     return;
   }
+  const int odd = p.wide ? lane & 1 : 0;
+  uint16_t* out = static_cast<uint16_t*>(p.out) + (token + odd) * p.N + ch + (p.wide ? lane & ~1 : lane);
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const __nv_bfloat162 h = __floats2bfloat162_rn(v[i].x, v[i].y);
     const uint32_t w = *reinterpret_cast<const uint32_t*>(&h);
-    stage[2 * i * 32 + lane] = static_cast<uint16_t>(w);
-    stage[(2 * i + 1) * 32 + lane] = static_cast<uint16_t>(w >> 16);
+    if (p.wide) {
+      const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, w, 1);
+      const uint32_t two = __byte_perm(w, got, odd ? 0x3276 : 0x5410);
+      if (on && 2 * i + odd < tokens) __stcs(reinterpret_cast<uint32_t*>(out), two);
+    } else {
+      if (on && 2 * i < tokens) out[0] = static_cast<uint16_t>(w);
+      if (on && 2 * i + 1 < tokens) out[p.N] = static_cast<uint16_t>(w >> 16);
+    }
+    out += 2 * static_cast<int64_t>(p.N);
   }
-  __syncwarp();
-  uint16_t* out = static_cast<uint16_t*>(p.out) + token * p.N + ch;
-  if (p.wide == 8) {
-    const int c = lane % 4 * 8;
-#pragma unroll
-    for (int t = lane / 4; t < 16; t += 8)
-      if (t < tokens && c < chs)
-        __stcs(reinterpret_cast<uint4*>(out + static_cast<int64_t>(t) * p.N + c),
-               *reinterpret_cast<const uint4*>(stage + t * 32 + c));
-  } else if (p.wide == 2) {
-    const int c = lane % 16 * 2;
-#pragma unroll
-    for (int t = lane / 16; t < 16; t += 2)
-      if (t < tokens && c < chs)
-        *reinterpret_cast<uint32_t*>(out + static_cast<int64_t>(t) * p.N + c) =
-            *reinterpret_cast<const uint32_t*>(stage + t * 32 + c);
-  } else {
-#pragma unroll
-    for (int t = 0; t < 16; ++t)
-      if (t < tokens && lane < chs) out[static_cast<int64_t>(t) * p.N + lane] = stage[t * 32 + lane];
-  }
-  __syncwarp();  // before the next 16 tokens take their place
 }
 
 __device__ __forceinline__ void i8_timeout(volatile int* abort, unsigned* status) {
@@ -433,7 +421,6 @@ __global__ void __launch_bounds__(I8Cfg<BN, PAIR>::kThreads, 1)
     const int et = threadIdx.x - 64;
     const int c0 = ((warp - 2) >> 2) * C::kChunk;  // this thread's first column
     const int rl = q * 32 + lane;                 // its channel within the tile
-    uint16_t* stage = reinterpret_cast<uint16_t*>(misc + C::kOutOff) + (warp - 2) * 512;
     Schedule sch(p, s_off, s_tiles, vb, vg, sub_row);
     I8Work w, next;
     // a tile's scales and biases are asked for one tile ahead
@@ -487,7 +474,7 @@ __global__ void __launch_bounds__(I8Cfg<BN, PAIR>::kThreads, 1)
 #pragma unroll
           for (int j = 0; j < 8; ++j) z[j] = act_value2<decltype(tag)::value>(z[j]);
         });
-        store_tokens16(p, stage, w.t0 + c, w.t_valid - c, w.n0 + q * 32, chs, lane, z);
+        store_tokens16(p, w.t0 + c, w.t_valid - c, w.n0 + q * 32, chs, lane, z);
       };
       auto load = [&](int c, uint32_t* r) __attribute__((always_inline)) {
         if constexpr (C::kLoad == 32) tmem_ld32(taddr + c, r);
@@ -605,8 +592,9 @@ I8Plan i8_plan(int64_t M, int64_t N, int64_t K, int groups) {
   pl.tiles_w = (N + step - 1) / step;
   int width = pl.BN;
   if (pl.pair && !groups) {
-    // A pair's K step takes about as long as loading 320 + width rows, and all pairs wait for the
-    // last round of tiles: the width with the shortest rounds in all.  (256 x 4096 x 4096: widths
+    // A K step of a pair moves 256 + width rows into and out of shared memory, which takes longer
+    // than its MMAs up to a width of 256 (measured: as 320 + width), and all pairs wait for the last
+    // round of tiles: the width with the shortest rounds in all.  (256 x 4096 x 4096: widths
     // 64 / 128 / 256 take 15.1 / 16.6 / 18.5 us, 1024 x 8192 x 8192 115 / 73 / 50.)
     int64_t best = INT64_MAX;
     for (int w = 64; w <= 256; w += 64) {
@@ -731,7 +719,7 @@ int launch_gemm_i8(const I8Problem& g, unsigned* status, cudaStream_t st, const 
   a.num_kb = pl.num_kb;
   a.out = g.D;
   a.out_bf16 = g.out_bf16;
-  a.wide = g.N % 8 == 0 ? 8 : g.N % 2 == 0 ? 2 : 1;
+  a.wide = g.N % 2 == 0;
   a.early_w = g.weights_ready && !g.num_groups;
   a.weights_once = g.num_groups ? pl.rows <= pl.BN : pl.tiles_t == 1;
   a.split = pl.split;
