@@ -18,7 +18,7 @@
 //   warp 1      owns TMEM; one lane issues four K = 32 MMAs a K step
 //   warps 2..   epilogue, four warps (one per TMEM lane quarter), or eight from 64 tokens on, which
 //               share out the columns; two accumulators, so that it overlaps the next tile
-// Above 64 tokens a tile is shared by a pair of CTAs: 256 channels x up to 256 tokens, each CTA loading
+// Wider tiles are shared by a pair of CTAs: 256 channels x up to 256 tokens, each CTA loading
 // its 128 channels and half of the tokens.  Its width is the tokens that share weights (one
 // expert's, or all) in equal parts, rounded up to 64: 530 rows are 3 x 192, not 2 x 256 and a rest.
 //
@@ -585,8 +585,19 @@ I8Plan i8_plan(int64_t M, int64_t N, int64_t K, int groups) {
   const int sms = num_sms(), pairs = sms / 2;
   const int64_t used = groups ? std::min<int64_t>(groups, M) : 1;  // experts with rows, at most
   pl.rows = (M + used - 1) / used;
-  pl.pair = pl.rows > 64;
-  pl.BN = pl.rows <= 16 ? 16 : pl.rows <= 32 ? 32 : pl.rows <= 64 ? 64 : 256;
+  if (groups) {
+    // Experts' rows fall unevenly: a tile that is wide enough for twice the average and more costs
+    // little, a second tile of an expert reads its weights again.  (32 experts of 5760 x 2880, tiles of
+    // 16 / 64 / pairs: 32 rows in all 59 / 69 / 57 us, 512 rows 113 / 87 / 92, 2048 rows 354 / 112 / 93.)
+    pl.pair = pl.rows > 32;
+    pl.BN = pl.pair ? 256 : pl.rows > 1 ? 64 : 16;
+  } else {
+    // Above 16 tokens a pair's whole tiles beat the pieces' sum where they are few and short.
+    // (64 x 5760 x 2880: pairs 11.9 us, split 14.8; 64 x 4096 x 4096 13.4 and 15.3; 64 x 8192 x 8192
+    // 22.5 and 21.3; 64 x 1024 x 8192 25.8 and 18.2; 16 x 4096 x 4096 12.3 and 10.4.)
+    pl.pair = pl.rows > 64 || (pl.rows > 16 && K <= 4096 && (N + 255) / 256 <= pairs);
+    pl.BN = pl.pair ? 256 : pl.rows <= 16 ? 16 : pl.rows <= 32 ? 32 : 64;
+  }
   const int step = pl.pair ? 256 : 128;
   pl.num_kb = static_cast<int>((K + step - 1) / step);
   pl.tiles_w = (N + step - 1) / step;

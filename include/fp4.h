@@ -509,7 +509,7 @@ fp4_status fp4_moe_dispatch_codes(const void* x_dev, int64_t tokens, int64_t col
 
 /* The same rows as fp4_quantize_i8 quantizes them: codes_dev [tokens * topk, cols], a scale each in
  * row_scales_dev [tokens * topk]; rows behind the last expert's are left as they were.
- * cols % 16 == 0. */
+ * cols % 16 == 0; non-finite elements as for fp4_moe_dispatch_codes. */
 fp4_status fp4_moe_dispatch_i8(const void* x_dev, int64_t tokens, int64_t cols, fp4_dtype in_dtype, int topk,
                                const int32_t* row_of_dev, int8_t* codes_dev, float* row_scales_dev, void* stream);
 

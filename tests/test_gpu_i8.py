@@ -62,7 +62,8 @@ def _gemm(a, sa, b, sb, bias=None, act="none", out=F32, flags=0, ws=None):
 
 SHAPES = [(1, 1, 16), (1, 128, 128), (3, 5, 48), (16, 256, 128), (16, 640, 4096), (17, 300, 272), (32, 129, 1024),
           (33, 1000, 512), (64, 257, 2880), (65, 130, 144), (100, 100, 16), (128, 512, 512), (129, 128, 256),
-          (200, 2000, 640), (256, 256, 256), (300, 5000, 320), (513, 2049, 1040), (1999, 1111, 912), (2500, 3000, 128)]
+          (200, 2000, 640), (256, 256, 256), (300, 5000, 320), (513, 2049, 1040), (1999, 1111, 912), (2500, 3000, 128),
+          (20, 300, 4400), (32, 1001, 4112), (50, 257, 4112), (64, 2000, 8192)]
 
 
 @pytest.mark.parametrize("m,n,k", SHAPES)
@@ -107,7 +108,8 @@ def test_gemm_of_the_largest_sums(m, k):
     assert want[0, 0] > 2 ** 14 * k * 1e-6 * 0.9
 
 
-@pytest.mark.parametrize("m,n,k", [(1, 8192, 8192), (16, 4096, 8192), (50, 3000, 4096), (128, 1024, 8192), (8192, 512, 512)])
+@pytest.mark.parametrize("m,n,k", [(1, 8192, 8192), (16, 4096, 8192), (50, 3000, 4096), (25, 3000, 8192), (60, 500, 8192), (128, 1024, 8192),
+                                   (8192, 512, 512)])
 def test_gemm_has_the_same_bits_every_time(m, n, k):
     (a, sa), (b, sb) = random_i8((m, k), 1), random_i8((n, k), 2)
     a, sa, b, sb = a.cuda(), sa.cuda(), b.cuda(), sb.cuda()
@@ -211,6 +213,36 @@ def test_two_captured_graphs_with_workspaces_of_their_own():
     torch.cuda.synchronize()
     for (_, d, ws), t in zip(graphs, want):
         assert torch.equal(d, t) and not ws.buf.any()
+
+
+def test_on_another_stream():
+    m, n, k = 100, 500, 1024
+    w = fp4.quantize_i8(random_input(n, k, 1, BF16, std=0.02).cuda())
+    x = random_input(m, k, 2, BF16).cuda()
+    want = fp4.gemm_i8(fp4.quantize_i8(x), w, out_dtype=F32)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = fp4.gemm_i8(fp4.quantize_i8(x, stream=side), w, out_dtype=F32, stream=side)
+    raw = torch.empty_like(want)
+    codes, scales = torch.empty(m, k, dtype=torch.int8, device="cuda"), torch.empty(m, device="cuda")
+    torch.cuda.synchronize()
+    fp4.fp4_quantize_i8(x, m, k, fp4.BF16, codes, scales, None, side.cuda_stream)
+    fp4.fp4_gemm_i8(codes, scales, w.codes, w.scales, m, n, k, None, fp4.ACT_NONE, raw, fp4.F32, stream=side)
+    side.synchronize()
+    assert torch.equal(got, want) and torch.equal(raw, want)
+
+
+def test_quantize_stops_at_a_row_count_on_the_device():
+    x = random_input(50, 256, 1, BF16)
+    x[30:] = float("nan")
+    q, s = i8_rows(x[:30])
+    for valid in (0, 17, 30):
+        codes, scales = torch.full((50, 256), 99, dtype=torch.int8, device="cuda"), torch.full((50,), -1.0, device="cuda")
+        fp4.fp4_quantize_i8(x.cuda(), 50, 256, fp4.BF16, codes, scales, torch.tensor([valid], dtype=torch.int32, device="cuda"))
+        assert fp4.fp4_get_status() == fp4.OK
+        assert torch.equal(codes[:valid].cpu(), q[:valid]) and torch.equal(scales[:valid].cpu(), s[:valid])
+        assert (codes[valid:] == 99).all() and (scales[valid:] == -1).all()
 
 
 def test_weights_beyond_32_bit_offsets():

@@ -215,6 +215,20 @@ def test_combine_backward(tokens, topk, experts, cols, src, dst, weighted):
         assert torch.equal(yd[:n], dy[:n]) and torch.equal(dw2, dw) and torch.equal(yd[n:].cpu(), y[n:])
 
 
+@pytest.mark.parametrize("cols", [64, 33, 129])
+def test_slots_without_an_expert_have_no_gradient(cols):
+    """0, whatever dout and the weights hold there; and a token without any touches nothing."""
+    row_of = torch.tensor([[1, -1], [-1, -1]], dtype=torch.int32, device="cuda")
+    dout = torch.full((2, cols), float("inf"), device="cuda")
+    w = torch.full((2, 2), float("nan"), device="cuda")
+    w[0, 0] = 1.0
+    y = torch.ones(4, cols, device="cuda")
+    dy, dw = torch.full((4, cols), 7.0, device="cuda"), torch.full((2, 2), 5.0, device="cuda")
+    fp4.fp4_moe_combine_backward(dout, y, fp4.F32, row_of, w, 2, 2, cols, dy, fp4.F32, dw)
+    assert torch.isinf(dw[0, 0]) and dw.flatten()[1:].tolist() == [0.0, 0.0, 0.0]
+    assert torch.isinf(dy[1]).all() and (dy[[0, 2, 3]] == 7.0).all()
+
+
 def test_gradients_against_differences():
     """The whole way x -> rows -> sum, whose derivative along a direction is a difference of values:
     FP32 values near 1, step 2^-4, and a map that is linear in x and in the weights, so that the
