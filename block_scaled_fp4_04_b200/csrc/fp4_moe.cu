@@ -589,32 +589,16 @@ __global__ void __launch_bounds__(kSumThreads, R == 2 ? 3 : 4) moe_combine_kerne
   const int64_t t = blockIdx.x, to = t * p.cols;
   const T* y = static_cast<const T*>(p.y);
   const RowSpan<V, WAY> span(to, p.cols);
-  if (WAY == kByShift && blockIdx.y == gridDim.y - 1) {
-    for (int i = threadIdx.x; i < span.singles(); i += blockDim.x) {
-      const int e = span.single(i);
-      float all[1] = {0.0f}, v[1];
-      for (int j = 0; j < p.topk; ++j) {
-        const int32_t row = __ldg(p.row_of + t * p.topk + j);
-        if (row < 0) continue;
-        RowVec<T, 1> one;
-        one.load(y + row * p.cols + e);
-        one.unpack(v);
-        all[0] = fmaf(p.weights ? __ldg(p.weights + t * p.topk + j) : 1.0f, v[0], all[0]);
-      }
-      if (p.res) {
-        load_row_any<1>(p.res, p.res_bf16, to + e, v);
-        all[0] += v[0];
-      }
-      store_row_vec<1>(p.out, p.out_bf16, to + e, all);
-    }
-    return;
-  }
   const int round = blockDim.x / 32 * LANES, lane = threadIdx.x % 32;
   const int w0 = blockIdx.y * round * W + threadIdx.x / 32 * LANES + lane;
   const int limit = span.words + (WAY == kByShift);  // the word behind the last is asked for too
-  float sum[W][V] = {};
+  // by shift: one of the single elements for each of the first block's first threads
+  const bool extra = WAY == kByShift && blockIdx.y == 0 && static_cast<int>(threadIdx.x) < span.singles();
+  const int single = extra ? span.single(threadIdx.x) : 0;
+  float sum[W][V] = {}, sum1[1] = {0.0f};
   for (int j0 = 0; j0 < p.topk; j0 += R) {
     RowVec<T, V> in[R][W];
+    RowVec<T, 1> in1[R];
     float weight[R];
     bool on[R];
     int off[R];
@@ -624,6 +608,8 @@ __global__ void __launch_bounds__(kSumThreads, R == 2 ? 3 : 4) moe_combine_kerne
       const int32_t row = j0 + j < p.topk ? __ldg(p.row_of + s) : -1;
       on[j] = row >= 0;
       off[j] = WAY == kByShift ? static_cast<int>(row * p.cols + span.first) & (V - 1) : 0;
+      in1[j].zero();
+      if (extra && on[j]) in1[j].load(y + row * p.cols + single);
       weight[j] = on[j] && p.weights ? __ldg(p.weights + s) : 1.0f;
 #pragma unroll
       for (int i = 0; i < W; ++i) {
@@ -644,7 +630,20 @@ __global__ void __launch_bounds__(kSumThreads, R == 2 ? 3 : 4) moe_combine_kerne
 #pragma unroll
         for (int k = 0; k < V; ++k) sum[i][k] = fmaf(weight[j], v[k], sum[i][k]);
       }
+      if constexpr (WAY == kByShift) {
+        float v[1];
+        in1[j].unpack(v);
+        sum1[0] = fmaf(weight[j], v[0], sum1[0]);
+      }
     }
+  }
+  if (extra) {
+    float r[1];
+    if (p.res) {
+      load_row_any<1>(p.res, p.res_bf16, to + single, r);
+      sum1[0] += r[0];
+    }
+    store_row_vec<1>(p.out, p.out_bf16, to + single, sum1);
   }
 #pragma unroll
   for (int i = 0; i < W; ++i) {
@@ -666,8 +665,7 @@ static cudaError_t combine_rows(const CombineProblem& p, cudaStream_t st) {
   const int way = row_way(p.cols, p.bf16);
   const int64_t words = p.cols / (way == kByElement ? 1 : p.bf16 ? 8 : 4);
   const int threads = row_threads(words, 8 / R, kSumThreads);
-  dim3 grid = row_grid(p.tokens, words, static_cast<int64_t>(way == kByShift ? threads / 32 * 31 : threads) * (8 / R));
-  if (way == kByShift) ++grid.y;  // the single elements
+  const dim3 grid = row_grid(p.tokens, words, static_cast<int64_t>(way == kByShift ? threads / 32 * 31 : threads) * (8 / R));
   return with_rows(p.bf16, way, [&](auto t, auto n) {
     return launch_rows(moe_combine_kernel<decltype(t), decltype(n)::value, R>, grid, threads, 0, st, p);
   });
@@ -706,42 +704,63 @@ __global__ void __launch_bounds__(kGradThreads, R == 8 ? 3 : 4) moe_combine_grad
       dot[j] = 0.0f;
     }
     if constexpr (WAY == kByShift) {
-      // words at each row's own offset; dout's values for them come from L1 after the first row
+      // Words at each row's own offset, so that every row takes dout's values for them anew (from L1
+      // after the first); all loads of a round are asked for before the first is needed.
       const int64_t from = t * p.cols;
+      int64_t at[R];
+      int first[R], words[R];
+      int most = 0;
 #pragma unroll
       for (int j = 0; j < R; ++j) {
-        if (row[j] < 0) continue;
-        const int64_t at = row[j] * p.cols;
-        const RowSpan<V, WAY> span(at, p.cols);
-#pragma unroll 2
-        for (int w = threadIdx.x; w < span.words; w += blockDim.x) {
-          const int e = span.first + w * V;
-          RowVec<T, V> in, yr;
-          in.load_any(dout, from + e);
-          yr.zero();
-          if (dots) yr.load(y + at + e);
+        at[j] = row[j] * p.cols;
+        const RowSpan<V, WAY> span(at[j], p.cols);
+        first[j] = span.first;
+        words[j] = row[j] >= 0 ? span.words : 0;
+        most = max(most, words[j]);
+      }
+      for (int w = threadIdx.x; w < most; w += blockDim.x) {
+        RowVec<T, V> a[R], b[R], yr[R];
+#pragma unroll
+        for (int j = 0; j < R; ++j) {
+          a[j].zero();
+          b[j].zero();
+          yr[j].zero();
+          if (w >= words[j]) continue;
+          const int e = first[j] + w * V;
+          a[j].hold(dout, from + e);
+          b[j].hold(dout, from + e + V);
+          if (dots) yr[j].load(y + at[j] + e);
+        }
+#pragma unroll
+        for (int j = 0; j < R; ++j) {
+          a[j].join(b[j], from + first[j]);
           float d[V], v[V];
-          in.unpack(d);
-          yr.unpack(v);
+          a[j].unpack(d);
+          yr[j].unpack(v);
 #pragma unroll
           for (int k = 0; k < V; ++k) {
             dot[j] = fmaf(d[k], v[k], dot[j]);
             v[k] = weight[j] * d[k];
           }
-          if (p.dy) store_row_vec<V>(p.dy, p.dy_bf16, at + e, v);
+          if (p.dy && w < words[j]) store_row_vec<V>(p.dy, p.dy_bf16, at[j] + first[j] + w * V, v);
         }
+      }
+#pragma unroll
+      for (int j = 0; j < R; ++j) {
+        if (row[j] < 0) continue;
+        const RowSpan<V, WAY> span(at[j], p.cols);
         for (int i = threadIdx.x; i < span.singles(); i += blockDim.x) {
           const int e = span.single(i);
           RowVec<T, 1> in, yr;
           in.load(dout + from + e);
           yr.zero();
-          if (dots) yr.load(y + at + e);
+          if (dots) yr.load(y + at[j] + e);
           float d[1], v[1];
           in.unpack(d);
           yr.unpack(v);
           dot[j] = fmaf(d[0], v[0], dot[j]);
           v[0] = weight[j] * d[0];
-          if (p.dy) store_row_vec<1>(p.dy, p.dy_bf16, at + e, v);
+          if (p.dy) store_row_vec<1>(p.dy, p.dy_bf16, at[j] + e, v);
         }
       }
     } else {
@@ -788,18 +807,20 @@ __global__ void __launch_bounds__(kGradThreads, R == 8 ? 3 : 4) moe_combine_grad
 }
 
 template <int R>
-static cudaError_t combine_grad_rows(const CombineGradProblem& p, cudaStream_t st) {
-  const int way = row_way(p.cols, p.bf16);
+static cudaError_t combine_grad_rows(const CombineGradProblem& p, int way, cudaStream_t st) {
   const int threads = row_threads(p.cols / (way == kByElement ? 1 : p.bf16 ? 8 : 4), 2, kGradThreads);
   const dim3 grid(static_cast<unsigned>(p.tokens));
   return with_rows(p.bf16, way, [&](auto t, auto n) {
-    return launch_rows(moe_combine_grad_kernel<decltype(t), decltype(n)::value, R>, grid, threads, 0, st, p);
+    // by shift a row takes three times the registers: eight at a time would spill
+    constexpr int kWay = decltype(n)::value, kRows = kWay == kByShift && R == 8 ? 4 : R;
+    return launch_rows(moe_combine_grad_kernel<decltype(t), kWay, kRows>, grid, threads, 0, st, p);
   });
 }
 
 cudaError_t launch_moe_combine_grad(const CombineGradProblem& p, cudaStream_t st) {
-  if (p.topk <= 2) return combine_grad_rows<2>(p, st);
-  return p.topk <= 4 ? combine_grad_rows<4>(p, st) : combine_grad_rows<8>(p, st);
+  const int way = row_way(p.cols, p.bf16);
+  if (p.topk <= 2) return combine_grad_rows<2>(p, way, st);
+  return p.topk <= 4 ? combine_grad_rows<4>(p, way, st) : combine_grad_rows<8>(p, way, st);
 }
 
 }  // namespace fp4

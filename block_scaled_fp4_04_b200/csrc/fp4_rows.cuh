@@ -53,8 +53,8 @@ struct RowVec {
     }
   }
   // 16 bytes from any element offset of a 16-byte aligned matrix.  load_any(): by the word that holds
-  // the first of them and the next one, which has to be there too.  Or hold(), the first of the two;
-  // then shift() by all lanes of the warp, where the next lane holds the next word.
+  // the first of them and the next one, which has to be there too.  Or hold(), one of the two; then
+  // join() with the next one, or shift() by all lanes of the warp, where the next lane holds it.
   __device__ __forceinline__ void hold(const T* base, int64_t at) {
     static_assert(V * sizeof(T) == 16, "one 16-byte word");
     const uint4 a = *reinterpret_cast<const uint4*>(base + (at & ~static_cast<int64_t>(V - 1)));
@@ -82,12 +82,15 @@ struct RowVec {
     }
     take(x, at);
   }
-  __device__ __forceinline__ void load_any(const T* base, int64_t at) {
-    RowVec a, b;
-    a.hold(base, at);
-    b.hold(base, at + V);
-    const uint32_t x[8] = {a.w[0], a.w[1], a.w[2], a.w[3], b.w[0], b.w[1], b.w[2], b.w[3]};
+  __device__ __forceinline__ void join(const RowVec& next, int64_t at) {
+    const uint32_t x[8] = {w[0], w[1], w[2], w[3], next.w[0], next.w[1], next.w[2], next.w[3]};
     take(x, at);
+  }
+  __device__ __forceinline__ void load_any(const T* base, int64_t at) {
+    RowVec next;
+    hold(base, at);
+    next.hold(base, at + V);
+    join(next, at);
   }
   // the same bits to another row of this type
   __device__ __forceinline__ void store(T* p) const {
