@@ -27,6 +27,13 @@
 // it has only a piece of in the workspace (one slot for a tile that it ends, one for a tile that
 // it starts); the one whose piece completes the tile's K steps adds up the others' slots, clears
 // them, and finishes the tile.  No CTA waits for another one.
+//
+// Measured: 8192 x 8192 x 8192 334 us in short bursts, 3.29e15 operations a second (the MMA loop alone
+// reaches 4.2 to 4.5e15, 128 cycles per 128 x 256 x 32), 385 to 400 us under the power cap at 1.3 GHz, where
+// the loop's own limit is 345; the tensor pipe is 90% busy at 4096 x 8192 x 8192.  16 x 28672 x 8192 streams its
+// weights at 5.1e12 bytes a second.  A pair's K step of 256 channels x 256 tokens moves as many bytes into
+// shared memory as the MMAs read from it, together what its bandwidth allows: narrower tiles are
+// bound by it, and the epilogue stays out of shared memory.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <cuda_bf16.h>

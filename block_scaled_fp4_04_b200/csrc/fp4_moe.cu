@@ -21,9 +21,9 @@ namespace fp4 {
 // segment of slots per expert in its own shared counters; prefix sums over warps and experts turn
 // the counts into first rows; then each warp passes over its segment again and hands out rows in
 // order, 32 slots at a time: equal experts within the 32 find one another by votes on the bits of
-// their numbers (16384 slots in one block: 16.0 us; with the match instruction 18.7), and a slot's place among them is the number of
-// lower lanes.  No atomic decides an order, so the result is the
-// same every time.
+// their numbers (16384 slots in one block: 16.0 us; with the match instruction 18.7), and a slot's
+// place among them is the number of lower lanes.  No atomic decides an order, so the result is the
+// same every time.  What bounds it: launches, barriers and the latency of a few dependent steps.
 //
 // Up to kSortOneBlock slots one block does it all, up to kSortCluster a cluster of eight whose blocks
 // read one another's counts: one launch.  Beyond, blocks of kSortChunk slots or more first write
@@ -267,7 +267,9 @@ cudaError_t launch_moe_sort(const void* ids, int id_bytes, int64_t slots, int E,
 // allow).  Other widths: the words of the matrix that is written (for the gradient, also of the one
 // that it shares rows with) still stand at 16 bytes, from some element of the row on, and the values
 // for them come from the two words of the other matrix that hold them (RowVec::load_any); the
-// elements before and behind go one by one.  Narrow rows go one by one altogether.
+// elements before and behind go one by one.  Narrow rows go one by one altogether.  (2000 tokens, 6
+// choices, 2049 BF16 columns, floor 8.8 / 8.8 / 16.3 us: dispatch 15 us, sum 24, gradient 28; one by one
+// 25, 31 and 53.)
 enum { kByElement = 0, kByWord = 1, kByShift = 2 };
 
 static int row_way(int64_t cols, int bf16) {
@@ -324,7 +326,8 @@ static int row_threads(int64_t words, int per, int most) {
 }
 
 // y[row_of[t, j]] = x[t]: a block copies kCopyWords words a thread of one token's row to its topk
-// places.
+// places.  Bound by the copy rate: 16384 x 8 x 4096 BF16 (a tenth of the slots without an expert)
+// 174 us, 168 at the rate; 4096 x 4 x 2880 21 us, 18 at the rate.
 constexpr int kCopyWords = 4, kCopyThreads = 256;
 
 template <typename T, int WAY>
@@ -391,7 +394,8 @@ cudaError_t launch_moe_dispatch(const DispatchProblem& p, cudaStream_t st) {
 // A token's row is encoded once, a block a thread; its codes go to row row_of[t, j], its scales to
 // row scale_row_of[t, j] of the grouped layout.  Blocks behind the tokens' write the layout's pads:
 // num_experts blocks the rows behind each expert's last, then one block per 128-row block of the
-// buffer, which clears it if it lies behind the last expert's.
+// buffer, which clears it if it lies behind the last expert's.  8192 x 4 x 2880 BF16 to MXFP4: 20 us, 15
+// at the copy rate (49 with the block's maximum over lanes and scales stored byte by byte).
 constexpr int kCodeThreads = 256;
 
 __device__ __forceinline__ void clear_scale_rows(uint8_t* scales, int64_t atoms, int64_t block, int first_row) {
@@ -481,7 +485,9 @@ cudaError_t launch_moe_dispatch_codes(const DispatchCodesProblem& p, unsigned* s
 // -------------------------------------------------------------------------------- 8-bit rows
 // q = rn(x (1 / s)), s = max|x| / 127 of the row, at least 2^-126 (its reciprocal is finite, so
 // that a zero stays zero), 1 for a zero row.  A block per row: its words stay in registers between
-// the maximum and the encoding (kI8Words a thread; longer rows are read again).
+// the maximum and the encoding (kI8Words a thread; longer rows are read again).  Bound by the copy
+// rate: 16384 x 8 x 4096 BF16 97 us, 94 at the rate; by the barrier between the two for fewer rows,
+// 8192 x 4 x 2880 28 us of 22.
 constexpr int kI8Words = 4, kI8Threads = 1024;
 
 template <int V>
@@ -573,12 +579,13 @@ cudaError_t launch_quantize_i8(const I8RowsProblem& p, unsigned* status, cudaStr
 // ----------------------------------------------------------------------------------- combine
 // out[t] = sum_j w[t, j] y[row_of[t, j]] + res[t], the sum in FP32 in the order of j, rounded once.
 // R rows' words (2 for up to two choices, else 4) are asked for before the first is needed, 8 in all
-// a thread; four blocks an SM with four rows (8192 tokens, 4 choices, 2880 BF16 columns: 41 us, 45
-// with the three that the registers would allow).  By shift a warp asks for 32 words of each row
-// for 31 of the sum, which leaves the registers for as many loads as by word (4095 x 2 x 8191 FP32: 86 us;
-// with both words loaded by each lane, half as many at a time, 107; 8192 columns 60).
-// Blocks that stay for many tokens and ask for the next one's row numbers ahead were slower: 16384 x 8
-// x 4096 BF16 177 us, so 165.
+// a thread, by four blocks an SM with four rows (three, which the registers would allow, were 9%
+// slower).  Bound by the copy rate for long batches (16384 x 8 x 4096 BF16 164 us, 168 at the rate) and by
+// a block's two dependent loads, row numbers and rows, for short ones (4096 x 4 x 2880 23 us of 18).
+// By shift a warp asks for 32 words of each row for 31 of the sum, which leaves the registers for as
+// many loads as by word (4095 x 2 x 8191 FP32: 85 us; with both words loaded by each lane, half as many
+// at a time, 107; 8192 columns 60).  Blocks that stay for many tokens and ask for the next one's row
+// numbers ahead were slower: 16384 x 8 x 4096 BF16 177 us.
 constexpr int kSumThreads = 256;
 
 template <typename T, int WAY, int R>
@@ -680,7 +687,7 @@ cudaError_t launch_moe_combine(const CombineProblem& p, cudaStream_t st) {
 // that dout is read once and each dot product is summed in one place, in a fixed order.
 // Rows are taken R at a time (as many as there are choices, up to 8), and all their words of a column
 // are asked for before the first is needed; with R fixed at 8 and word after word it took 210 us
-// where it takes 70 (8192 tokens, 4 choices, 2880 BF16 columns).
+// where it takes 68 (8192 tokens, 4 choices, 2880 BF16 columns; 65 at the copy rate, its bound).
 constexpr int kGradThreads = 256;
 
 template <typename T, int WAY, int R>
