@@ -582,15 +582,17 @@ cudaError_t launch_quantize_i8(const I8RowsProblem& p, unsigned* status, cudaStr
 // a thread, by four blocks an SM with four rows (three, which the registers would allow, were 9%
 // slower).  Bound by the copy rate for long batches (16384 x 8 x 4096 BF16 164 us, 168 at the rate) and by
 // a block's two dependent loads, row numbers and rows, for short ones (4096 x 4 x 2880 23 us of 18).
-// By shift a warp asks for 32 words of each row for 31 of the sum, which leaves the registers for as
-// many loads as by word (4095 x 2 x 8191 FP32: 85 us; with both words loaded by each lane, half as many
-// at a time, 107; 8192 columns 60).  Blocks that stay for many tokens and ask for the next one's row
+// By shift a warp asks for 32 words of each row for 31 of the sum, instead of both words by each lane
+// (4095 x 2 x 8191 FP32: 107 us so, 82 with 8 words and three blocks, 74 with 4 words and five; with four
+// rows the other way round, 4766 x 3 x 3855 FP32 50 and 58 us).  Blocks that stay for many tokens and ask for the next one's row
 // numbers ahead were slower: 16384 x 8 x 4096 BF16 177 us.
 constexpr int kSumThreads = 256;
+template <int WAY, int R>
+__host__ __device__ constexpr int sum_words() { return WAY == kByShift && R == 2 ? 2 : 8 / R; }
 
 template <typename T, int WAY, int R>
-__global__ void __launch_bounds__(kSumThreads, R == 2 ? 3 : 4) moe_combine_kernel(const CombineProblem p) {
-  constexpr int V = word_size<T, WAY>(), W = 8 / R, LANES = WAY == kByShift ? 31 : 32;
+__global__ void __launch_bounds__(kSumThreads, R == 4 ? 4 : WAY == kByShift ? 5 : 3) moe_combine_kernel(const CombineProblem p) {
+  constexpr int V = word_size<T, WAY>(), W = sum_words<WAY, R>(), LANES = WAY == kByShift ? 31 : 32;
   rows_wait_prior();
   rows_allow_dependents();
   const int64_t t = blockIdx.x, to = t * p.cols;
@@ -671,8 +673,9 @@ template <int R>
 static cudaError_t combine_rows(const CombineProblem& p, cudaStream_t st) {
   const int way = row_way(p.cols, p.bf16);
   const int64_t words = p.cols / (way == kByElement ? 1 : p.bf16 ? 8 : 4);
-  const int threads = row_threads(words, 8 / R, kSumThreads);
-  const dim3 grid = row_grid(p.tokens, words, static_cast<int64_t>(way == kByShift ? threads / 32 * 31 : threads) * (8 / R));
+  const int each = way == kByShift ? sum_words<kByShift, R>() : sum_words<kByWord, R>();
+  const int threads = row_threads(words, each, kSumThreads);
+  const dim3 grid = row_grid(p.tokens, words, static_cast<int64_t>(way == kByShift ? threads / 32 * 31 : threads) * each);
   return with_rows(p.bf16, way, [&](auto t, auto n) {
     return launch_rows(moe_combine_kernel<decltype(t), decltype(n)::value, R>, grid, threads, 0, st, p);
   });

@@ -53,15 +53,12 @@ struct RowVec {
     }
   }
   // 16 bytes from any element offset of a 16-byte aligned matrix.  load_any(): by the word that holds
-  // the first of them and the next one, which has to be there too.  Or hold(), one of the two; then
-  // join() with the next one, or shift() by all lanes of the warp, where the next lane holds it.
+  // the first of them and the next one, which has to be there too (both through L1: neighbours share
+  // them).  Or hold(), one of the two; then join() with the next one, or shift() by all lanes of the
+  // warp, where the next lane holds it.
   __device__ __forceinline__ void hold(const T* base, int64_t at) {
     static_assert(V * sizeof(T) == 16, "one 16-byte word");
-    const uint4 a = *reinterpret_cast<const uint4*>(base + (at & ~static_cast<int64_t>(V - 1)));
-    w[0] = a.x;
-    w[1] = a.y;
-    w[2] = a.z;
-    w[3] = a.w;
+    load(base + (at & ~static_cast<int64_t>(V - 1)));
   }
   __device__ __forceinline__ void take(const uint32_t (&x)[8], int64_t at) {
     const int off = static_cast<int>(at) & (V - 1), words = off * static_cast<int>(sizeof(T)) / 4;
@@ -87,10 +84,10 @@ struct RowVec {
     take(x, at);
   }
   __device__ __forceinline__ void load_any(const T* base, int64_t at) {
-    RowVec next;
-    hold(base, at);
-    next.hold(base, at + V);
-    join(next, at);
+    const uint4* q = reinterpret_cast<const uint4*>(base + (at & ~static_cast<int64_t>(V - 1)));
+    const uint4 a = q[0], b = q[1];
+    const uint32_t x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    take(x, at);
   }
   // the same bits to another row of this type
   __device__ __forceinline__ void store(T* p) const {
