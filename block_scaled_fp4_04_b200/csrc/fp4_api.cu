@@ -893,6 +893,7 @@ fp4_status fp4_moe_dispatch_codes(const void* x, int64_t tokens, int64_t cols, f
   DispatchCodesProblem p{};
   const fp4_status cs = check_codes(fmt, codes, scales, global, cols, &p.q);
   if (cs != FP4_OK) return cs;
+  if (static_cast<const void*>(codes) == x) return fail(FP4_ERR_INVALID_ARG, "codes must not be x");
   unsigned* status;
   const fp4_status s = device_state(&status);
   if (s != FP4_OK) return s;
@@ -913,6 +914,7 @@ static fp4_status i8_rows(const void* x, int64_t rows, int64_t cols, fp4_dtype i
                           const int32_t* valid, int8_t* codes, float* row_scales, void* stream) {
   if (!x || !codes || !row_scales) return fail(FP4_ERR_INVALID_ARG, "null pointer");
   if (cols % 16 != 0) return fail(FP4_ERR_INVALID_ARG, "8-bit rows need cols % 16 == 0");
+  if (static_cast<const void*>(codes) == x) return fail(FP4_ERR_INVALID_ARG, "codes must not be x");
   if (!aligned16(x) || !aligned16(codes)) return fail(FP4_ERR_INVALID_ARG, "x and codes must be 16-byte aligned");
   if (!aligned4(row_scales) || !aligned4(valid)) return fail(FP4_ERR_INVALID_ARG, "row_scales / rows_valid alignment");
   unsigned* status;

@@ -512,9 +512,10 @@ __global__ void __launch_bounds__(I8Cfg<BN, PAIR>::kThreads, 1)
           const int all = atomicAdd(cnt, w.kb1 - w.kb0) + w.kb1 - w.kb0;
           done = all == p.num_kb;
           if (done) *cnt = 0;
+          __threadfence();
         }
         done = __shfl_sync(0xFFFFFFFFu, done, 0);
-        if (done) __threadfence();
+        __syncwarp();  // lane 0's fences hold for the warp: the sums before its count, the others' after
       }
       if (done) {
 #pragma unroll 1

@@ -53,23 +53,23 @@ def test_dispatch_sizes():
     assert _call("fp4_moe_dispatch", DISP, tokens=(1 << 29) + 1) == fp4.ERR_UNSUPPORTED
 
 
-CODES = dict(x=16, tokens=8, cols=64, dt=fp4.F32, topk=2, row=16, srow=16, E=4, off=16, fmt=fp4.NVFP4, codes=16, scales=32,
+CODES = dict(x=48, tokens=8, cols=64, dt=fp4.F32, topk=2, row=16, srow=16, E=4, off=16, fmt=fp4.NVFP4, codes=16, scales=32,
              g=16, stream=None)
 
 
 @pytest.mark.parametrize("kw", [
     dict(x=None), dict(row=None), dict(srow=None), dict(off=None), dict(codes=None), dict(scales=None), dict(g=None),
     dict(E=0), dict(E=1025), dict(fmt=fp4.MXFP8), dict(fmt=7), dict(cols=48), dict(tokens=0), dict(dt=9), dict(x=8),
-    dict(codes=8), dict(scales=8), dict(g=2), dict(srow=2), dict(off=1)])
+    dict(codes=8), dict(scales=8), dict(g=2), dict(srow=2), dict(off=1), dict(codes=48)])
 def test_dispatch_codes_refuses(kw):
     assert _call("fp4_moe_dispatch_codes", CODES, **kw) == fp4.ERR_INVALID_ARG
 
 
-I8D = dict(x=16, tokens=8, cols=64, dt=fp4.F32, topk=2, row=16, codes=16, scales=16, stream=None)
+I8D = dict(x=32, tokens=8, cols=64, dt=fp4.F32, topk=2, row=16, codes=16, scales=16, stream=None)
 
 
 @pytest.mark.parametrize("kw", [dict(x=None), dict(row=None), dict(codes=None), dict(scales=None), dict(cols=40),
-                                dict(tokens=0), dict(dt=3), dict(x=8), dict(codes=24), dict(scales=2)])
+                                dict(tokens=0), dict(dt=3), dict(x=8), dict(codes=24), dict(scales=2), dict(codes=32)])
 def test_dispatch_i8_refuses(kw):
     assert _call("fp4_moe_dispatch_i8", I8D, **kw) == fp4.ERR_INVALID_ARG
 
@@ -95,11 +95,11 @@ def test_combine_backward_refuses(kw):
     assert _call("fp4_moe_combine_backward", GRAD, **kw) == fp4.ERR_INVALID_ARG
 
 
-Q8 = dict(x=16, rows=8, cols=64, dt=fp4.F32, codes=16, scales=16, valid=16, stream=None)
+Q8 = dict(x=32, rows=8, cols=64, dt=fp4.F32, codes=16, scales=16, valid=16, stream=None)
 
 
 @pytest.mark.parametrize("kw", [dict(x=None), dict(codes=None), dict(scales=None), dict(rows=0), dict(cols=0), dict(cols=24),
-                                dict(dt=2), dict(x=8), dict(codes=8), dict(scales=2), dict(valid=2)])
+                                dict(dt=2), dict(x=8), dict(codes=8), dict(scales=2), dict(valid=2), dict(codes=32)])
 def test_quantize_i8_refuses(kw):
     assert _call("fp4_quantize_i8", Q8, **kw) == fp4.ERR_INVALID_ARG
 
