@@ -42,6 +42,10 @@ struct SortArgs {
 constexpr int kSortThreads = 1024;
 constexpr int64_t kSortOneBlock = 512, kSortCluster = 32768, kSortChunk = 4096;
 constexpr int kSortClusterBlocks = 8, kSortMaxBlocks = 128, kSortKeys = 16;
+// Shared memory of a block: a column of counters for each warp, three more, and two launches' partial sums.
+constexpr size_t sort_smem(int threads, int E, bool parts) {
+  return (static_cast<size_t>(threads / 32) * (E + 1) + 3 * E + (parts ? 2 * threads : 0)) * 4;
+}
 
 template <typename ID>
 __device__ __forceinline__ int sort_key(const SortArgs& a, int64_t s, int64_t hi) {
@@ -234,11 +238,18 @@ static cudaError_t sort_typed(const SortArgs& a, cudaStream_t st) {
   // one block: as many warps as segments of 32 slots, but at least one expert's column a thread
   const int64_t want = std::max<int64_t>((std::min(a.chunk, a.slots) + 31) / 32 * 32, (std::min(a.E, 256) + 31) / 32 * 32);
   const int threads = a.hist ? kSortThreads : static_cast<int>(std::min<int64_t>(kSortThreads, want));
-  const size_t smem = (static_cast<size_t>(threads / 32) * (a.E + 1) + 3 * a.E + (a.hist ? 2 * threads : 0)) * 4;
+  const size_t smem = sort_smem(threads, a.E, a.hist != nullptr);
   cudaError_t e = cudaSuccess;
-  if (smem > 48 * 1024) {
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  // The limit is one for all calls of a kernel on a device, from all host threads: the largest sort's, and
+  // never less again (with each call's own size a call could find another's, and be refused).
+  static bool attr_done[64] = {false};
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (smem > 48 * 1024 && (dev < 0 || dev >= 64 || !attr_done[dev])) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(sort_smem(kSortThreads, kMaxGroups, true)));
     if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < 64) attr_done[dev] = true;
   }
   if (a.hist) {
     e = launch_rows(moe_hist_kernel<ID>, dim3(a.blocks), kSortThreads, static_cast<size_t>(a.E + 1) * 4, st, a);
