@@ -98,6 +98,12 @@ struct I8Cfg {
   static_assert((2 * kStages + 5) * 8 + 16 <= kScaleOff, "barriers");
 };
 
+// A pair's tile width: the rows that share weights in `tiles` equal parts, rounded up to 64.  (Unsigned: the
+// sum passes 2^31 below the largest number of rows.)
+__host__ __device__ __forceinline__ int pair_width(uint32_t rows, uint32_t tiles) {
+  return static_cast<int>((rows + tiles - 1) / tiles + 63) / 64 * 64;
+}
+
 // Token rows of a pair's boxes: half of a tile's width of 64, 128, 192 or 256.
 struct I8TokenMaps {
   CUtensorMap box[4];
@@ -165,7 +171,7 @@ struct I8Sched {
     w.n0 = wt * kRows + sub_row;
     w.n_valid = max(0, min(128, p.N - w.n0));
     w.w_row = w.group * p.N + w.n0;
-    w.width = PAIR ? ((row_end - row0 + tts - 1) / tts + 63) / 64 * 64 : BN;
+    w.width = PAIR ? pair_width(row_end - row0, tts) : BN;
     w.t0 = row0 + tt * w.width;
     w.t_valid = min(w.width, row_end - w.t0);
     w.x_row = w.t0 + (sub_row ? w.width / 2 : 0);
@@ -713,7 +719,7 @@ int launch_gemm_i8(const I8Problem& g, unsigned* status, cudaStream_t st, const 
     return 1;
   }
   const int64_t rows_w = g.N * std::max(1, g.num_groups);
-  const int64_t width = ((g.M + pl.tiles_t - 1) / pl.tiles_t + 63) / 64 * 64;  // as the kernel has it
+  const int width = pair_width(static_cast<uint32_t>(g.M), static_cast<uint32_t>(pl.tiles_t));
   CUtensorMap w;
   I8TokenMaps x{};
   bool ok = make_tensor_map_u8(&w, g.B, static_cast<uint64_t>(g.K), static_cast<uint64_t>(rows_w), 128);
