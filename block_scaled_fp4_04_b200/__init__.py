@@ -826,6 +826,8 @@ def quantize_i8(x: torch.Tensor, offsets: Optional[torch.Tensor] = None, stream=
     _dense("x", x, x, x.shape)
     if offsets is not None:
         _dense("offsets", offsets, x, (offsets.numel(),), torch.int32)
+        if offsets.numel() < 2:  # (an empty tensor's address is none, which would mean all rows)
+            raise ValueError("offsets must be [experts + 1]")
     rows, cols = x.numel() // max(1, x.shape[-1]), x.shape[-1]
     with _on(x, stream) as s:
         codes = torch.empty(x.shape, dtype=torch.int8, device=x.device)
