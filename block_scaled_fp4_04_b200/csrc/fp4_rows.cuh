@@ -26,7 +26,6 @@ __device__ __forceinline__ void rows_wait_prior() { asm volatile("griddepcontrol
 // element.
 template <typename T, int V>
 struct RowVec {
-  static constexpr int kElements = V;
   static constexpr int kWords = V == 1 ? 1 : V * static_cast<int>(sizeof(T)) / 4;
   uint32_t w[kWords];
   __device__ __forceinline__ void zero() {
