@@ -279,8 +279,8 @@ cudaError_t launch_moe_sort(const void* ids, int id_bytes, int64_t slots, int E,
 // that it shares rows with) still stand at 16 bytes, from some element of the row on, and the values
 // for them come from the two words of the other matrix that hold them (RowVec::load_any); the
 // elements before and behind go one by one.  Narrow rows go one by one altogether.  (2000 tokens, 6
-// choices, 2049 BF16 columns, floor 8.8 / 8.8 / 16.3 us: dispatch 15 us, sum 24, gradient 28; one by one
-// 25, 31 and 53.)
+// choices, 2049 BF16 columns, floor 8.8 / 8.8 / 16.3 us: dispatch 12.5 us, sum 24, gradient 26.7; one by one
+// 20, 32 and 53.)
 enum { kByElement = 0, kByWord = 1, kByShift = 2 };
 
 static int row_way(int64_t cols, int bf16) {
@@ -406,7 +406,8 @@ cudaError_t launch_moe_dispatch(const DispatchProblem& p, cudaStream_t st) {
 // row scale_row_of[t, j] of the grouped layout.  Blocks behind the tokens' write the layout's pads:
 // num_experts blocks the rows behind each expert's last, then one block per 128-row block of the
 // buffer, which clears it if it lies behind the last expert's.  8192 x 4 x 2880 BF16 to MXFP4: 20 us, 15
-// at the copy rate (49 with the block's maximum over lanes and scales stored byte by byte).
+// at the copy rate (49 with the block's maximum over lanes and scales stored byte by byte); to NVFP4, whose blocks
+// are half as long, 28 us of 15.
 constexpr int kCodeThreads = 256;
 
 __device__ __forceinline__ void clear_scale_rows(uint8_t* scales, int64_t atoms, int64_t block, int first_row) {
@@ -590,13 +591,15 @@ cudaError_t launch_quantize_i8(const I8RowsProblem& p, unsigned* status, cudaStr
 // ----------------------------------------------------------------------------------- combine
 // out[t] = sum_j w[t, j] y[row_of[t, j]] + res[t], the sum in FP32 in the order of j, rounded once.
 // R rows' words (2 for up to two choices, else 4) are asked for before the first is needed, 8 in all
-// a thread, by four blocks an SM with four rows (three, which the registers would allow, were 9%
-// slower).  Bound by the copy rate for long batches (16384 x 8 x 4096 BF16 164 us, 168 at the rate) and by
-// a block's two dependent loads, row numbers and rows, for short ones (4096 x 4 x 2880 23 us of 18).
+// a thread, by four blocks an SM with four rows.  (Three blocks are 1 to 6% slower for FP32 rows by word:
+// 4096 x 4 x 2880 41.7 us, with four 39.5.  BF16 ones spill 40 bytes in four blocks' 64 registers, and three
+// are up to 7% faster there, 21.8 us for 23.4, but 1% slower for 2000 x 6 x 2048.)  Bound by the copy rate for
+// long batches (16384 x 8 x 4096 BF16 164 us, 168 at the rate) and by a block's two dependent loads, row
+// numbers and rows, for short ones (4096 x 4 x 2880 23 us of 18).
 // By shift a warp asks for 32 words of each row for 31 of the sum, instead of both words by each lane
 // (4095 x 2 x 8191 FP32: 107 us so, 82 with 8 words and three blocks, 74 with 4 words and five; with four
-// rows the other way round, 4766 x 3 x 3855 FP32 50 and 58 us).  Blocks that stay for many tokens and ask for the next one's row
-// numbers ahead were slower: 16384 x 8 x 4096 BF16 177 us.
+// rows the other way round, 4766 x 3 x 3855 FP32 50 and 58 us).  Blocks that stay for many tokens and ask
+// for the next one's row numbers ahead were slower: 16384 x 8 x 4096 BF16 177 us.
 constexpr int kSumThreads = 256;
 template <int WAY, int R>
 __host__ __device__ constexpr int sum_words() { return WAY == kByShift && R == 2 ? 2 : 8 / R; }
@@ -725,8 +728,10 @@ __global__ void __launch_bounds__(kGradThreads, R == 8 ? 3 : 4) moe_combine_grad
       dot[j] = 0.0f;
     }
     if constexpr (WAY == kByShift) {
-      // Words at each row's own offset, so that every row takes dout's values for them anew (from L1
-      // after the first); all loads of a round are asked for before the first is needed.
+      // Words at each row's own offset, so that every row takes dout's two words around them anew; all
+      // loads of a round are asked for before the first is needed.  They pass L1 by: through it 8192 x 4 x
+      // 2881 BF16 took 103 us for 93.5, 4766 x 3 x 3855 FP32 104 for 99, 2000 x 6 x 2049 BF16 27.2 for 26.6; only
+      // 4095 x 2 x 8191 FP32 (138.8 for 139.8) and 300 x 4 x 2050 BF16 (6.2 for 6.7) were faster.
       const int64_t from = t * p.cols;
       int64_t at[R];
       int first[R], words[R];
