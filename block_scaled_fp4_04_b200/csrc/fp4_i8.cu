@@ -56,7 +56,8 @@ struct I8Args {
   int early_w;         // weights may be read before the preceding kernel finishes
   // A weight's tokens fit one tile (by experts: on average, whatever the offsets say): it need not stay in
   // L2.  Asking each tile on the device instead made no difference for even experts, nor for 64 rows of one
-  // of 64 experts of 5760 x 2880 (25.7 us), and 100 rows of one of 100 of 28672 x 8192 took 267 us for 233.
+  // of 64 experts of 5760 x 2880, and 100 rows of one of 100 experts of 28672 x 8192 took 254 us for 248
+  // (medians of 62 bursts in turn, 248-270 and 225-264).
   int weights_once;
   int split;
   int tiles_w, tiles_t;  // tiles along the channels, along the tokens (dense)
